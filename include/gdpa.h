@@ -25,6 +25,11 @@
  * (gdpa_bwd, gdpa_bwd_sliding).  gdpa_fwd_mx takes q and k in MXFP8,
  * gdpa_fwd_mxfp8 q, k and v.
  *
+ * For serving, keys and values of earlier calls stay in a paged cache of e4m3
+ * codes (gdpa_cache_t): gdpa_cache_append stores new tokens, rotating them by
+ * their position on the way, and gdpa_cache_fwd attends from new tokens to
+ * everything that is stored.
+ *
  * An empty key set gives o_i = 0.  The GELU's tanh is rewritten as a
  * logistic function, gelu(x) = x sigma(2u), whose sigma takes one of two
  * routes (gdpa_act_route_t): the special-function unit's exp2 and reciprocal
@@ -408,6 +413,128 @@ gdpa_status_t gdpa_device_status(void* stream);
  * failure path: no fault, trap or hang is involved.
  */
 gdpa_status_t gdpa_wait_selftest(int timeout_ms, void* stream);
+
+/* How gdpa_cache_append pairs the coordinates it rotates (rot_dim of a head's D). */
+typedef enum {
+  GDPA_ROPE_HALF = 0,        /* pairs (i, i + rot_dim / 2) */
+  GDPA_ROPE_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1) */
+} gdpa_rope_style_t;
+
+/*
+ * A paged key/value cache in 8 bits.  The struct and every buffer it names
+ * are the caller's; the calls below read the struct only while they run.
+ *
+ *   k_codes, v_codes  device uint8 [num_pages, H, page_tokens, D]  OCP e4m3
+ *   k_sf, v_sf        device uint8 [num_pages, H, page_tokens/16]  OCP E8M0
+ *   value = e4m3(code) * 2^(sf - 127), one scale for 16 tokens of one head
+ *
+ * Token t of sequence b lies in page page_table[b, t / page_tokens] at slot
+ * t % page_tokens.  H is the number of key/value heads, D 64 or 128,
+ * page_tokens a power of two from 16 to 1024.  Codes must be 16-byte aligned.
+ * A new page needs no clearing: a block's scale and codes are not read before
+ * they were written.
+ *
+ * inv_freq: HOST double [rot_dim / 2], radians per position of each rotated
+ * pair (NULL with rot_dim 0: no rotation); rot_dim: how many leading
+ * coordinates of a head turn, a multiple of 16 up to D.
+ */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_sf;
+  void* v_sf;
+  int32_t num_pages;
+  int32_t page_tokens;
+  int32_t H;
+  int32_t D;
+  const double* inv_freq;
+  int32_t rot_dim;
+  int32_t rope_style; /* gdpa_rope_style_t */
+} gdpa_cache_t;
+
+/*
+ * gdpa_cache_append -- stores the keys and values of new tokens, and rotates
+ * keys and (optionally) queries by their positions.
+ *
+ *   k, v   device bf16, row t at k + t * k_stride (elements): [H, D]
+ *   q      device bf16, row t at q + t * q_stride: [Hq, D]; may be NULL
+ *          (Hq, q_stride and q_out are ignored then)
+ *   q_out  device bf16 [T, Hq, D] contiguous: the rotated queries (may be q
+ *          itself if q is contiguous)
+ *   offsets     device int32 [B+1], offsets[0] = 0, non-decreasing: rows
+ *               [offsets[b], offsets[b+1]) are the new tokens of sequence b
+ *   kv_lens     device int32 [B]: tokens of each sequence AFTER this call, so
+ *               new row i of sequence b has position
+ *               kv_lens[b] - (offsets[b+1] - offsets[b]) + i
+ *   page_table  device int32 [B, max_pages]; entries behind a sequence's last
+ *               page are not read
+ *   T           rows of q, k and v; rows from offsets[B] on are padding, not
+ *               read, and q_out keeps what it held there
+ *
+ * A pair (x, y) at position p turns by p * inv_freq: (x cos - y sin, y cos + x
+ * sin).  The angle is exact to 2^-32 turns at every position (a 64-bit
+ * fraction of a turn, times p, modulo 1), sine and cosine are fp32.
+ *
+ * Quantisation: for the tokens that this call adds to a block of 16 and one
+ * head, A = the largest finite magnitude; e = the smallest integer >= -127
+ * with A <= 448 * 2^e.  If the block holds earlier tokens, e is at least its
+ * present exponent, and where it grows the earlier codes are rounded again to
+ * e4m3(code * 2^(e_old - e)).  Codes are rounded to nearest even; what is not
+ * finite becomes the NaN code.
+ *
+ * Strides are in elements, multiples of 8, and at least H * D (Hq * D); q, k,
+ * v and q_out 16-byte aligned.  Two sequences may share pages that both only
+ * read; a block into which both append has undefined contents.
+ *
+ * Asynchronous on `stream`, one kernel, no allocation, no host read of device
+ * data: it may be captured into a graph, which then reads offsets, lengths and
+ * table anew at each replay.  Offsets, lengths or page numbers out of range
+ * never make it write outside the buffers: the tokens concerned are skipped
+ * and gdpa_device_status() returns GDPA_ERR_INVALID_ARG.
+ */
+gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, const int32_t* offsets,
+                                const int32_t* kv_lens, const int32_t* page_table, int64_t T, int B, int Hq,
+                                int max_pages, void* q_out, void* stream);
+
+/*
+ * gdpa_cache_fwd -- softmax attention of new tokens over the cache:
+ *   o = sum_j exp(scale <q, k_j> - m) v_j / sum_j exp(scale <q, k_j> - m)
+ * Query head h reads key/value head h / (Hq / H); Hq must be a multiple of H.
+ * Row i of sequence b (n rows, kv_lens[b] = L tokens in the cache) sees
+ *   causal = 1: the keys j <= L - n + i (its own position: the rows are the
+ *               last n tokens); with window_tokens W > 0 only those with
+ *               j > L - n + i - W as well
+ *   causal = 0: all L keys (window_tokens must be 0)
+ * A row that sees no key gives 0, and -inf in lse.  Keys that a row does not
+ * see never influence it, whatever they hold (infinite and NaN values included).
+ *
+ *   q      device bf16, row t at q + t * q_stride (elements): [Hq, D]
+ *   out    device bf16 [T, Hq, D] contiguous; rows from offsets[B] on keep
+ *          what they held
+ *   lse    optional (may be NULL) device fp32 [T, Hq]: ln sum_j exp(scale <q, k_j>)
+ *   offsets, kv_lens, page_table, max_pages, T, B  as gdpa_cache_append; the
+ *          cache must already hold the kv_lens[b] tokens
+ *   max_q  the most rows any sequence has, as far as the caller knows: it
+ *          picks the kernel; sequences with more rows are still computed
+ *   workspace  device memory, 16-byte aligned, of at least
+ *          gdpa_cache_workspace_size() bytes, the caller's.  It holds nothing
+ *          between calls; calls (or captured graphs) that may run at the same
+ *          time need one each
+ *
+ * Asynchronous on `stream`, no allocation, no host read of device data (may
+ * be captured).  Offsets, lengths or page numbers out of range are handled as
+ * in gdpa_cache_append: keys on a page out of range are not seen.  A workspace
+ * that is too small returns GDPA_ERR_NO_MEMORY.
+ */
+gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q, int64_t q_stride, const int32_t* offsets,
+                             const int32_t* kv_lens, const int32_t* page_table, int64_t T, int B, int Hq,
+                             int max_pages, int max_q, int causal, int window_tokens, float scale, void* out,
+                             float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdpa_cache_fwd needs on the current device for Hq query
+ * heads and max_q rows a sequence. */
+gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes);
 
 /* Human-readable name of a status code (static string). */
 const char* gdpa_status_string(int status);

@@ -1,7 +1,8 @@
 """Builds ``libgdpa.so`` in-tree with nvcc for sm_103a.
 
-Four translation units are compiled in parallel (the kernels, the API layer,
-the host planner, the allocation-free entry point) and linked into one shared library next to this file.  The
+The translation units (the forward and backward kernels, the API layer, the
+host planner, the allocation-free entry point, the paged cache) are compiled
+in parallel and linked into one shared library next to this file.  The
 CUDA runtime is linked statically, so the library needs only the driver at
 run time.  Nothing here needs a GPU: nvcc cross-compiles for sm_103a.
 """
@@ -20,7 +21,7 @@ LIB = os.path.join(HERE, "libgdpa.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["gdpa_kernels.cu", "gdpa_bwd.cu", "gdpa_api.cu", "gdpa_plan.cpp", "gdpa_noalloc.cu"]
+SOURCES = ["gdpa_kernels.cu", "gdpa_bwd.cu", "gdpa_api.cu", "gdpa_plan.cpp", "gdpa_noalloc.cu", "gdpa_cache.cu"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,199 @@
+// gdpa_cache.cu -- the C ABI of the paged key/value cache (gdpa_cache_append,
+// gdpa_cache_fwd; declared in include/gdpa.h): argument checks and launches.
+// Nothing here allocates, synchronises or reads device data.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "gdpa_cache_append.cuh"
+#include "gdpa_cache_fwd.cuh"
+#include "gdpa_internal.h"
+
+namespace gdpa {
+
+int* device_status_word(int device);  // gdpa_kernels.cu
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Device {
+  int id = 0, sms = 0;
+  int* status = nullptr;
+};
+
+// The current device, its SM count and status word.  The first call on a
+// device may load the module there, which a strictly captured thread must be
+// allowed to do.
+gdpa_status_t current_device(Device* d) {
+  if (cudaGetDevice(&d->id) != cudaSuccess) return GDPA_ERR_CUDA;
+  if (d->id < 0 || d->id >= kMaxDevices) return GDPA_ERR_UNSUPPORTED;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
+  d->status = device_status_word(d->id);
+  const bool ok = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) == cudaSuccess && d->sms > 0;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess || !ok || !d->status) return GDPA_ERR_CUDA;
+  return GDPA_OK;
+}
+
+gdpa_status_t check_cache(const gdpa_cache_t* c) {
+  if (!c) return GDPA_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->H <= 0 || c->page_tokens <= 0 || c->rot_dim < 0) return GDPA_ERR_INVALID_ARG;
+  if (c->rope_style != GDPA_ROPE_HALF && c->rope_style != GDPA_ROPE_INTERLEAVED) return GDPA_ERR_INVALID_ARG;
+  if (c->D != 64 && c->D != 128) return GDPA_ERR_UNSUPPORTED;
+  if (c->page_tokens < kCacheBlock || c->page_tokens > 1024 || (c->page_tokens & (c->page_tokens - 1)))
+    return GDPA_ERR_UNSUPPORTED;
+  if ((int64_t)c->H * c->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  if (c->rot_dim > c->D) return GDPA_ERR_INVALID_ARG;
+  if (c->rot_dim % 16) return GDPA_ERR_UNSUPPORTED;
+  if (c->rot_dim > 0) {
+    if (!c->inv_freq) return GDPA_ERR_INVALID_ARG;
+    for (int i = 0; i < c->rot_dim / 2; ++i)
+      if (!std::isfinite(c->inv_freq[i])) return GDPA_ERR_INVALID_ARG;
+  }
+  if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_sf || !c->v_sf || !aligned(c->k_codes, 16) ||
+                           !aligned(c->v_codes, 16)))
+    return GDPA_ERR_INVALID_ARG;
+  return GDPA_OK;
+}
+
+// Rows of H heads of D at a stride: both in elements.
+gdpa_status_t check_rows(const void* p, int64_t stride, int64_t H, int64_t D) {
+  if (!p || !aligned(p, 16) || stride < H * D) return GDPA_ERR_INVALID_ARG;
+  return stride % 8 ? GDPA_ERR_UNSUPPORTED : GDPA_OK;
+}
+
+gdpa_status_t check_batch(const gdpa_cache_t* c, int64_t T, int B, int max_pages) {
+  if (T < 0 || B < 0 || max_pages < 0) return GDPA_ERR_INVALID_ARG;
+  if (T >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * c->page_tokens >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
+  return GDPA_OK;
+}
+
+CacheView view(const gdpa_cache_t* c) {
+  int lp = 0;
+  while ((1 << lp) < c->page_tokens) ++lp;
+  return CacheView{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes),
+                   static_cast<uint8_t*>(c->k_sf),    static_cast<uint8_t*>(c->v_sf),
+                   c->num_pages,                      lp,
+                   c->H};
+}
+
+// f / 2 pi modulo 1 as a 64-bit fraction.
+unsigned long long turn_fraction(double f) {
+  double t = f * 0.15915494309189535;  // 1 / 2 pi
+  t -= std::floor(t);
+  if (t >= 1.0) t = 0.0;
+  const double hi = std::floor(t * 4294967296.0);
+  const double lo = std::floor((t * 4294967296.0 - hi) * 4294967296.0);
+  return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
+}
+
+}  // namespace
+}  // namespace gdpa
+
+using namespace gdpa;
+
+extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_t q_stride, const void* k,
+                                           int64_t k_stride, const void* v, int64_t v_stride, const int32_t* offsets,
+                                           const int32_t* kv_lens, const int32_t* page_table, int64_t T, int B,
+                                           int Hq, int max_pages, void* q_out, void* stream) {
+  gdpa_status_t st = check_cache(cache);
+  if (st != GDPA_OK) return st;
+  if ((st = check_batch(cache, T, B, max_pages)) != GDPA_OK) return st;
+  if (q && Hq <= 0) return GDPA_ERR_INVALID_ARG;
+  if (q && (int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return GDPA_OK;
+  if ((st = check_rows(k, k_stride, cache->H, cache->D)) != GDPA_OK) return st;
+  if ((st = check_rows(v, v_stride, cache->H, cache->D)) != GDPA_OK) return st;
+  if (q) {
+    if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
+    if ((st = check_rows(q_out, (int64_t)Hq * cache->D, Hq, cache->D)) != GDPA_OK) return st;
+  }
+  if (!offsets || !kv_lens || !page_table || max_pages == 0) return GDPA_ERR_INVALID_ARG;
+  Device dev;
+  if ((st = current_device(&dev)) != GDPA_OK) return st;
+  AppendParams p;
+  p.cache = view(cache);
+  p.batch = CacheBatch{offsets, kv_lens, page_table, static_cast<int>(T), B, max_pages, dev.status};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.Hq = q ? Hq : 0;
+  p.rot = cache->rot_dim;
+  p.interleaved = cache->rope_style == GDPA_ROPE_INTERLEAVED ? 1 : 0;
+  for (int i = 0; i < 64; ++i) p.freq[i] = i < p.rot / 2 ? turn_fraction(cache->inv_freq[i]) : 0;
+  const int rows = T > 4 * (int64_t)B ? 16 : 1;
+  const int64_t groups = (T + rows - 1) / rows;
+  const int y = groups >= 2 * dev.sms ? 1 : 2;
+  const size_t smem = (size_t)(rows + kCacheBlock - 1) * (p.rot / 2) * sizeof(float2);
+  const dim3 grid(static_cast<unsigned>(groups), y);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->D == 128)
+    gdpa_cache_append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p, rows);
+  else
+    gdpa_cache_append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p, rows);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes) {
+  if (!bytes) return GDPA_ERR_INVALID_ARG;
+  *bytes = 0;
+  const gdpa_status_t st = check_cache(cache);
+  if (st != GDPA_OK) return st;
+  if (Hq <= 0 || Hq % cache->H || max_q <= 0) return GDPA_ERR_INVALID_ARG;
+  if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  *bytes = 16;
+  return GDPA_OK;
+}
+
+extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q, int64_t q_stride,
+                                        const int32_t* offsets, const int32_t* kv_lens, const int32_t* page_table,
+                                        int64_t T, int B, int Hq, int max_pages, int max_q, int causal,
+                                        int window_tokens, float scale, void* out, float* lse, void* workspace,
+                                        int64_t workspace_bytes, void* stream) {
+  gdpa_status_t st = check_cache(cache);
+  if (st != GDPA_OK) return st;
+  if ((st = check_batch(cache, T, B, max_pages)) != GDPA_OK) return st;
+  if (Hq <= 0 || Hq % cache->H || max_q <= 0 || window_tokens < 0 || (causal != 0 && causal != 1) ||
+      (window_tokens > 0 && !causal) || !std::isfinite(scale))
+    return GDPA_ERR_INVALID_ARG;
+  if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return GDPA_OK;
+  if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
+  if ((st = check_rows(out, (int64_t)Hq * cache->D, Hq, cache->D)) != GDPA_OK) return st;
+  if (!offsets || !kv_lens || !page_table || max_pages == 0 || !aligned(lse, 4)) return GDPA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 16)) return GDPA_ERR_INVALID_ARG;
+  int64_t need = 0;
+  if ((st = gdpa_cache_workspace_size(cache, Hq, max_q, &need)) != GDPA_OK) return st;
+  if (workspace_bytes < need) return GDPA_ERR_NO_MEMORY;
+  Device dev;
+  if ((st = current_device(&dev)) != GDPA_OK) return st;
+  CacheFwdParams p;
+  p.cache = view(cache);
+  p.batch = CacheBatch{offsets, kv_lens, page_table, static_cast<int>(T), B, max_pages, dev.status};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.G = Hq / cache->H;
+  p.causal = causal;
+  p.window = window_tokens;
+  p.scale2 = scale * 1.4426950408889634f;
+  const int64_t blocks = (T * Hq + 3) / 4;
+  if (blocks >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->D == 128)
+    gdpa_cache_fwd_row_kernel<128><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+  else
+    gdpa_cache_fwd_row_kernel<64><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}

@@ -1,0 +1,296 @@
+// gdpa_cache_append.cuh -- stores new tokens in the paged e4m3 cache, with
+// the position rotation of keys and queries on the way.
+//
+// Mathematics.  A pair (x, y) at position p turns by theta = p f.  With
+// F = f / 2 pi as a 64-bit fraction of a turn, p F modulo 2^64 IS theta
+// modulo one turn, with an error of p 2^-65 turns: one integer product, no
+// argument reduction and no 64-bit floating point at any position.  The top 32
+// bits go to sincospif.  A block of 16 tokens of one head has one scale 2^e,
+// e the smallest integer with amax <= 448 2^e, so from the bits of amax
+// (exponent field E, mantissa M): e + 127 = E - 8 + (M > 0.75 2^23).
+//
+// Bound: memory.  Per new token Hq D 4 bytes (queries in and out) and
+// H D (4 + 2) (keys and values in, codes out) against about 3 flops an element.
+//
+// Work split.  A scale block takes its new tokens from consecutive rows, so
+// the row that is the first of them owns the block, and whoever finds the row
+// needs no plan and no list: a CTA looks at a group of rows, keeps the owners,
+// tabulates sine and cosine of their blocks' rows (shared by all heads), and
+// its warps take tasks of up to 128 items of 16 elements: keys of (block,
+// head), values of (block, head), or a run of the block's query items.  A warp
+// holds all 2048 elements of a key or value task in registers (64 a lane), so
+// the largest magnitude is known before anything is written and memory is read
+// once.
+#pragma once
+
+#include "gdpa_cache.cuh"
+
+namespace gdpa {
+
+struct AppendParams {
+  CacheView cache;
+  CacheBatch batch;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;
+  int Hq;
+  int rot;         // rotated coordinates
+  int interleaved;
+  unsigned long long freq[64];  // fraction of a turn a position, times 2^64
+};
+
+constexpr int kAppendThreads = 256;
+
+// cos, sin of position pos times fraction F of a turn.
+__device__ __forceinline__ float2 rope_angle(unsigned long long F, int pos) {
+  const int turn = static_cast<int>((static_cast<unsigned long long>(pos) * F) >> 32);  // [-1/2, 1/2) turns, 2^-32 units
+  float s, c;
+  sincospif(static_cast<float>(turn) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+  return make_float2(c, s);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __int_as_float(w[i] << 16);
+    x[2 * i + 1] = __int_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]), ptx::pack_bf16x2(x[4], x[5]),
+                    ptx::pack_bf16x2(x[6], x[7]));
+}
+
+// An item: 16 coordinates of one head as two chunks of 8, at d0 and d1.
+// Rotated items hold whole pairs: across the chunks (half) or inside them
+// (interleaved).
+struct ItemAt {
+  int d0, d1, pair;  // pair: first rotated pair of the item, -1 if none
+};
+__device__ __forceinline__ ItemAt item_at(int it, int rot, int interleaved) {
+  if (16 * it < rot && !interleaved) return ItemAt{8 * it, (rot >> 1) + 8 * it, 8 * it};
+  return ItemAt{16 * it, 16 * it + 8, 16 * it < rot ? 8 * it : -1};
+}
+
+__device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, const float2* __restrict__ cs,
+                                            float (&a)[8], float (&b)[8]) {
+  if (at.pair < 0) return;
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t0 = cs[at.pair + i], t1 = cs[at.pair + 4 + i];
+      const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
+      a[2 * i] = x0 * t0.x - y0 * t0.y;
+      a[2 * i + 1] = y0 * t0.x + x0 * t0.y;
+      b[2 * i] = x1 * t1.x - y1 * t1.y;
+      b[2 * i + 1] = y1 * t1.x + x1 * t1.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 t = cs[at.pair + i];
+      const float x = a[i], y = b[i];
+      a[i] = x * t.x - y * t.y;
+      b[i] = y * t.x + x * t.y;
+    }
+  }
+}
+
+// Eight values times `inv` (a power of two) as e4m3 codes; what is not finite
+// becomes the NaN code (the saturating conversion would make an infinity 448).
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = fabsf(x[i]) <= 3.4028235e38f ? x[i] * inv : __int_as_float(0x7fffffff);
+  return make_uint2(ptx::pack_e4m3x4(y[0], y[1], y[2], y[3]), ptx::pack_e4m3x4(y[4], y[5], y[6], y[7]));
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
+  uint32_t h;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(two));
+  float2 f;
+  asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.f32.f16 %0, lo; cvt.f32.f16 %1, hi; }"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// Four codes times f (a power of two), rounded to codes again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  const float2 a = e4m3x2_to_float2(w & 0xffffu), b = e4m3x2_to_float2(w >> 16);
+  return ptx::pack_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+
+// A scale block that this launch writes to: `cnt` new tokens from row `row`
+// on, the first at position `pos`.
+struct OwnedBlock {
+  int row, cnt, pos, page, tab;  // tab: its first row in the angle table
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
+                                                                           int rows_per_cta) {
+  constexpr int IPR = D / 16;             // items of a row and head
+  constexpr int KV_ITEMS = 16 * IPR / 32; // items a lane of a whole block
+  __shared__ OwnedBlock s_own[16];
+  __shared__ int s_n;
+  extern __shared__ float2 s_cs[];  // [rows][rot / 2]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const CacheBatch& bt = p.batch;
+  const int g0 = blockIdx.x * rows_per_cta;
+
+  if (warp == 0) {
+    OwnedBlock o{0, 0, 0, -1, 0};
+    const int r = g0 + lane;
+    if (lane < rows_per_cta && r < bt.T) {
+      const int b = find_sequence(bt.offsets, bt.B, r);
+      if (b < bt.B) {
+        const CacheSeq s = load_sequence(bt, p.cache.lp, b);
+        const int pos = s.len - s.n + (r - s.first);
+        if (s.ok && s.len < s.n) atomicOr(bt.status, kStatusBadPlan);
+        if (s.ok && s.len >= s.n && r >= s.first && (r == s.first || (pos & 15) == 0)) {
+          o.row = r;
+          o.pos = pos;
+          o.cnt = min(kCacheBlock - (pos & 15), s.first + s.n - r);
+          o.page = load_page(p.cache, bt, b, pos);
+        }
+      }
+    }
+    int tab = o.cnt;  // running sum of the owners' row counts
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, tab, d);
+      if (lane >= d) tab += t;
+    }
+    o.tab = tab - o.cnt;
+    // Blocks of one group never overlap, so that their rows fit the table;
+    // offsets that decrease can make them, and are caught here.
+    if (o.cnt > 0 && tab > rows_per_cta + kCacheBlock - 1) {
+      o.cnt = 0;
+      atomicOr(bt.status, kStatusBadPlan);
+    }
+    const unsigned owners = __ballot_sync(0xffffffffu, o.cnt > 0);
+    if (o.cnt > 0) s_own[__popc(owners & ((1u << lane) - 1))] = o;
+    if (lane == 0) s_n = __popc(owners);
+  }
+  __syncthreads();
+  const int n = s_n;
+  if (n == 0) return;
+  const int half = p.rot >> 1;
+  if (half > 0) {
+    for (int j = 0; j < n; ++j) {
+      const OwnedBlock o = s_own[j];
+      for (int i = tid; i < o.cnt * half; i += kAppendThreads) {
+        const int t = i / half, f = i - t * half;
+        s_cs[(o.tab + t) * half + f] = rope_angle(p.freq[f], o.pos + t);
+      }
+    }
+    __syncthreads();
+  }
+
+  const int H = p.cache.H;
+  const int workers = (kAppendThreads / 32) * gridDim.y;
+  int w = blockIdx.y * (kAppendThreads / 32) + warp;  // the next task of this warp, counted over all blocks
+  for (int j = 0; j < n; ++j) {
+    const OwnedBlock o = s_own[j];
+    const int q_items = p.q ? o.cnt * p.Hq * IPR : 0;
+    const int q_tasks = (q_items + 127) >> 7;
+    const int tasks = 2 * H + q_tasks;
+    for (; w < tasks; w += workers) {
+      if (w >= 2 * H) {  // queries: rotate and store
+        const int i0 = ((w - 2 * H) << 7) + lane;
+        uint4 ua[4], ub[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + 32 * u;
+          if (i < q_items) {
+            const int t = i / (p.Hq * IPR), rest = i - t * (p.Hq * IPR);
+            const ItemAt at = item_at(rest % IPR, p.rot, p.interleaved);
+            const __nv_bfloat16* src = p.q + (o.row + t) * p.q_stride + (rest / IPR) * D;
+            ua[u] = *reinterpret_cast<const uint4*>(src + at.d0);
+            ub[u] = *reinterpret_cast<const uint4*>(src + at.d1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + 32 * u;
+          if (i < q_items) {
+            const int t = i / (p.Hq * IPR), rest = i - t * (p.Hq * IPR);
+            const ItemAt at = item_at(rest % IPR, p.rot, p.interleaved);
+            float a[8], b[8];
+            unpack8(ua[u], a);
+            unpack8(ub[u], b);
+            rotate_item(at, p.interleaved, s_cs + (o.tab + t) * half, a, b);
+            __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(o.row + t) * p.Hq + rest / IPR) * D;
+            *reinterpret_cast<uint4*>(dst + at.d0) = pack8(a);
+            *reinterpret_cast<uint4*>(dst + at.d1) = pack8(b);
+          }
+        }
+        continue;
+      }
+      if (o.page < 0) continue;
+      const int is_v = w >= H, h = is_v ? w - H : w;
+      const int rot = is_v ? 0 : p.rot;
+      const __nv_bfloat16* src = (is_v ? p.v + o.row * p.v_stride : p.k + o.row * p.k_stride) + h * D;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const int slot = o.pos & ((1 << p.cache.lp) - 1);
+      uint8_t* codes = (is_v ? p.cache.v : p.cache.k) + cache_row(p.cache, o.page, h, slot) * D;
+      uint8_t* sf = (is_v ? p.cache.v_sf : p.cache.k_sf) + cache_sf(p.cache, o.page, h, slot);
+      const int held = o.pos & 15;  // earlier tokens of the block
+      float a[KV_ITEMS][8], b[KV_ITEMS][8];
+      float amax = 0.0f;
+#pragma unroll
+      for (int u = 0; u < KV_ITEMS; ++u) {
+        const int i = lane + 32 * u, t = i / IPR;
+        if (t < o.cnt) {
+          const ItemAt at = item_at(i % IPR, rot, p.interleaved);
+          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d0), a[u]);
+          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d1), b[u]);
+          rotate_item(at, p.interleaved, s_cs + (o.tab + t) * half, a[u], b[u]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = fabsf(a[u][e]), y = fabsf(b[u][e]);
+            if (x <= 3.4028235e38f) amax = fmaxf(amax, x);
+            if (y <= 3.4028235e38f) amax = fmaxf(amax, y);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      const uint32_t bits = __float_as_uint(amax);
+      int code = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+      if (held > 0) {
+        const int before = *sf;
+        if (before < code) {  // the earlier tokens follow the larger scale
+          const float f = sf_value(127 - min(code - before, 126));
+          uint8_t* old = codes - held * D;
+          for (int i = lane; i < held * IPR; i += 32) {
+            uint4 x = *reinterpret_cast<uint4*>(old + 16 * i);
+            x = make_uint4(rescale4(x.x, f), rescale4(x.y, f), rescale4(x.z, f), rescale4(x.w, f));
+            *reinterpret_cast<uint4*>(old + 16 * i) = x;
+          }
+        }
+        code = max(code, before);
+        __syncwarp();  // every lane has read the scale
+      }
+      if (lane == 0) *sf = static_cast<uint8_t>(code);
+      const float inv = sf_value(max(254 - code, 0));  // code <= 247 for what this kernel stored (amax < 2^128)
+#pragma unroll
+      for (int u = 0; u < KV_ITEMS; ++u) {
+        const int i = lane + 32 * u, t = i / IPR;
+        if (t < o.cnt) {
+          const ItemAt at = item_at(i % IPR, rot, p.interleaved);
+          *reinterpret_cast<uint2*>(codes + t * D + at.d0) = quantise8(a[u], inv);
+          *reinterpret_cast<uint2*>(codes + t * D + at.d1) = quantise8(b[u], inv);
+        }
+      }
+    }
+    w -= tasks;
+  }
+}
+
+}  // namespace gdpa

@@ -22,6 +22,9 @@ GDPA_ACT_GELU_TANH = 1
 GDPA_ROUTE_SFU = 0
 GDPA_ROUTE_ALU = 1
 
+GDPA_ROPE_HALF = 0
+GDPA_ROPE_INTERLEAVED = 1
+
 GDPA_OK = 0
 GDPA_ERR_INVALID_ARG = 1
 GDPA_ERR_UNSUPPORTED = 2
@@ -32,7 +35,8 @@ GDPA_ERR_NO_MEMORY = 5
 # Every symbol include/gdpa.h declares.
 EXPORTS = ("gdpa_fwd", "gdpa_fwd_async", "gdpa_fwd_lse", "gdpa_fwd_sliding", "gdpa_fwd_mx", "gdpa_fwd_mxfp8", "gdpa_bwd", "gdpa_bwd_sliding", "gdpa_fwd_noalloc", "gdpa_plan_create", "gdpa_plan_create_sliding", "gdpa_fwd_planned", "gdpa_plan_destroy", "gdpa_plan_num_items",
            "gdpa_plan_num_ctas", "gdpa_fwd_host", "gdpa_plan_enumerate", "gdpa_act_eval", "gdpa_set_act_route",
-           "gdpa_get_act_route", "gdpa_device_status", "gdpa_wait_selftest", "gdpa_status_string", "gdpa_version")
+           "gdpa_get_act_route", "gdpa_device_status", "gdpa_wait_selftest", "gdpa_status_string", "gdpa_version",
+           "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size")
 
 
 class GdpaError(RuntimeError):
@@ -43,6 +47,14 @@ class GdpaError(RuntimeError):
 
 class WorkItem(ctypes.Structure):
     _fields_ = [("seq", ctypes.c_int32), ("head", ctypes.c_int32), ("q0", ctypes.c_int32), ("kv0", ctypes.c_int32)]
+
+
+class _CacheDesc(ctypes.Structure):
+    """gdpa_cache_t"""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_sf", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int32), ("rope_style", ctypes.c_int32)]
 
 
 _lib = None
@@ -83,12 +95,16 @@ def lib() -> ctypes.CDLL:
     L.gdpa_get_act_route.restype = I
     L.gdpa_device_status.argtypes = [P]
     L.gdpa_wait_selftest.argtypes = [I, P]
+    L.gdpa_cache_append.argtypes = [P, P, I64, P, I64, P, I64, P, P, P, I64, I, I, I, P, P]
+    L.gdpa_cache_fwd.argtypes = [P, P, I64, P, P, P, I64, I, I, I, I, I, I, F, P, P, P, I64, P]
+    L.gdpa_cache_workspace_size.argtypes = [P, I, I, ctypes.POINTER(I64)]
     L.gdpa_status_string.argtypes = [I]
     L.gdpa_status_string.restype = ctypes.c_char_p
     L.gdpa_version.argtypes = []
     L.gdpa_version.restype = ctypes.c_char_p
     for name in ("gdpa_fwd", "gdpa_fwd_async", "gdpa_fwd_lse", "gdpa_fwd_sliding", "gdpa_fwd_mxfp8", "gdpa_bwd", "gdpa_bwd_sliding", "gdpa_fwd_noalloc", "gdpa_plan_create", "gdpa_plan_create_sliding", "gdpa_fwd_planned", "gdpa_plan_num_ctas", "gdpa_fwd_host",
-                 "gdpa_plan_enumerate", "gdpa_act_eval", "gdpa_set_act_route", "gdpa_device_status", "gdpa_wait_selftest"):
+                 "gdpa_plan_enumerate", "gdpa_act_eval", "gdpa_set_act_route", "gdpa_device_status", "gdpa_wait_selftest",
+                 "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -316,3 +332,72 @@ def gdpa_device_status(stream=None) -> int:
 
 def gdpa_wait_selftest(timeout_ms: int, stream=None):
     _check(lib().gdpa_wait_selftest(int(timeout_ms), _stream(stream)), "gdpa_wait_selftest")
+
+
+def _on_gpu(where, dtype, *tensors) -> None:
+    """Refuses a tensor of another type than ``dtype`` or on another device than the current one (addresses pass)."""
+    import torch
+    want = getattr(torch, dtype)
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype != want:
+            raise TypeError("%s: %s wanted, got %s" % (where, want, t.dtype))
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
+
+
+class KvCache:
+    """A gdpa_cache_t over the caller's tensors, which it keeps alive: codes uint8 ``[num_pages, H, page_tokens, D]``
+    (e4m3), scales uint8 ``[num_pages, H, page_tokens // 16]`` (E8M0), ``inv_freq`` host float64 ``[rot_dim // 2]``
+    (radians per position; None: no rotation) and the pairing (GDPA_ROPE_HALF or GDPA_ROPE_INTERLEAVED)."""
+
+    def __init__(self, k_codes, v_codes, k_sf, v_sf, inv_freq=None, rope_style=GDPA_ROPE_HALF):
+        pages, H, tokens, D = (int(n) for n in k_codes.shape)
+        for name, t, shape in (("k_codes", k_codes, (pages, H, tokens, D)), ("v_codes", v_codes, (pages, H, tokens, D)),
+                               ("k_sf", k_sf, (pages, H, tokens // 16)), ("v_sf", v_sf, (pages, H, tokens // 16))):
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError("KvCache: %s must be contiguous %r, got %r" % (name, shape, tuple(t.shape)))
+        _on_gpu("KvCache", "uint8", k_codes, v_codes, k_sf, v_sf)
+        self.tensors = (k_codes, v_codes, k_sf, v_sf)
+        self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
+        n = 0 if self.inv_freq is None else self.inv_freq.size
+        self.desc = _CacheDesc(_addr(k_codes), _addr(v_codes), _addr(k_sf), _addr(v_sf), pages, tokens, H, D,
+                               self.inv_freq.ctypes.data if n else None, 2 * n, int(rope_style))
+        self.addr = ctypes.addressof(self.desc)
+
+
+def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, offsets, kv_lens, page_table, T, B, Hq,
+                      max_pages, q_out, stream=None):
+    """Stores the new tokens' ``k`` and ``v`` in the cache (``k`` rotated by position) and the rotated ``q`` in
+    ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
+    _on_gpu("gdpa_cache_append", "bfloat16", q, k, v, q_out)
+    _on_gpu("gdpa_cache_append", "int32", offsets, kv_lens, page_table)
+    _check(lib().gdpa_cache_append(cache.addr, _addr(q), int(q_stride), _addr(k), int(k_stride), _addr(v),
+                                   int(v_stride), _addr(offsets), _addr(kv_lens), _addr(page_table), int(T), int(B),
+                                   int(Hq), int(max_pages), _addr(q_out), _stream(stream)), "gdpa_cache_append")
+
+
+def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
+                   window_tokens, scale, out, lse, workspace, workspace_bytes=None, stream=None):
+    """Attention of the new tokens' ``q`` over the cache.  ``workspace``: a device tensor of at least
+    gdpa_cache_workspace_size() bytes (or an address, with its ``workspace_bytes``); calls that may overlap need one
+    each."""
+    _on_gpu("gdpa_cache_fwd", "bfloat16", q, out)
+    _on_gpu("gdpa_cache_fwd", "int32", offsets, kv_lens, page_table)
+    _on_gpu("gdpa_cache_fwd", "float32", lse)
+    _on_gpu("gdpa_cache_fwd", "uint8", workspace)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
+    _check(lib().gdpa_cache_fwd(cache.addr, _addr(q), int(q_stride), _addr(offsets), _addr(kv_lens),
+                                _addr(page_table), int(T), int(B), int(Hq), int(max_pages), int(max_q), int(causal),
+                                int(window_tokens), float(scale), _addr(out), _addr(lse), _addr(workspace),
+                                int(workspace_bytes), _stream(stream)), "gdpa_cache_fwd")
+
+
+def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:
+    """Bytes of workspace gdpa_cache_fwd needs on the current device."""
+    n = ctypes.c_int64(0)
+    _check(lib().gdpa_cache_workspace_size(cache.addr, int(Hq), int(max_q), ctypes.byref(n)),
+           "gdpa_cache_workspace_size")
+    return n.value
