@@ -3,8 +3,10 @@
 // Nothing here allocates, synchronises or reads device data.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "gdpa_cache_append.cuh"
 #include "gdpa_cache_fwd.cuh"
@@ -92,6 +94,51 @@ unsigned long long turn_fraction(double f) {
   return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
 }
 
+// Query rows of a segment, in eights: the fewest that hold one sequence's rows
+// of a key head, at most four.
+int split_columns(int max_q, int G) {
+  const int64_t rows = (int64_t)max_q * G;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+
+int split_ctas(int nt) { return nt == 1 ? SplitCfg<128, 1>::CTAS : nt == 2 ? SplitCfg<128, 2>::CTAS : SplitCfg<128, 4>::CTAS; }
+
+int64_t split_workspace(int64_t ctas, int rows, int D) {
+  return ctas * 2 * (8 * sizeof(int) + (int64_t)rows * (D + 2) * sizeof(float));
+}
+
+template <int D, int NT>
+gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  using C = SplitCfg<D, NT>;
+  static_assert(C::SMEM <= 227 * 1024, "shared memory of a CTA");
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev.id]) {
+      if (cudaFuncSetAttribute(gdpa_cache_split_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+          cudaSuccess)
+        return GDPA_ERR_CUDA;
+      done[dev.id] = true;
+    }
+  }
+  // Keys a segment can have, as far as the host knows: up to 512 of them (two
+  // fills of the rings) are not worth a second kernel.
+  int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
+  if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock);
+  p.no_split = keys <= 512 ? 1 : 0;
+  const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;  // at most
+  const int64_t runs = p.no_split ? segments : segments * ((keys + 4 * kUnitKeys - 1) / (4 * kUnitKeys));
+  const int ctas = static_cast<int>(std::min<int64_t>(runs, (int64_t)dev.sms * C::CTAS));
+  p.meta = static_cast<int*>(workspace);
+  p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * 2 * 8);
+  gdpa_cache_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return GDPA_ERR_CUDA;
+  if (p.no_split) return GDPA_OK;
+  gdpa_cache_join_kernel<D, C::ROWS><<<ctas, 512, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace gdpa
 
@@ -146,11 +193,14 @@ extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void
 extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes) {
   if (!bytes) return GDPA_ERR_INVALID_ARG;
   *bytes = 0;
-  const gdpa_status_t st = check_cache(cache);
+  gdpa_status_t st = check_cache(cache);
   if (st != GDPA_OK) return st;
   if (Hq <= 0 || Hq % cache->H || max_q <= 0) return GDPA_ERR_INVALID_ARG;
   if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
-  *bytes = 16;
+  Device dev;
+  if ((st = current_device(&dev)) != GDPA_OK) return st;
+  const int nt = split_columns(max_q, Hq / cache->H);
+  *bytes = split_workspace(dev.sms * split_ctas(nt), 8 * nt, cache->D);
   return GDPA_OK;
 }
 
@@ -188,12 +238,13 @@ extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q
   p.causal = causal;
   p.window = window_tokens;
   p.scale2 = scale * 1.4426950408889634f;
-  const int64_t blocks = (T * Hq + 3) / 4;
-  if (blocks >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int nt = split_columns(max_q, p.G);
   if (cache->D == 128)
-    gdpa_cache_fwd_row_kernel<128><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
-  else
-    gdpa_cache_fwd_row_kernel<64><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+    return nt == 1 ? launch_split<128, 1>(p, workspace, max_q, dev, s)
+                   : nt == 2 ? launch_split<128, 2>(p, workspace, max_q, dev, s)
+                             : launch_split<128, 4>(p, workspace, max_q, dev, s);
+  return nt == 1 ? launch_split<64, 1>(p, workspace, max_q, dev, s)
+                 : nt == 2 ? launch_split<64, 2>(p, workspace, max_q, dev, s)
+                           : launch_split<64, 4>(p, workspace, max_q, dev, s);
 }
