@@ -430,8 +430,8 @@ typedef enum {
  *
  * Token t of sequence b lies in page page_table[b, t / page_tokens] at slot
  * t % page_tokens.  H is the number of key/value heads, D 64 or 128,
- * page_tokens a power of two from 16 to 1024.  Codes must be 16-byte aligned.
- * A new page needs no clearing: a block's scale and codes are not read before
+ * page_tokens a power of two from 16 to 1024.  Codes must be 16-byte aligned,
+ * scales 4-byte.  A new page needs no clearing: a block's scale and codes are not read before
  * they were written.
  *
  * inv_freq: HOST double [rot_dim / 2], radians per position of each rotated

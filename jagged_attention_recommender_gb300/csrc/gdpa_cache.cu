@@ -57,7 +57,7 @@ gdpa_status_t check_cache(const gdpa_cache_t* c) {
       if (!std::isfinite(c->inv_freq[i])) return GDPA_ERR_INVALID_ARG;
   }
   if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_sf || !c->v_sf || !aligned(c->k_codes, 16) ||
-                           !aligned(c->v_codes, 16)))
+                           !aligned(c->v_codes, 16) || !aligned(c->k_sf, 4) || !aligned(c->v_sf, 4)))
     return GDPA_ERR_INVALID_ARG;
   return GDPA_OK;
 }
@@ -101,10 +101,13 @@ int split_columns(int max_q, int G) {
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-int split_ctas(int nt) { return nt == 1 ? SplitCfg<128, 1>::CTAS : nt == 2 ? SplitCfg<128, 2>::CTAS : SplitCfg<128, 4>::CTAS; }
+int split_ctas(int nt, int D) {
+  if (D == 64) return nt == 1 ? SplitCfg<64, 1>::CTAS : nt == 2 ? SplitCfg<64, 2>::CTAS : SplitCfg<64, 4>::CTAS;
+  return nt == 1 ? SplitCfg<128, 1>::CTAS : nt == 2 ? SplitCfg<128, 2>::CTAS : SplitCfg<128, 4>::CTAS;
+}
 
 int64_t split_workspace(int64_t ctas, int rows, int D) {
-  return ctas * 2 * (8 * sizeof(int) + (int64_t)rows * (D + 2) * sizeof(float));
+  return ctas * 4 * 2 * (8 * sizeof(int) + (int64_t)rows * (D + 2) * sizeof(float));  // four warps a CTA
 }
 
 template <int D, int NT>
@@ -127,16 +130,28 @@ gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const 
   int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock);
   p.no_split = keys <= 512 ? 1 : 0;
-  const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;  // at most
-  const int64_t runs = p.no_split ? segments : segments * ((keys + 4 * kUnitKeys - 1) / (4 * kUnitKeys));
-  const int ctas = static_cast<int>(std::min<int64_t>(runs, (int64_t)dev.sms * C::CTAS));
+  // workers that can have a run, at most
+  const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;
+  const int64_t workers = segments * ((keys / C::SPAN + 1 + kStart) / kRunSteps + 1);
+  const int ctas = static_cast<int>(
+      std::min<int64_t>((workers + C::WARPS - 1) / C::WARPS, (int64_t)dev.sms * C::CTAS));
   p.meta = static_cast<int*>(workspace);
-  p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * 2 * 8);
+  p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * C::WARPS * 16);
   gdpa_cache_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return GDPA_ERR_CUDA;
   if (p.no_split) return GDPA_OK;
-  gdpa_cache_join_kernel<D, C::ROWS><<<ctas, 512, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+  // the join's blocks are placed while the last of the first kernel's CTAs
+  // finish, and wait there
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gdpa_cache_join_kernel<D, C::ROWS>, p) == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 }  // namespace
@@ -200,7 +215,7 @@ extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, in
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
   const int nt = split_columns(max_q, Hq / cache->H);
-  *bytes = split_workspace(dev.sms * split_ctas(nt), 8 * nt, cache->D);
+  *bytes = split_workspace(dev.sms * split_ctas(nt, cache->D), 8 * nt, cache->D);
   return GDPA_OK;
 }
 

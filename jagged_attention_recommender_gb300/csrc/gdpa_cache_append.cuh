@@ -17,10 +17,11 @@
 // needs no plan and no list: a CTA looks at a group of rows, keeps the owners,
 // tabulates sine and cosine of their blocks' rows (shared by all heads), and
 // its warps take tasks of up to 128 items of 16 elements: keys of (block,
-// head), values of (block, head), or a run of the block's query items.  A warp
-// holds all 2048 elements of a key or value task in registers (64 a lane), so
+// head), values of (block, head), or query items of a few rows.  A warp holds
+// all 2048 elements of a key or value task as loaded (32 registers a lane), so
 // the largest magnitude is known before anything is written and memory is read
-// once.
+// once; keys are rotated twice, which costs less than the registers that would
+// keep them.
 #pragma once
 
 #include "gdpa_cache.cuh"
@@ -76,13 +77,23 @@ __device__ __forceinline__ ItemAt item_at(int it, int rot, int interleaved) {
   return ItemAt{16 * it, 16 * it + 8, 16 * it < rot ? 8 * it : -1};
 }
 
-__device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, const float2* __restrict__ cs,
-                                            float (&a)[8], float (&b)[8]) {
+// The (cos, sin) of an item's eight pairs.
+__device__ __forceinline__ void load_angles(const float2* src, float2 (&cs)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 u = reinterpret_cast<const float4*>(src)[i];
+    cs[2 * i] = make_float2(u.x, u.y);
+    cs[2 * i + 1] = make_float2(u.z, u.w);
+  }
+}
+
+__device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, const float2 (&cs)[8], float (&a)[8],
+                                            float (&b)[8]) {
   if (at.pair < 0) return;
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 t0 = cs[at.pair + i], t1 = cs[at.pair + 4 + i];
+      const float2 t0 = cs[i], t1 = cs[4 + i];
       const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
       a[2 * i] = x0 * t0.x - y0 * t0.y;
       a[2 * i + 1] = y0 * t0.x + x0 * t0.y;
@@ -92,7 +103,7 @@ __device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, c
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[at.pair + i];
+      const float2 t = cs[i];
       const float x = a[i], y = b[i];
       a[i] = x * t.x - y * t.y;
       b[i] = y * t.x + x * t.y;
@@ -100,12 +111,18 @@ __device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, c
   }
 }
 
-// Eight values times `inv` (a power of two) as e4m3 codes; what is not finite
-// becomes the NaN code (the saturating conversion would make an infinity 448).
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
+// Eight values times `inv` (a power of two) as e4m3 codes.  What is not finite
+// becomes the NaN code: the conversion does that to NaN, but makes an infinity
+// 448, so a task that holds one (`inf`, uniform) replaces it first.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv, bool inf) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = fabsf(x[i]) <= 3.4028235e38f ? x[i] * inv : __int_as_float(0x7fffffff);
+  for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+  if (inf) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(x[i]) == INFINITY) y[i] = __int_as_float(0x7fffffff);
+  }
   return make_uint2(ptx::pack_e4m3x4(y[0], y[1], y[2], y[3]), ptx::pack_e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
@@ -125,6 +142,12 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return ptx::pack_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+
 // A scale block that this launch writes to: `cnt` new tokens from row `row`
 // on, the first at position `pos`.
 struct OwnedBlock {
@@ -132,13 +155,14 @@ struct OwnedBlock {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
+__global__ void __launch_bounds__(kAppendThreads, 2) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
                                                                            int rows_per_cta) {
   constexpr int IPR = D / 16;             // items of a row and head
-  constexpr int KV_ITEMS = 16 * IPR / 32; // items a lane of a whole block
+  constexpr int HPW = 32 / IPR;           // heads (or rows of one head) whose items a warp holds once
+  constexpr int KV_ITEMS = 16 / HPW;      // items a lane of a whole block
   __shared__ OwnedBlock s_own[16];
   __shared__ int s_n;
-  extern __shared__ float2 s_cs[];  // [rows][rot / 2]
+  extern __shared__ __align__(16) float2 s_cs[];  // [rows][rot / 2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const CacheBatch& bt = p.batch;
   const int g0 = blockIdx.x * rows_per_cta;
@@ -194,38 +218,43 @@ __global__ void __launch_bounds__(kAppendThreads) gdpa_cache_append_kernel(const
 
   const int H = p.cache.H;
   const int workers = (kAppendThreads / 32) * gridDim.y;
-  int w = blockIdx.y * (kAppendThreads / 32) + warp;  // the next task of this warp, counted over all blocks
+  const int it = lane % IPR;  // a lane's items are the same one of several heads or rows
+  const int groups = p.q ? (p.Hq + HPW - 1) / HPW : 0;  // a row's heads, in warps
+  const int span = groups >= 3 ? 4 : max(groups, 1);    // groups of a row in a task ...
+  const int trows = 4 / span;                           // ... and rows of a task
+  const int per_row = (groups + 3) / 4;                 // tasks of a row where trows is 1
+  int w = blockIdx.y * (kAppendThreads / 32) + warp;    // this warp's next task, counted over all blocks
   for (int j = 0; j < n; ++j) {
     const OwnedBlock o = s_own[j];
-    const int q_items = p.q ? o.cnt * p.Hq * IPR : 0;
-    const int q_tasks = (q_items + 127) >> 7;
+    const int q_tasks = groups == 0 ? 0 : trows == 1 ? o.cnt * per_row : (o.cnt + trows - 1) / trows;
     const int tasks = 2 * H + q_tasks;
     for (; w < tasks; w += workers) {
       if (w >= 2 * H) {  // queries: rotate and store
-        const int i0 = ((w - 2 * H) << 7) + lane;
+        const int task = w - 2 * H;
+        const int t0 = trows == 1 ? task / per_row : task * trows;
+        const int h0 = (trows == 1 ? task % per_row * 4 * HPW : 0) + lane / IPR;
+        const ItemAt at = item_at(it, p.rot, p.interleaved);
         uint4 ua[4], ub[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int i = i0 + 32 * u;
-          if (i < q_items) {
-            const int t = i / (p.Hq * IPR), rest = i - t * (p.Hq * IPR);
-            const ItemAt at = item_at(rest % IPR, p.rot, p.interleaved);
-            const __nv_bfloat16* src = p.q + (o.row + t) * p.q_stride + (rest / IPR) * D;
+          const int t = t0 + u / span, head = h0 + u % span * HPW;
+          if (t < o.cnt && head < p.Hq) {
+            const __nv_bfloat16* src = p.q + (o.row + t) * p.q_stride + head * D;
             ua[u] = *reinterpret_cast<const uint4*>(src + at.d0);
             ub[u] = *reinterpret_cast<const uint4*>(src + at.d1);
           }
         }
+        float2 cs[8];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int i = i0 + 32 * u;
-          if (i < q_items) {
-            const int t = i / (p.Hq * IPR), rest = i - t * (p.Hq * IPR);
-            const ItemAt at = item_at(rest % IPR, p.rot, p.interleaved);
+          const int t = t0 + u / span, head = h0 + u % span * HPW;
+          if (u % span == 0 && at.pair >= 0 && t < o.cnt) load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
+          if (t < o.cnt && head < p.Hq) {
             float a[8], b[8];
             unpack8(ua[u], a);
             unpack8(ub[u], b);
-            rotate_item(at, p.interleaved, s_cs + (o.tab + t) * half, a, b);
-            __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(o.row + t) * p.Hq + rest / IPR) * D;
+            rotate_item(at, p.interleaved, cs, a, b);
+            __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(o.row + t) * p.Hq + head) * D;
             *reinterpret_cast<uint4*>(dst + at.d0) = pack8(a);
             *reinterpret_cast<uint4*>(dst + at.d1) = pack8(b);
           }
@@ -241,26 +270,60 @@ __global__ void __launch_bounds__(kAppendThreads) gdpa_cache_append_kernel(const
       uint8_t* codes = (is_v ? p.cache.v : p.cache.k) + cache_row(p.cache, o.page, h, slot) * D;
       uint8_t* sf = (is_v ? p.cache.v_sf : p.cache.k_sf) + cache_sf(p.cache, o.page, h, slot);
       const int held = o.pos & 15;  // earlier tokens of the block
-      float a[KV_ITEMS][8], b[KV_ITEMS][8];
+      const ItemAt at = item_at(it, rot, p.interleaved);
+      uint4 ua[KV_ITEMS], ub[KV_ITEMS];
+#pragma unroll
+      for (int u = 0; u < KV_ITEMS; ++u) {
+        const int t = lane / IPR + u * HPW;
+        ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
+        if (t < o.cnt) {
+          ua[u] = *reinterpret_cast<const uint4*>(src + t * stride + at.d0);
+          ub[u] = *reinterpret_cast<const uint4*>(src + t * stride + at.d1);
+        }
+      }
+      // item u, rotated
+      auto item = [&](int u, float (&a)[8], float (&b)[8]) {
+        unpack8(ua[u], a);
+        unpack8(ub[u], b);
+        if (at.pair >= 0) {
+          const int t = min(lane / IPR + u * HPW, o.cnt - 1);
+          float2 cs[8];
+          load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
+          rotate_item(at, p.interleaved, cs, a, b);
+        }
+      };
       float amax = 0.0f;
 #pragma unroll
       for (int u = 0; u < KV_ITEMS; ++u) {
-        const int i = lane + 32 * u, t = i / IPR;
-        if (t < o.cnt) {
-          const ItemAt at = item_at(i % IPR, rot, p.interleaved);
-          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d0), a[u]);
-          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d1), b[u]);
-          rotate_item(at, p.interleaved, s_cs + (o.tab + t) * half, a[u], b[u]);
+        float a[8], b[8];
+        item(u, a, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));  // NaN never wins
+      }
+      amax = warp_max(amax);
+      const bool inf = amax == INFINITY;
+      if (inf) {  // again without what is not finite
+        amax = 0.0f;
+#pragma unroll 1
+        for (int u = 0; u < KV_ITEMS; ++u) {
+          const int t = lane / IPR + u * HPW;
+          if (t >= o.cnt) break;
+          float a[8], b[8];
+          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d0), a);
+          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d1), b);
+          if (at.pair >= 0) {
+            float2 cs[8];
+            load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
+            rotate_item(at, p.interleaved, cs, a, b);
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = fabsf(a[u][e]), y = fabsf(b[u][e]);
-            if (x <= 3.4028235e38f) amax = fmaxf(amax, x);
-            if (y <= 3.4028235e38f) amax = fmaxf(amax, y);
+            if (fabsf(a[e]) < INFINITY) amax = fmaxf(amax, fabsf(a[e]));
+            if (fabsf(b[e]) < INFINITY) amax = fmaxf(amax, fabsf(b[e]));
           }
         }
+        amax = warp_max(amax);
       }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
       const uint32_t bits = __float_as_uint(amax);
       int code = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
       if (held > 0) {
@@ -281,11 +344,12 @@ __global__ void __launch_bounds__(kAppendThreads) gdpa_cache_append_kernel(const
       const float inv = sf_value(max(254 - code, 0));  // code <= 247 for what this kernel stored (amax < 2^128)
 #pragma unroll
       for (int u = 0; u < KV_ITEMS; ++u) {
-        const int i = lane + 32 * u, t = i / IPR;
+        const int t = lane / IPR + u * HPW;
         if (t < o.cnt) {
-          const ItemAt at = item_at(i % IPR, rot, p.interleaved);
-          *reinterpret_cast<uint2*>(codes + t * D + at.d0) = quantise8(a[u], inv);
-          *reinterpret_cast<uint2*>(codes + t * D + at.d1) = quantise8(b[u], inv);
+          float a[8], b[8];
+          item(u, a, b);
+          *reinterpret_cast<uint2*>(codes + t * D + at.d0) = quantise8(a, inv, inf);
+          *reinterpret_cast<uint2*>(codes + t * D + at.d1) = quantise8(b, inv, inf);
         }
       }
     }

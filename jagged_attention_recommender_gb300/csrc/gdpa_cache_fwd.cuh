@@ -18,19 +18,20 @@
 // and nothing above 2^-31 of it is lost.  The row sum takes the weights before
 // their rounding to fp16.
 //
-// Bound: memory, 2 D bytes a key and head.  A warp owns a ring of 16-key tiles
-// in shared memory that its own asynchronous copies fill (rows behind the
-// sequence's end are zero-filled), so warps never wait for one another until
-// the keys of their segment are done.
+// Bound: memory, 2 D bytes a key and head, with the instruction issue close
+// behind (the codes' conversions and byte shuffles).
 //
 // Work split.  A segment is (sequence, up to 8 NT query rows of one key head);
-// a unit is 64 keys of it, one tile for each of the CTA's four warps.  The
-// units of all segments are counted from the lengths on the device by every
-// CTA, and each takes an equal run of them, so a batch of any raggedness, or
-// one very long sequence, loads every SM alike and nothing is planned on the
-// host.  A segment that lies in several CTAs' runs leaves its parts (maximum,
-// sum, output) in the workspace and the second kernel joins them in the order
-// of the keys: results do not depend on timing.
+// a step is SPAN keys of it.  The steps of all segments are counted from the
+// lengths on the device, and every warp takes an equal run of them (a segment's
+// start is counted as kStart steps more), so a batch of any raggedness, or one
+// very long sequence, loads all SMs alike and nothing is planned on the host.
+// Warps never wait for one another.  Each owns a ring of stages in shared
+// memory that its own asynchronous copies fill, STAGES - 1 steps ahead and
+// across the ends of segments (rows that are not stored are zero-filled).  A
+// segment that lies in several warps' runs leaves its parts (reference, sum,
+// output) in the workspace and the second kernel joins them in the order of the
+// keys: results do not depend on timing.
 #pragma once
 
 #include "gdpa_cache.cuh"
@@ -48,40 +49,49 @@ struct CacheFwdParams {
   int causal, window;
   float scale2;    // scale * log2(e)
   int no_split;    // one segment is never cut: `part` is not used
-  int* meta;       // [CTAs][2][8]: the segment a CTA left a part of (see SplitMeta)
-  float* part;     // [CTAs][2][rows (D + 2)]
+  int* meta;       // [workers][2][8]: the segments a warp left a part of
+  float* part;     // [workers][2][rows (D + 2)]
 };
 
-constexpr int kUnitKeys = 64;
+// Parts of a cut segment: worker `first` holds the first in its slot 1, the
+// `pieces - 1` workers behind it the next ones in their slots 0.  Beside each
+// part stand {first, pieces, first row of the sequence, its rows, row tile, head}.
 
-// Parts of a cut segment: CTA `first` holds the first in its slot 1, the
-// `pieces - 1` CTAs behind it the next ones in their slots 0.
-struct SplitMeta {
-  int first, pieces, row0, n, tile, head;
-};
+constexpr int kStart = 2;     // what a segment's start costs, in steps
+constexpr int kRunSteps = 6;  // the fewest steps (starts included) that are worth a worker
 
 template <int D, int NT>
 struct SplitCfg {
   static constexpr int THREADS = 128, WARPS = 4;
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
+#ifndef XNB
+#define XNB 2
+#define XS (D == 64 ? 2 : 3)
+#define XC (D == 64 ? 3 : 2)
+#endif
+  static constexpr int NB = NT == 1 ? XNB : 1;     // 16-key tiles of a step
+  static constexpr int SPAN = NB * kCacheBlock;
   // CTAs an SM, and ring stages: enough tiles in flight to cover the memory's
   // latency (an SM's share of 6.8 TB/s is 45 KB a microsecond) at the
   // registers that the accumulators leave
-  static constexpr int CTAS = NT == 1 ? 4 : NT == 2 ? 3 : 2;
-  static constexpr int STAGES = (NT == 1 ? 3 : NT == 2 ? 4 : 5) * (D == 64 ? 2 : 1) - (D == 64 ? 1 : 0);
-  static constexpr int RING = WARPS * STAGES * 2 * TILE;
-  static constexpr int MERGE = WARPS * ROWS * D * 4;  // takes the ring's place when the keys are done
-  static constexpr int AREA = RING > MERGE ? RING : MERGE;
+  static constexpr int CTAS = NT == 1 ? XC : NT == 2 ? 3 : 2;
+  static constexpr int STAGES = NT == 1 ? (D == 64 ? (2 * XS * XNB > 8 ? 8 / XNB : 2 * XS) : XS) : D == 64 ? 6 : NT == 2 ? 3 : 4;
+  static_assert(STAGES * NB <= 8, "a nibble of state for each tile of the ring");
+  static constexpr int STAGE = NB * 2 * TILE;
+  static constexpr int RING = STAGES * STAGE;      // of a warp
   static constexpr int KSTEPS = D / 16;
-  static constexpr int QFRAG = NT > 1 ? KSTEPS * NT * 32 * 8 : 0;  // query fragments, shared by the warps
-  static constexpr int SMEM = AREA + QFRAG;
+  static constexpr int QFRAG = NT > 1 ? KSTEPS * NT * 32 * 8 : 0;  // a warp's query fragments
+  static constexpr int SMEM = WARPS * (RING + QFRAG);
 };
 
 namespace split {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -103,6 +113,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with nothing added to the product.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Two codes (the low or the high half of w) as two fp16 values.
@@ -144,32 +164,87 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (r >> 1) * 128 + (((r ^ (r >> 1)) & 1) << 6) + ((c ^ ((r >> 1) & 2)) << 4);
 }
 
-// Units of so many keys (a length may be as large as 2^31 - 16).
-__device__ __forceinline__ int key_units(int keys) {
-  return static_cast<int>((static_cast<unsigned>(max(keys, 0)) + kUnitKeys - 1) / kUnitKeys);
-}
-
 // A sequence's share of the work.
 struct SeqWork {
   CacheSeq s;
-  int kbase;      // first key any of its rows sees, rounded down to a block
-  int units;      // of one segment
-  int64_t total;  // of all its segments
+  int kbase;  // first key any of its rows sees, rounded down to SPAN keys
+  int steps;  // of one segment
+  int tiles;  // row tiles: segments of a key head
 };
-template <int ROWS>
+template <class C>
 __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
   SeqWork w;
   w.s = load_sequence(p.batch, p.cache.lp, b);
   w.kbase = 0;
-  w.units = 1;
-  w.total = 0;
+  w.steps = 0;
+  w.tiles = 0;
   if (!w.s.ok || w.s.n == 0) return w;
-  if (p.window > 0) w.kbase = max(0, w.s.len - w.s.n - p.window + 1) & ~(kCacheBlock - 1);
-  if (!p.no_split) w.units = max(1, key_units(w.s.len - w.kbase));
-  const int64_t tiles = (static_cast<int64_t>(w.s.n) * p.G + ROWS - 1) / ROWS;
-  w.total = tiles * p.cache.H * w.units;
+  if (p.window > 0) w.kbase = max(0, w.s.len - w.s.n - p.window + 1) & ~(C::SPAN - 1);
+  // (a length may be as large as 2^31 - 16)
+  w.steps = static_cast<int>((static_cast<unsigned>(max(w.s.len - w.kbase, 1)) + C::SPAN - 1) / C::SPAN);
+  w.tiles = static_cast<int>((static_cast<int64_t>(w.s.n) * p.G + C::ROWS - 1) / C::ROWS);
   return w;
 }
+__device__ __forceinline__ int64_t seq_cost(const CacheFwdParams& p, const SeqWork& w) {
+  return static_cast<int64_t>(w.tiles) * p.cache.H * (w.steps + kStart);
+}
+
+// Walks the segments of a worker's run [at, stop) of the work.
+template <class C>
+struct Walk {
+  SeqWork w;
+  int64_t start;  // of the present segment
+  int b, h, tile;
+  int64_t row0;   // its first query row (of the sequence and key head)
+  int rows;
+  int u0, u1;     // its steps that are in the run and hold visible keys
+  int lo_min, hi_max;  // keys any of its rows sees: [lo_min, hi_max)
+
+  __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
+    b = seq;
+    w = seq_work<C>(p, b);
+    const int64_t cost = w.steps + kStart, seg = (at - base) / cost;
+    start = base + seg * cost;
+    tile = static_cast<int>(seg / p.cache.H);
+    h = static_cast<int>(seg - static_cast<int64_t>(tile) * p.cache.H);
+  }
+  __device__ __forceinline__ void next(const CacheFwdParams& p) {
+    start += w.steps + kStart;
+    if (++h < p.cache.H) return;
+    h = 0;
+    if (++tile < w.tiles) return;
+    tile = 0;
+    do {
+      if (++b >= p.batch.B) return;
+      w = seq_work<C>(p, b);
+    } while (w.tiles == 0);
+  }
+  __device__ __forceinline__ bool more(const CacheFwdParams& p, int64_t stop) const {
+    return b < p.batch.B && start < stop;
+  }
+  // The present segment's rows and steps; false if none of it is this run's.
+  __device__ __forceinline__ bool enter(const CacheFwdParams& p, int64_t at, int64_t stop) {
+    const CacheSeq& s = w.s;
+    if (p.no_split) {  // a segment belongs to the run it starts in
+      if (start < at) return false;
+      u0 = 0;
+      u1 = w.steps;
+    } else {
+      u0 = static_cast<int>(max(at - start - kStart, (int64_t)0));
+      u1 = static_cast<int>(min(stop - start - kStart, (int64_t)w.steps));
+      if (u1 <= u0) return false;
+    }
+    row0 = static_cast<int64_t>(tile) * C::ROWS;
+    rows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(s.n) * p.G - row0));
+    const int pos0 = s.len - s.n + static_cast<int>(row0 / p.G);
+    const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
+    lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+    hi_max = max(0, p.causal ? min(s.len, pos1 + 1) : s.len);
+    u0 = max(u0, (lo_min - w.kbase) / C::SPAN);
+    u1 = hi_max > w.kbase ? min(u1, (hi_max - 1 - w.kbase) / C::SPAN + 1) : u0;
+    return true;
+  }
+};
 
 }  // namespace split
 
@@ -179,20 +254,22 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   using C = SplitCfg<D, NT>;
   constexpr int KS = C::KSTEPS, ND = D / 16;  // k-steps of S^T; 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[4];
-  __shared__ int64_t s_start;
-  __shared__ int s_seq;
-  __shared__ float s_ml[C::WARPS][C::ROWS][2];
-  __shared__ uint8_t s_sf[C::WARPS][C::STAGES][2];
+  __shared__ int64_t s_scan[C::WARPS];
+  __shared__ int64_t s_base[C::WARPS];
+  __shared__ int s_seq[C::WARPS];
+  __shared__ __align__(8) uint32_t s_sf[C::WARPS][C::STAGES][2 * C::NB];  // words that hold the scale codes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const CacheBatch& bt = p.batch;
+  const int worker = blockIdx.x * C::WARPS + warp;
 
-  // ---- this CTA's run of units, and the sequence it begins in
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up beside this
+
+  // ---- the workers' runs, and the sequence in which each begins
   int64_t mine = 0;
   const int per = (bt.B + C::THREADS - 1) / C::THREADS;
   const int b_lo = min(bt.B, tid * per), b_hi = min(bt.B, b_lo + per);
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_work<C::ROWS>(p, b).total;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_cost(p, seq_work<C>(p, b));
   int64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -200,7 +277,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
     if (lane >= d) incl += x;
   }
   if (lane == 31) s_scan[warp] = incl;
-  if (tid < 2 && !p.no_split) p.meta[(blockIdx.x * 2 + tid) * 8 + 1] = 0;  // no parts yet
+  if (lane == 0 && !p.no_split) p.meta[worker * 16 + 1] = p.meta[worker * 16 + 9] = 0;  // no parts yet
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
@@ -208,50 +285,132 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
     if (w < warp) incl += s_scan[w];
     total += s_scan[w];
   }
-  // a run is at least four units of one segment, or one segment
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t chunk = p.no_split ? max(even, (int64_t)1) : max(even, (int64_t)4);
-  int64_t at = chunk * blockIdx.x;
-  const int64_t stop = min(total, at + chunk);
-  if (at >= stop) return;
-  if (at >= incl - mine && at < incl) {
-    int64_t base = incl - mine;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const int64_t n = seq_work<C::ROWS>(p, b).total;
-      if (at < base + n) break;
-      base += n;
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WARPS;
+  const int64_t chunk = max((total + workers - 1) / workers, (int64_t)kRunSteps);
+#pragma unroll 1
+  for (int w = 0; w < C::WARPS; ++w) {
+    const int64_t from = chunk * (blockIdx.x * C::WARPS + w);
+    if (from < total && from >= incl - mine && from < incl) {
+      int64_t base = incl - mine;
+      int b = b_lo;
+      for (; b < b_hi; ++b) {
+        const int64_t n = seq_cost(p, seq_work<C>(p, b));
+        if (from < base + n) break;
+        base += n;
+      }
+      s_seq[w] = b;
+      s_base[w] = base;
     }
-    s_seq = b;
-    s_start = base;
   }
   __syncthreads();
-  int b = s_seq;
-  int64_t base = s_start;
+  const int64_t at = chunk * worker, stop = min(total, at + chunk);
+  if (at >= stop) return;
 
-  const uint32_t ring = ptx::smem_u32(smem) + warp * C::STAGES * 2 * C::TILE;
-  uint2* qfrag = reinterpret_cast<uint2*>(smem + C::AREA);
-  SeqWork sw = seq_work<C::ROWS>(p, b);
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
+  uint2* qfrag = reinterpret_cast<uint2*>(smem + C::WARPS * C::RING + warp * C::QFRAG);
+  const uint32_t sf_at = ptx::smem_u32(&s_sf[warp][0][0]);
+  const int pmask = (1 << p.cache.lp) - 1;
+  const int64_t sf_bytes = static_cast<int64_t>(p.cache.num_pages) * p.cache.H << (p.cache.lp - 4);
 
-  while (at < stop) {
-    if (at >= base + sw.total) {
-      base += sw.total;
-      sw = seq_work<C::ROWS>(p, ++b);
-      continue;
+  // ---- the copies: a walk that runs ahead of the one that computes
+  Walk<C> ahead;
+  ahead.begin(p, s_seq[warp], s_base[warp], at);
+  Walk<C> now = ahead;
+  int ahead_u = 0;
+  bool ahead_more = false;
+  // its next step: page of each tile, -1: nothing to read
+  int page_next[C::NB];
+  auto look = [&]() {
+    while (!ahead_more || ahead_u >= ahead.u1) {
+      if (ahead_more) ahead.next(p);
+      ahead_more = true;
+      if (!ahead.more(p, stop)) {
+        ahead_u = ahead.u1 = -1;  // done
+        ahead_more = false;
+        return;
+      }
+      if (ahead.enter(p, at, stop)) ahead_u = ahead.u0; else ahead_u = ahead.u1 = 0;
     }
-    const CacheSeq s = sw.s;
-    const int64_t seg = (at - base) / sw.units;
-    const int u0 = static_cast<int>((at - base) - seg * sw.units);
-    const int u1 = static_cast<int>(min(static_cast<int64_t>(sw.units), u0 + (stop - at)));
-    const int h = static_cast<int>(seg % p.cache.H), tile = static_cast<int>(seg / p.cache.H);
-    const int64_t row0 = static_cast<int64_t>(tile) * C::ROWS;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(s.n) * p.G - row0));
+    const int kb = ahead.w.kbase + ahead_u * C::SPAN;
+    const int32_t* table = bt.table + static_cast<int64_t>(ahead.b) * bt.max_pages;
+#pragma unroll
+    for (int n = 0; n < C::NB; ++n) {
+      const int k = kb + n * kCacheBlock;
+      page_next[n] = -1;
+      if (k < ahead.hi_max && k + kCacheBlock > ahead.lo_min) {
+        if (n > 0 && p.cache.lp > 4 && page_next[0] >= 0) {  // a step lies in one page, unless pages are single tiles
+          page_next[n] = page_next[0];
+        } else {
+          page_next[n] = __ldg(table + (k >> p.cache.lp));
+          if (page_next[n] < 0 || page_next[n] >= p.cache.num_pages) {
+            if (lane == 0) atomicOr(bt.status, kStatusBadPlan);
+            page_next[n] = -1;
+          }
+        }
+      }
+    }
+  };
+  // A nibble for each tile of the ring: bit 0 the tile is there, bits 1-2
+  // which byte of its words the scale codes are.
+  uint32_t state = 0;
+  auto issue = [&](int stage) {
+    state &= ~(((1u << 4 * C::NB) - 1) << (stage * 4 * C::NB));
+    if (ahead_more) {
+      const int kb = ahead.w.kbase + ahead_u * C::SPAN;
+      const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) {
+        const int page = page_next[n], slot = (kb + n * kCacheBlock) & pmask;
+        const int valid = page >= 0 ? ahead.w.s.len - (kb + n * kCacheBlock) : 0;
+        const int64_t row = cache_row(p.cache, max(page, 0), ahead.h, slot);
+        const uint8_t* ks = p.cache.k + row * D + lane * 16;
+        const uint8_t* vs = p.cache.v + row * D + lane * 16;
+        const uint32_t kd = dst + n * 2 * C::TILE, vd = kd + C::TILE;
+        if (valid >= kCacheBlock) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
+            cp_async16(kd + tile_at<D>(r, c), ks + 512 * j, 16);
+            cp_async16(vd + tile_at<D>(r, c), vs + 512 * j, 16);
+          }
+        } else {  // rows that are not stored: zeros
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
+            const int bytes = r < valid ? 16 : 0;
+            cp_async16(kd + tile_at<D>(r, c), ks + 512 * j, bytes);
+            cp_async16(vd + tile_at<D>(r, c), vs + 512 * j, bytes);
+          }
+        }
+        if (page >= 0) {
+          const int64_t block = row >> 4, word = block & ~(int64_t)3;
+          state |= (1u | static_cast<uint32_t>(block & 3) << 1) << ((stage * C::NB + n) * 4);
+          if (lane >> 1 == n)  // lanes 2n and 2n + 1: K's word and V's
+            cp_async4(sf_at + (stage * 2 * C::NB + lane) * 4, ((lane & 1) ? p.cache.v_sf : p.cache.k_sf) + word,
+                      static_cast<int>(min((int64_t)4, sf_bytes - word)));
+        }
+      }
+      ++ahead_u;
+      look();
+    }
+    cp_commit();
+  };
+  look();
+#pragma unroll 1
+  for (int i = 0; i < C::STAGES - 1; ++i) issue(i);
+  int stage = 0;
+
+#pragma unroll 1
+  for (; now.more(p, stop); now.next(p)) {
+    if (!now.enter(p, at, stop)) continue;
+    const CacheSeq s = now.w.s;
+    const int h = now.h, rows = now.rows;
+    const int64_t row0 = now.row0;
 
     // ---- query fragments, and what each column (query row) sees
     uint32_t qf[NT == 1 ? KS : 1][2];
     float fac[NT][2];
     int lo[NT][2], hi[NT][2];
-    int lo_max = 0, hi_min = s.len, lo_min = 0x7fffffff, hi_max = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
@@ -290,7 +449,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         if (NT == 1) {
           qf[NT == 1 ? k : 0][0] = b0;
           qf[NT == 1 ? k : 0][1] = b1;
-        } else if (warp == nt % C::WARPS) {
+        } else {
           qfrag[(k * NT + nt) * 32 + lane] = make_uint2(b0, b1);
         }
       }
@@ -303,150 +462,117 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         hi[nt][c] = col < rows ? (p.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
     }
-    {  // over the valid rows: they are in the order of their positions
-      const int pos0 = s.len - s.n + static_cast<int>(row0 / p.G);
-      const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
-      lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
-      lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
-      hi_min = p.causal ? min(s.len, pos0 + 1) : s.len;
-      hi_max = p.causal ? min(s.len, pos1 + 1) : s.len;
-    }
-    if (NT > 1) __syncthreads();
-
-    // ---- this warp's tiles: kb(i) = kbase + 64 (u0 + i) + 16 warp
-    const int first_kb = sw.kbase + u0 * kUnitKeys + warp * kCacheBlock;
-    const int n_it = p.no_split ? key_units(s.len - sw.kbase) : u1 - u0;
-    const int pmask = (1 << p.cache.lp) - 1;
-    const int32_t* table = bt.table + static_cast<int64_t>(b) * bt.max_pages;
-    auto live = [&](int kb) { return kb < hi_max && kb + kCacheBlock > lo_min; };
-    auto page_of = [&](int i) {  // -1: nothing to read
-      const int kb = first_kb + i * kUnitKeys;
-      if (i >= n_it || !live(kb)) return -1;
-      const int page = __ldg(table + (kb >> p.cache.lp));
-      if (page >= 0 && page < p.cache.num_pages) return page;
-      if (lane == 0) atomicOr(bt.status, kStatusBadPlan);
-      return -1;
-    };
-    uint32_t filled = 0;   // bit s: stage s holds a tile
-    int page_next = page_of(0);
-    // Starts the copies of tile i; lanes 0 and 1 load its scale codes (K's,
-    // V's) into `sf`, to be put beside the stage when they have arrived.
-    auto issue = [&](int i, int stage, uint32_t& sf) {
-      const int kb = first_kb + i * kUnitKeys, page = page_next;
-      page_next = page_of(i + 1);
-      if (page >= 0) {
-        filled |= 1u << stage;
-        const int slot = kb & pmask, valid = s.len - kb;  // rows from `valid` on are not stored yet: zeros
-        const int64_t row = cache_row(p.cache, page, h, slot);
-        const uint8_t* ks = p.cache.k + row * D + lane * 16;
-        const uint8_t* vs = p.cache.v + row * D + lane * 16;
-        const uint32_t dst = ring + stage * 2 * C::TILE;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
-          const int bytes = r < valid ? 16 : 0;
-          cp_async16(dst + tile_at<D>(r, c), ks + 512 * j, bytes);
-          cp_async16(dst + C::TILE + tile_at<D>(r, c), vs + 512 * j, bytes);
-        }
-        if (lane < 2) sf = (lane ? p.cache.v_sf : p.cache.k_sf)[cache_sf(p.cache, page, h, slot)];
-      } else {
-        filled &= ~(1u << stage);
-      }
-      cp_commit();
-    };
-    auto keep_sf = [&](int stage, uint32_t sf) {
-      if (lane < 2) s_sf[warp][stage][lane] = static_cast<uint8_t>(sf);
-    };
+    // the keys that all of its rows see: [lo_max, hi_min)
+    const int lo_min = now.lo_min, hi_max = now.hi_max;
+    const int pos0 = s.len - s.n + static_cast<int>(row0 / p.G);
+    const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
+    const int lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
+    const int hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
+    if (NT > 1) __syncwarp();
 
     float acc[ND][NT][4];
-    float mref[NT][2], sum[NT][2];
+    // the softmax's reference of each column, and by how much a score may
+    // exceed it (not at all while there is none)
+    float ref[NT][2], room[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) mref[nt][c] = -INFINITY, sum[nt][c] = 0.0f;
+      for (int c = 0; c < 2; ++c) ref[nt][c] = 0.0f, room[nt][c] = -INFINITY, sum[nt][c] = 0.0f;
 #pragma unroll
       for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.0f;
     }
 
-    uint32_t sf[C::STAGES - 1];
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) sf[i] = 0, issue(i, i, sf[i]);
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) keep_sf(i, sf[i]);
-    int stage = 0;
-    uint32_t sf_next = sf[C::STAGES - 2];
 #pragma unroll 1
-    for (int i = 0; i < n_it; ++i) {
-      const int behind = stage == 0 ? C::STAGES - 1 : stage - 1;  // the stage this iteration refills
-      keep_sf(behind == 0 ? C::STAGES - 1 : behind - 1, sf_next);  // ... and the one the last iteration did
+    for (int u = now.u0; u < now.u1; ++u) {
       cp_wait<C::STAGES - 2>();
       __syncwarp();
-      issue(i + C::STAGES - 1, behind, sf_next);
-      const uint32_t kt = ring + stage * 2 * C::TILE, vt = kt + C::TILE;
+      issue(stage == 0 ? C::STAGES - 1 : stage - 1);
+      const uint32_t kt = ring + stage * C::STAGE;
       const int cur = stage;
+      const uint32_t there = state >> (cur * 4 * C::NB);
       stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-      if (!(filled >> cur & 1)) continue;
-      const int kb = first_kb + i * kUnitKeys;
-      const float sk = sf_value(s_sf[warp][cur][0]), sv = sf_value(s_sf[warp][cur][1]);
+      const uint32_t all = C::NB == 2 ? 0x11u : 1u;
+      if ((there & all) == 0) continue;
+      const int kb = now.w.kbase + u * C::SPAN;
 
       // S^T = K Q^T: rows g and g + 8 are keys, columns 2t and 2t + 1 queries
-      float st[NT][4];
+      float st[C::NB][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) st[nt][c] = 0.0f;
+        for (int n = 0; n < C::NB; ++n) {
+          uint32_t ka[4], kc[4];
+          const int c = D == 128 ? 2 * t + j : t;
+          lds128(kt + n * 2 * C::TILE + tile_at<D>(g, c), ka);
+          lds128(kt + n * 2 * C::TILE + tile_at<D>(g + 8, c), kc);
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        uint32_t ka[4], kc[4];
-        const int c = D == 128 ? 2 * t + j : t;
-        lds128(kt + tile_at<D>(g, c), ka);
-        lds128(kt + tile_at<D>(g + 8, c), kc);
+          for (int w = 0; w < 4; ++w) {
+            const int k = 4 * j + w;
+            const uint32_t a0 = codes_lo(ka[w]), a2 = codes_hi(ka[w]), a1 = codes_lo(kc[w]), a3 = codes_hi(kc[w]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int k = 4 * j + w;
-          const uint32_t a0 = codes_lo(ka[w]), a2 = codes_hi(ka[w]), a1 = codes_lo(kc[w]), a3 = codes_hi(kc[w]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (NT == 1) {
-              mma_f16(st[nt], a0, a1, a2, a3, qf[NT == 1 ? k : 0][0], qf[NT == 1 ? k : 0][1]);
-            } else {
-              const uint2 qq = qfrag[(k * NT + nt) * 32 + lane];
-              mma_f16(st[nt], a0, a1, a2, a3, qq.x, qq.y);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t q0, q1;
+              if (NT == 1) {
+                q0 = qf[NT == 1 ? k : 0][0], q1 = qf[NT == 1 ? k : 0][1];
+              } else {
+                const uint2 qq = qfrag[(k * NT + nt) * 32 + lane];
+                q0 = qq.x, q1 = qq.y;
+              }
+              if (k == 0)
+                mma_f16_new(st[n][nt], a0, a1, a2, a3, q0, q1);
+              else
+                mma_f16(st[n][nt], a0, a1, a2, a3, q0, q1);
             }
           }
         }
-      }
 
-      // scores in units of log2, hidden keys -inf; does one leave the range?
-      const bool edge = kb < lo_max || kb + kCacheBlock > hi_min;
+      // scores in units of log2, less the reference; hidden keys -inf; does
+      // one leave the range?
+      const bool edge = kb < lo_max || kb > hi_min - C::SPAN || (there & all) != all;
+      float sv[C::NB];
       bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int n = 0; n < C::NB; ++n) {
+        uint32_t kw, vw;
+        lds64(sf_at + (cur * C::NB + n) * 8, kw, vw);
+        const bool here = there >> (4 * n) & 1;
+        const int byte = (there >> (4 * n) & 6) * 4;
+        const float sk = sf_value(here ? kw >> byte & 0xff : 127);
+        sv[n] = sf_value(here ? vw >> byte & 0xff : 127);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x = st[nt][c] * (fac[nt][c & 1] * sk);
-          if (edge) {
-            const int key = kb + g + (c & 2) * 4;
-            if (key < lo[nt][c & 1] || key >= hi[nt][c & 1]) x = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x = fmaf(st[n][nt][c], fac[nt][c & 1] * sk, -ref[nt][c & 1]);
+            if (edge) {
+              const int key = kb + n * kCacheBlock + g + (c & 2) * 4;
+              if (key < lo[nt][c & 1] || key >= hi[nt][c & 1] || !here) x = -INFINITY;
+            }
+            st[n][nt][c] = x;
+            over |= x > room[nt][c & 1];
           }
-          st[nt][c] = x;
-          over |= x > mref[nt][c & 1] + 15.0f;
-        }
+      }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(st[nt][c], st[nt][c + 2]);
+            float top = fmaxf(st[0][nt][c], st[0][nt][c + 2]);
+#pragma unroll
+            for (int n = 1; n < C::NB; ++n) top = fmaxf(top, fmaxf(st[n][nt][c], st[n][nt][c + 2]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float ref = fmaxf(mref[nt][c], top - 7.0f);
-            const float keep = ptx::ex2_approx(mref[nt][c] - (ref == -INFINITY ? 0.0f : ref));
-            mref[nt][c] = ref;
+            const bool none = room[nt][c] == -INFINITY;
+            const float up = none ? (top == -INFINITY ? 0.0f : top - 7.0f) : fmaxf(top - 7.0f, 0.0f);
+            const float keep = none ? 0.0f : ptx::ex2_approx(-up);
+            if (top != -INFINITY) room[nt][c] = 15.0f;
+            ref[nt][c] += up;
             sum[nt][c] *= keep;
+#pragma unroll
+            for (int n = 0; n < C::NB; ++n) st[n][nt][c] -= up, st[n][nt][c + 2] -= up;
 #pragma unroll
             for (int i2 = 0; i2 < ND; ++i2) {
               acc[i2][nt][c] *= keep;
@@ -454,203 +580,214 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
             }
           }
       }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = mref[nt][0] == -INFINITY ? 0.0f : mref[nt][0];
-        const float r1 = mref[nt][1] == -INFINITY ? 0.0f : mref[nt][1];
-        const float p0 = ptx::ex2_approx(st[nt][0] - r0), p1 = ptx::ex2_approx(st[nt][1] - r1);
-        const float p2 = ptx::ex2_approx(st[nt][2] - r0), p3 = ptx::ex2_approx(st[nt][3] - r1);
-        sum[nt][0] += p0 + p2;
-        sum[nt][1] += p1 + p3;
-        pb[nt][0] = transpose8x8(pack_f16x2(p0, p1));
-        pb[nt][1] = transpose8x8(pack_f16x2(p2, p3));
-      }
-
-      // O^T += V^T P^T: lane (g, t) holds D/8 coordinates of tokens 2t, 2t+1, 2t+8, 2t+9
-      uint32_t v[4][D / 32];
+      for (int n = 0; n < C::NB; ++n) {
+        uint32_t pb[NT][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 2 * t + (j & 1) + (j & 2) * 4;
-        if (D == 128) {
-          uint32_t x[4];
-          lds128(vt + tile_at<D>(r, g), x);
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) v[j][w] = x[w];
-        } else {
-          lds64(vt + tile_at<D>(r, g >> 1) + (g & 1) * 8, v[j][0], v[j][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const float p0 = ptx::ex2_approx(st[n][nt][0]), p1 = ptx::ex2_approx(st[n][nt][1]);
+          const float p2 = ptx::ex2_approx(st[n][nt][2]), p3 = ptx::ex2_approx(st[n][nt][3]);
+          sum[nt][0] += p0 + p2;
+          sum[nt][1] += p1 + p3;
+          pb[nt][0] = transpose8x8(pack_f16x2(p0, p1));
+          pb[nt][1] = transpose8x8(pack_f16x2(p2, p3));
         }
-      }
-      // At an edge a token may be hidden from some rows only, and 0 times a
-      // NaN value is NaN: such a tile is added token by token to the rows
-      // that see it.  Tokens hidden from all rows are cleared.
-      bool by_token = false;
-      if (edge) {
-        bool nan = false;
+
+        // O^T += V^T P^T: lane (g, t) holds D/8 coordinates of tokens 2t, 2t+1, 2t+8, 2t+9
+        const uint32_t vt = kt + n * 2 * C::TILE + C::TILE;
+        uint32_t v[4][D / 32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int key = kb + 2 * t + (j & 1) + (j & 2) * 4;
+          const int r = 2 * t + (j & 1) + (j & 2) * 4;
+          if (D == 128) {
+            uint32_t x[4];
+            lds128(vt + tile_at<D>(r, g), x);
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            if (key < lo_min || key >= hi_max) v[j][w] = 0;
-            nan |= has_nan_code(v[j][w]);
+            for (int w = 0; w < D / 32; ++w) v[j][w] = x[w];
+          } else {
+            lds64(vt + tile_at<D>(r, g >> 1) + (g & 1) * 8, v[j][0], v[j][1]);
           }
         }
-        by_token = __any_sync(0xffffffffu, nan);
-      }
-      if (!by_token) {
+        // At an edge a token may be hidden from some rows only, and 0 times a
+        // NaN value is NaN: such a tile is added token by token to the rows
+        // that see it.  Tokens hidden from all rows are cleared.
+        bool by_token = false;
+        if (edge) {
+          bool nan = false;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w)
+          for (int j = 0; j < 4; ++j) {
+            const int key = kb + n * kCacheBlock + 2 * t + (j & 1) + (j & 2) * 4;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t x01 = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
-            const uint32_t x23 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
-            const uint32_t a0 = codes_lo(x01), a1 = codes_hi(x01), a2 = codes_lo(x23), a3 = codes_hi(x23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_f16(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[2 * w + half][nt][c] = fmaf(o[c], sv, acc[2 * w + half][nt][c]);
+            for (int w = 0; w < D / 32; ++w) {
+              if (key < lo_min || key >= hi_max) v[j][w] = 0;
+              nan |= has_nan_code(v[j][w]);
             }
           }
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < kCacheBlock; ++k) {
-          const int key = kb + k;
+          by_token = __any_sync(0xffffffffu, nan);
+        }
+        if (!by_token) {
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t y[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = 2 * t + (j & 1) + (j & 2) * 4 == k ? v[j][w] : 0;
-              const uint32_t x01 = __byte_perm(y[0], y[1], half ? 0x7362 : 0x5140);
-              const uint32_t x23 = __byte_perm(y[2], y[3], half ? 0x7362 : 0x5140);
+              const uint32_t x01 = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
+              const uint32_t x23 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
               const uint32_t a0 = codes_lo(x01), a1 = codes_hi(x01), a2 = codes_lo(x23), a3 = codes_hi(x23);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                float o[4];
+                mma_f16_new(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  if (key >= lo[nt][c & 1] && key < hi[nt][c & 1])
-                    acc[2 * w + half][nt][c] = fmaf(o[c], sv, acc[2 * w + half][nt][c]);
+                for (int c = 0; c < 4; ++c) acc[2 * w + half][nt][c] = fmaf(o[c], sv[n], acc[2 * w + half][nt][c]);
               }
             }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < kCacheBlock; ++k) {
+            const int key = kb + n * kCacheBlock + k;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = 2 * t + (j & 1) + (j & 2) * 4 == k ? v[j][w] : 0;
+                const uint32_t x01 = __byte_perm(y[0], y[1], half ? 0x7362 : 0x5140);
+                const uint32_t x23 = __byte_perm(y[2], y[3], half ? 0x7362 : 0x5140);
+                const uint32_t a0 = codes_lo(x01), a1 = codes_hi(x01), a2 = codes_lo(x23), a3 = codes_hi(x23);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float o[4];
+                  mma_f16_new(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    if (key >= lo[nt][c & 1] && key < hi[nt][c & 1])
+                      acc[2 * w + half][nt][c] = fmaf(o[c], sv[n], acc[2 * w + half][nt][c]);
+                }
+              }
+          }
         }
       }
     }
-    cp_wait<0>();
-
-    // ---- the four warps' results, joined in shared memory
+    // ---- the segment's result, or this run's part of it
+    const int64_t unit0 = now.start + kStart;
+    const int first = static_cast<int>(unit0 / chunk);
+    const int pieces = p.no_split ? 1 : static_cast<int>((unit0 + now.w.steps - 1) / chunk) - first + 1;
+    const int slot = first == worker ? 1 : 0;
+    float* part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * C::ROWS * (D + 2);
+    if (pieces > 1 && lane == 0) {
+      int* m = p.meta + worker * 16 + slot * 8;
+      m[0] = first, m[1] = pieces, m[2] = s.first, m[3] = s.n, m[4] = now.tile, m[5] = h;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = sum[nt][c];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) {
-          s_ml[warp][nt * 8 + 2 * t + c][0] = mref[nt][c];
-          s_ml[warp][nt * 8 + 2 * t + c][1] = x;
+        float l = sum[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int r = nt * 8 + 2 * t + c;
+        const float m = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
+        if (r >= rows) continue;
+        if (pieces == 1) {
+          const int64_t rr = row0 + r;
+          const int64_t at_row = (s.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          uint32_t o[ND];
+#pragma unroll
+          for (int i = 0; i < ND; ++i) o[i] = ptx::pack_bf16x2(acc[i][nt][c] * inv, acc[i][nt][c + 2] * inv);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at_row * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < ND / 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          if (p.lse && g == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          if (g == 0) part[2 * r] = m, part[2 * r + 1] = l;
+          float4* dst = reinterpret_cast<float4*>(part + 2 * C::ROWS + r * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < ND / 2; ++i)
+            dst[i] = make_float4(acc[2 * i][nt][c], acc[2 * i][nt][c + 2], acc[2 * i + 1][nt][c],
+                                 acc[2 * i + 1][nt][c + 2]);
         }
       }
-    __syncthreads();  // every warp is done with its ring
-    float* merge = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float* dst = merge + (static_cast<int64_t>(warp) * C::ROWS + nt * 8 + 2 * t + c) * D + g * (D / 8);
-#pragma unroll
-        for (int i = 0; i < ND; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(acc[i][nt][c], acc[i][nt][c + 2], acc[i + 1][nt][c], acc[i + 1][nt][c + 2]);
-      }
-    __syncthreads();
-    const int64_t seg_start = base + seg * sw.units;
-    const int first = static_cast<int>(seg_start / chunk);
-    const int pieces = p.no_split ? 1 : static_cast<int>((seg_start + sw.units - 1) / chunk) - first + 1;
-    const int slot = first == static_cast<int>(blockIdx.x) ? 1 : 0;
-    float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::ROWS * (D + 2);
-    for (int i = tid; i < rows * (D / 8); i += C::THREADS) {
-      const int r = i / (D / 8), d = (i % (D / 8)) * 8;
-      float ref = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) ref = fmaxf(ref, s_ml[w][r][0]);
-      float l = 0.0f, o[8] = {};
-#pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) {
-        const float f = ptx::ex2_approx(s_ml[w][r][0] - (ref == -INFINITY ? 0.0f : ref));
-        l += s_ml[w][r][1] * f;
-        const float* src = merge + (static_cast<int64_t>(w) * C::ROWS + r) * D + d;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += src[e] * f;
-      }
-      if (pieces == 1) {
-        const int64_t rr = row0 + r;
-        const int64_t at_row = (s.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint4 u;
-        u.x = ptx::pack_bf16x2(o[0] * inv, o[1] * inv);
-        u.y = ptx::pack_bf16x2(o[2] * inv, o[3] * inv);
-        u.z = ptx::pack_bf16x2(o[4] * inv, o[5] * inv);
-        u.w = ptx::pack_bf16x2(o[6] * inv, o[7] * inv);
-        *reinterpret_cast<uint4*>(p.out + at_row * D + d) = u;
-        if (p.lse && d == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-      } else {
-        if (d == 0) part[2 * r] = ref, part[2 * r + 1] = l;
-        float4* dst = reinterpret_cast<float4*>(part + 2 * C::ROWS + r * D + d);
-        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-      }
-    }
-    if (pieces > 1 && tid == 0) {
-      int* m = p.meta + (blockIdx.x * 2 + slot) * 8;
-      m[0] = first, m[1] = pieces, m[2] = s.first, m[3] = s.n, m[4] = tile, m[5] = h;
-    }
-    __syncthreads();  // the merge area is a ring again
-    at += u1 - u0;
   }
 }
 
-// Joins the parts of cut segments.  Block c is a member of up to two of them
-// (the segment that its CTA's run begins inside, slot 0, and the one it ends
-// inside, slot 1); the members of a segment share its rows.  Up to 16 parts: a
-// warp takes a row.  More: the 16 warps take a row together, each a run of the
-// parts.
+// Joins the parts of cut segments.  A worker is a member of up to two of them
+// (the segment that its run begins inside, slot 0, and the one it ends inside,
+// slot 1), and the members of a segment share its rows evenly; a block stands
+// for the four workers of a CTA.  Up to kJoinFew parts: a warp takes a row.
+// More: the block's warps take a row together, each a run of the parts.  Either
+// way 32 parts at a time: their references and sums are read by a lane each, the
+// weights that follow are handed round as the outputs are added.
+constexpr int kJoinWarps = 16, kJoinFew = 16;
+
 template <int D, int ROWS>
-__global__ void __launch_bounds__(512) gdpa_cache_join_kernel(const CacheFwdParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) gdpa_cache_join_kernel(const CacheFwdParams p) {
   constexpr int E = D / 32;
-  __shared__ float s_part[16][D + 2];
+  __shared__ float s_part[kJoinWarps][D + 2];
+  __shared__ int s_meta[8][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int slot = 0; slot < 2; ++slot) {
-    const int* m = p.meta + (blockIdx.x * 2 + slot) * 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  if (threadIdx.x < 64) s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 64 + threadIdx.x];
+  __syncthreads();
+  int task = 0;  // rows so far, for the warps to take in turn
+#pragma unroll 1
+  for (int slot = 0; slot < 8; ++slot) {
+    const int* m = s_meta[slot];
     const int pieces = m[1];
     if (pieces == 0) continue;
     const int first = m[0], row_first = m[2], n = m[3], tile = m[4], h = m[5];
-    const int member = blockIdx.x - first;
+    const int member = blockIdx.x * 4 + (slot >> 1) - first;
     const int64_t row0 = static_cast<int64_t>(tile) * ROWS;
     const int rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(n) * p.G - row0));
-    const bool together = pieces > 16;
-    const int j0 = together ? pieces * warp / 16 : 0, j1 = together ? pieces * (warp + 1) / 16 : pieces;
-    for (int r = member + (together ? 0 : warp * pieces); r < rows; r += together ? pieces : 16 * pieces) {
+    const bool together = pieces > kJoinFew;
+    const int j0 = together ? pieces * warp / kJoinWarps : 0, j1 = together ? pieces * (warp + 1) / kJoinWarps : pieces;
+    // rows r with r pieces / rows == member
+    const int r0 = (member * rows + pieces - 1) / pieces, r1 = ((member + 1) * rows + pieces - 1) / pieces;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      if (!together && task++ % kJoinWarps != warp) continue;
       float ref = -INFINITY, l = 0.0f, o[E] = {};
-#pragma unroll 4
-      for (int j = j0; j < j1; ++j) {
-        const float* part = p.part + (static_cast<int64_t>(first + j) * 2 + (j == 0)) * ROWS * (D + 2);
-        const float r2 = part[2 * r], l2 = part[2 * r + 1];
-        float x[E];
+#pragma unroll 1
+      for (int j = j0; j < j1; j += 32) {
+        const int cnt = min(32, j1 - j);
+        // slot 1 for the first part, 0 for the others
+        const float* part = p.part + (static_cast<int64_t>(first + j) * 2) * ROWS * (D + 2);
+        constexpr int step = 2 * ROWS * (D + 2);
+        const int skip = j == 0 ? ROWS * (D + 2) : 0;
+        float r2 = -INFINITY, l2 = 0.0f;
+        if (lane < cnt) {
+          const float* mine = part + static_cast<int64_t>(lane) * step + (lane == 0 ? skip : 0) + 2 * r;
+          r2 = mine[0];
+          l2 = mine[1];
+        }
+        float top = fmaxf(ref, r2);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = part[2 * ROWS + r * D + lane * E + e];
-        const float top = fmaxf(ref, r2), zero = top == -INFINITY ? 0.0f : top;
-        const float f1 = ptx::ex2_approx(ref - zero), f2 = ptx::ex2_approx(r2 - zero);
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float zero = top == -INFINITY ? 0.0f : top;
+        const float keep = ptx::ex2_approx(ref - zero), f = ptx::ex2_approx(r2 - zero);
+        float add = l2 * f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
         ref = top;
-        l = l * f1 + l2 * f2;
+        l = l * keep + add;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f1 + x[e] * f2;
+        for (int e = 0; e < E; ++e) o[e] *= keep;
+        const float* src = part + 2 * ROWS + r * D + lane * E;
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+          const float w = __shfl_sync(0xffffffffu, f, i);
+          const float* x = src + static_cast<int64_t>(i) * step + (i == 0 ? skip : 0);
+          if (E == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(x);
+            o[0] = fmaf(y.x, w, o[0]), o[1] = fmaf(y.y, w, o[1]);
+            o[E - 2] = fmaf(y.z, w, o[E - 2]), o[E - 1] = fmaf(y.w, w, o[E - 1]);
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(x);
+            o[0] = fmaf(y.x, w, o[0]), o[1] = fmaf(y.y, w, o[1]);
+          }
+        }
       }
       if (together) {
         __syncthreads();
@@ -660,11 +797,11 @@ __global__ void __launch_bounds__(512) gdpa_cache_join_kernel(const CacheFwdPara
         __syncthreads();
         if (warp != 0) continue;
         ref = -INFINITY;
-        for (int w = 0; w < 16; ++w) ref = fmaxf(ref, s_part[w][D]);
+        for (int w = 0; w < kJoinWarps; ++w) ref = fmaxf(ref, s_part[w][D]);
         l = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.0f;
-        for (int w = 0; w < 16; ++w) {
+        for (int w = 0; w < kJoinWarps; ++w) {
           const float f = ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref));
           l += s_part[w][D + 1] * f;
 #pragma unroll

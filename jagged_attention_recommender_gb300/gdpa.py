@@ -334,16 +334,27 @@ def gdpa_wait_selftest(timeout_ms: int, stream=None):
     _check(lib().gdpa_wait_selftest(int(timeout_ms), _stream(stream)), "gdpa_wait_selftest")
 
 
-def _on_gpu(where, dtype, *tensors) -> None:
-    """Refuses a tensor of another type than ``dtype`` or on another device than the current one (addresses pass)."""
-    import torch
-    want = getattr(torch, dtype)
+_torch = None
+
+
+def _device() -> int:
+    """The current CUDA device."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device() if _torch.cuda.is_initialized() or _torch.cuda.is_available() else -2
+
+
+def _on_gpu(where, device, dtype, *tensors) -> None:
+    """Refuses a tensor of another type than ``dtype`` or on another device than ``device`` (addresses pass)."""
+    want = getattr(_torch, dtype)
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
             continue
-        if t.dtype != want:
+        if t.dtype is not want:
             raise TypeError("%s: %s wanted, got %s" % (where, want, t.dtype))
-        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        if t.get_device() != device:
             raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
 
 
@@ -358,7 +369,7 @@ class KvCache:
                                ("k_sf", k_sf, (pages, H, tokens // 16)), ("v_sf", v_sf, (pages, H, tokens // 16))):
             if tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("KvCache: %s must be contiguous %r, got %r" % (name, shape, tuple(t.shape)))
-        _on_gpu("KvCache", "uint8", k_codes, v_codes, k_sf, v_sf)
+        _on_gpu("KvCache", _device(), "uint8", k_codes, v_codes, k_sf, v_sf)
         self.tensors = (k_codes, v_codes, k_sf, v_sf)
         self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
         n = 0 if self.inv_freq is None else self.inv_freq.size
@@ -371,8 +382,9 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
                       max_pages, q_out, stream=None):
     """Stores the new tokens' ``k`` and ``v`` in the cache (``k`` rotated by position) and the rotated ``q`` in
     ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
-    _on_gpu("gdpa_cache_append", "bfloat16", q, k, v, q_out)
-    _on_gpu("gdpa_cache_append", "int32", offsets, kv_lens, page_table)
+    device = _device()
+    _on_gpu("gdpa_cache_append", device, "bfloat16", q, k, v, q_out)
+    _on_gpu("gdpa_cache_append", device, "int32", offsets, kv_lens, page_table)
     _check(lib().gdpa_cache_append(cache.addr, _addr(q), int(q_stride), _addr(k), int(k_stride), _addr(v),
                                    int(v_stride), _addr(offsets), _addr(kv_lens), _addr(page_table), int(T), int(B),
                                    int(Hq), int(max_pages), _addr(q_out), _stream(stream)), "gdpa_cache_append")
@@ -383,10 +395,11 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     """Attention of the new tokens' ``q`` over the cache.  ``workspace``: a device tensor of at least
     gdpa_cache_workspace_size() bytes (or an address, with its ``workspace_bytes``); calls that may overlap need one
     each."""
-    _on_gpu("gdpa_cache_fwd", "bfloat16", q, out)
-    _on_gpu("gdpa_cache_fwd", "int32", offsets, kv_lens, page_table)
-    _on_gpu("gdpa_cache_fwd", "float32", lse)
-    _on_gpu("gdpa_cache_fwd", "uint8", workspace)
+    device = _device()
+    _on_gpu("gdpa_cache_fwd", device, "bfloat16", q, out)
+    _on_gpu("gdpa_cache_fwd", device, "int32", offsets, kv_lens, page_table)
+    _on_gpu("gdpa_cache_fwd", device, "float32", lse)
+    _on_gpu("gdpa_cache_fwd", device, "uint8", workspace)
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
     _check(lib().gdpa_cache_fwd(cache.addr, _addr(q), int(q_stride), _addr(offsets), _addr(kv_lens),

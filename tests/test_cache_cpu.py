@@ -60,7 +60,7 @@ BAD_DESC = [
     (dict(D=96), UNS), (dict(D=256), UNS), (dict(page_tokens=8), UNS), (dict(page_tokens=48), UNS),
     (dict(page_tokens=2048), UNS), (dict(page_tokens=0), INV), (dict(page_tokens=-64), INV), (dict(H=0), INV),
     (dict(H=-1), INV), (dict(H=1 << 14), UNS), (dict(num_pages=-1), INV), (dict(k_codes=None), INV),
-    (dict(v_codes=A + 8), INV), (dict(k_sf=None), INV), (dict(v_sf=None), INV), (dict(rot_dim=-16), INV),
+    (dict(v_codes=A + 8), INV), (dict(k_sf=None), INV), (dict(k_sf=A + 2), INV), (dict(v_sf=A + 1), INV), (dict(v_sf=None), INV), (dict(rot_dim=-16), INV),
     (dict(rot_dim=144), INV), (dict(rot_dim=24), UNS), (dict(inv_freq=None), INV), (dict(rope_style=2), INV),
     (dict(freq=math.nan), INV), (dict(freq=math.inf), INV),
 ]
