@@ -717,13 +717,13 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
 // (the segment that its run begins inside, slot 0, and the one it ends inside,
 // slot 1), and the members of a segment share its rows evenly; a block stands
 // for the four workers of a CTA.  Up to kJoinFew parts: a warp takes a row.
-// More: the block's warps take a row together, each a run of the parts.  Either
-// way 32 parts at a time: their references and sums are read by a lane each, the
-// weights that follow are handed round as the outputs are added.
-constexpr int kJoinWarps = 16, kJoinFew = 16;
+// More: the block's warps take a row together, each a run of the parts.  All that
+// is read of up to 8 parts is under way at once: what this kernel takes is the
+// latency of two dependent reads.
+constexpr int kJoinWarps = 8, kJoinFew = 8;
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(32 * kJoinWarps) gdpa_cache_join_kernel(const CacheFwdParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(const CacheFwdParams p) {
   constexpr int E = D / 32;
   __shared__ float s_part[kJoinWarps][D + 2];
   __shared__ int s_meta[8][8];
@@ -750,18 +750,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdpa_cache_join_kernel(const 
       if (!together && task++ % kJoinWarps != warp) continue;
       float ref = -INFINITY, l = 0.0f, o[E] = {};
 #pragma unroll 1
-      for (int j = j0; j < j1; j += 32) {
-        const int cnt = min(32, j1 - j);
+      for (int j = j0; j < j1; j += kJoinFew) {
+        const int cnt = min(kJoinFew, j1 - j);
         // slot 1 for the first part, 0 for the others
         const float* part = p.part + (static_cast<int64_t>(first + j) * 2) * ROWS * (D + 2);
         constexpr int step = 2 * ROWS * (D + 2);
         const int skip = j == 0 ? ROWS * (D + 2) : 0;
-        float r2 = -INFINITY, l2 = 0.0f;
+        float r2 = -INFINITY, l2 = 0.0f, x[kJoinFew][E];
         if (lane < cnt) {
-          const float* mine = part + static_cast<int64_t>(lane) * step + (lane == 0 ? skip : 0) + 2 * r;
-          r2 = mine[0];
-          l2 = mine[1];
+          const float2 y = *reinterpret_cast<const float2*>(part + lane * step + (lane == 0 ? skip : 0) + 2 * r);
+          r2 = y.x;
+          l2 = y.y;
         }
+        const float* src = part + 2 * ROWS + r * D + lane * E;
+#pragma unroll
+        for (int i = 0; i < kJoinFew; ++i)
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            float2 y = make_float2(0.0f, 0.0f);
+            if (i < cnt) y = *reinterpret_cast<const float2*>(src + i * step + (i == 0 ? skip : 0) + e);
+            x[i][e] = y.x, x[i][e + 1] = y.y;
+          }
         float top = fmaxf(ref, r2);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -774,19 +783,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdpa_cache_join_kernel(const 
         l = l * keep + add;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= keep;
-        const float* src = part + 2 * ROWS + r * D + lane * E;
-#pragma unroll 8
-        for (int i = 0; i < cnt; ++i) {
+#pragma unroll
+        for (int i = 0; i < kJoinFew; ++i) {
           const float w = __shfl_sync(0xffffffffu, f, i);
-          const float* x = src + static_cast<int64_t>(i) * step + (i == 0 ? skip : 0);
-          if (E == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(x);
-            o[0] = fmaf(y.x, w, o[0]), o[1] = fmaf(y.y, w, o[1]);
-            o[E - 2] = fmaf(y.z, w, o[E - 2]), o[E - 1] = fmaf(y.w, w, o[E - 1]);
-          } else {
-            const float2 y = *reinterpret_cast<const float2*>(x);
-            o[0] = fmaf(y.x, w, o[0]), o[1] = fmaf(y.y, w, o[1]);
-          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], w, o[e]);  // 0 * 0 behind the last part
         }
       }
       if (together) {

@@ -129,6 +129,12 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream or None
 
 
+def _stream_on(device: int) -> int | None:
+    """The address of the current stream of ``device``."""
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object is made where torch offers that
+    return (raw(device) if raw else _torch.cuda.current_stream(device).cuda_stream) or None
+
+
 def _check(code: int, where: str):
     if code != GDPA_OK:
         raise GdpaError(code, where)
@@ -335,27 +341,28 @@ def gdpa_wait_selftest(timeout_ms: int, stream=None):
 
 
 _torch = None
+_dtypes = None
 
 
 def _device() -> int:
-    """The current CUDA device."""
-    global _torch
+    """The current CUDA device (-2: there is none)."""
+    global _torch, _dtypes
     if _torch is None:
         import torch
+        _dtypes = {n: getattr(torch, n) for n in ("bfloat16", "int32", "float32", "uint8")}
         _torch = torch
-    return _torch.cuda.current_device() if _torch.cuda.is_initialized() or _torch.cuda.is_available() else -2
+    return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
 
 
-def _on_gpu(where, device, dtype, *tensors) -> None:
-    """Refuses a tensor of another type than ``dtype`` or on another device than ``device`` (addresses pass)."""
-    want = getattr(_torch, dtype)
-    for t in tensors:
-        if t is None or t.__class__ is int:
-            continue
-        if t.dtype is not want:
-            raise TypeError("%s: %s wanted, got %s" % (where, want, t.dtype))
-        if t.get_device() != device:
-            raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
+def _at(where, device, dtype, t):
+    """The address of a tensor of type ``dtype`` on ``device``; another one is refused (addresses and None pass)."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not _dtypes[dtype]:
+        raise TypeError("%s: %s wanted, got %s" % (where, dtype, t.dtype))
+    if t.get_device() != device:
+        raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
+    return t.data_ptr()
 
 
 class KvCache:
@@ -369,11 +376,12 @@ class KvCache:
                                ("k_sf", k_sf, (pages, H, tokens // 16)), ("v_sf", v_sf, (pages, H, tokens // 16))):
             if tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("KvCache: %s must be contiguous %r, got %r" % (name, shape, tuple(t.shape)))
-        _on_gpu("KvCache", _device(), "uint8", k_codes, v_codes, k_sf, v_sf)
+        device = _device()
+        at = [_at("KvCache", device, "uint8", t) for t in (k_codes, v_codes, k_sf, v_sf)]
         self.tensors = (k_codes, v_codes, k_sf, v_sf)
         self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
         n = 0 if self.inv_freq is None else self.inv_freq.size
-        self.desc = _CacheDesc(_addr(k_codes), _addr(v_codes), _addr(k_sf), _addr(v_sf), pages, tokens, H, D,
+        self.desc = _CacheDesc(*at, pages, tokens, H, D,
                                self.inv_freq.ctypes.data if n else None, 2 * n, int(rope_style))
         self.addr = ctypes.addressof(self.desc)
 
@@ -382,12 +390,12 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
                       max_pages, q_out, stream=None):
     """Stores the new tokens' ``k`` and ``v`` in the cache (``k`` rotated by position) and the rotated ``q`` in
     ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
-    device = _device()
-    _on_gpu("gdpa_cache_append", device, "bfloat16", q, k, v, q_out)
-    _on_gpu("gdpa_cache_append", device, "int32", offsets, kv_lens, page_table)
-    _check(lib().gdpa_cache_append(cache.addr, _addr(q), int(q_stride), _addr(k), int(k_stride), _addr(v),
-                                   int(v_stride), _addr(offsets), _addr(kv_lens), _addr(page_table), int(T), int(B),
-                                   int(Hq), int(max_pages), _addr(q_out), _stream(stream)), "gdpa_cache_append")
+    d, where = _device(), "gdpa_cache_append"
+    _check(lib().gdpa_cache_append(
+        cache.addr, _at(where, d, "bfloat16", q), q_stride, _at(where, d, "bfloat16", k), k_stride,
+        _at(where, d, "bfloat16", v), v_stride, _at(where, d, "int32", offsets), _at(where, d, "int32", kv_lens),
+        _at(where, d, "int32", page_table), T, B, Hq, max_pages, _at(where, d, "bfloat16", q_out),
+        _stream_on(d) if stream is None else _stream(stream)), where)
 
 
 def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
@@ -395,17 +403,14 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     """Attention of the new tokens' ``q`` over the cache.  ``workspace``: a device tensor of at least
     gdpa_cache_workspace_size() bytes (or an address, with its ``workspace_bytes``); calls that may overlap need one
     each."""
-    device = _device()
-    _on_gpu("gdpa_cache_fwd", device, "bfloat16", q, out)
-    _on_gpu("gdpa_cache_fwd", device, "int32", offsets, kv_lens, page_table)
-    _on_gpu("gdpa_cache_fwd", device, "float32", lse)
-    _on_gpu("gdpa_cache_fwd", device, "uint8", workspace)
+    d, where = _device(), "gdpa_cache_fwd"
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
-    _check(lib().gdpa_cache_fwd(cache.addr, _addr(q), int(q_stride), _addr(offsets), _addr(kv_lens),
-                                _addr(page_table), int(T), int(B), int(Hq), int(max_pages), int(max_q), int(causal),
-                                int(window_tokens), float(scale), _addr(out), _addr(lse), _addr(workspace),
-                                int(workspace_bytes), _stream(stream)), "gdpa_cache_fwd")
+    _check(lib().gdpa_cache_fwd(
+        cache.addr, _at(where, d, "bfloat16", q), q_stride, _at(where, d, "int32", offsets),
+        _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, max_q, causal,
+        window_tokens, scale, _at(where, d, "bfloat16", out), _at(where, d, "float32", lse),
+        _at(where, d, "uint8", workspace), workspace_bytes, _stream_on(d) if stream is None else _stream(stream)), where)
 
 
 def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:
