@@ -10,11 +10,14 @@
 
 #include "gdpa_cache_append.cuh"
 #include "gdpa_cache_fwd.cuh"
+#include "gdpa_cache_tile.cuh"
 #include "gdpa_internal.h"
 
 namespace gdpa {
 
-int* device_status_word(int device);  // gdpa_kernels.cu
+// gdpa_kernels.cu
+int* device_status_word(int device);
+unsigned long long bounded_wait_ns();
 
 namespace {
 
@@ -94,54 +97,70 @@ unsigned long long turn_fraction(double f) {
   return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
 }
 
-// Query rows of a segment, in eights: the fewest that hold one sequence's rows
-// of a key head, at most four.
+// The kernel for so many query rows of a key head: eights of rows of the one
+// for few rows, or 0: the one for many.
 int split_columns(int max_q, int G) {
   const int64_t rows = (int64_t)max_q * G;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
 }
 
-int split_ctas(int nt, int D) {
-  if (D == 64) return nt == 1 ? SplitCfg<64, 1>::CTAS : nt == 2 ? SplitCfg<64, 2>::CTAS : SplitCfg<64, 4>::CTAS;
-  return nt == 1 ? SplitCfg<128, 1>::CTAS : nt == 2 ? SplitCfg<128, 2>::CTAS : SplitCfg<128, 4>::CTAS;
+// Bytes of meta data and parts for so many workers.
+int64_t part_bytes(int64_t workers, int rows, int D) {
+  return workers * 2 * (8 * sizeof(int) + (int64_t)rows * (D + 2) * sizeof(float));
 }
 
-int64_t split_workspace(int64_t ctas, int rows, int D) {
-  return ctas * 4 * 2 * (8 * sizeof(int) + (int64_t)rows * (D + 2) * sizeof(float));  // four warps a CTA
+template <class C>
+int64_t workspace_of(const Device& dev, int D) {
+  return part_bytes((int64_t)dev.sms * C::CTAS * C::WORKERS, C::ROWS, D);
 }
 
-template <int D, int NT>
-gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
-  using C = SplitCfg<D, NT>;
-  static_assert(C::SMEM <= 227 * 1024, "shared memory of a CTA");
-  static std::mutex mu;
-  static bool done[kMaxDevices] = {};
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!done[dev.id]) {
-      if (cudaFuncSetAttribute(gdpa_cache_split_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
-          cudaSuccess)
-        return GDPA_ERR_CUDA;
-      done[dev.id] = true;
-    }
-  }
-  // Keys a segment can have, as far as the host knows: up to 512 of them (two
-  // fills of the rings) are not worth a second kernel.
+template <int D>
+int64_t workspace_bytes(const Device& dev, int max_q, int G) {
+  const int nt = split_columns(max_q, G);
+  return nt == 1 ? workspace_of<SplitCfg<D, 1>>(dev, D)
+                 : nt == 2 ? workspace_of<SplitCfg<D, 2>>(dev, D) : workspace_of<TileCfg<D>>(dev, D);
+}
+
+// Shared memory above 48 KB has to be asked for, once a device and kernel.
+// `min_regs`: a kernel that trades registers between its warpgroups needs that
+// many at launch, or its increase would wait for ever; such a build is refused.
+template <typename Kernel>
+gdpa_status_t allow_smem(Kernel kernel, int bytes, int min_regs, int device, std::mutex& mu, bool* done) {
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[device]) return GDPA_OK;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return GDPA_ERR_CUDA;
+  if (fa.numRegs < min_regs) return GDPA_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return GDPA_ERR_CUDA;
+  done[device] = true;
+  return GDPA_OK;
+}
+
+// Sets up a launch of configuration C: whether segments may be cut, the
+// workspace, and how many CTAs have work at most.
+template <class C>
+int prepare_launch(CacheFwdParams& p, void* workspace, int max_q, const Device& dev) {
+  // Keys a segment can have, as far as the host knows: up to 512 of them are
+  // not worth a second kernel.
   int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock);
   p.no_split = keys <= 512 ? 1 : 0;
-  // workers that can have a run, at most
   const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;
-  const int64_t workers = segments * ((keys / C::SPAN + 1 + kStart) / kRunSteps + 1);
+  const int64_t workers = segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
   const int ctas = static_cast<int>(
-      std::min<int64_t>((workers + C::WARPS - 1) / C::WARPS, (int64_t)dev.sms * C::CTAS));
+      std::min<int64_t>((workers + C::WORKERS - 1) / C::WORKERS, (int64_t)dev.sms * C::CTAS));
   p.meta = static_cast<int*>(workspace);
-  p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * C::WARPS * 16);
-  gdpa_cache_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * C::WORKERS * 16);
+  return ctas;
+}
+
+// The second kernel.  Its blocks are placed while the last of the first
+// kernel's CTAs finish, and wait there.
+template <int D, class C>
+gdpa_status_t launch_join(const CacheFwdParams& p, int ctas, cudaStream_t s) {
   if (cudaGetLastError() != cudaSuccess) return GDPA_ERR_CUDA;
   if (p.no_split) return GDPA_OK;
-  // the join's blocks are placed while the last of the first kernel's CTAs
-  // finish, and wait there
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -151,7 +170,40 @@ gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const 
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdpa_cache_join_kernel<D, C::ROWS>, p) == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, gdpa_cache_join_kernel<D, C::ROWS, C::WORKERS>, p) == cudaSuccess ? GDPA_OK
+                                                                                                    : GDPA_ERR_CUDA;
+}
+
+template <int D, int NT>
+gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  using C = SplitCfg<D, NT>;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  const gdpa_status_t st = allow_smem(gdpa_cache_split_kernel<D, NT>, C::SMEM, 0, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  const int ctas = prepare_launch<C>(p, workspace, max_q, dev);
+  gdpa_cache_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  return launch_join<D, C>(p, ctas, s);
+}
+
+template <int D>
+gdpa_status_t launch_tile(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  using C = TileCfg<D>;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  const gdpa_status_t st = allow_smem(gdpa_cache_tile_kernel<D>, C::SMEM, C::LAUNCH_REGS, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  const int ctas = prepare_launch<C>(p, workspace, max_q, dev);
+  gdpa_cache_tile_kernel<D><<<ctas, C::THREADS, C::SMEM, s>>>(p, bounded_wait_ns());
+  return launch_join<D, C>(p, ctas, s);
+}
+
+template <int D>
+gdpa_status_t launch_fwd(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  const int nt = split_columns(max_q, p.G);
+  return nt == 1 ? launch_split<D, 1>(p, workspace, max_q, dev, s)
+                 : nt == 2 ? launch_split<D, 2>(p, workspace, max_q, dev, s)
+                           : launch_tile<D>(p, workspace, max_q, dev, s);
 }
 
 }  // namespace
@@ -214,8 +266,8 @@ extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, in
   if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
-  const int nt = split_columns(max_q, Hq / cache->H);
-  *bytes = split_workspace(dev.sms * split_ctas(nt, cache->D), 8 * nt, cache->D);
+  const int G = Hq / cache->H;
+  *bytes = cache->D == 128 ? gdpa::workspace_bytes<128>(dev, max_q, G) : gdpa::workspace_bytes<64>(dev, max_q, G);
   return GDPA_OK;
 }
 
@@ -254,12 +306,5 @@ extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q
   p.window = window_tokens;
   p.scale2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int nt = split_columns(max_q, p.G);
-  if (cache->D == 128)
-    return nt == 1 ? launch_split<128, 1>(p, workspace, max_q, dev, s)
-                   : nt == 2 ? launch_split<128, 2>(p, workspace, max_q, dev, s)
-                             : launch_split<128, 4>(p, workspace, max_q, dev, s);
-  return nt == 1 ? launch_split<64, 1>(p, workspace, max_q, dev, s)
-                 : nt == 2 ? launch_split<64, 2>(p, workspace, max_q, dev, s)
-                           : launch_split<64, 4>(p, workspace, max_q, dev, s);
+  return cache->D == 128 ? launch_fwd<128>(p, workspace, max_q, dev, s) : launch_fwd<64>(p, workspace, max_q, dev, s);
 }

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -45,6 +46,15 @@ __device__ __forceinline__ int64_t cache_sf(const CacheView& c, int page, int he
 // 2^(code - 127); code 0 is the subnormal 2^-127, 255 is NaN (E8M0).
 __device__ __forceinline__ float sf_value(int code) {
   return code == 255 ? __int_as_float(0x7fc00000) : code ? __int_as_float(code << 23) : __int_as_float(0x00400000);
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
+  float f;
+  asm("{ .reg .b16 t, lo, hi; .reg .b32 h; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 h, t; mov.b32 {lo, hi}, h;"
+      " cvt.f32.f16 %0, lo; }"
+      : "=f"(f)
+      : "r"(byte));
+  return f;
 }
 
 // The sequence that holds row r of the new tokens, or B if none does: the

@@ -57,12 +57,12 @@ struct CacheFwdParams {
 // `pieces - 1` workers behind it the next ones in their slots 0.  Beside each
 // part stand {first, pieces, first row of the sequence, its rows, row tile, head}.
 
-constexpr int kStart = 2;     // what a segment's start costs, in steps
-constexpr int kRunSteps = 6;  // the fewest steps (starts included) that are worth a worker
-
 template <int D, int NT>
 struct SplitCfg {
   static constexpr int THREADS = 128, WARPS = 4;
+  static constexpr int WORKERS = 4;    // of a CTA: its warps
+  static constexpr int START = 2;      // what a segment's start costs, in steps
+  static constexpr int RUN_STEPS = 6;  // the fewest steps (starts included) that are worth a worker
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
 #ifndef XNB
@@ -185,8 +185,57 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
   w.tiles = static_cast<int>((static_cast<int64_t>(w.s.n) * p.G + C::ROWS - 1) / C::ROWS);
   return w;
 }
+template <class C>
 __device__ __forceinline__ int64_t seq_cost(const CacheFwdParams& p, const SeqWork& w) {
-  return static_cast<int64_t>(w.tiles) * p.cache.H * (w.steps + kStart);
+  return static_cast<int64_t>(w.tiles) * p.cache.H * (w.steps + C::START);
+}
+
+// The runs of a CTA's workers: where each begins.  All threads take part.
+template <class C>
+struct Schedule {
+  int64_t scan[C::THREADS / 32];
+  int64_t base[C::WORKERS];  // the work in front of the sequence in which the worker's run begins
+  int seq[C::WORKERS];
+};
+template <class C>
+__device__ __forceinline__ void schedule(const CacheFwdParams& p, Schedule<C>& sh, int64_t& total, int64_t& chunk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.batch.B;
+  int64_t mine = 0;
+  const int per = (B + C::THREADS - 1) / C::THREADS;
+  const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_cost<C>(p, seq_work<C>(p, b));
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += x;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) incl += sh.scan[w];
+    total += sh.scan[w];
+  }
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WORKERS;
+  chunk = max((total + workers - 1) / workers, (int64_t)C::RUN_STEPS);
+#pragma unroll 1
+  for (int w = 0; w < C::WORKERS; ++w) {
+    const int64_t from = chunk * (static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
+    if (from < total && from >= incl - mine && from < incl) {
+      int64_t base = incl - mine;
+      int b = b_lo;
+      for (; b < b_hi; ++b) {
+        const int64_t n = seq_cost<C>(p, seq_work<C>(p, b));
+        if (from < base + n) break;
+        base += n;
+      }
+      sh.seq[w] = b;
+      sh.base[w] = base;
+    }
+  }
+  __syncthreads();
 }
 
 // Walks the segments of a worker's run [at, stop) of the work.
@@ -203,13 +252,13 @@ struct Walk {
   __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
     b = seq;
     w = seq_work<C>(p, b);
-    const int64_t cost = w.steps + kStart, seg = (at - base) / cost;
+    const int64_t cost = w.steps + C::START, seg = (at - base) / cost;
     start = base + seg * cost;
     tile = static_cast<int>(seg / p.cache.H);
     h = static_cast<int>(seg - static_cast<int64_t>(tile) * p.cache.H);
   }
   __device__ __forceinline__ void next(const CacheFwdParams& p) {
-    start += w.steps + kStart;
+    start += w.steps + C::START;
     if (++h < p.cache.H) return;
     h = 0;
     if (++tile < w.tiles) return;
@@ -230,8 +279,8 @@ struct Walk {
       u0 = 0;
       u1 = w.steps;
     } else {
-      u0 = static_cast<int>(max(at - start - kStart, (int64_t)0));
-      u1 = static_cast<int>(min(stop - start - kStart, (int64_t)w.steps));
+      u0 = static_cast<int>(max(at - start - C::START, (int64_t)0));
+      u1 = static_cast<int>(min(stop - start - C::START, (int64_t)w.steps));
       if (u1 <= u0) return false;
     }
     row0 = static_cast<int64_t>(tile) * C::ROWS;
@@ -254,9 +303,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   using C = SplitCfg<D, NT>;
   constexpr int KS = C::KSTEPS, ND = D / 16;  // k-steps of S^T; 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[C::WARPS];
-  __shared__ int64_t s_base[C::WARPS];
-  __shared__ int s_seq[C::WARPS];
+  __shared__ Schedule<C> sh;
   __shared__ __align__(8) uint32_t s_sf[C::WARPS][C::STAGES][2 * C::NB];  // words that hold the scale codes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -265,44 +312,9 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up beside this
 
-  // ---- the workers' runs, and the sequence in which each begins
-  int64_t mine = 0;
-  const int per = (bt.B + C::THREADS - 1) / C::THREADS;
-  const int b_lo = min(bt.B, tid * per), b_hi = min(bt.B, b_lo + per);
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_cost(p, seq_work<C>(p, b));
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += x;
-  }
-  if (lane == 31) s_scan[warp] = incl;
   if (lane == 0 && !p.no_split) p.meta[worker * 16 + 1] = p.meta[worker * 16 + 9] = 0;  // no parts yet
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) incl += s_scan[w];
-    total += s_scan[w];
-  }
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WARPS;
-  const int64_t chunk = max((total + workers - 1) / workers, (int64_t)kRunSteps);
-#pragma unroll 1
-  for (int w = 0; w < C::WARPS; ++w) {
-    const int64_t from = chunk * (blockIdx.x * C::WARPS + w);
-    if (from < total && from >= incl - mine && from < incl) {
-      int64_t base = incl - mine;
-      int b = b_lo;
-      for (; b < b_hi; ++b) {
-        const int64_t n = seq_cost(p, seq_work<C>(p, b));
-        if (from < base + n) break;
-        base += n;
-      }
-      s_seq[w] = b;
-      s_base[w] = base;
-    }
-  }
-  __syncthreads();
+  int64_t total, chunk;
+  schedule<C>(p, sh, total, chunk);
   const int64_t at = chunk * worker, stop = min(total, at + chunk);
   if (at >= stop) return;
 
@@ -314,7 +326,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
 
   // ---- the copies: a walk that runs ahead of the one that computes
   Walk<C> ahead;
-  ahead.begin(p, s_seq[warp], s_base[warp], at);
+  ahead.begin(p, sh.seq[warp], sh.base[warp], at);
   Walk<C> now = ahead;
   int ahead_u = 0;
   bool ahead_more = false;
@@ -670,7 +682,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
       }
     }
     // ---- the segment's result, or this run's part of it
-    const int64_t unit0 = now.start + kStart;
+    const int64_t unit0 = now.start + C::START;
     const int first = static_cast<int>(unit0 / chunk);
     const int pieces = p.no_split ? 1 : static_cast<int>((unit0 + now.w.steps - 1) / chunk) - first + 1;
     const int slot = first == worker ? 1 : 0;
@@ -716,29 +728,30 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
 // Joins the parts of cut segments.  A worker is a member of up to two of them
 // (the segment that its run begins inside, slot 0, and the one it ends inside,
 // slot 1), and the members of a segment share its rows evenly; a block stands
-// for the four workers of a CTA.  Up to kJoinFew parts: a warp takes a row.
+// for the WORKERS workers of a CTA.  Up to kJoinFew parts: a warp takes a row.
 // More: the block's warps take a row together, each a run of the parts.  All that
 // is read of up to 8 parts is under way at once: what this kernel takes is the
 // latency of two dependent reads.
 constexpr int kJoinWarps = 8, kJoinFew = 8;
 
-template <int D, int ROWS>
+template <int D, int ROWS, int WORKERS>
 __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(const CacheFwdParams p) {
   constexpr int E = D / 32;
   __shared__ float s_part[kJoinWarps][D + 2];
-  __shared__ int s_meta[8][8];
+  __shared__ int s_meta[2 * WORKERS][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
-  if (threadIdx.x < 64) s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 64 + threadIdx.x];
+  if (threadIdx.x < 16 * WORKERS)
+    s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 16 * WORKERS + threadIdx.x];
   __syncthreads();
   int task = 0;  // rows so far, for the warps to take in turn
 #pragma unroll 1
-  for (int slot = 0; slot < 8; ++slot) {
+  for (int slot = 0; slot < 2 * WORKERS; ++slot) {
     const int* m = s_meta[slot];
     const int pieces = m[1];
     if (pieces == 0) continue;
     const int first = m[0], row_first = m[2], n = m[3], tile = m[4], h = m[5];
-    const int member = blockIdx.x * 4 + (slot >> 1) - first;
+    const int member = blockIdx.x * WORKERS + (slot >> 1) - first;
     const int64_t row0 = static_cast<int64_t>(tile) * ROWS;
     const int rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(n) * p.G - row0));
     const bool together = pieces > kJoinFew;

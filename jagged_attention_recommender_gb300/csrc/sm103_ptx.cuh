@@ -160,6 +160,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn_major) 
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with fp16 A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // Instruction descriptor, kind::mxf8f6f4 with block scaling: e4m3 A and B,
 // both K-major, fp32 accumulator, E8M0 scales (bit 23), shape M x N.  Each
 // operand's scales sit in TMEM as 32-bit words of four E8M0 codes; `sf_id`
