@@ -248,6 +248,7 @@ struct Walk {
   int rows;
   int u0, u1;     // its steps that are in the run and hold visible keys
   int lo_min, hi_max;  // keys any of its rows sees: [lo_min, hi_max)
+  int lo_max, hi_min;  // keys all of them see: [lo_max, hi_min)
 
   __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
     b = seq;
@@ -289,6 +290,8 @@ struct Walk {
     const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
     lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
     hi_max = max(0, p.causal ? min(s.len, pos1 + 1) : s.len);
+    lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
+    hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
     u0 = max(u0, (lo_min - w.kbase) / C::SPAN);
     u1 = hi_max > w.kbase ? min(u1, (hi_max - 1 - w.kbase) / C::SPAN + 1) : u0;
     return true;
@@ -474,12 +477,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         hi[nt][c] = col < rows ? (p.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
     }
-    // the keys that all of its rows see: [lo_max, hi_min)
-    const int lo_min = now.lo_min, hi_max = now.hi_max;
-    const int pos0 = s.len - s.n + static_cast<int>(row0 / p.G);
-    const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
-    const int lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
-    const int hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
+    const int lo_min = now.lo_min, hi_max = now.hi_max, lo_max = now.lo_max, hi_min = now.hi_min;
     if (NT > 1) __syncwarp();
 
     float acc[ND][NT][4];

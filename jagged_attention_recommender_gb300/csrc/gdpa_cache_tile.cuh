@@ -2,16 +2,20 @@
 // (pieces of prompts, candidates, many drafted tokens): 128 query rows of a
 // key head at a time on the 5th-generation tensor cores.
 //
-// Mathematics.  S = Q K^T with fp16 operands: e4m3 codes are fp16 exactly, a
-// query row is divided by a power of two (as in the kernel for few rows), and
-// the 16-key blocks' scales multiply the scores.  O += P V with bf16 operands:
-// bf16 holds code times scale exactly, so V is scaled as it is converted, and
-// weights, at most 2^8, are rounded to bf16 (relative 2^-9, as in the forward
-// over unquantised keys).  Sums stay in fp32; the row sum takes the weights
-// before their rounding.
+// Mathematics.  Both products take fp16 operands.  e4m3 codes are fp16
+// exactly, and a query row is divided by a power of two (as in the kernel for
+// few rows).  K stays as codes: the scales of the 16-key blocks multiply the
+// scores.  V is multiplied by its block's scale over 2^E, E the largest scale's
+// exponent so far (raised when a block exceeds it by 7, the output following):
+// exact while a block is less than 2^15 below it, and a block of other than
+// zeros further below sends its segment to the plain form.  Weights are 2^(x - r)
+// with a reference r 7 below the running maximum, moved when a score exceeds it
+// by 15, and rounded to fp16, as in the kernel for few rows.  Sums stay in fp32;
+// the row sum takes the weights before their rounding.
 //
-// Bound: the tensor core and the special-function unit alike (a 128 x 64 tile
-// takes 512 cycles of either at D = 128), the conversions close behind.
+// Bound: the instruction issue (softmax and conversions), the tensor core and
+// the special-function unit (512 cycles each of a 128 x 64 tile at D = 128)
+// close behind.
 //
 // Work split.  Segments (sequence, 128 rows, key head) and runs as in the
 // kernel for few rows, a CTA being the worker and 64 keys a step; a cut
@@ -20,14 +24,14 @@
 //   warps 0-3  softmax, a query row a thread: load Q of the segment into
 //              shared memory, then for every tile S -> P (over S in TMEM), and
 //              the output;
-//   warps 4-7  read codes a tile ahead, convert and store K and V tiles
-//              (128-byte swizzle) in two stages;
+//   warps 4-7  copy codes to shared memory a tile ahead, convert and store K
+//              and V tiles (128-byte swizzle) in two stages;
 //   warp 8     issues the MMAs, S one tile ahead of P V (warps 9-11 only give
 //              their registers to the softmax).
 //
 // A value that is NaN must not reach rows that do not see its token, and 0
 // times NaN is NaN: a segment with a NaN value in a tile that some row sees
-// only in part is computed again, row by row, without the tensor core.
+// only in part takes the plain form too (row by row, after the other).
 #pragma once
 
 #include "gdpa_cache_fwd.cuh"
@@ -45,15 +49,17 @@ struct TileCfg {
   static constexpr int Q_CHUNK = ROWS * 128, KV_CHUNK = SPAN * 128;
   static constexpr int Q_BYTES = CHUNKS * Q_CHUNK, KV_BYTES = CHUNKS * KV_CHUNK;
   static constexpr int OFF_K = Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES;
-  static constexpr int USED = OFF_V + 2 * KV_BYTES + 1024;  // + slack for 1024-byte alignment
-  // two CTAs an SM and no more, for the TMEM's sake
+  static constexpr int OFF_RAW = OFF_V + 2 * KV_BYTES;   // codes of the next tile, K then V
+  static constexpr int RAW = SPAN * D;
+  // the barrier block behind it; two CTAs an SM and no more, for the TMEM's sake
+  static constexpr int USED = OFF_RAW + 2 * RAW + 1024;
   static constexpr int SMEM = USED > 98 * 1024 ? USED : 98 * 1024;
   // registers a thread after the warpgroups have traded them: together what
   // the launch allocates, three times LAUNCH_REGS
   static constexpr int LAUNCH_REGS = 80, REGS_SOFTMAX = 128, REGS_CONVERT = 72, REGS_MMA = 40;
   static_assert(REGS_SOFTMAX + REGS_CONVERT + REGS_MMA <= 3 * LAUNCH_REGS, "registers");
   static constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLS = 256;  // two S buffers of 64 columns, O
-  static_assert(2 * (SMEM + 4096) <= 228 * 1024, "two CTAs an SM");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
 namespace tile {
@@ -71,7 +77,8 @@ struct Bars {
 // refill of an entry waits for S(i + 2), which waits for P(i).
 struct Notes {
   float k_scale[4][4];  // of the tile's blocks; -1: no page, hidden from all rows
-  int nan[4][4];        // a warp found NaN values where only some rows look
+  int plain[4][4];      // a warp found what only the plain form takes
+  int exponent[4];      // E
 };
 
 // One row of a segment over keys [j0, j1), one warp, D / 32 coordinates a lane:
@@ -162,6 +169,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
     const int steps = w.u1 - w.u0;
     float m = -INFINITY, l = 0.0f;
     bool dirty = false;
+    int exponent = 0;
     if (steps > 0) {
       // ---- this row of Q, divided by its largest power of two, as fp16
       // (read twice: registers are short, the row is in L1)
@@ -193,10 +201,6 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(&B.q_full);
 
-      const int pos0 = s.len - s.n + static_cast<int>(w.row0 / p.G);
-      const int pos1 = s.len - s.n + static_cast<int>((w.row0 + w.rows - 1) / p.G);
-      const int lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
-      const int hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
       const bool live = quarter * 32 < w.rows;  // a warp without rows keeps the barriers' protocol
       const bool fold = p.scale2 > 0.0f;
 #pragma unroll 1
@@ -219,11 +223,12 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
             const float sk = *const_cast<volatile const float*>(&notes.k_scale[gi & 3][j]);
             gone |= sk < 0.0f ? 1u << j : 0u;
             f[j] = fac * sk;
-            dirty |= *const_cast<volatile const int*>(&notes.nan[gi & 3][j]) != 0;
+            dirty |= *const_cast<volatile const int*>(&notes.plain[gi & 3][j]) != 0;
           }
+          const int e_now = *const_cast<volatile const int*>(&notes.exponent[gi & 3]);
           ptx::tmem_wait_ld_r64(sr);
           float mx = -INFINITY;
-          const bool edge = kb < lo_max || kb > hi_min - C::SPAN || gone != 0 || !fold;
+          const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN || gone != 0 || !fold;
           if (!edge) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -247,17 +252,23 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = 1.0f;
           }
-          // the reference moves when a score exceeds it by 8 (weights stay
-          // below 2^8); the output then follows, once P V of the last tile is in
-          // (where nothing was added yet there is nothing to follow)
+          // the reference moves when a score exceeds it by 15, to 7 below it;
+          // the output follows, once P V of the last tile is in (where nothing
+          // was added yet there is nothing to follow)
           float alpha = 1.0f;
           bool follow = false;
-          if (mx > m + 8.0f || m == -INFINITY) {
-            alpha = m == -INFINITY ? 0.0f : ptx::ex2_approx(m - mx);
+          if (mx > m + 15.0f || m == -INFINITY) {
+            const float up = fmaxf(m, mx - 7.0f);
+            alpha = m == -INFINITY ? 0.0f : ptx::ex2_approx(m - up);
             follow = i > 0 && l != 0.0f;
             l *= alpha;
-            m = fmaxf(m, mx);
+            m = up;
           }
+          if (i > 0 && e_now != exponent) {  // so it does V's exponent
+            alpha *= exponent - e_now < -126 ? 0.0f : sf_value(127 + exponent - e_now);
+            follow = l != 0.0f || follow;
+          }
+          exponent = e_now;
           if (__any_sync(0xffffffffu, follow)) {
             // S of this tile came after P V of the tile before the last, so
             // that pv_done is in the phase waited for, or has left it
@@ -287,7 +298,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
               const float a = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v]), f[v >> 3], neg));
               const float c = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v + 1]), f[v >> 3], neg));
               add[u & 1] = ptx::f2_add(add[u & 1], ptx::f2_pack(a, c));
-              pk[u] = ptx::pack_bf16x2(a, c);
+              pk[u] = split::pack_f16x2(a, c);
             }
             ptx::tmem_st16(s_addr + 16 * half, pk);
           }
@@ -334,7 +345,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
       }
       continue;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l, unit = sf_value(min(max(127 + exponent, 0), 254));
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
@@ -354,13 +365,19 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
           uint32_t y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv, __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+            y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv * unit,
+                                    __uint_as_float(o[8 * u + 2 * e + 1]) * inv * unit);
           dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
         }
       } else {
         uint4* dst = reinterpret_cast<uint4*>(to.part + 2 * C::ROWS + r * D + c);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        for (int u = 0; u < 8; ++u) {
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = __float_as_uint(__uint_as_float(o[4 * u + e]) * unit);
+          dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
       }
     }
     if (valid) {
@@ -392,10 +409,11 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
   const int pmask = (1 << p.cache.lp) - 1;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
-  bool entered = false, more = true;
-  int u = 0, edge = 0;  // the tile that is being read, and whether some row sees only part of it
+  bool entered = false, more = true, first = true;  // first: of its segment
+  int u = 0;  // the tile that is being read
   auto advance = [&]() {
     ++u;
+    first = false;
     while (!entered || u >= w.u1) {
       if (entered) w.next(p);
       entered = false;
@@ -405,40 +423,49 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         return;
       }
       entered = true;
+      first = true;
       u = w.u0;
     }
-    const CacheSeq& s = w.w.s;
-    const int kb = w.w.kbase + u * C::SPAN;
-    const int pos0 = s.len - s.n + static_cast<int>(w.row0 / p.G);
-    const int pos1 = s.len - s.n + static_cast<int>((w.row0 + w.rows - 1) / p.G);
-    const int lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
-    const int hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
-    edge = kb < lo_max || kb > hi_min - C::SPAN;
   };
-  // This thread's chunks of the tile's codes and their scales (-1: no page).
-  // Tokens that no row sees may hold anything: zeros.
-  auto load = [&](const uint8_t* codes, const uint8_t* sf, uint4 (&x)[NI], int (&f)[NI], bool flag) {
-    const int kb = w.w.kbase + u * C::SPAN;
-    const int32_t* table = p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages;
+  // Starts the copies of this thread's chunks of the tile's codes (tokens that
+  // no row sees may hold anything: zeros), and reads its blocks' scale codes
+  // (K's in the low byte, V's in the next; -1: no page).
+  const uint32_t raw = ptx::smem_u32(sm + C::OFF_RAW) + tid * 16;
+  int sf[4];
+  auto fetch = [&]() {
+    if (more) {
+      const int kb = w.w.kbase + u * C::SPAN;
+      const int32_t* table = p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages;
+      int64_t row[4];
+      int page = -1;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int key = kb + r0 + RPI * j, block = key & ~(kCacheBlock - 1);
-      x[j] = make_uint4(0, 0, 0, 0);
-      f[j] = -1;
-      if (more && block < w.hi_max && block + kCacheBlock > w.lo_min) {
-        const int page = __ldg(table + (block >> p.cache.lp));
-        if (page >= 0 && page < p.cache.num_pages) {
-          const int64_t row = cache_row(p.cache, page, w.h, key & pmask);
-          f[j] = sf[row >> 4];
-          if (key < w.hi_max && key >= w.lo_min) x[j] = *reinterpret_cast<const uint4*>(codes + row * D + 16 * c);
-        } else if (flag && lane == 0) {
-          atomicOr(p.batch.status, kStatusBadPlan);
+      for (int j = 0; j < 4; ++j) {
+        const int block = kb + kCacheBlock * j;
+        sf[j] = -1;
+        row[j] = -1;
+        if (block < w.hi_max && block + kCacheBlock > w.lo_min) {
+          if (page < 0 || (block & pmask) == 0) page = __ldg(table + (block >> p.cache.lp));
+          if (page >= 0 && page < p.cache.num_pages) {
+            row[j] = cache_row(p.cache, page, w.h, block & pmask);
+            sf[j] = p.cache.k_sf[row[j] >> 4] | p.cache.v_sf[row[j] >> 4] << 8;
+          } else {
+            page = -1;
+            if (tid == 0) atomicOr(p.batch.status, kStatusBadPlan);
+          }
         }
       }
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int in = r0 + RPI * j, key = kb + in;  // RPI is 16 or 32: in >> 4 is j, or 2 j + (r0 >> 4)
+        const int64_t block = RPI == 16 ? row[j & 3] : r0 >= 16 ? row[(2 * j + 1) & 3] : row[(2 * j) & 3];
+        const bool there = block >= 0 && key < w.hi_max && key >= w.lo_min;
+        const int64_t off = ((block >= 0 ? block : 0) + (in & 15)) * D + 16 * c;
+        split::cp_async16(raw + j * 2048, p.cache.k + off, there ? 16 : 0);
+        split::cp_async16(raw + C::RAW + j * 2048, p.cache.v + off, there ? 16 : 0);
+      }
     }
+    split::cp_commit();
   };
-  uint4 kr[NI], vr[NI];
-  int ks[NI], vs[NI];
   // 16 codes of row r as two 16-byte pieces of the swizzled tile, in an order
   // that keeps the eight lanes of a row on different banks
   auto put = [&](uint32_t base, int r, const uint32_t (&x)[8]) {
@@ -456,9 +483,9 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
   };
   uint32_t gi = 0;
   bool ok = true;
+  int exponent = 0;
   advance();
-  load(p.cache.k, p.cache.k_sf, kr, ks, true);
-  load(p.cache.v, p.cache.v_sf, vr, vs, false);
+  fetch();
 #pragma unroll 1
   for (; ok && more; ++gi) {
     const int st = gi & 1;
@@ -466,8 +493,28 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     ok = ptx::mbar_wait(&B.k_free[st], par, limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    bool nan = false;
+    split::cp_wait<0>();  // this thread's own copies
+    uint4 kr[NI], vr[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      uint32_t x[4];
+      split::lds128(raw + j * 2048, x);
+      kr[j] = make_uint4(x[0], x[1], x[2], x[3]);
+      split::lds128(raw + C::RAW + j * 2048, x);
+      vr[j] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    // V's exponent E
+    int top = -1000;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (sf[j] >= 0) top = max(top, (sf[j] >> 8) - 127);
+    if (top > -1000 && (first || exponent == -1000 || top > exponent + 7)) exponent = top;
+    else if (first) exponent = -1000;  // nothing is there yet
+    const int kb = w.w.kbase + u * C::SPAN;
+    const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN;
+    bool plain = false;
     const uint32_t k_at = ptx::smem_u32(sm + C::OFF_K + st * C::KV_BYTES);
+    uint32_t sv[NI];  // V's scale over 2^E, twice in fp16
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const uint32_t x[4] = {kr[j].x, kr[j].y, kr[j].z, kr[j].w};
@@ -475,21 +522,26 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[2 * e] = split::codes_lo(x[e]), y[2 * e + 1] = split::codes_hi(x[e]);
       put(k_at, r0 + RPI * j, y);
+      const int f = RPI == 16 ? sf[j & 3] : r0 >= 16 ? sf[(2 * j + 1) & 3] : sf[(2 * j) & 3];
+      const int up = f < 0 ? 0 : (f >> 8) - 127 - exponent;  // at most 7
+      sv[j] = up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
       // one thread of each block notes its scale
       if (c == 0 && ((r0 + RPI * j) & (kCacheBlock - 1)) == 0)
-        notes.k_scale[gi & 3][(r0 + RPI * j) >> 4] = ks[j] < 0 ? -1.0f : sf_value(ks[j]);
+        notes.k_scale[gi & 3][(r0 + RPI * j) >> 4] = f < 0 ? -1.0f : sf_value(f & 0xff);
+      const uint32_t z[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
+      plain |= static_cast<bool>((up < -15) & (((z[0] | z[1] | z[2] | z[3]) & 0x7f7f7f7fu) != 0));
       if (edge) {
-        const uint32_t z[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) nan |= split::has_nan_code(z[e]);
+        for (int e = 0; e < 4; ++e) plain |= split::has_nan_code(z[e]);
       }
     }
-    nan = __any_sync(0xffffffffu, nan);
-    if (lane == 0) notes.nan[gi & 3][warp] = nan;
+    plain = __any_sync(0xffffffffu, plain);
+    if (lane == 0) notes.plain[gi & 3][warp] = plain;
+    if (tid == 0) notes.exponent[gi & 3] = exponent;
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(&B.k_full[st]);
     advance();
-    load(p.cache.k, p.cache.k_sf, kr, ks, true);
+    fetch();
     ok = ptx::mbar_wait(&B.v_free[st], par, limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
@@ -497,20 +549,18 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const uint32_t x[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
-      const float sv = sf_value(vs[j] < 0 ? 127 : vs[j]);
       uint32_t y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t h2 = e & 1 ? split::codes_hi(x[e >> 1]) : split::codes_lo(x[e >> 1]);
-        const __half2 hh = *reinterpret_cast<const __half2*>(&h2);
-        y[e] = ptx::pack_bf16x2(__low2float(hh) * sv, __high2float(hh) * sv);
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(h2), "r"(sv[j]));
       }
       put(v_at, r0 + RPI * j, y);
     }
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(&B.v_full[st]);
-    load(p.cache.v, p.cache.v_sf, vr, vs, false);
   }
+  split::cp_wait<0>();
   if (!ok && lane == 0) {
     *abort = 1;
     atomicOr(p.batch.status, kStatusProducer);
@@ -529,7 +579,7 @@ __device__ __forceinline__ bool issue_pv(Bars& B, uint8_t* sm, uint32_t tmem, ui
   if (!ptx::mbar_wait(&B.v_full[st], par, limit, abort)) return false;
   ptx::tc_fence_after();
   const uint32_t v_base = ptx::smem_u32(sm + C::OFF_V + st * C::KV_BYTES);
-  constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 1);
+  constexpr uint32_t idesc = ptx::idesc_f16(128, D, 1);
 #pragma unroll
   for (int kk = 0; kk < C::SPAN / 16; ++kk)
     // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
@@ -550,7 +600,7 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
   uint32_t gi = 0, seg = 0;
   bool ok = true;
   const uint32_t q_base = ptx::smem_u32(sm);
-  constexpr uint32_t idesc = ptx::idesc_f16(128, C::SPAN);
+  constexpr uint32_t idesc = ptx::idesc_f16(128, C::SPAN, 0);
 #pragma unroll 1
   for (; ok && w.more(p, stop); w.next(p)) {
     if (!w.enter(p, at, stop) || w.u1 <= w.u0) continue;
@@ -591,11 +641,23 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
 template <int D>
 __global__ void __launch_bounds__(384, 2) gdpa_cache_tile_kernel(const CacheFwdParams p, unsigned long long limit) {
   using C = TileCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ tile::Bars B;
-  __shared__ tile::Notes notes;
-  __shared__ split::Schedule<C> sh;
-  uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  // All of it dynamic: two CTAs take the SM's last byte.  Nothing static in
+  // front of it, so that it begins on the 1024 bytes that the swizzle wants.
+  extern __shared__ __align__(1024) uint8_t sm[];
+  struct Block {
+    tile::Bars bars;
+    tile::Notes notes;
+    split::Schedule<C> schedule;
+  };
+  static_assert(sizeof(Block) <= 1024, "barrier block");
+  Block& block = *reinterpret_cast<Block*>(sm + C::OFF_RAW + 2 * C::RAW);
+  tile::Bars& B = block.bars;
+  tile::Notes& notes = block.notes;
+  split::Schedule<C>& sh = block.schedule;
+  if (ptx::smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.batch.status, kStatusProducer);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0 && !p.no_split) p.meta[blockIdx.x * 16 + 1] = p.meta[blockIdx.x * 16 + 9] = 0;  // no parts yet

@@ -207,15 +207,13 @@ def attend(x: Batch, causal, window, scale, q=None):
     return out, lse, mag, big
 
 
-def attend_bounds(x: Batch, out, lse, mag, big, rows=None):
+def attend_bounds(x: Batch, out, lse, mag, big):
     """How far a result may be off.  A score is a sum of D products in fp32, in any order and grouping: off by at
     most d = (D + 8) 2^-23 times the sum of their magnitudes (2^-23, not 2^-24: the tensor core may cut where others
     round); exp2 adds 2^-21 (its own 2^-22 and its argument's rounding for the few units it spans here).  A weight is
-    then off by a factor 1 +- d, and its rounding adds 2^-11 (fp16; up to 16 query rows of a key head) or 2^-8 (bf16;
-    more rows): both move a weighted mean by at most their size times sum p |v| / sum p (twice for d: numerator and
-    sum).  The result is rounded to bf16: 2^-8 of it.  `rows`: query rows of a key head, if not the batch's."""
-    rows = max(1, max(x.new)) * (x.Hq // x.H) if rows is None else rows
-    w = 2.0 ** -11 if rows <= 16 else 2.0 ** -8
+    then off by a factor 1 +- d, and its rounding to fp16 adds 2^-11: both move a weighted mean by at most their size
+    times sum p |v| / sum p (twice for d: numerator and sum).  The result is rounded to bf16: 2^-8 of it."""
+    w = 2.0 ** -11
     d = (x.D + 8) * 2.0 ** -23 * big + 2.0 ** -21
     tol = 2.0 ** -8 * np.abs(out) + (w + 2 * d[..., None]) * mag * 1.01 + 1e-38
     return tol, np.where(np.isfinite(lse), d + 2.0 ** -22 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0))), 0)
