@@ -17,17 +17,22 @@
 // the special-function unit (512 cycles each of a 128 x 64 tile at D = 128)
 // close behind.
 //
-// Work split.  Segments (sequence, 128 rows, key head) and runs as in the
+// Work split.  Segments (sequence, 256 rows, key head) and runs as in the
 // kernel for few rows, a CTA being the worker and 64 keys a step; a cut
-// segment's parts are joined by the same second kernel.  Two CTAs an SM, each
-// with 256 of the 512 TMEM columns, fill each other's gaps.  Roles:
-//   warps 0-3  softmax, a query row a thread: load Q of the segment into
-//              shared memory, then for every tile S -> P (over S in TMEM), and
-//              the output;
-//   warps 4-7  copy codes to shared memory a tile ahead, convert and store K
-//              and V tiles (128-byte swizzle) in two stages;
-//   warp 8     issues the MMAs, S one tile ahead of P V (warps 9-11 only give
-//              their registers to the softmax).
+// segment's parts are joined by the same second kernel.  A CTA works on two
+// halves of 128 rows.  Where a segment has more than 128 rows they are its
+// first and second 128, and every converted tile serves both; where it has
+// fewer, both hold the same rows and take every other tile, and the second half
+// hands its result to the first through shared memory.  Roles:
+//   warps 0-3, 4-7    softmax of a half, a query row a thread: load Q, then for
+//                     every tile S -> P (over S in TMEM), and the output;
+//   warps 8-11        convert K tiles (128-byte swizzle, two stages);
+//   warps 12-15       convert V tiles;
+//   warp 16           issues the MMAs, S one tile ahead of P V;
+//   warp 17           finds pages and scales, and brings codes to shared memory
+//                     by bulk copies, RAWS tiles ahead.
+// (Conversion by the warps that also looked up pages and copied, one tile ahead
+// and two CTAs of 128 rows an SM, took 435 us where this takes TIME_PROMPTS.)
 //
 // A value that is NaN must not reach rows that do not see its token, and 0
 // times NaN is NaN: a segment with a NaN value in a tile that some row sees
@@ -41,44 +46,61 @@ namespace gdpa {
 template <int D_>
 struct TileCfg {
   static constexpr int D = D_;
-  static constexpr int THREADS = 384, WORKERS = 1;  // three warpgroups
+  static constexpr int THREADS = 640, WORKERS = 1;  // five warpgroups
   static constexpr int START = 3, RUN_STEPS = 8;
-  static constexpr int ROWS = 128, SPAN = 64;
-  static constexpr int CTAS = 2;
-  static constexpr int CHUNKS = D / 64;              // 128-byte column chunks
-  static constexpr int Q_CHUNK = ROWS * 128, KV_CHUNK = SPAN * 128;
-  static constexpr int Q_BYTES = CHUNKS * Q_CHUNK, KV_BYTES = CHUNKS * KV_CHUNK;
-  static constexpr int OFF_K = Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES;
-  static constexpr int OFF_RAW = OFF_V + 2 * KV_BYTES;   // codes of the next tile, K then V
-  static constexpr int RAW = SPAN * D;
-  // the barrier block behind it; two CTAs an SM and no more, for the TMEM's sake
-  static constexpr int USED = OFF_RAW + 2 * RAW + 1024;
-  static constexpr int SMEM = USED > 98 * 1024 ? USED : 98 * 1024;
+  static constexpr int HALF = 128, ROWS = 2 * HALF, SPAN = 64;
+  static constexpr int CTAS = 1;
+  static constexpr int Q_CHUNK = HALF * 128, KV_CHUNK = SPAN * 128;  // 64 columns of a tile
+  static constexpr int Q_BYTES = D / 64 * Q_CHUNK, KV_BYTES = D / 64 * KV_CHUNK;
+  static constexpr int RAW = SPAN * D;      // codes of a tile of K or V
+  static constexpr int RAWS = D == 64 ? 8 : 5;
+  static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES, OFF_RAW = OFF_V + 2 * KV_BYTES;
+  static constexpr int OFF_BLOCK = OFF_RAW + RAWS * 2 * RAW;  // barriers and notes
+  static constexpr int USED = OFF_BLOCK + 3072;
+  // one CTA an SM (all of its TMEM)
+  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
+  static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S: half, buffer, 64 columns; O: half, 128
   // registers a thread after the warpgroups have traded them: together what
-  // the launch allocates, three times LAUNCH_REGS
-  static constexpr int LAUNCH_REGS = 80, REGS_SOFTMAX = 128, REGS_CONVERT = 72, REGS_MMA = 40;
-  static_assert(REGS_SOFTMAX + REGS_CONVERT + REGS_MMA <= 3 * LAUNCH_REGS, "registers");
-  static constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLS = 256;  // two S buffers of 64 columns, O
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
+  // the launch allocates, five times LAUNCH_REGS
+  static constexpr int LAUNCH_REGS = 96, REGS_SOFTMAX = 144, REGS_CONVERT = 72, REGS_ISSUE = 48;
+  static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * LAUNCH_REGS, "registers");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(2 * Q_BYTES >= HALF * D * 4, "a half's output fits Q's room");
 };
 
 namespace tile {
 
 struct Bars {
-  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
-  uint64_t pv_done;  // after every P V
-  uint64_t o_full;   // after a segment's last
+  uint64_t raw_full[8], raw_free[8];
+  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // of a half (and S buffer)
+  uint64_t o_full;                                  // after a segment's last P V
+  uint64_t x_full, x_free;                          // the second half's result is there, is read
   uint64_t drain;
   uint32_t tmem;
   int abort;
 };
 
-// What the converting warps tell the softmax of tile i, in a ring of four: the
-// refill of an entry waits for S(i + 2), which waits for P(i).
+// Beside the codes of a tile, in their ring.
+struct RawNote {
+  uint32_t state;     // bit 0 it exists, 1 the first of its segment, 2 some row sees only part of it
+  int exponent;       // E
+  int kb, lo, hi;     // its first key; keys that any row sees
+  float k_scale[4];   // of its blocks; -1: no page, or nobody sees it
+  uint32_t v_mul[4];  // V's scale over 2^E, twice in fp16; 0: none
+  uint32_t low;       // bit j: block j's scale is too far below 2^E for that
+};
+
 struct Notes {
-  float k_scale[4][4];  // of the tile's blocks; -1: no page, hidden from all rows
-  int plain[4][4];      // a warp found what only the plain form takes
-  int exponent[4];      // E
+  RawNote raw[8];
+  // For the softmax of tile i, in a ring of four: the refill of an entry waits
+  // for S(i + 2), which waits for P(i).
+  float k_scale[4][4];
+  int exponent[4];
+  // Segments of this CTA, in a ring: some tile takes the plain form.  Entries
+  // are cleared four segments before their use.
+  int plain[8];
+  float x_ref[128], x_sum[128];  // the second half's references and sums
 };
 
 // One row of a segment over keys [j0, j1), one warp, D / 32 coordinates a lane:
@@ -140,42 +162,52 @@ __device__ __forceinline__ Target target(const CacheFwdParams& p, const split::W
 
 // ------------------------------------------------------------------ softmax
 template <int D>
-__device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const Notes& notes, uint32_t tmem,
+__device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes& notes, uint32_t tmem,
                             const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, int64_t chunk,
                             unsigned long long limit) {
   using C = TileCfg<D>;
-  const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5, r = threadIdx.x;
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 7, r = threadIdx.x & 127, quarter = r >> 5;
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-  const uint32_t o_addr = tmem + lane_off + C::TM_O;
+  const uint32_t o_addr = tmem + lane_off + C::TM_O + half * 128;
   volatile int* abort = &B.abort;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
-  uint32_t gi = 0, seg = 0;  // tiles, and segments with tiles, so far
-  bool ok = true;
+  uint32_t gi = 0, ti = 0, seg = 0, xs = 0;  // tiles of the CTA, of this half; segments with tiles; exchanges
+  bool ok = true, exchanged = false;
 #pragma unroll 1
   for (; ok && w.more(p, stop); w.next(p)) {
     if (!w.enter(p, at, stop)) continue;
     const CacheSeq s = w.w.s;
     const Target to = target<C>(p, w, chunk, blockIdx.x);
-    const int64_t rr = w.row0 + r;
-    const bool valid = r < w.rows;
+    const bool pair = w.rows > C::HALF;  // the halves hold different rows
+    const int ri = pair ? half * C::HALF + r : r;
+    const int64_t rr = w.row0 + ri;
+    const bool valid = ri < w.rows;
     const int head = w.h * p.G + static_cast<int>(rr % p.G);
-    const int64_t q_at = (s.first + rr / p.G) * p.q_stride + static_cast<int64_t>(head) * D;
-    const int64_t out_row = (s.first + rr / p.G) * p.Hq + head;
+    const int64_t tok = s.first + rr / p.G;
+    const int64_t q_at = tok * p.q_stride + static_cast<int64_t>(head) * D;
+    const int64_t out_row = tok * p.Hq + head;
     const int pos = s.len - s.n + static_cast<int>(rr / p.G);
     // keys this row sees: [lo, hi)
     const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     const int hi = valid ? max(0, p.causal ? min(s.len, pos + 1) : s.len) : 0;
     const int steps = w.u1 - w.u0;
+    const bool live = (ri & ~31) < w.rows;  // a warp without rows keeps the barriers' protocol
     float m = -INFINITY, l = 0.0f;
-    bool dirty = false;
-    int exponent = 0;
+    int exponent = 0, mine = 0;  // V's exponent; tiles of this half in this segment
+    bool plain = false;
     if (steps > 0) {
+      if (exchanged) {  // Q's room held the last segment's exchange
+        ok = ptx::mbar_wait(&B.x_free, (xs - 1) & 1, limit, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        exchanged = false;
+      }
       // ---- this row of Q, divided by its largest power of two, as fp16
       // (read twice: registers are short, the row is in L1)
       const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at);
       float amax = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < D / 8; ++i) {
         const uint4 u = valid ? src[i] : make_uint4(0, 0, 0, 0);
         const uint32_t x[4] = {u.x, u.y, u.z, u.w};
@@ -187,8 +219,8 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
       }
       const int e2 = amax > 0.0f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 127) : 0;
       const float inv = sf_value(127 - e2), fac = sf_value(127 + e2) * p.scale2;
-      const uint32_t q_smem = ptx::smem_u32(sm);
-#pragma unroll 4
+      const uint32_t q_smem = ptx::smem_u32(sm) + half * C::Q_BYTES;
+#pragma unroll 8
       for (int i = 0; i < D / 8; ++i) {
         const uint4 u = valid ? src[i] : make_uint4(0, 0, 0, 0);
         const uint32_t x[4] = {u.x, u.y, u.z, u.w};
@@ -201,18 +233,18 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(&B.q_full);
 
-      const bool live = quarter * 32 < w.rows;  // a warp without rows keeps the barriers' protocol
       const bool fold = p.scale2 > 0.0f;
 #pragma unroll 1
       for (int i = 0; i < steps; ++i, ++gi) {
-        const int sb = gi & 1;
-        ok = ptx::mbar_wait(&B.s_full[sb], (gi >> 1) & 1, limit, abort);
+        if (!pair && (i & 1) != half) continue;
+        const int sb = ti & 1;
+        ok = ptx::mbar_wait(&B.s_full[half][sb], (ti >> 1) & 1, limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
         if (live) {
           const int kb = w.w.kbase + (w.u0 + i) * C::SPAN;
-          const uint32_t s_addr = tmem + lane_off + C::TM_S + sb * 64;
+          const uint32_t s_addr = tmem + lane_off + C::TM_S + half * 128 + sb * 64;
           uint32_t sr[64];
           ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
           ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
@@ -223,7 +255,6 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
             const float sk = *const_cast<volatile const float*>(&notes.k_scale[gi & 3][j]);
             gone |= sk < 0.0f ? 1u << j : 0u;
             f[j] = fac * sk;
-            dirty |= *const_cast<volatile const int*>(&notes.plain[gi & 3][j]) != 0;
           }
           const int e_now = *const_cast<volatile const int*>(&notes.exponent[gi & 3]);
           ptx::tmem_wait_ld_r64(sr);
@@ -260,19 +291,19 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
           if (mx > m + 15.0f || m == -INFINITY) {
             const float up = fmaxf(m, mx - 7.0f);
             alpha = m == -INFINITY ? 0.0f : ptx::ex2_approx(m - up);
-            follow = i > 0 && l != 0.0f;
+            follow = mine > 0 && l != 0.0f;
             l *= alpha;
             m = up;
           }
-          if (i > 0 && e_now != exponent) {  // so it does V's exponent
+          if (mine > 0 && e_now != exponent) {  // so it does V's exponent
             alpha *= exponent - e_now < -126 ? 0.0f : sf_value(127 + exponent - e_now);
             follow = l != 0.0f || follow;
           }
           exponent = e_now;
           if (__any_sync(0xffffffffu, follow)) {
-            // S of this tile came after P V of the tile before the last, so
-            // that pv_done is in the phase waited for, or has left it
-            ok = ptx::mbar_wait(&B.pv_done, (gi - 1) & 1, limit, abort);
+            // S of this tile came after P V of this half's tile before the
+            // last, so that pv_done is in the phase waited for, or has left it
+            ok = ptx::mbar_wait(&B.pv_done[half], (ti - 1) & 1, limit, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -290,17 +321,17 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
           const float neg = m == -INFINITY ? 0.0f : -m;
           uint64_t add[2] = {0, 0};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int part = 0; part < 2; ++part) {
             uint32_t pk[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-              const int v = 16 * half + u;
+              const int v = 16 * part + u;
               const float a = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v]), f[v >> 3], neg));
               const float c = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v + 1]), f[v >> 3], neg));
               add[u & 1] = ptx::f2_add(add[u & 1], ptx::f2_pack(a, c));
               pk[u] = split::pack_f16x2(a, c);
             }
-            ptx::tmem_st16(s_addr + 16 * half, pk);
+            ptx::tmem_st16(s_addr + 16 * part, pk);
           }
           float x, y;
           ptx::f2_unpack(ptx::f2_add(add[0], add[1]), x, y);
@@ -308,27 +339,32 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&B.p_full[sb]);
+        ptx::mbar_arrive(&B.p_full[half][sb]);
+        ++ti;
+        ++mine;
       }
       if (!ok) break;
-      ok = ptx::mbar_wait(&B.o_full, seg++ & 1, limit, abort);
+      ok = ptx::mbar_wait(&B.o_full, seg & 1, limit, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
+      plain = *const_cast<volatile int*>(&notes.plain[seg & 7]) != 0;
+      if (threadIdx.x == 0) notes.plain[(seg + 4) & 7] = 0;
+      ++seg;
     }
     // ---- the result
-    if (quarter * 32 >= w.rows) continue;
-    if (__any_sync(0xffffffffu, dirty)) {
+    if (plain) {
+      if (!live || (!pair && half == 1)) continue;
       const int k0 = w.w.kbase + w.u0 * C::SPAN, k1 = w.w.kbase + w.u1 * C::SPAN;
 #pragma unroll 1
-      for (int row = 0; row < 32 && quarter * 32 + row < w.rows; ++row) {
+      for (int row = 0; row < 32 && (ri & ~31) + row < w.rows; ++row) {
         constexpr int E = D / 32;
         float top, total, o[E];
         const int64_t row_q = __shfl_sync(0xffffffffu, q_at, row), row_o = __shfl_sync(0xffffffffu, out_row, row);
         attend_row<D>(p, w.b, w.h, row_q, max(k0, __shfl_sync(0xffffffffu, lo, row)),
                       min(k1, __shfl_sync(0xffffffffu, hi, row)), top, total, o);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const int at_row = quarter * 32 + row;
+        const int at_row = (ri & ~31) + row;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           if (to.pieces == 1)
@@ -345,46 +381,100 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
       }
       continue;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l, unit = sf_value(min(max(127 + exponent, 0), 254));
+    // this half's output is in units of 2^exponent
+    float unit = sf_value(min(max(127 + exponent, 0), 254));
+    float other = 0.0f;  // weight of the second half's output
+    const uint32_t x_row = ptx::smem_u32(sm) + r * D * 4;
+    if (!pair && steps > 0) {
+      if (half == 1) {  // hand over: reference, sum, output
+        if (live) {
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      uint32_t o[32];
-      if (steps > 0) {
-        ptx::tmem_ld32(o_addr + c, o);
-        ptx::tmem_wait_ld_r32(o);
-      }
-      if (steps == 0 || l == 0.0f) {  // nothing was seen
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld32(o_addr + c, o);
+            ptx::tmem_wait_ld_r32(o);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) o[u] = 0;
-      }
-      if (!valid) continue;
-      if (to.pieces == 1) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c);
+            for (int u = 0; u < 8; ++u) {
+              uint32_t y[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv * unit,
-                                    __uint_as_float(o[8 * u + 2 * e + 1]) * inv * unit);
-          dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int e = 0; e < 4; ++e)
+                y[e] = l == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[4 * u + e]) * unit);
+              ptx::st_shared_v4(x_row + (((c / 4 + u) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+            }
+          }
+          notes.x_ref[r] = m;
+          notes.x_sum[r] = l;
         }
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(to.part + 2 * C::ROWS + r * D + c);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = __float_as_uint(__uint_as_float(o[4 * u + e]) * unit);
-          dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
-        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&B.x_full);
+        exchanged = true;
+        ++xs;
+        continue;
+      }
+      ok = ptx::mbar_wait(&B.x_full, xs & 1, limit, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (live) {
+        const float m2 = *const_cast<volatile float*>(&notes.x_ref[r]), l2 = *const_cast<volatile float*>(&notes.x_sum[r]);
+        const float top = fmaxf(m, m2), zero = top == -INFINITY ? 0.0f : top;
+        const float f1 = ptx::ex2_approx(m - zero);
+        other = l2 == 0.0f ? 0.0f : ptx::ex2_approx(m2 - zero);
+        unit *= f1;
+        if (l == 0.0f) unit = 0.0f;
+        l = l * f1 + l2 * other;
+        m = top;
       }
     }
-    if (valid) {
-      if (to.pieces > 1)
-        to.part[2 * r] = m, to.part[2 * r + 1] = l;
-      else if (p.lse)
-        p.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (live) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (mine > 0) {
+          ptx::tmem_ld32(o_addr + c, o);
+          ptx::tmem_wait_ld_r32(o);
+        }
+#pragma unroll
+        for (int u = 0; u < 32; ++u)  // (where this half saw nothing its output may be anything)
+          o[u] = mine == 0 || unit == 0.0f || l == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[u]) * unit);
+        if (other != 0.0f) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t y[4];
+            split::lds128(x_row + (((c / 4 + u) ^ (r & 7)) << 4), y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[4 * u + e] = __float_as_uint(fmaf(__uint_as_float(y[e]), other, __uint_as_float(o[4 * u + e])));
+          }
+        }
+        if (!valid) continue;
+        if (to.pieces == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv, __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+            dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(to.part + 2 * C::ROWS + ri * D + c);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
+      }
+      if (valid) {
+        if (to.pieces > 1)
+          to.part[2 * ri] = m, to.part[2 * ri + 1] = l;
+        else if (p.lse)
+          p.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+    if (!pair && steps > 0) {
+      ptx::mbar_arrive(&B.x_free);
+      exchanged = true;
+      ++xs;
     }
     ptx::tc_fence_before();  // O has been read when the next segment's P allows its first product
   }
@@ -394,173 +484,189 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, const
   }
 }
 
-// ------------------------------------------------------------------ conversion
+// ------------------------------------------------------------------ codes
 template <int D>
-__device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes& notes,
-                            const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop,
-                            unsigned long long limit) {
+__device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes& notes,
+                           const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop,
+                           unsigned long long limit) {
   using C = TileCfg<D>;
-  constexpr int CPR = D / 16;               // 16-code chunks of a row
-  constexpr int RPI = 128 / CPR;            // rows that 128 threads read at once
-  constexpr int NI = C::SPAN / RPI;         // ... and how often for a tile
-  const int tid = threadIdx.x - 128, lane = tid & 31, warp = tid >> 5;
-  const int c = tid % CPR, r0 = tid / CPR;
+  const int lane = threadIdx.x & 31, j = lane & 3;  // lanes 0-3: a block each (the others repeat them)
   volatile int* abort = &B.abort;
   const int pmask = (1 << p.cache.lp) - 1;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
-  bool entered = false, more = true, first = true;  // first: of its segment
-  int u = 0;  // the tile that is being read
-  auto advance = [&]() {
+  bool entered = false, more = true, ok = true;
+  int u = 0, exponent = 0;
+  // the tile whose copies were started last, to be announced when its scales are there
+  int p_slot = -1, p_kb = 0, p_lo = 0, p_hi = 0, p_k = 0, p_v = 0;
+  uint32_t p_state = 0;
+  bool p_there = false;
+  auto announce = [&]() {
+    if (p_slot < 0) return;
+    const int ev = p_there ? p_v - 127 : -1000;
+    int top = max(ev, __shfl_xor_sync(0xffffffffu, ev, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if ((p_state & 2) || top > exponent + 7) exponent = top;  // -1000: nothing is there yet
+    const int up = ev - exponent;  // at most 7
+    const uint32_t mul = !p_there ? 0 : up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
+    const uint32_t low = __ballot_sync(0xffffffffu, p_there && up < -15) & 15;
+    RawNote& n = notes.raw[p_slot];
+    if (lane < 4) {
+      n.k_scale[j] = p_there ? sf_value(p_k) : -1.0f;
+      n.v_mul[j] = mul;
+    }
+    if (lane == 0) {
+      n.state = p_state;
+      n.exponent = exponent;
+      n.kb = p_kb, n.lo = p_lo, n.hi = p_hi;
+      n.low = low;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&B.raw_full[p_slot]);
+    p_slot = -1;
+  };
+  uint32_t gi = 0;
+#pragma unroll 1
+  while (ok) {
+    uint32_t state = 1;
     ++u;
-    first = false;
-    while (!entered || u >= w.u1) {
+    while (more && (!entered || u >= w.u1)) {
       if (entered) w.next(p);
       entered = false;
       while (w.more(p, stop) && !w.enter(p, at, stop)) w.next(p);
       if (!w.more(p, stop)) {
         more = false;
-        return;
-      }
-      entered = true;
-      first = true;
-      u = w.u0;
-    }
-  };
-  // Starts the copies of this thread's chunks of the tile's codes (tokens that
-  // no row sees may hold anything: zeros), and reads its blocks' scale codes
-  // (K's in the low byte, V's in the next; -1: no page).
-  const uint32_t raw = ptx::smem_u32(sm + C::OFF_RAW) + tid * 16;
-  int sf[4];
-  auto fetch = [&]() {
-    if (more) {
-      const int kb = w.w.kbase + u * C::SPAN;
-      const int32_t* table = p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages;
-      int64_t row[4];
-      int page = -1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int block = kb + kCacheBlock * j;
-        sf[j] = -1;
-        row[j] = -1;
-        if (block < w.hi_max && block + kCacheBlock > w.lo_min) {
-          if (page < 0 || (block & pmask) == 0) page = __ldg(table + (block >> p.cache.lp));
-          if (page >= 0 && page < p.cache.num_pages) {
-            row[j] = cache_row(p.cache, page, w.h, block & pmask);
-            sf[j] = p.cache.k_sf[row[j] >> 4] | p.cache.v_sf[row[j] >> 4] << 8;
-          } else {
-            page = -1;
-            if (tid == 0) atomicOr(p.batch.status, kStatusBadPlan);
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int in = r0 + RPI * j, key = kb + in;  // RPI is 16 or 32: in >> 4 is j, or 2 j + (r0 >> 4)
-        const int64_t block = RPI == 16 ? row[j & 3] : r0 >= 16 ? row[(2 * j + 1) & 3] : row[(2 * j) & 3];
-        const bool there = block >= 0 && key < w.hi_max && key >= w.lo_min;
-        const int64_t off = ((block >= 0 ? block : 0) + (in & 15)) * D + 16 * c;
-        split::cp_async16(raw + j * 2048, p.cache.k + off, there ? 16 : 0);
-        split::cp_async16(raw + C::RAW + j * 2048, p.cache.v + off, there ? 16 : 0);
+      } else {
+        entered = true;
+        state = 3;
+        u = w.u0;
       }
     }
-    split::cp_commit();
-  };
-  // 16 codes of row r as two 16-byte pieces of the swizzled tile, in an order
-  // that keeps the eight lanes of a row on different banks
-  auto put = [&](uint32_t base, int r, const uint32_t (&x)[8]) {
-    const uint32_t row = base + (c >> 2) * C::KV_CHUNK + r * 128;
-    const int swap = c >> 2 & 1;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = h ^ swap;
-      const uint32_t dst = row + (((2 * (c & 3) + e) ^ (r & 7)) << 4);
-      if (e == 0)
-        ptx::st_shared_v4(dst, x[0], x[1], x[2], x[3]);
-      else
-        ptx::st_shared_v4(dst, x[4], x[5], x[6], x[7]);
+    const int slot = gi % C::RAWS;
+    ok = ptx::mbar_wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    ++gi;
+    if (!more) {  // the last entry: no tile
+      announce();
+      p_slot = slot, p_state = 0, p_there = false;
+      announce();
+      break;
     }
-  };
-  uint32_t gi = 0;
+    const int kb = w.w.kbase + u * C::SPAN, block = kb + kCacheBlock * j;
+    if (kb < w.lo_max || kb > w.hi_min - C::SPAN) state |= 4;
+    bool there = block < w.hi_max && block + kCacheBlock > w.lo_min;
+    int64_t row = 0;
+    if (there) {
+      const int page = __ldg(p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages + (block >> p.cache.lp));
+      if (page >= 0 && page < p.cache.num_pages) {
+        row = cache_row(p.cache, page, w.h, block & pmask);
+      } else {
+        there = false;
+        atomicOr(p.batch.status, kStatusBadPlan);
+      }
+    }
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, there) & 15);
+    if (lane == 0 && n > 0) ptx::mbar_expect_tx(&B.raw_full[slot], n * 2 * kCacheBlock * D);
+    __syncwarp();
+    if (there && lane < 4) {
+      const uint32_t dst = ptx::smem_u32(sm + C::OFF_RAW) + slot * 2 * C::RAW + j * kCacheBlock * D;
+      ptx::bulk_load(dst, p.cache.k + row * D, kCacheBlock * D, &B.raw_full[slot]);
+      ptx::bulk_load(dst + C::RAW, p.cache.v + row * D, kCacheBlock * D, &B.raw_full[slot]);
+    }
+    announce();  // the tile before
+    p_k = there ? p.cache.k_sf[row >> 4] : 0;
+    p_v = there ? p.cache.v_sf[row >> 4] : 0;
+    p_slot = slot, p_state = state, p_there = there;
+    p_kb = kb, p_lo = w.lo_min, p_hi = w.hi_max;
+  }
+  if (!ok) {
+    if (lane == 0) {
+      *abort = 1;
+      atomicOr(p.batch.status, kStatusProducer);
+    }
+    announce();
+  }
+  // no copy may land after the CTA has ended
+  const int never = 0;
+  for (uint32_t g = gi > C::RAWS ? gi - C::RAWS : 0; g < gi; ++g)
+    ptx::mbar_wait(&B.raw_full[g % C::RAWS], (g / C::RAWS) & 1, 100000000ull, &never);
+}
+
+// ------------------------------------------------------------------ conversion
+// Warps of one warpgroup convert K, of another V.
+template <int D, bool V>
+__device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes& notes, unsigned long long limit) {
+  using C = TileCfg<D>;
+  constexpr int CPR = D / 16;               // 16-code chunks of a row
+  constexpr int RPI = 128 / CPR;            // rows that 128 threads convert at once
+  constexpr int NI = C::SPAN / RPI;         // ... and how often for a tile
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const int c = tid % CPR, r0 = tid / CPR;
+  volatile int* abort = &B.abort;
+  const int swap = c >> 2 & 1;
+  uint32_t seg = 0xffffffffu;  // the segment's number
   bool ok = true;
-  int exponent = 0;
-  advance();
-  fetch();
 #pragma unroll 1
-  for (; ok && more; ++gi) {
-    const int st = gi & 1;
-    const uint32_t par = ((gi >> 1) & 1) ^ 1;
-    ok = ptx::mbar_wait(&B.k_free[st], par, limit, abort);
+  for (uint32_t gi = 0;; ++gi) {
+    const int slot = gi % C::RAWS, st = gi & 1;
+    ok = ptx::mbar_wait(&B.raw_full[slot], (gi / C::RAWS) & 1, limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    split::cp_wait<0>();  // this thread's own copies
-    uint4 kr[NI], vr[NI];
+    const RawNote& n = notes.raw[slot];
+    const uint32_t state = *const_cast<volatile const uint32_t*>(&n.state);
+    if (!(state & 1)) break;
+    seg += state >> 1 & 1;
+    ok = ptx::mbar_wait(V ? &B.v_free[st] : &B.k_free[st], ((gi >> 1) & 1) ^ 1, limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const uint32_t from = ptx::smem_u32(sm + C::OFF_RAW) + slot * 2 * C::RAW + (V ? C::RAW : 0) + tid * 16;
+    const uint32_t to = ptx::smem_u32(sm + (V ? C::OFF_V : C::OFF_K)) + st * C::KV_BYTES + (c >> 2) * C::KV_CHUNK;
+    uint32_t x[NI][4];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      uint32_t x[4];
-      split::lds128(raw + j * 2048, x);
-      kr[j] = make_uint4(x[0], x[1], x[2], x[3]);
-      split::lds128(raw + C::RAW + j * 2048, x);
-      vr[j] = make_uint4(x[0], x[1], x[2], x[3]);
-    }
-    // V's exponent E
-    int top = -1000;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (sf[j] >= 0) top = max(top, (sf[j] >> 8) - 127);
-    if (top > -1000 && (first || exponent == -1000 || top > exponent + 7)) exponent = top;
-    else if (first) exponent = -1000;  // nothing is there yet
-    const int kb = w.w.kbase + u * C::SPAN;
-    const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN;
+    for (int j = 0; j < NI; ++j) split::lds128(from + j * 2048, x[j]);
     bool plain = false;
-    const uint32_t k_at = ptx::smem_u32(sm + C::OFF_K + st * C::KV_BYTES);
-    uint32_t sv[NI];  // V's scale over 2^E, twice in fp16
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const uint32_t x[4] = {kr[j].x, kr[j].y, kr[j].z, kr[j].w};
-      uint32_t y[8];
+      const int r = r0 + RPI * j;
+      uint32_t mul = 0;
+      if (V) {
+        mul = *const_cast<volatile const uint32_t*>(&n.v_mul[r >> 4]);
+        // tokens that no row sees (and blocks on no page) may hold anything: zeros
+        const int key = n.kb + r;
+        if (mul == 0 || key < n.lo || key >= n.hi) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0;
+        if (state & 4) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[2 * e] = split::codes_lo(x[e]), y[2 * e + 1] = split::codes_hi(x[e]);
-      put(k_at, r0 + RPI * j, y);
-      const int f = RPI == 16 ? sf[j & 3] : r0 >= 16 ? sf[(2 * j + 1) & 3] : sf[(2 * j) & 3];
-      const int up = f < 0 ? 0 : (f >> 8) - 127 - exponent;  // at most 7
-      sv[j] = up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
-      // one thread of each block notes its scale
-      if (c == 0 && ((r0 + RPI * j) & (kCacheBlock - 1)) == 0)
-        notes.k_scale[gi & 3][(r0 + RPI * j) >> 4] = f < 0 ? -1.0f : sf_value(f & 0xff);
-      const uint32_t z[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
-      plain |= static_cast<bool>((up < -15) & (((z[0] | z[1] | z[2] | z[3]) & 0x7f7f7f7fu) != 0));
-      if (edge) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) plain |= split::has_nan_code(z[e]);
+          for (int e = 0; e < 4; ++e) plain |= split::has_nan_code(x[j][e]);
+        }
+        if (n.low >> (r >> 4) & 1) plain |= ((x[j][0] | x[j][1] | x[j][2] | x[j][3]) & 0x7f7f7f7fu) != 0;
       }
-    }
-    plain = __any_sync(0xffffffffu, plain);
-    if (lane == 0) notes.plain[gi & 3][warp] = plain;
-    if (tid == 0) notes.exponent[gi & 3] = exponent;
-    ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(&B.k_full[st]);
-    advance();
-    fetch();
-    ok = ptx::mbar_wait(&B.v_free[st], par, limit, abort);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const uint32_t v_at = ptx::smem_u32(sm + C::OFF_V + st * C::KV_BYTES);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const uint32_t x[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
       uint32_t y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t h2 = e & 1 ? split::codes_hi(x[e >> 1]) : split::codes_lo(x[e >> 1]);
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(h2), "r"(sv[j]));
+        y[e] = e & 1 ? split::codes_hi(x[j][e >> 1]) : split::codes_lo(x[j][e >> 1]);
+        if (V) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(y[e]), "r"(mul));
       }
-      put(v_at, r0 + RPI * j, y);
+      // two 16-byte pieces of the swizzled row, in an order that keeps the
+      // eight lanes of a row on different banks
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t dst = to + r * 128 + (((2 * (c & 3) + (h ^ swap)) ^ (r & 7)) << 4);
+        const bool second = h ^ swap;
+        ptx::st_shared_v4(dst, second ? y[4] : y[0], second ? y[5] : y[1], second ? y[6] : y[2], second ? y[7] : y[3]);
+      }
+    }
+    if (V) {
+      if (__any_sync(0xffffffffu, plain) && lane == 0) *const_cast<volatile int*>(&notes.plain[seg & 7]) = 1;
+    } else if (tid < 4) {
+      notes.k_scale[gi & 3][tid] = n.k_scale[tid];
+    } else if (tid == 4) {
+      notes.exponent[gi & 3] = n.exponent;
     }
     ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(&B.v_full[st]);
+    ptx::mbar_arrive(V ? &B.v_full[st] : &B.k_full[st]);
+    ptx::mbar_arrive(&B.raw_free[slot]);
   }
-  split::cp_wait<0>();
   if (!ok && lane == 0) {
     *abort = 1;
     atomicOr(p.batch.status, kStatusProducer);
@@ -568,25 +674,36 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
 }
 
 // ------------------------------------------------------------------ MMA
+// P V of tile gi, for each half that has it.
+struct Pending {
+  uint32_t gi;
+  int halves;          // bits
+  uint32_t ti[2];      // the halves' tile numbers
+  int first[2];        // the half's first in this segment
+};
 template <int D>
-__device__ __forceinline__ bool issue_pv(Bars& B, uint8_t* sm, uint32_t tmem, uint32_t gi, bool first,
+__device__ __forceinline__ bool issue_pv(Bars& B, uint8_t* sm, uint32_t tmem, const Pending& t,
                                          unsigned long long limit) {
   using C = TileCfg<D>;
-  const int st = gi & 1;
-  const uint32_t par = (gi >> 1) & 1;
+  const int vs = t.gi & 1;
   volatile int* abort = &B.abort;
-  if (!ptx::mbar_wait(&B.p_full[st], par, limit, abort)) return false;
-  if (!ptx::mbar_wait(&B.v_full[st], par, limit, abort)) return false;
-  ptx::tc_fence_after();
-  const uint32_t v_base = ptx::smem_u32(sm + C::OFF_V + st * C::KV_BYTES);
+  if (!ptx::mbar_wait(&B.v_full[vs], (t.gi >> 1) & 1, limit, abort)) return false;
+  const uint32_t v_base = ptx::smem_u32(sm + C::OFF_V + vs * C::KV_BYTES);
   constexpr uint32_t idesc = ptx::idesc_f16(128, D, 1);
 #pragma unroll
-  for (int kk = 0; kk < C::SPAN / 16; ++kk)
-    // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
-    ptx::mma_ts_elect(tmem + C::TM_O, tmem + C::TM_S + st * 64 + 8 * kk,
-                      ptx::sdesc_sw128(v_base + kk * 2048, C::KV_CHUNK, 1024), idesc, first && kk == 0 ? 0u : 1u);
-  ptx::mma_commit_elect(&B.v_free[st]);
-  ptx::mma_commit_elect(&B.pv_done);
+  for (int h = 0; h < 2; ++h) {
+    if (!(t.halves >> h & 1)) continue;
+    const uint32_t sb = t.ti[h] & 1;
+    if (!ptx::mbar_wait(&B.p_full[h][sb], (t.ti[h] >> 1) & 1, limit, abort)) return false;
+    ptx::tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < C::SPAN / 16; ++kk)
+      // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
+      ptx::mma_ts_elect(tmem + C::TM_O + h * 128, tmem + C::TM_S + h * 128 + sb * 64 + 8 * kk,
+                        ptx::sdesc_sw128(v_base + kk * 2048, C::KV_CHUNK, 1024), idesc, t.first[h] && kk == 0 ? 0u : 1u);
+    ptx::mma_commit_elect(&B.pv_done[h]);
+  }
+  ptx::mma_commit_elect(&B.v_free[vs]);
   return true;
 }
 
@@ -597,7 +714,7 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
   volatile int* abort = &B.abort;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
-  uint32_t gi = 0, seg = 0;
+  uint32_t gi = 0, seg = 0, ti[2] = {0, 0};
   bool ok = true;
   const uint32_t q_base = ptx::smem_u32(sm);
   constexpr uint32_t idesc = ptx::idesc_f16(128, C::SPAN, 0);
@@ -606,24 +723,34 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
     if (!w.enter(p, at, stop) || w.u1 <= w.u0) continue;
     ok = ptx::mbar_wait(&B.q_full, seg++ & 1, limit, abort);
     const int steps = w.u1 - w.u0;
+    const bool pair = w.rows > C::HALF;
+    Pending last = {0, 0, {0, 0}, {0, 0}};
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++gi) {
-      const int st = gi & 1;
-      ok = ptx::mbar_wait(&B.k_full[st], (gi >> 1) & 1, limit, abort);
+      const int ks = gi & 1;
+      ok = ptx::mbar_wait(&B.k_full[ks], (gi >> 1) & 1, limit, abort);
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t k_base = ptx::smem_u32(sm + C::OFF_K + st * C::KV_BYTES);
+      const uint32_t k_base = ptx::smem_u32(sm + C::OFF_K + ks * C::KV_BYTES);
+      Pending now = {gi, pair ? 3 : 1 << (i & 1), {ti[0], ti[1]}, {i < (pair ? 1 : 2), i < (pair ? 1 : 2)}};
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss_elect(tmem + C::TM_S + st * 64,
-                          ptx::sdesc_sw128(q_base + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32, 16, 1024),
-                          ptx::sdesc_sw128(k_base + (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32, 16, 1024), idesc,
-                          kk > 0 ? 1u : 0u);
-      ptx::mma_commit_elect(&B.s_full[st]);
-      ptx::mma_commit_elect(&B.k_free[st]);
-      if (i > 0) ok = issue_pv<D>(B, sm, tmem, gi - 1, i == 1, limit);
+      for (int h = 0; h < 2; ++h) {
+        if (!(now.halves >> h & 1)) continue;
+        const uint32_t sb = ti[h] & 1;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ptx::mma_ss_elect(tmem + C::TM_S + h * 128 + sb * 64,
+                            ptx::sdesc_sw128(q_base + h * C::Q_BYTES + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32, 16, 1024),
+                            ptx::sdesc_sw128(k_base + (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32, 16, 1024), idesc,
+                            kk > 0 ? 1u : 0u);
+        ptx::mma_commit_elect(&B.s_full[h][sb]);
+        ++ti[h];
+      }
+      ptx::mma_commit_elect(&B.k_free[ks]);
+      if (i > 0) ok = issue_pv<D>(B, sm, tmem, last, limit);
+      last = now;
     }
-    if (ok) ok = issue_pv<D>(B, sm, tmem, gi - 1, steps == 1, limit);
+    if (ok) ok = issue_pv<D>(B, sm, tmem, last, limit);
     ptx::mma_commit_elect(&B.o_full);
   }
   if (!ok && (threadIdx.x & 31) == 0) {
@@ -639,49 +766,58 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
 }  // namespace tile
 
 template <int D>
-__global__ void __launch_bounds__(384, 2) gdpa_cache_tile_kernel(const CacheFwdParams p, unsigned long long limit) {
+__global__ void __launch_bounds__(640, 1) gdpa_cache_tile_kernel(const CacheFwdParams p, unsigned long long limit) {
   using C = TileCfg<D>;
-  // All of it dynamic: two CTAs take the SM's last byte.  Nothing static in
-  // front of it, so that it begins on the 1024 bytes that the swizzle wants.
+  // All of it dynamic: nothing static in front of it, so that it begins on the
+  // 1024 bytes that the swizzle wants.
   extern __shared__ __align__(1024) uint8_t sm[];
   struct Block {
     tile::Bars bars;
     tile::Notes notes;
     split::Schedule<C> schedule;
   };
-  static_assert(sizeof(Block) <= 1024, "barrier block");
-  Block& block = *reinterpret_cast<Block*>(sm + C::OFF_RAW + 2 * C::RAW);
+  static_assert(sizeof(Block) <= 3072, "barrier block");
+  Block& block = *reinterpret_cast<Block*>(sm + C::OFF_BLOCK);
   tile::Bars& B = block.bars;
   tile::Notes& notes = block.notes;
   split::Schedule<C>& sh = block.schedule;
-  if (ptx::smem_u32(sm) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(p.batch.status, kStatusProducer);
-    return;
-  }
   const int tid = threadIdx.x, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0 && !p.no_split) p.meta[blockIdx.x * 16 + 1] = p.meta[blockIdx.x * 16 + 9] = 0;  // no parts yet
+  if (ptx::smem_u32(sm) & 1023u) {
+    if (tid == 0) atomicOr(p.batch.status, kStatusProducer);
+    return;
+  }
   if (tid == 0) {
-    ptx::mbar_init(&B.q_full, 128);
+    for (int i = 0; i < C::RAWS; ++i) {
+      ptx::mbar_init(&B.raw_full[i], 1);
+      ptx::mbar_init(&B.raw_free[i], 256);
+    }
+    ptx::mbar_init(&B.q_full, 256);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&B.k_full[i], 128);
       ptx::mbar_init(&B.k_free[i], 1);
       ptx::mbar_init(&B.v_full[i], 128);
       ptx::mbar_init(&B.v_free[i], 1);
-      ptx::mbar_init(&B.s_full[i], 1);
-      ptx::mbar_init(&B.p_full[i], 128);
+      for (int h = 0; h < 2; ++h) {
+        ptx::mbar_init(&B.s_full[h][i], 1);
+        ptx::mbar_init(&B.p_full[h][i], 128);
+      }
+      ptx::mbar_init(&B.pv_done[i], 1);
     }
-    ptx::mbar_init(&B.pv_done, 1);
     ptx::mbar_init(&B.o_full, 1);
+    ptx::mbar_init(&B.x_full, 128);
+    ptx::mbar_init(&B.x_free, 128);
     ptx::mbar_init(&B.drain, 1);
     B.abort = 0;
     ptx::fence_mbar_init();
   }
+  if (tid < 8) notes.plain[tid] = 0;
   int64_t total, chunk;
   split::schedule<C>(p, sh, total, chunk);  // synchronises: the barriers are there
   const int64_t at = chunk * blockIdx.x, stop = min(total, at + chunk);
   if (at >= stop) return;
-  if (warp == 8) {
+  if (warp == 16) {
     ptx::tmem_alloc(&B.tmem, C::TM_COLS);
     ptx::tmem_relinquish();
   }
@@ -689,21 +825,25 @@ __global__ void __launch_bounds__(384, 2) gdpa_cache_tile_kernel(const CacheFwdP
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = B.tmem;
-  if (warp < 4) {
+  if (warp < 8) {
     ptx::regs_inc<C::REGS_SOFTMAX>();
     tile::run_softmax<D>(p, sm, B, notes, tmem, sh, at, stop, chunk, limit);
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     ptx::regs_dec<C::REGS_CONVERT>();
-    tile::run_convert<D>(p, sm, B, notes, sh, at, stop, limit);
+    if (warp < 12)
+      tile::run_convert<D, false>(p, sm, B, notes, limit);
+    else
+      tile::run_convert<D, true>(p, sm, B, notes, limit);
   } else {
-    ptx::regs_dec<C::REGS_MMA>();
-    if (warp == 8) tile::run_mma<D>(p, sm, B, tmem, sh, at, stop, limit);
+    ptx::regs_dec<C::REGS_ISSUE>();
+    if (warp == 16) tile::run_mma<D>(p, sm, B, tmem, sh, at, stop, limit);
+    if (warp == 17) tile::run_copies<D>(p, sm, B, notes, sh, at, stop, limit);
   }
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 8) ptx::tmem_dealloc(tmem, C::TM_COLS);
+  if (warp == 16) ptx::tmem_dealloc(tmem, C::TM_COLS);
 }
 
 }  // namespace gdpa
