@@ -522,6 +522,8 @@ gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_
  *          between calls; calls (or captured graphs) that may run at the same
  *          time need one each
  *
+ * T * Hq / H must be below 2^31 - 256.
+ *
  * Asynchronous on `stream`, no allocation, no host read of device data (may
  * be captured).  Offsets, lengths or page numbers out of range are handled as
  * in gdpa_cache_append: keys on a page out of range are not seen.  A workspace

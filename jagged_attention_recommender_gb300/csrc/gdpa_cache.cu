@@ -283,6 +283,7 @@ extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q
       (window_tokens > 0 && !causal) || !std::isfinite(scale))
     return GDPA_ERR_INVALID_ARG;
   if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  if (T * (Hq / cache->H) >= ((int64_t)1 << 31) - 256) return GDPA_ERR_UNSUPPORTED;  // query rows of a key head
   if (T == 0 || B == 0) return GDPA_OK;
   if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
   if ((st = check_rows(out, (int64_t)Hq * cache->D, Hq, cache->D)) != GDPA_OK) return st;

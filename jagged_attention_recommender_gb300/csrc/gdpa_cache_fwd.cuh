@@ -182,7 +182,7 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
   if (p.window > 0) w.kbase = max(0, w.s.len - w.s.n - p.window + 1) & ~(C::SPAN - 1);
   // (a length may be as large as 2^31 - 16)
   w.steps = static_cast<int>((static_cast<unsigned>(max(w.s.len - w.kbase, 1)) + C::SPAN - 1) / C::SPAN);
-  w.tiles = static_cast<int>((static_cast<int64_t>(w.s.n) * p.G + C::ROWS - 1) / C::ROWS);
+  w.tiles = static_cast<int>((static_cast<unsigned>(w.s.n) * p.G + C::ROWS - 1) / C::ROWS);  // T G is below 2^31
   return w;
 }
 template <class C>
@@ -244,7 +244,7 @@ struct Walk {
   SeqWork w;
   int64_t start;  // of the present segment
   int b, h, tile;
-  int64_t row0;   // its first query row (of the sequence and key head)
+  int row0;       // its first query row (of the sequence and key head)
   int rows;
   int u0, u1;     // its steps that are in the run and hold visible keys
   int lo_min, hi_max;  // keys any of its rows sees: [lo_min, hi_max)
@@ -284,10 +284,10 @@ struct Walk {
       u1 = static_cast<int>(min(stop - start - C::START, (int64_t)w.steps));
       if (u1 <= u0) return false;
     }
-    row0 = static_cast<int64_t>(tile) * C::ROWS;
-    rows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(s.n) * p.G - row0));
-    const int pos0 = s.len - s.n + static_cast<int>(row0 / p.G);
-    const int pos1 = s.len - s.n + static_cast<int>((row0 + rows - 1) / p.G);
+    row0 = tile * C::ROWS;
+    rows = min(C::ROWS, s.n * p.G - row0);
+    const int pos0 = s.len - s.n + row0 / p.G;
+    const int pos1 = s.len - s.n + (row0 + rows - 1) / p.G;
     lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
     hi_max = max(0, p.causal ? min(s.len, pos1 + 1) : s.len);
     lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
     if (!now.enter(p, at, stop)) continue;
     const CacheSeq s = now.w.s;
     const int h = now.h, rows = now.rows;
-    const int64_t row0 = now.row0;
+    const int row0 = now.row0;
 
     // ---- query fragments, and what each column (query row) sees
     uint32_t qf[NT == 1 ? KS : 1][2];
@@ -432,9 +432,8 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
       float x[D / 4];
       float amax = 0.0f;
       if (r < rows) {
-        const int64_t rr = row0 + r;
-        const __nv_bfloat16* src =
-            p.q + (s.first + rr / p.G) * p.q_stride + (h * p.G + static_cast<int>(rr % p.G)) * D + t * (D / 4);
+        const int rr = row0 + r, i = rr / p.G;
+        const __nv_bfloat16* src = p.q + (s.first + i) * p.q_stride + (h * p.G + rr - i * p.G) * D + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
       for (int c = 0; c < 2; ++c) {
         const int col = nt * 8 + 2 * t + c;
         fac[nt][c] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * c);
-        const int pos = s.len - s.n + static_cast<int>((row0 + col) / p.G);
+        const int pos = s.len - s.n + (row0 + col) / p.G;
         lo[nt][c] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         hi[nt][c] = col < rows ? (p.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
@@ -701,8 +700,8 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         const float m = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
         if (r >= rows) continue;
         if (pieces == 1) {
-          const int64_t rr = row0 + r;
-          const int64_t at_row = (s.first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+          const int rr = row0 + r, i = rr / p.G;
+          const int64_t at_row = static_cast<int64_t>(s.first + i) * p.Hq + h * p.G + rr - i * p.G;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           uint32_t o[ND];
 #pragma unroll
@@ -750,8 +749,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
     if (pieces == 0) continue;
     const int first = m[0], row_first = m[2], n = m[3], tile = m[4], h = m[5];
     const int member = blockIdx.x * WORKERS + (slot >> 1) - first;
-    const int64_t row0 = static_cast<int64_t>(tile) * ROWS;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(n) * p.G - row0));
+    const int row0 = tile * ROWS, rows = min(ROWS, n * p.G - row0);
     const bool together = pieces > kJoinFew;
     const int j0 = together ? pieces * warp / kJoinWarps : 0, j1 = together ? pieces * (warp + 1) / kJoinWarps : pieces;
     // rows r with r pieces / rows == member
@@ -820,8 +818,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
           for (int e = 0; e < E; ++e) o[e] += s_part[w][lane * E + e] * f;
         }
       }
-      const int64_t rr = row0 + r;
-      const int64_t at_row = (row_first + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+      const int rr = row0 + r, i = rr / p.G;
+      const int64_t at_row = static_cast<int64_t>(row_first + i) * p.Hq + h * p.G + rr - i * p.G;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
       for (int e = 0; e < E; e += 2)

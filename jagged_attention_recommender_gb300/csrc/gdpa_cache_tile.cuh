@@ -28,7 +28,7 @@
 //                     every tile S -> P (over S in TMEM), and the output;
 //   warps 8-11        convert K tiles (128-byte swizzle, two stages);
 //   warps 12-15       convert V tiles;
-//   warp 16           issues the MMAs, S one tile ahead of P V;
+//   warp 16           issues the MMAs, S ahead of P V;
 //   warp 17           finds pages and scales, and brings codes to shared memory
 //                     by bulk copies, RAWS tiles ahead.
 // (Conversion by the warps that also looked up pages and copied, one tile ahead
@@ -62,7 +62,7 @@ struct TileCfg {
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // S: half, buffer, 64 columns; O: half, 128
   // registers a thread after the warpgroups have traded them: together what
   // the launch allocates, five times LAUNCH_REGS
-  static constexpr int LAUNCH_REGS = 96, REGS_SOFTMAX = 144, REGS_CONVERT = 72, REGS_ISSUE = 48;
+  static constexpr int LAUNCH_REGS = 96, REGS_SOFTMAX = 144, REGS_CONVERT = 64, REGS_ISSUE = 64;
   static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * LAUNCH_REGS, "registers");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(2 * Q_BYTES >= HALF * D * 4, "a half's output fits Q's room");
@@ -82,21 +82,22 @@ struct Bars {
 };
 
 // Beside the codes of a tile, in their ring.
-struct RawNote {
-  uint32_t state;     // bit 0 it exists, 1 the first of its segment, 2 some row sees only part of it
-  int exponent;       // E
-  int kb, lo, hi;     // its first key; keys that any row sees
+struct __align__(16) RawNote {
   float k_scale[4];   // of its blocks; -1: no page, or nobody sees it
   uint32_t v_mul[4];  // V's scale over 2^E, twice in fp16; 0: none
+  uint32_t state;     // bit 0 it exists, 1 the first of its segment, 2 some row sees only part of it,
+                      // 3 all of V's codes and scales are plain to use
+  int exponent;       // E
+  int kb, lo, hi;     // its first key; keys that any row sees
   uint32_t low;       // bit j: block j's scale is too far below 2^E for that
 };
 
 struct Notes {
   RawNote raw[8];
-  // For the softmax of tile i, in a ring of four: the refill of an entry waits
-  // for S(i + 2), which waits for P(i).
-  float k_scale[4][4];
-  int exponent[4];
+  // For the softmax of tile i, in a ring of eight: the refill of an entry waits
+  // for S(i + 6), which waits for P(i + 3) at least.
+  float4 k_scale[8];
+  int exponent[8];
   // Segments of this CTA, in a ring: some tile takes the plain form.  Entries
   // are cleared four segments before their use.
   int plain[8];
@@ -181,13 +182,13 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     const Target to = target<C>(p, w, chunk, blockIdx.x);
     const bool pair = w.rows > C::HALF;  // the halves hold different rows
     const int ri = pair ? half * C::HALF + r : r;
-    const int64_t rr = w.row0 + ri;
+    const int rr = w.row0 + ri;
     const bool valid = ri < w.rows;
-    const int head = w.h * p.G + static_cast<int>(rr % p.G);
-    const int64_t tok = s.first + rr / p.G;
+    const int in_seq = rr / p.G, head = w.h * p.G + rr - in_seq * p.G;
+    const int64_t tok = s.first + in_seq;
     const int64_t q_at = tok * p.q_stride + static_cast<int64_t>(head) * D;
     const int64_t out_row = tok * p.Hq + head;
-    const int pos = s.len - s.n + static_cast<int>(rr / p.G);
+    const int pos = s.len - s.n + in_seq;
     // keys this row sees: [lo, hi)
     const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     const int hi = valid ? max(0, p.causal ? min(s.len, pos + 1) : s.len) : 0;
@@ -204,13 +205,14 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         exchanged = false;
       }
       // ---- this row of Q, divided by its largest power of two, as fp16
-      // (read twice: registers are short, the row is in L1)
       const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at);
+      uint4 raw[D / 8];
       float amax = 0.0f;
-#pragma unroll 8
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) raw[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 u = valid ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           amax = fmaxf(amax, fabsf(__uint_as_float(x[e] << 16)));
@@ -220,10 +222,9 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
       const int e2 = amax > 0.0f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 127) : 0;
       const float inv = sf_value(127 - e2), fac = sf_value(127 + e2) * p.scale2;
       const uint32_t q_smem = ptx::smem_u32(sm) + half * C::Q_BYTES;
-#pragma unroll 8
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 u = valid ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         uint32_t y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -248,15 +249,10 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
           uint32_t sr[64];
           ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
           ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-          float f[4];
-          uint32_t gone = 0;  // blocks on no page
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float sk = *const_cast<volatile const float*>(&notes.k_scale[gi & 3][j]);
-            gone |= sk < 0.0f ? 1u << j : 0u;
-            f[j] = fac * sk;
-          }
-          const int e_now = *const_cast<volatile const int*>(&notes.exponent[gi & 3]);
+          const float4 sk = *reinterpret_cast<const float4*>(&notes.k_scale[gi & 7]);
+          const int e_now = notes.exponent[gi & 7];
+          float f[4] = {fac * sk.x, fac * sk.y, fac * sk.z, fac * sk.w};
+          const uint32_t gone = (sk.x < 0.0f) | (sk.y < 0.0f) << 1 | (sk.z < 0.0f) << 2 | (sk.w < 0.0f) << 3;  // blocks on no page
           ptx::tmem_wait_ld_r64(sr);
           float mx = -INFINITY;
           const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN || gone != 0 || !fold;
@@ -302,7 +298,8 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
           exponent = e_now;
           if (__any_sync(0xffffffffu, follow)) {
             // S of this tile came after P V of this half's tile before the
-            // last, so that pv_done is in the phase waited for, or has left it
+            // last (its P is in the same buffer), so that pv_done is in the
+            // phase waited for, or has left it
             ok = ptx::mbar_wait(&B.pv_done[half], (ti - 1) & 1, limit, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -490,102 +487,101 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
                            const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop,
                            unsigned long long limit) {
   using C = TileCfg<D>;
-  const int lane = threadIdx.x & 31, j = lane & 3;  // lanes 0-3: a block each (the others repeat them)
+  // Eight tiles at a time: a lane looks after one block of one of them, so that
+  // the latency of page and scales is met once for all.
+  const int lane = threadIdx.x & 31, mine = lane >> 2, j = lane & 3;
   volatile int* abort = &B.abort;
   const int pmask = (1 << p.cache.lp) - 1;
+  const uint32_t raw = ptx::smem_u32(sm + C::OFF_RAW) + j * kCacheBlock * D;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
-  bool entered = false, more = true, ok = true;
-  int u = 0, exponent = 0;
-  // the tile whose copies were started last, to be announced when its scales are there
-  int p_slot = -1, p_kb = 0, p_lo = 0, p_hi = 0, p_k = 0, p_v = 0;
-  uint32_t p_state = 0;
-  bool p_there = false;
-  auto announce = [&]() {
-    if (p_slot < 0) return;
-    const int ev = p_there ? p_v - 127 : -1000;
-    int top = max(ev, __shfl_xor_sync(0xffffffffu, ev, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    if ((p_state & 2) || top > exponent + 7) exponent = top;  // -1000: nothing is there yet
-    const int up = ev - exponent;  // at most 7
-    const uint32_t mul = !p_there ? 0 : up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
-    const uint32_t low = __ballot_sync(0xffffffffu, p_there && up < -15) & 15;
-    RawNote& n = notes.raw[p_slot];
-    if (lane < 4) {
-      n.k_scale[j] = p_there ? sf_value(p_k) : -1.0f;
-      n.v_mul[j] = mul;
-    }
-    if (lane == 0) {
-      n.state = p_state;
-      n.exponent = exponent;
-      n.kb = p_kb, n.lo = p_lo, n.hi = p_hi;
-      n.low = low;
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&B.raw_full[p_slot]);
-    p_slot = -1;
-  };
+  bool ok = true;
+  int exponent = 0;
   uint32_t gi = 0;
 #pragma unroll 1
-  while (ok) {
-    uint32_t state = 1;
-    ++u;
-    while (more && (!entered || u >= w.u1)) {
-      if (entered) w.next(p);
-      entered = false;
-      while (w.more(p, stop) && !w.enter(p, at, stop)) w.next(p);
-      if (!w.more(p, stop)) {
-        more = false;
-      } else {
-        entered = true;
-        state = 3;
-        u = w.u0;
+  for (; ok && w.more(p, stop); w.next(p)) {
+    if (!w.enter(p, at, stop)) continue;
+    const int32_t* table = p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages;
+#pragma unroll 1
+    for (int u = w.u0; ok && u < w.u1; u += 8) {
+      const int cnt = min(8, w.u1 - u);
+      const int block = w.w.kbase + (u + mine) * C::SPAN + kCacheBlock * j;
+      bool there = mine < cnt && block < w.hi_max && block + kCacheBlock > w.lo_min;
+      int64_t row = 0;
+      int sk = 127, sv = 127;
+      if (there) {
+        const int page = __ldg(table + (block >> p.cache.lp));
+        if (page >= 0 && page < p.cache.num_pages) {
+          row = cache_row(p.cache, page, w.h, block & pmask);
+          sk = p.cache.k_sf[row >> 4];
+          sv = p.cache.v_sf[row >> 4];
+        } else {
+          there = false;
+          atomicOr(p.batch.status, kStatusBadPlan);
+        }
+      }
+      const uint32_t blocks = __ballot_sync(0xffffffffu, there);
+      // blocks that lie one behind the other in memory travel together
+      const int64_t before = __shfl_up_sync(0xffffffffu, row, 1);
+      const bool joins = there && j > 0 && (blocks >> (lane - 1) & 1) && row == before + kCacheBlock;
+      const uint32_t run = __ballot_sync(0xffffffffu, joins) >> (lane & 28) >> j >> 1;  // bit i: block j + 1 + i joins
+      const uint32_t bytes = there && !joins ? (1 + __ffs(~run) - 1) * kCacheBlock * D : 0;
+      const int ev = there ? sv - 127 : -1000;
+      int top = max(ev, __shfl_xor_sync(0xffffffffu, ev, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll 1
+      for (int t = 0; t < cnt; ++t) {
+        const int slot = gi % C::RAWS;
+        ok = ptx::mbar_wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++gi;
+        const uint32_t have = blocks >> (4 * t) & 15;
+        if (lane == 0 && have) ptx::mbar_expect_tx(&B.raw_full[slot], __popc(have) * 2 * kCacheBlock * D);
+        __syncwarp();
+        if (bytes && mine == t) {
+          const uint32_t dst = raw + slot * 2 * C::RAW;
+          ptx::bulk_load(dst, p.cache.k + row * D, bytes, &B.raw_full[slot]);
+          ptx::bulk_load(dst + C::RAW, p.cache.v + row * D, bytes, &B.raw_full[slot]);
+        }
+        const bool first = t == 0 && u == w.u0;
+        const int tile_top = __shfl_sync(0xffffffffu, top, 4 * t);
+        if (first || tile_top > exponent + 7) exponent = tile_top;  // -1000: nothing is there yet
+        const int up = ev - exponent;  // at most 7
+        const uint32_t low = __ballot_sync(0xffffffffu, there && up < -15) >> (4 * t) & 15;
+        RawNote& n = notes.raw[slot];
+        if (mine == t) {
+          n.k_scale[j] = there ? sf_value(sk) : -1.0f;
+          n.v_mul[j] = !there ? 0 : up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
+        }
+        if (lane == 0) {
+          const int kb = w.w.kbase + (u + t) * C::SPAN;
+          const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN;
+          n.state = 1 | (first ? 2 : 0) | (edge ? 4 : 0) | (!edge && have == 15 && low == 0 ? 8 : 0);
+          n.exponent = exponent;
+          n.kb = kb, n.lo = w.lo_min, n.hi = w.hi_max;
+          n.low = low;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&B.raw_full[slot]);
       }
     }
+  }
+  if (ok) {  // the last entry: no tile
     const int slot = gi % C::RAWS;
     ok = ptx::mbar_wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, abort);
     ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    ++gi;
-    if (!more) {  // the last entry: no tile
-      announce();
-      p_slot = slot, p_state = 0, p_there = false;
-      announce();
-      break;
-    }
-    const int kb = w.w.kbase + u * C::SPAN, block = kb + kCacheBlock * j;
-    if (kb < w.lo_max || kb > w.hi_min - C::SPAN) state |= 4;
-    bool there = block < w.hi_max && block + kCacheBlock > w.lo_min;
-    int64_t row = 0;
-    if (there) {
-      const int page = __ldg(p.batch.table + static_cast<int64_t>(w.b) * p.batch.max_pages + (block >> p.cache.lp));
-      if (page >= 0 && page < p.cache.num_pages) {
-        row = cache_row(p.cache, page, w.h, block & pmask);
-      } else {
-        there = false;
-        atomicOr(p.batch.status, kStatusBadPlan);
+    if (ok) {
+      ++gi;
+      if (lane == 0) {
+        notes.raw[slot].state = 0;
+        ptx::mbar_arrive(&B.raw_full[slot]);
       }
     }
-    const uint32_t n = __popc(__ballot_sync(0xffffffffu, there) & 15);
-    if (lane == 0 && n > 0) ptx::mbar_expect_tx(&B.raw_full[slot], n * 2 * kCacheBlock * D);
-    __syncwarp();
-    if (there && lane < 4) {
-      const uint32_t dst = ptx::smem_u32(sm + C::OFF_RAW) + slot * 2 * C::RAW + j * kCacheBlock * D;
-      ptx::bulk_load(dst, p.cache.k + row * D, kCacheBlock * D, &B.raw_full[slot]);
-      ptx::bulk_load(dst + C::RAW, p.cache.v + row * D, kCacheBlock * D, &B.raw_full[slot]);
-    }
-    announce();  // the tile before
-    p_k = there ? p.cache.k_sf[row >> 4] : 0;
-    p_v = there ? p.cache.v_sf[row >> 4] : 0;
-    p_slot = slot, p_state = state, p_there = there;
-    p_kb = kb, p_lo = w.lo_min, p_hi = w.hi_max;
   }
-  if (!ok) {
-    if (lane == 0) {
-      *abort = 1;
-      atomicOr(p.batch.status, kStatusProducer);
-    }
-    announce();
+  if (!ok && lane == 0) {
+    *abort = 1;
+    atomicOr(p.batch.status, kStatusProducer);
   }
   // no copy may land after the CTA has ended
   const int never = 0;
@@ -625,27 +621,35 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     uint32_t x[NI][4];
 #pragma unroll
     for (int j = 0; j < NI; ++j) split::lds128(from + j * 2048, x[j]);
-    bool plain = false;
+    uint32_t mul[4];
+    if (V) {
+      const uint4 u = *reinterpret_cast<const uint4*>(n.v_mul);
+      mul[0] = u.x, mul[1] = u.y, mul[2] = u.z, mul[3] = u.w;
+      if (!(state & 8)) {
+        bool plain = false;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          const int r = r0 + RPI * j, key = n.kb + r;
+          // tokens that no row sees (and blocks on no page) may hold anything: zeros
+          if (n.v_mul[r >> 4] == 0 || key < n.lo || key >= n.hi) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0;
+          if (state & 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) plain |= split::has_nan_code(x[j][e]);
+          }
+          if (n.low >> (r >> 4) & 1) plain |= ((x[j][0] | x[j][1] | x[j][2] | x[j][3]) & 0x7f7f7f7fu) != 0;
+        }
+        if (__any_sync(0xffffffffu, plain) && lane == 0) *const_cast<volatile int*>(&notes.plain[seg & 7]) = 1;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int r = r0 + RPI * j;
-      uint32_t mul = 0;
-      if (V) {
-        mul = *const_cast<volatile const uint32_t*>(&n.v_mul[r >> 4]);
-        // tokens that no row sees (and blocks on no page) may hold anything: zeros
-        const int key = n.kb + r;
-        if (mul == 0 || key < n.lo || key >= n.hi) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0;
-        if (state & 4) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) plain |= split::has_nan_code(x[j][e]);
-        }
-        if (n.low >> (r >> 4) & 1) plain |= ((x[j][0] | x[j][1] | x[j][2] | x[j][3]) & 0x7f7f7f7fu) != 0;
-      }
+      const int r = r0 + RPI * j;  // in block j (16 rows at once), or 2 j and 2 j + 1
+      const uint32_t f = !V ? 0 : RPI == 16 ? mul[j & 3] : r0 >= 16 ? mul[(2 * j + 1) & 3] : mul[(2 * j) & 3];
       uint32_t y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         y[e] = e & 1 ? split::codes_hi(x[j][e >> 1]) : split::codes_lo(x[j][e >> 1]);
-        if (V) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(y[e]), "r"(mul));
+        if (V) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(y[e]), "r"(f));
       }
       // two 16-byte pieces of the swizzled row, in an order that keeps the
       // eight lanes of a row on different banks
@@ -656,12 +660,9 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         ptx::st_shared_v4(dst, second ? y[4] : y[0], second ? y[5] : y[1], second ? y[6] : y[2], second ? y[7] : y[3]);
       }
     }
-    if (V) {
-      if (__any_sync(0xffffffffu, plain) && lane == 0) *const_cast<volatile int*>(&notes.plain[seg & 7]) = 1;
-    } else if (tid < 4) {
-      notes.k_scale[gi & 3][tid] = n.k_scale[tid];
-    } else if (tid == 4) {
-      notes.exponent[gi & 3] = n.exponent;
+    if (!V && tid == 0) {
+      notes.k_scale[gi & 7] = *reinterpret_cast<const float4*>(n.k_scale);
+      notes.exponent[gi & 7] = n.exponent;
     }
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(V ? &B.v_full[st] : &B.k_full[st]);
@@ -724,7 +725,9 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
     ok = ptx::mbar_wait(&B.q_full, seg++ & 1, limit, abort);
     const int steps = w.u1 - w.u0;
     const bool pair = w.rows > C::HALF;
-    Pending last = {0, 0, {0, 0}, {0, 0}};
+    // P V follows S by a tile, or by two where the halves take turns (each
+    // half's softmax then always finds its next S)
+    Pending last = {0, 0, {0, 0}, {0, 0}}, older = last;
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++gi) {
       const int ks = gi & 1;
@@ -747,9 +750,11 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
         ++ti[h];
       }
       ptx::mma_commit_elect(&B.k_free[ks]);
-      if (i > 0) ok = issue_pv<D>(B, sm, tmem, last, limit);
+      if (pair ? i > 0 : i > 1) ok = issue_pv<D>(B, sm, tmem, pair ? last : older, limit);
+      older = last;
       last = now;
     }
+    if (ok && !pair && steps > 1) ok = issue_pv<D>(B, sm, tmem, older, limit);
     if (ok) ok = issue_pv<D>(B, sm, tmem, last, limit);
     ptx::mma_commit_elect(&B.o_full);
   }

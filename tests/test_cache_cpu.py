@@ -92,7 +92,7 @@ def test_append_refuses(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), INV), (dict(B=-1), INV), (dict(max_pages=0), INV), (dict(T=1 << 31), UNS),
+    (dict(T=-1), INV), (dict(B=-1), INV), (dict(max_pages=0), INV), (dict(T=1 << 31), UNS), (dict(T=1 << 29), UNS),
     (dict(max_pages=1 << 25), UNS), (dict(Hq=0), INV), (dict(Hq=7), INV), (dict(Hq=1 << 14), UNS), (dict(max_q=0), INV),
     (dict(causal=2), INV), (dict(causal=-1), INV), (dict(window_tokens=-1), INV),
     (dict(causal=0, window_tokens=5), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV),
