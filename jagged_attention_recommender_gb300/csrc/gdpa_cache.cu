@@ -137,6 +137,18 @@ gdpa_status_t allow_smem(Kernel kernel, int bytes, int min_regs, int device, std
   return GDPA_OK;
 }
 
+template <int D>
+gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int rows, int smem, const Device& dev,
+                            cudaStream_t s) {
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  constexpr int most = (2 * kCacheBlock - 1) * (D / 2) * (int)sizeof(float2) + kAppendThreads / 32 * 4096;
+  const gdpa_status_t st = allow_smem(gdpa_cache_append_kernel<D>, most, 0, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  gdpa_cache_append_kernel<D><<<static_cast<unsigned>(groups), kAppendThreads, smem, s>>>(p, rows);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
 // Sets up a launch of configuration C: whether segments may be cut, the
 // workspace, and how many CTAs have work at most.
 template <class C>
@@ -244,17 +256,17 @@ extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void
   p.rot = cache->rot_dim;
   p.interleaved = cache->rope_style == GDPA_ROPE_INTERLEAVED ? 1 : 0;
   for (int i = 0; i < 64; ++i) p.freq[i] = i < p.rot / 2 ? turn_fraction(cache->inv_freq[i]) : 0;
-  const int rows = T > 4 * (int64_t)B ? 16 : 1;
+  // Rows of a CTA: 16 where sequences bring several tokens (a scale block's
+  // worth); for single tokens as few as keep its eight warps busy.
+  const int items = cache->D / 16;
+  const int64_t row_tasks = 2 * ((int64_t)cache->H * items + 127) / 128 + ((int64_t)p.Hq * items + 127) / 128;
+  int rows = 16;
+  while (T <= 4 * (int64_t)B && rows > 1 && rows * row_tasks > kAppendThreads / 32) rows >>= 1;
   const int64_t groups = (T + rows - 1) / rows;
-  const int y = groups >= 2 * dev.sms ? 1 : 2;
-  const size_t smem = (size_t)(rows + kCacheBlock - 1) * (p.rot / 2) * sizeof(float2);
-  const dim3 grid(static_cast<unsigned>(groups), y);
+  const int smem = (rows + kCacheBlock - 1) * (p.rot / 2) * (int)sizeof(float2) + kAppendThreads / 32 * 4096;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->D == 128)
-    gdpa_cache_append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p, rows);
-  else
-    gdpa_cache_append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p, rows);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+  return cache->D == 128 ? launch_append<128>(p, groups, rows, smem, dev, s)
+                         : launch_append<64>(p, groups, rows, smem, dev, s);
 }
 
 extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes) {

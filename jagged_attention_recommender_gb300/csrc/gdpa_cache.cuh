@@ -69,6 +69,21 @@ __device__ __forceinline__ int find_sequence(const int32_t* __restrict__ offsets
   return lo;
 }
 
+// The same by all lanes of a warp, for the same row: 32 places a step.
+__device__ __forceinline__ int find_sequence_warp(const int32_t* __restrict__ offsets, int B, int r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;  // the answer is in lo..hi
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, at = min(lo + step * (lane + 1), hi) - 1;
+    // lanes whose place still lies in front of the answer
+    const unsigned before = __ballot_sync(0xffffffffu, __ldg(offsets + at + 1) <= r);
+    const int n = before == 0xffffffffu ? 32 : __ffs(~before) - 1;
+    lo = min(lo + step * n, hi);
+    if (n < 32) hi = min(lo + step - 1, hi);
+  }
+  return lo;
+}
+
 // Sequence b's rows and length.  ok = 0 (and the launch is flagged) when its
 // offsets do not describe rows of the tensors or its length does not fit the
 // page table.

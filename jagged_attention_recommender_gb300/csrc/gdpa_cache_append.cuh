@@ -16,12 +16,12 @@
 // the row that is the first of them owns the block, and whoever finds the row
 // needs no plan and no list: a CTA looks at a group of rows, keeps the owners,
 // tabulates sine and cosine of their blocks' rows (shared by all heads), and
-// its warps take tasks of up to 128 items of 16 elements: keys of (block,
-// head), values of (block, head), or query items of a few rows.  A warp holds
-// all 2048 elements of a key or value task as loaded (32 registers a lane), so
-// the largest magnitude is known before anything is written and memory is read
-// once; keys are rotated twice, which costs less than the registers that would
-// keep them.
+// its warps take tasks of up to 128 items of 16 elements: keys or values of a
+// block and as many heads as that makes (one for 16 tokens, 16 for a single
+// one of 128), or query items of a few rows.  A task's elements come to shared
+// memory by the lanes' own asynchronous copies (4 KB a warp, 32 warps an SM)
+// and are read from there twice, for the largest magnitude and for the codes:
+// held in registers they left room for 16 warps and took TIME_REGS.
 #pragma once
 
 #include "gdpa_cache.cuh"
@@ -142,10 +142,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return ptx::pack_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-  return x;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// This thread's own copies have arrived.
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
+  return u;
 }
 
 // A scale block that this launch writes to: `cnt` new tokens from row `row`
@@ -155,11 +162,10 @@ struct OwnedBlock {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 2) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
+__global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
                                                                            int rows_per_cta) {
   constexpr int IPR = D / 16;             // items of a row and head
   constexpr int HPW = 32 / IPR;           // heads (or rows of one head) whose items a warp holds once
-  constexpr int KV_ITEMS = 16 / HPW;      // items a lane of a whole block
   __shared__ OwnedBlock s_own[16];
   __shared__ int s_n;
   extern __shared__ __align__(16) float2 s_cs[];  // [rows][rot / 2]
@@ -170,8 +176,14 @@ __global__ void __launch_bounds__(kAppendThreads, 2) gdpa_cache_append_kernel(co
   if (warp == 0) {
     OwnedBlock o{0, 0, 0, -1, 0};
     const int r = g0 + lane;
+    // the group's first sequence by all lanes, then each row's among the next 32
+    const int b0 = find_sequence_warp(bt.offsets, bt.B, g0);
+    const int end = b0 + lane < bt.B ? __ldg(bt.offsets + b0 + lane + 1) : 0x7fffffff;
+    int b = b0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) b += __shfl_sync(0xffffffffu, end, i) <= r ? 1 : 0;
     if (lane < rows_per_cta && r < bt.T) {
-      const int b = find_sequence(bt.offsets, bt.B, r);
+      if (b == b0 + 32) b = find_sequence(bt.offsets, bt.B, r);  // many empty sequences
       if (b < bt.B) {
         const CacheSeq s = load_sequence(bt, p.cache.lp, b);
         const int pos = s.len - s.n + (r - s.first);
@@ -217,43 +229,57 @@ __global__ void __launch_bounds__(kAppendThreads, 2) gdpa_cache_append_kernel(co
   }
 
   const int H = p.cache.H;
-  const int workers = (kAppendThreads / 32) * gridDim.y;
+  constexpr int workers = kAppendThreads / 32;
   const int it = lane % IPR;  // a lane's items are the same one of several heads or rows
   const int groups = p.q ? (p.Hq + HPW - 1) / HPW : 0;  // a row's heads, in warps
   const int span = groups >= 3 ? 4 : max(groups, 1);    // groups of a row in a task ...
   const int trows = 4 / span;                           // ... and rows of a task
   const int per_row = (groups + 3) / 4;                 // tasks of a row where trows is 1
-  int w = blockIdx.y * (kAppendThreads / 32) + warp;    // this warp's next task, counted over all blocks
+  // this lane's 16-byte pieces of a task: first chunks of its four items, then second ones
+  const uint32_t stage = ptx::smem_u32(s_cs) + static_cast<uint32_t>((rows_per_cta + kCacheBlock - 1) * half) * 8 +
+                         warp * 4096 + lane * 16;
+  auto item = [&](int u, const ItemAt& at, const float2* cs, float (&a)[8], float (&b)[8]) {
+    unpack8(lds16(stage + u * 512), a);
+    unpack8(lds16(stage + 2048 + u * 512), b);
+    if (at.pair >= 0) {
+      float2 t[8];
+      load_angles(cs + at.pair, t);
+      rotate_item(at, p.interleaved, t, a, b);
+    }
+  };
+  int w = warp;  // this warp's next task, counted over all blocks
   for (int j = 0; j < n; ++j) {
     const OwnedBlock o = s_own[j];
+    // keys and values: tokens (to a power of two) times items of a head; the
+    // heads of a task; lanes, and steps of 32 items, of a head
+    const int ltok = o.cnt > 1 ? 32 - __clz(o.cnt - 1) : 0, lhead = ltok + (IPR == 8 ? 3 : 2);
+    const int heads = 128 >> lhead, L = min(32, 1 << lhead), steps = max(1, (1 << lhead) >> 5);
+    const int kv_tasks = (H + heads - 1) / heads;
     const int q_tasks = groups == 0 ? 0 : trows == 1 ? o.cnt * per_row : (o.cnt + trows - 1) / trows;
-    const int tasks = 2 * H + q_tasks;
+    const int tasks = 2 * kv_tasks + q_tasks;
+#pragma unroll 1
     for (; w < tasks; w += workers) {
-      if (w >= 2 * H) {  // queries: rotate and store
-        const int task = w - 2 * H;
+      if (w >= 2 * kv_tasks) {  // queries: rotate and store
+        const int task = w - 2 * kv_tasks;
         const int t0 = trows == 1 ? task / per_row : task * trows;
         const int h0 = (trows == 1 ? task % per_row * 4 * HPW : 0) + lane / IPR;
         const ItemAt at = item_at(it, p.rot, p.interleaved);
-        uint4 ua[4], ub[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int t = t0 + u / span, head = h0 + u % span * HPW;
           if (t < o.cnt && head < p.Hq) {
             const __nv_bfloat16* src = p.q + (o.row + t) * p.q_stride + head * D;
-            ua[u] = *reinterpret_cast<const uint4*>(src + at.d0);
-            ub[u] = *reinterpret_cast<const uint4*>(src + at.d1);
+            copy16(stage + u * 512, src + at.d0);
+            copy16(stage + 2048 + u * 512, src + at.d1);
           }
         }
-        float2 cs[8];
-#pragma unroll
+        copies_wait();
+#pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           const int t = t0 + u / span, head = h0 + u % span * HPW;
-          if (u % span == 0 && at.pair >= 0 && t < o.cnt) load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
           if (t < o.cnt && head < p.Hq) {
             float a[8], b[8];
-            unpack8(ua[u], a);
-            unpack8(ub[u], b);
-            rotate_item(at, p.interleaved, cs, a, b);
+            item(u, at, s_cs + (o.tab + t) * half, a, b);
             __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(o.row + t) * p.Hq + head) * D;
             *reinterpret_cast<uint4*>(dst + at.d0) = pack8(a);
             *reinterpret_cast<uint4*>(dst + at.d1) = pack8(b);
@@ -262,94 +288,98 @@ __global__ void __launch_bounds__(kAppendThreads, 2) gdpa_cache_append_kernel(co
         continue;
       }
       if (o.page < 0) continue;
-      const int is_v = w >= H, h = is_v ? w - H : w;
-      const int rot = is_v ? 0 : p.rot;
-      const __nv_bfloat16* src = (is_v ? p.v + o.row * p.v_stride : p.k + o.row * p.k_stride) + h * D;
+      const int is_v = w >= kv_tasks, h0 = (is_v ? w - kv_tasks : w) * heads;
+      const ItemAt at = item_at(it, is_v ? 0 : p.rot, p.interleaved);
       const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const __nv_bfloat16* src = is_v ? p.v + o.row * p.v_stride : p.k + o.row * p.k_stride;
       const int slot = o.pos & ((1 << p.cache.lp) - 1);
-      uint8_t* codes = (is_v ? p.cache.v : p.cache.k) + cache_row(p.cache, o.page, h, slot) * D;
-      uint8_t* sf = (is_v ? p.cache.v_sf : p.cache.k_sf) + cache_sf(p.cache, o.page, h, slot);
+      uint8_t* const codes = is_v ? p.cache.v : p.cache.k;
+      uint8_t* const sfs = is_v ? p.cache.v_sf : p.cache.k_sf;
       const int held = o.pos & 15;  // earlier tokens of the block
-      const ItemAt at = item_at(it, rot, p.interleaved);
-      uint4 ua[KV_ITEMS], ub[KV_ITEMS];
-#pragma unroll
-      for (int u = 0; u < KV_ITEMS; ++u) {
-        const int t = lane / IPR + u * HPW;
-        ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
-        if (t < o.cnt) {
-          ua[u] = *reinterpret_cast<const uint4*>(src + t * stride + at.d0);
-          ub[u] = *reinterpret_cast<const uint4*>(src + t * stride + at.d1);
-        }
-      }
-      // item u, rotated
-      auto item = [&](int u, float (&a)[8], float (&b)[8]) {
-        unpack8(ua[u], a);
-        unpack8(ub[u], b);
-        if (at.pair >= 0) {
-          const int t = min(lane / IPR + u * HPW, o.cnt - 1);
-          float2 cs[8];
-          load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
-          rotate_item(at, p.interleaved, cs, a, b);
-        }
+      // item u of this lane: its head and token
+      auto where = [&](int u, int& h, int& t) {
+        const int idx = 32 * u + lane;
+        h = h0 + (idx >> lhead);
+        t = (idx & ((1 << lhead) - 1)) / IPR;
+        return h < H && t < o.cnt;
       };
-      float amax = 0.0f;
 #pragma unroll
-      for (int u = 0; u < KV_ITEMS; ++u) {
-        float a[8], b[8];
-        item(u, a, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));  // NaN never wins
+      for (int u = 0; u < 4; ++u) {
+        int h, t;
+        if (where(u, h, t)) {
+          copy16(stage + u * 512, src + t * stride + h * D + at.d0);
+          copy16(stage + 2048 + u * 512, src + t * stride + h * D + at.d1);
+        }
       }
-      amax = warp_max(amax);
-      const bool inf = amax == INFINITY;
-      if (inf) {  // again without what is not finite
-        amax = 0.0f;
+      copies_wait();
+      // largest magnitudes, a head at a time: `steps` steps of 32 items, or 32 / L heads a step
 #pragma unroll 1
-        for (int u = 0; u < KV_ITEMS; ++u) {
-          const int t = lane / IPR + u * HPW;
-          if (t >= o.cnt) break;
-          float a[8], b[8];
-          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d0), a);
-          unpack8(*reinterpret_cast<const uint4*>(src + t * stride + at.d1), b);
-          if (at.pair >= 0) {
-            float2 cs[8];
-            load_angles(s_cs + (o.tab + t) * half + at.pair, cs);
-            rotate_item(at, p.interleaved, cs, a, b);
+      for (int u0 = 0; u0 < 4; u0 += steps) {
+        const int h = h0 + (32 * u0 + lane >> lhead);
+        if (__all_sync(0xffffffffu, h >= H)) break;
+        float amax = 0.0f;
+        bool inf = false;
+#pragma unroll 1
+        for (int again = 0; again < 2; ++again) {  // again without what is not finite, where there is some
+          amax = 0.0f;
+#pragma unroll 1
+          for (int u = u0; u < u0 + steps; ++u) {
+            int hh, t;
+            if (!where(u, hh, t)) continue;
+            float a[8], b[8];
+            item(u, at, s_cs + (o.tab + t) * half, a, b);
+            if (again) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (fabsf(a[e]) == INFINITY) a[e] = 0.0f;
+                if (fabsf(b[e]) == INFINITY) b[e] = 0.0f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));  // NaN never wins
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (fabsf(a[e]) < INFINITY) amax = fmaxf(amax, fabsf(a[e]));
-            if (fabsf(b[e]) < INFINITY) amax = fmaxf(amax, fabsf(b[e]));
+          for (int d = 16; d > 0; d >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, amax, d);
+            if (d < L) amax = fmaxf(amax, x);
           }
+          if (again || !__any_sync(0xffffffffu, amax == INFINITY)) break;
+          inf = true;
         }
-        amax = warp_max(amax);
-      }
-      const uint32_t bits = __float_as_uint(amax);
-      int code = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
-      if (held > 0) {
-        const int before = *sf;
-        if (before < code) {  // the earlier tokens follow the larger scale
-          const float f = sf_value(127 - min(code - before, 126));
-          uint8_t* old = codes - held * D;
-          for (int i = lane; i < held * IPR; i += 32) {
-            uint4 x = *reinterpret_cast<uint4*>(old + 16 * i);
-            x = make_uint4(rescale4(x.x, f), rescale4(x.y, f), rescale4(x.z, f), rescale4(x.w, f));
-            *reinterpret_cast<uint4*>(old + 16 * i) = x;
+        const uint32_t bits = __float_as_uint(amax);
+        int code = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+        const int64_t row = cache_row(p.cache, o.page, min(h, H - 1), slot);
+        uint8_t* const sf = sfs + (row >> 4);
+        if (held > 0) {
+          const int before = *sf;
+          // where the scale grows the earlier tokens follow it, head by head
+          uint32_t grow = __ballot_sync(0xffffffffu, h < H && before < code && lane % L == 0);
+          const float f = sf_value(127 - min(max(code - before, 0), 126));
+          while (grow) {
+            const int from = __ffs(grow) - 1;
+            grow &= grow - 1;
+            const float ff = __shfl_sync(0xffffffffu, f, from);
+            uint8_t* const old = codes + (__shfl_sync(0xffffffffu, row, from) - held) * D;
+            for (int i = lane; i < held * IPR; i += 32) {
+              uint4 x = *reinterpret_cast<uint4*>(old + 16 * i);
+              x = make_uint4(rescale4(x.x, ff), rescale4(x.y, ff), rescale4(x.z, ff), rescale4(x.w, ff));
+              *reinterpret_cast<uint4*>(old + 16 * i) = x;
+            }
           }
+          code = max(code, before);
+          __syncwarp();  // every lane has read the scale
         }
-        code = max(code, before);
-        __syncwarp();  // every lane has read the scale
-      }
-      if (lane == 0) *sf = static_cast<uint8_t>(code);
-      const float inv = sf_value(max(254 - code, 0));  // code <= 247 for what this kernel stored (amax < 2^128)
-#pragma unroll
-      for (int u = 0; u < KV_ITEMS; ++u) {
-        const int t = lane / IPR + u * HPW;
-        if (t < o.cnt) {
+        if (h < H && lane % L == 0) *sf = static_cast<uint8_t>(code);
+        const float inv = sf_value(max(254 - code, 0));  // code <= 247 for what this kernel stored (amax < 2^128)
+#pragma unroll 1
+        for (int u = u0; u < u0 + steps; ++u) {
+          int hh, t;
+          if (!where(u, hh, t)) continue;
           float a[8], b[8];
-          item(u, a, b);
-          *reinterpret_cast<uint2*>(codes + t * D + at.d0) = quantise8(a, inv, inf);
-          *reinterpret_cast<uint2*>(codes + t * D + at.d1) = quantise8(b, inv, inf);
+          item(u, at, s_cs + (o.tab + t) * half, a, b);
+          uint8_t* const to = codes + (row + t) * D;
+          *reinterpret_cast<uint2*>(to + at.d0) = quantise8(a, inv, inf);
+          *reinterpret_cast<uint2*>(to + at.d1) = quantise8(b, inv, inf);
         }
       }
     }
