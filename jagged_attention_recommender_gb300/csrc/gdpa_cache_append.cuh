@@ -19,9 +19,10 @@
 // its warps take tasks of up to 128 items of 16 elements: keys or values of a
 // block and as many heads as that makes (one for 16 tokens, 16 for a single
 // one of 128), or query items of a few rows.  A task's elements come to shared
-// memory by the lanes' own asynchronous copies (4 KB a warp, 32 warps an SM)
+// memory by the lanes' own asynchronous copies (4 KB a warp, 24 warps an SM)
 // and are read from there twice, for the largest magnitude and for the codes:
-// held in registers they left room for 16 warps and took TIME_REGS.
+// held in registers they left room for 16 warps and took 387 us for 68 423 tokens
+// of 32 query and 8 key heads of 128, where this takes 284 (5.4 TB/s).
 #pragma once
 
 #include "gdpa_cache.cuh"
@@ -52,18 +53,22 @@ __device__ __forceinline__ float2 rope_angle(unsigned long long F, int pos) {
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+// Eight bf16 as four pairs of fp32 (the arithmetic below is on packed pairs).
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __int_as_float(w[i] << 16);
-    x[2 * i + 1] = __int_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = ptx::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]), ptx::pack_bf16x2(x[4], x[5]),
-                    ptx::pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    ptx::f2_unpack(x[i], lo, hi);
+    w[i] = ptx::pack_bf16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // An item: 16 coordinates of one head as two chunks of 8, at d0 and d1.
@@ -77,51 +82,79 @@ __device__ __forceinline__ ItemAt item_at(int it, int rot, int interleaved) {
   return ItemAt{16 * it, 16 * it + 8, 16 * it < rot ? 8 * it : -1};
 }
 
-// The (cos, sin) of an item's eight pairs.
-__device__ __forceinline__ void load_angles(const float2* src, float2 (&cs)[8]) {
+// Cosines and sines of an item's eight pairs, two in a word.
+struct Angles {
+  uint64_t c[4], s[4];
+};
+__device__ __forceinline__ Angles load_angles(const float* cos_at, const float* sin_at) {
+  Angles t;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 u = reinterpret_cast<const float4*>(src)[i];
-    cs[2 * i] = make_float2(u.x, u.y);
-    cs[2 * i + 1] = make_float2(u.z, u.w);
+  for (int i = 0; i < 2; ++i) {
+    const ulonglong2 c = reinterpret_cast<const ulonglong2*>(cos_at)[i], s = reinterpret_cast<const ulonglong2*>(sin_at)[i];
+    t.c[2 * i] = c.x, t.c[2 * i + 1] = c.y;
+    t.s[2 * i] = s.x, t.s[2 * i + 1] = s.y;
   }
+  return t;
 }
 
-__device__ __forceinline__ void rotate_item(const ItemAt& at, int interleaved, const float2 (&cs)[8], float (&a)[8],
-                                            float (&b)[8]) {
-  if (at.pair < 0) return;
+// Rotates an item: x[0..3] its first chunk, x[4..7] its second.
+__device__ __forceinline__ void rotate_item(int interleaved, const Angles& t, uint64_t (&x)[8]) {
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t0 = cs[i], t1 = cs[4 + i];
-      const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
-      a[2 * i] = x0 * t0.x - y0 * t0.y;
-      a[2 * i + 1] = y0 * t0.x + x0 * t0.y;
-      b[2 * i] = x1 * t1.x - y1 * t1.y;
-      b[2 * i + 1] = y1 * t1.x + x1 * t1.y;
+    for (int i = 0; i < 8; ++i) {
+      float a, b, c, s, c2, s2;
+      ptx::f2_unpack(x[i], a, b);
+      ptx::f2_unpack(t.c[i >> 1], c, c2);
+      ptx::f2_unpack(t.s[i >> 1], s, s2);
+      if (i & 1) c = c2, s = s2;
+      x[i] = ptx::f2_pack(a * c - b * s, b * c + a * s);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[i];
-      const float x = a[i], y = b[i];
-      a[i] = x * t.x - y * t.y;
-      b[i] = y * t.x + x * t.y;
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = x[i], b = x[4 + i];
+      x[i] = ptx::f2_fma(a, t.c[i], ptx::f2_mul(b, t.s[i] ^ 0x8000000080000000ull));
+      x[4 + i] = ptx::f2_fma(b, t.c[i], ptx::f2_mul(a, t.s[i]));
     }
   }
+}
+
+// The largest magnitude of an item, NaN left out.
+__device__ __forceinline__ float item_max(const uint64_t (&x)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    ptx::f2_unpack(x[i], a, b);
+    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  }
+  return m;
+}
+// The same of 16 values as loaded.
+__device__ __forceinline__ float raw_max(const uint4& u, const uint4& v) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
 // Eight values times `inv` (a power of two) as e4m3 codes.  What is not finite
 // becomes the NaN code: the conversion does that to NaN, but makes an infinity
 // 448, so a task that holds one (`inf`, uniform) replaces it first.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv, bool inf) {
+__device__ __forceinline__ uint2 quantise8(const uint64_t* x, float inv, bool inf) {
+  const uint64_t f = ptx::f2_splat(inv);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+  for (int i = 0; i < 4; ++i) ptx::f2_unpack(ptx::f2_mul(x[i], f), y[2 * i], y[2 * i + 1]);
   if (inf) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (fabsf(x[i]) == INFINITY) y[i] = __int_as_float(0x7fffffff);
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      ptx::f2_unpack(x[i], a, b);
+      if (fabsf(a) == INFINITY) y[2 * i] = __int_as_float(0x7fffffff);
+      if (fabsf(b) == INFINITY) y[2 * i + 1] = __int_as_float(0x7fffffff);
+    }
   }
   return make_uint2(ptx::pack_e4m3x4(y[0], y[1], y[2], y[3]), ptx::pack_e4m3x4(y[4], y[5], y[6], y[7]));
 }
@@ -155,6 +188,16 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return u;
 }
 
+// The largest of each L lanes (a power of two).
+__device__ __forceinline__ float head_max(float x, int L) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, d);
+    if (d < L) x = fmaxf(x, y);
+  }
+  return x;
+}
+
 // A scale block that this launch writes to: `cnt` new tokens from row `row`
 // on, the first at position `pos`.
 struct OwnedBlock {
@@ -162,13 +205,13 @@ struct OwnedBlock {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
+__global__ void __launch_bounds__(kAppendThreads, 3) gdpa_cache_append_kernel(const __grid_constant__ AppendParams p,
                                                                            int rows_per_cta) {
   constexpr int IPR = D / 16;             // items of a row and head
   constexpr int HPW = 32 / IPR;           // heads (or rows of one head) whose items a warp holds once
   __shared__ OwnedBlock s_own[16];
   __shared__ int s_n;
-  extern __shared__ __align__(16) float2 s_cs[];  // [rows][rot / 2]
+  extern __shared__ __align__(16) float s_cos[];  // [rows][rot / 2], and the sines behind them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const CacheBatch& bt = p.batch;
   const int g0 = blockIdx.x * rows_per_cta;
@@ -217,12 +260,15 @@ __global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(co
   const int n = s_n;
   if (n == 0) return;
   const int half = p.rot >> 1;
+  float* const s_sin = s_cos + (rows_per_cta + kCacheBlock - 1) * half;
   if (half > 0) {
     for (int j = 0; j < n; ++j) {
       const OwnedBlock o = s_own[j];
       for (int i = tid; i < o.cnt * half; i += kAppendThreads) {
         const int t = i / half, f = i - t * half;
-        s_cs[(o.tab + t) * half + f] = rope_angle(p.freq[f], o.pos + t);
+        const float2 cs = rope_angle(p.freq[f], o.pos + t);
+        s_cos[(o.tab + t) * half + f] = cs.x;
+        s_sin[(o.tab + t) * half + f] = cs.y;
       }
     }
     __syncthreads();
@@ -236,16 +282,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(co
   const int trows = 4 / span;                           // ... and rows of a task
   const int per_row = (groups + 3) / 4;                 // tasks of a row where trows is 1
   // this lane's 16-byte pieces of a task: first chunks of its four items, then second ones
-  const uint32_t stage = ptx::smem_u32(s_cs) + static_cast<uint32_t>((rows_per_cta + kCacheBlock - 1) * half) * 8 +
+  const uint32_t stage = ptx::smem_u32(s_cos) + static_cast<uint32_t>((rows_per_cta + kCacheBlock - 1) * half) * 8 +
                          warp * 4096 + lane * 16;
-  auto item = [&](int u, const ItemAt& at, const float2* cs, float (&a)[8], float (&b)[8]) {
-    unpack8(lds16(stage + u * 512), a);
-    unpack8(lds16(stage + 2048 + u * 512), b);
-    if (at.pair >= 0) {
-      float2 t[8];
-      load_angles(cs + at.pair, t);
-      rotate_item(at, p.interleaved, t, a, b);
-    }
+  auto angles = [&](int row, const ItemAt& at) {
+    const int i = row * half + at.pair;
+    return load_angles(s_cos + i, s_sin + i);
   };
   int w = warp;  // this warp's next task, counted over all blocks
   for (int j = 0; j < n; ++j) {
@@ -274,15 +315,19 @@ __global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(co
           }
         }
         copies_wait();
-#pragma unroll 1
+        Angles cs;
+#pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int t = t0 + u / span, head = h0 + u % span * HPW;
+          if (u % span == 0 && at.pair >= 0 && t < o.cnt) cs = angles(o.tab + t, at);
           if (t < o.cnt && head < p.Hq) {
-            float a[8], b[8];
-            item(u, at, s_cs + (o.tab + t) * half, a, b);
+            uint64_t x[8];
+            unpack8(lds16(stage + u * 512), x);
+            unpack8(lds16(stage + 2048 + u * 512), x + 4);
+            if (at.pair >= 0) rotate_item(p.interleaved, cs, x);
             __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(o.row + t) * p.Hq + head) * D;
-            *reinterpret_cast<uint4*>(dst + at.d0) = pack8(a);
-            *reinterpret_cast<uint4*>(dst + at.d1) = pack8(b);
+            *reinterpret_cast<uint4*>(dst + at.d0) = pack8(x);
+            *reinterpret_cast<uint4*>(dst + at.d1) = pack8(x + 4);
           }
         }
         continue;
@@ -317,34 +362,43 @@ __global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(co
       for (int u0 = 0; u0 < 4; u0 += steps) {
         const int h = h0 + (32 * u0 + lane >> lhead);
         if (__all_sync(0xffffffffu, h >= H)) break;
+        auto item = [&](int u, int t, uint64_t (&x)[8]) {
+          unpack8(lds16(stage + u * 512), x);
+          unpack8(lds16(stage + 2048 + u * 512), x + 4);
+          if (at.pair >= 0) rotate_item(p.interleaved, angles(o.tab + t, at), x);
+        };
         float amax = 0.0f;
-        bool inf = false;
 #pragma unroll 1
-        for (int again = 0; again < 2; ++again) {  // again without what is not finite, where there is some
+        for (int u = u0; u < u0 + steps; ++u) {
+          int hh, t;
+          if (!where(u, hh, t)) continue;
+          if (at.pair < 0) {
+            amax = fmaxf(amax, raw_max(lds16(stage + u * 512), lds16(stage + 2048 + u * 512)));
+          } else {
+            uint64_t x[8];
+            item(u, t, x);
+            amax = fmaxf(amax, item_max(x));
+          }
+        }
+        amax = head_max(amax, L);
+        const bool inf = __any_sync(0xffffffffu, amax == INFINITY);
+        if (inf) {  // again without what is not finite
           amax = 0.0f;
 #pragma unroll 1
           for (int u = u0; u < u0 + steps; ++u) {
             int hh, t;
             if (!where(u, hh, t)) continue;
-            float a[8], b[8];
-            item(u, at, s_cs + (o.tab + t) * half, a, b);
-            if (again) {
+            uint64_t x[8];
+            item(u, t, x);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (fabsf(a[e]) == INFINITY) a[e] = 0.0f;
-                if (fabsf(b[e]) == INFINITY) b[e] = 0.0f;
-              }
+            for (int i = 0; i < 8; ++i) {
+              float a, b;
+              ptx::f2_unpack(x[i], a, b);
+              if (fabsf(a) < INFINITY) amax = fmaxf(amax, fabsf(a));
+              if (fabsf(b) < INFINITY) amax = fmaxf(amax, fabsf(b));
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));  // NaN never wins
           }
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) {
-            const float x = __shfl_xor_sync(0xffffffffu, amax, d);
-            if (d < L) amax = fmaxf(amax, x);
-          }
-          if (again || !__any_sync(0xffffffffu, amax == INFINITY)) break;
-          inf = true;
+          amax = head_max(amax, L);
         }
         const uint32_t bits = __float_as_uint(amax);
         int code = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
@@ -375,11 +429,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) gdpa_cache_append_kernel(co
         for (int u = u0; u < u0 + steps; ++u) {
           int hh, t;
           if (!where(u, hh, t)) continue;
-          float a[8], b[8];
-          item(u, at, s_cs + (o.tab + t) * half, a, b);
+          uint64_t x[8];
+          item(u, t, x);
           uint8_t* const to = codes + (row + t) * D;
-          *reinterpret_cast<uint2*>(to + at.d0) = quantise8(a, inv, inf);
-          *reinterpret_cast<uint2*>(to + at.d1) = quantise8(b, inv, inf);
+          *reinterpret_cast<uint2*>(to + at.d0) = quantise8(x, inv, inf);
+          *reinterpret_cast<uint2*>(to + at.d1) = quantise8(x + 4, inv, inf);
         }
       }
     }
