@@ -153,15 +153,19 @@ gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int rows, int
 // workspace, and how many CTAs have work at most.
 template <class C>
 int prepare_launch(CacheFwdParams& p, void* workspace, int max_q, const Device& dev) {
-  // Keys a segment can have, as far as the host knows: up to 512 of them are
-  // not worth a second kernel.
+  // Keys a segment can have, as far as the host knows, and segments.
   int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock);
-  p.no_split = keys <= 512 ? 1 : 0;
   const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;
+  const int64_t most = (int64_t)dev.sms * C::CTAS;
+  // The second kernel costs a call about 5 us (of it 2 on the GPU): up to 2048
+  // keys the four warps of a CTA are done with a segment of their own sooner,
+  // if every segment has a CTA; up to 512 keys one warp is.
+  p.team = C::WORKERS > 1 && keys <= 2048 && segments <= most;
+  p.no_split = p.team || keys <= 512;
   const int64_t workers = segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
   const int ctas = static_cast<int>(
-      std::min<int64_t>((workers + C::WORKERS - 1) / C::WORKERS, (int64_t)dev.sms * C::CTAS));
+      std::min<int64_t>(p.team ? segments : (workers + C::WORKERS - 1) / C::WORKERS, most));
   p.meta = static_cast<int*>(workspace);
   p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * C::WORKERS * 16);
   return ctas;

@@ -48,7 +48,8 @@ struct CacheFwdParams {
   int Hq, G;       // query heads, query heads of a key/value head
   int causal, window;
   float scale2;    // scale * log2(e)
-  int no_split;    // one segment is never cut: `part` is not used
+  int no_split;    // segments are never cut: `part` is not used
+  int team;        // ... and a CTA's four warps share one, a CTA having one at most
   int* meta;       // [workers][2][8]: the segments a warp left a part of
   float* part;     // [workers][2][rows (D + 2)]
 };
@@ -187,7 +188,7 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
 }
 template <class C>
 __device__ __forceinline__ int64_t seq_cost(const CacheFwdParams& p, const SeqWork& w) {
-  return static_cast<int64_t>(w.tiles) * p.cache.H * (w.steps + C::START);
+  return static_cast<int64_t>(w.tiles) * p.cache.H * (p.team ? 1 : w.steps + C::START);
 }
 
 // The runs of a CTA's workers: where each begins.  All threads take part.
@@ -218,11 +219,11 @@ __device__ __forceinline__ void schedule(const CacheFwdParams& p, Schedule<C>& s
     if (w < warp) incl += sh.scan[w];
     total += sh.scan[w];
   }
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WORKERS;
-  chunk = max((total + workers - 1) / workers, (int64_t)C::RUN_STEPS);
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * (p.team ? 1 : C::WORKERS);
+  chunk = max((total + workers - 1) / workers, p.team ? (int64_t)1 : (int64_t)C::RUN_STEPS);
 #pragma unroll 1
   for (int w = 0; w < C::WORKERS; ++w) {
-    const int64_t from = chunk * (static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
+    const int64_t from = chunk * (p.team ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
     if (from < total && from >= incl - mine && from < incl) {
       int64_t base = incl - mine;
       int b = b_lo;
@@ -253,13 +254,13 @@ struct Walk {
   __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
     b = seq;
     w = seq_work<C>(p, b);
-    const int64_t cost = w.steps + C::START, seg = (at - base) / cost;
+    const int64_t cost = p.team ? 1 : w.steps + C::START, seg = (at - base) / cost;
     start = base + seg * cost;
     tile = static_cast<int>(seg / p.cache.H);
     h = static_cast<int>(seg - static_cast<int64_t>(tile) * p.cache.H);
   }
   __device__ __forceinline__ void next(const CacheFwdParams& p) {
-    start += w.steps + C::START;
+    start += p.team ? 1 : w.steps + C::START;
     if (++h < p.cache.H) return;
     h = 0;
     if (++tile < w.tiles) return;
@@ -300,6 +301,60 @@ struct Walk {
 
 }  // namespace split
 
+// A segment that the CTA's four warps shared: their references, sums and
+// outputs meet in shared memory, and each thread joins pieces of rows.
+template <int D, int NT>
+__device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem,
+                                          float (&s_team)[SplitCfg<D, NT>::WARPS][SplitCfg<D, NT>::ROWS][2],
+                                          const float (&acc)[D / 16][NT][4], const float (&ref)[NT][2],
+                                          const float (&room)[NT][2], const float (&sum)[NT][2], const CacheSeq& s,
+                                          int h, int row0, int rows) {
+  using C = SplitCfg<D, NT>;
+  static_assert(C::WARPS * C::ROWS * D * 4 <= C::WARPS * C::RING, "the rings hold the outputs");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  split::cp_wait<0>();
+  __syncthreads();  // every warp is done with its ring
+  float* merge = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float l = sum[nt][c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int r = nt * 8 + 2 * t + c;
+      if (g == 0) s_team[warp][r][0] = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c], s_team[warp][r][1] = l;
+      float4* dst = reinterpret_cast<float4*>(merge + (warp * C::ROWS + r) * D + g * (D / 8));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        dst[i] = make_float4(acc[2 * i][nt][c], acc[2 * i][nt][c + 2], acc[2 * i + 1][nt][c], acc[2 * i + 1][nt][c + 2]);
+    }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 8); i += C::THREADS) {
+    const int r = i / (D / 8), d = i % (D / 8) * 8;
+    float top = -INFINITY, l = 0.0f, o[8] = {};
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, s_team[w][r][0]);
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) {
+      const float f = ptx::ex2_approx(s_team[w][r][0] - (top == -INFINITY ? 0.0f : top));
+      l += s_team[w][r][1] * f;
+      const float4* src = reinterpret_cast<const float4*>(merge + (w * C::ROWS + r) * D + d);
+      const float4 x = src[0], y = src[1];
+      o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
+      o[4] += y.x * f, o[5] += y.y * f, o[6] += y.z * f, o[7] += y.w * f;
+    }
+    const int rr = row0 + r, tok = rr / p.G;
+    const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + rr - tok * p.G;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint4*>(p.out + at_row * D + d) =
+        make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
+                   ptx::pack_bf16x2(o[4] * inv, o[5] * inv), ptx::pack_bf16x2(o[6] * inv, o[7] * inv));
+    if (p.lse && d == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split_kernel(const CacheFwdParams p) {
   using namespace split;
@@ -307,6 +362,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   constexpr int KS = C::KSTEPS, ND = D / 16;  // k-steps of S^T; 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Schedule<C> sh;
+  __shared__ float s_team[C::WARPS][C::ROWS][2];
   __shared__ __align__(8) uint32_t s_sf[C::WARPS][C::STAGES][2 * C::NB];  // words that hold the scale codes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -318,7 +374,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   if (lane == 0 && !p.no_split) p.meta[worker * 16 + 1] = p.meta[worker * 16 + 9] = 0;  // no parts yet
   int64_t total, chunk;
   schedule<C>(p, sh, total, chunk);
-  const int64_t at = chunk * worker, stop = min(total, at + chunk);
+  const int64_t at = chunk * (p.team ? blockIdx.x : worker), stop = min(total, at + chunk);
   if (at >= stop) return;
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
@@ -326,6 +382,8 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   const uint32_t sf_at = ptx::smem_u32(&s_sf[warp][0][0]);
   const int pmask = (1 << p.cache.lp) - 1;
   const int64_t sf_bytes = static_cast<int64_t>(p.cache.num_pages) * p.cache.H << (p.cache.lp - 4);
+
+  const int stride = p.team ? C::WARPS : 1, skip = p.team ? warp : 0;  // a team's warps take its steps in turn
 
   // ---- the copies: a walk that runs ahead of the one that computes
   Walk<C> ahead;
@@ -344,7 +402,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         ahead_more = false;
         return;
       }
-      if (ahead.enter(p, at, stop)) ahead_u = ahead.u0; else ahead_u = ahead.u1 = 0;
+      if (ahead.enter(p, at, stop)) ahead_u = ahead.u0 + skip; else ahead_u = ahead.u1 = 0;
     }
     const int kb = ahead.w.kbase + ahead_u * C::SPAN;
     const int32_t* table = bt.table + static_cast<int64_t>(ahead.b) * bt.max_pages;
@@ -405,7 +463,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
                       static_cast<int>(min((int64_t)4, sf_bytes - word)));
         }
       }
-      ++ahead_u;
+      ahead_u += stride;
       look();
     }
     cp_commit();
@@ -494,7 +552,7 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
     }
 
 #pragma unroll 1
-    for (int u = now.u0; u < now.u1; ++u) {
+    for (int u = now.u0 + skip; u < now.u1; u += stride) {
       cp_wait<C::STAGES - 2>();
       __syncwarp();
       issue(stage == 0 ? C::STAGES - 1 : stage - 1);
@@ -678,6 +736,11 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         }
       }
     }
+    if (p.team) {  // join the four warps' results in the rings' room
+      team_join<D, NT>(p, smem, s_team, acc, ref, room, sum, s, h, row0, rows);
+      break;  // a CTA has one segment
+    }
+
     // ---- the segment's result, or this run's part of it
     const int64_t unit0 = now.start + C::START;
     const int first = static_cast<int>(unit0 / chunk);

@@ -297,6 +297,11 @@ ATTEND = [
     ([3000], [1], True, 0),
     ([1500, 12], [33, 0], True, 100),
     ([64] * 40, [1] * 40, True, 1),
+    # more segments than CTAs: runs of whole short ones, and of cut longer ones
+    ([(37 * i) % 300 for i in range(160)], [1] * 160, True, 0),
+    ([(97 * i) % 900 for i in range(160)], [1 + i % 2 for i in range(160)], True, 0),
+    ([2500, 40, 2100], [3, 1, 2], True, 0),
+    ([2100, 3000], [70, 33], True, 0),
 ]
 
 
