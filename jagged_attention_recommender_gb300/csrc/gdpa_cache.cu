@@ -97,11 +97,25 @@ unsigned long long turn_fraction(double f) {
   return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
 }
 
+// Keys a segment can have, as far as the host knows.
+int64_t most_keys(const CacheFwdParams& p, int max_q) {
+  const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
+  return p.window > 0 ? std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock) : keys;
+}
+
+// Segments of so many rows, at most.
+int64_t most_segments(const CacheFwdParams& p, int rows) {
+  return ((int64_t)p.batch.T * p.G / rows + p.batch.B) * p.cache.H;
+}
+
 // The kernel for so many query rows of a key head: eights of rows of the one
-// for few rows, or 0: the one for many.
-int split_columns(int max_q, int G) {
-  const int64_t rows = (int64_t)max_q * G;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+// for few rows, or 0: the one for many.  A segment costs the latter about 5 us
+// of an SM's time and 0.8 us (up to 128 rows; 1.4 us up to 256) for 64 keys; the
+// former about 0.2 us and 0.9 us for 32 rows and 64 keys.
+int split_columns(int64_t rows, int64_t keys) {
+  if (rows <= 16) return rows <= 8 ? 1 : 2;
+  const int64_t tiles = (rows + 31) / 32;
+  return tiles == 1 || tiles * keys <= 512 ? 4 : 0;
 }
 
 // Bytes of meta data and parts for so many workers.
@@ -114,11 +128,14 @@ int64_t workspace_of(const Device& dev, int D) {
   return part_bytes((int64_t)dev.sms * C::CTAS * C::WORKERS, C::ROWS, D);
 }
 
+// ... whatever the number of keys
 template <int D>
 int64_t workspace_bytes(const Device& dev, int max_q, int G) {
-  const int nt = split_columns(max_q, G);
-  return nt == 1 ? workspace_of<SplitCfg<D, 1>>(dev, D)
-                 : nt == 2 ? workspace_of<SplitCfg<D, 2>>(dev, D) : workspace_of<TileCfg<D>>(dev, D);
+  const int64_t rows = (int64_t)max_q * G;
+  if (rows <= 8) return workspace_of<SplitCfg<D, 1>>(dev, D);
+  if (rows <= 16) return workspace_of<SplitCfg<D, 2>>(dev, D);
+  const int64_t few = workspace_of<SplitCfg<D, 4>>(dev, D);
+  return rows <= 32 ? few : std::max(few, workspace_of<TileCfg<D>>(dev, D));
 }
 
 // Shared memory above 48 KB has to be asked for, once a device and kernel.
@@ -138,14 +155,14 @@ gdpa_status_t allow_smem(Kernel kernel, int bytes, int min_regs, int device, std
 }
 
 template <int D>
-gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int rows, int smem, const Device& dev,
+gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int share, int rows, int smem, const Device& dev,
                             cudaStream_t s) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   constexpr int most = (2 * kCacheBlock - 1) * (D / 2) * (int)sizeof(float2) + kAppendThreads / 32 * 4096;
   const gdpa_status_t st = allow_smem(gdpa_cache_append_kernel<D>, most, 0, dev.id, mu, done);
   if (st != GDPA_OK) return st;
-  gdpa_cache_append_kernel<D><<<static_cast<unsigned>(groups), kAppendThreads, smem, s>>>(p, rows);
+  gdpa_cache_append_kernel<D><<<dim3(static_cast<unsigned>(groups), share), kAppendThreads, smem, s>>>(p, rows);
   return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
@@ -153,19 +170,11 @@ gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int rows, int
 // workspace, and how many CTAs have work at most.
 template <class C>
 int prepare_launch(CacheFwdParams& p, void* workspace, int max_q, const Device& dev) {
-  // Keys a segment can have, as far as the host knows, and segments.
-  int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
-  if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + max_q + kCacheBlock);
-  const int64_t segments = ((int64_t)p.batch.T * p.G / C::ROWS + p.batch.B) * p.cache.H;
-  const int64_t most = (int64_t)dev.sms * C::CTAS;
-  // The second kernel costs a call about 5 us (of it 2 on the GPU): up to 2048
-  // keys the four warps of a CTA are done with a segment of their own sooner,
-  // if every segment has a CTA; up to 512 keys one warp is.
-  p.team = C::WORKERS > 1 && keys <= 2048 && segments <= most;
-  p.no_split = p.team || keys <= 512;
-  const int64_t workers = segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
+  const int64_t keys = most_keys(p, max_q), segments = most_segments(p, C::ROWS);
+  p.no_split = C::TEAM || keys <= 512;  // one warp is done with so many before a second kernel had begun
+  const int64_t workers = C::TEAM ? segments : segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
   const int ctas = static_cast<int>(
-      std::min<int64_t>(p.team ? segments : (workers + C::WORKERS - 1) / C::WORKERS, most));
+      std::min<int64_t>((workers + C::WORKERS - 1) / C::WORKERS, (int64_t)dev.sms * C::CTAS));
   p.meta = static_cast<int*>(workspace);
   p.part = reinterpret_cast<float*>(p.meta + (int64_t)ctas * C::WORKERS * 16);
   return ctas;
@@ -190,16 +199,28 @@ gdpa_status_t launch_join(const CacheFwdParams& p, int ctas, cudaStream_t s) {
                                                                                                     : GDPA_ERR_CUDA;
 }
 
-template <int D, int NT>
-gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
-  using C = SplitCfg<D, NT>;
+template <int D, int NT, bool TEAM>
+gdpa_status_t launch_split_as(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  using C = SplitCfg<D, NT, TEAM>;
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
-  const gdpa_status_t st = allow_smem(gdpa_cache_split_kernel<D, NT>, C::SMEM, 0, dev.id, mu, done);
+  const gdpa_status_t st = allow_smem(gdpa_cache_split_kernel<D, NT, TEAM>, C::SMEM, 0, dev.id, mu, done);
   if (st != GDPA_OK) return st;
   const int ctas = prepare_launch<C>(p, workspace, max_q, dev);
-  gdpa_cache_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
-  return launch_join<D, C>(p, ctas, s);
+  gdpa_cache_split_kernel<D, NT, TEAM><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  if constexpr (TEAM)
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+  else
+    return launch_join<D, C>(p, ctas, s);
+}
+
+// A second kernel costs a call about 5 us: up to 2048 keys the eight warps of a
+// CTA are done with a whole segment sooner, if every segment has an SM.
+template <int D, int NT>
+gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
+  const bool team = most_keys(p, max_q) <= 2048 && most_segments(p, 8 * NT) <= dev.sms;
+  return team ? launch_split_as<D, NT, true>(p, workspace, max_q, dev, s)
+              : launch_split_as<D, NT, false>(p, workspace, max_q, dev, s);
 }
 
 template <int D>
@@ -216,10 +237,12 @@ gdpa_status_t launch_tile(CacheFwdParams& p, void* workspace, int max_q, const D
 
 template <int D>
 gdpa_status_t launch_fwd(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
-  const int nt = split_columns(max_q, p.G);
-  return nt == 1 ? launch_split<D, 1>(p, workspace, max_q, dev, s)
-                 : nt == 2 ? launch_split<D, 2>(p, workspace, max_q, dev, s)
-                           : launch_tile<D>(p, workspace, max_q, dev, s);
+  switch (split_columns((int64_t)max_q * p.G, most_keys(p, max_q))) {
+    case 1: return launch_split<D, 1>(p, workspace, max_q, dev, s);
+    case 2: return launch_split<D, 2>(p, workspace, max_q, dev, s);
+    case 4: return launch_split<D, 4>(p, workspace, max_q, dev, s);
+    default: return launch_tile<D>(p, workspace, max_q, dev, s);
+  }
 }
 
 }  // namespace
@@ -267,10 +290,14 @@ extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void
   int rows = 16;
   while (T <= 4 * (int64_t)B && rows > 1 && rows * row_tasks > kAppendThreads / 32) rows >>= 1;
   const int64_t groups = (T + rows - 1) / rows;
+  // Few groups: several CTAs share the tasks of one (each finds its rows and
+  // angles again).
+  const int64_t spare = (int64_t)dev.sms * 3 / groups, useful = (rows * row_tasks + 7) / 8;
+  const int share = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(spare, useful)));
   const int smem = (rows + kCacheBlock - 1) * (p.rot / 2) * (int)sizeof(float2) + kAppendThreads / 32 * 4096;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cache->D == 128 ? launch_append<128>(p, groups, rows, smem, dev, s)
-                         : launch_append<64>(p, groups, rows, smem, dev, s);
+  return cache->D == 128 ? launch_append<128>(p, groups, share, rows, smem, dev, s)
+                         : launch_append<64>(p, groups, share, rows, smem, dev, s);
 }
 
 extern "C" gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes) {

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) gdpa_cache_append_kernel(co
   }
 
   const int H = p.cache.H;
-  constexpr int workers = kAppendThreads / 32;
+  const int workers = (kAppendThreads / 32) * gridDim.y;
   const int it = lane % IPR;  // a lane's items are the same one of several heads or rows
   const int groups = p.q ? (p.Hq + HPW - 1) / HPW : 0;  // a row's heads, in warps
   const int span = groups >= 3 ? 4 : max(groups, 1);    // groups of a row in a task ...
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) gdpa_cache_append_kernel(co
     const int i = row * half + at.pair;
     return load_angles(s_cos + i, s_sin + i);
   };
-  int w = warp;  // this warp's next task, counted over all blocks
+  int w = blockIdx.y * (kAppendThreads / 32) + warp;  // this warp's next task, counted over all blocks
   for (int j = 0; j < n; ++j) {
     const OwnedBlock o = s_own[j];
     // keys and values: tokens (to a power of two) times items of a head; the

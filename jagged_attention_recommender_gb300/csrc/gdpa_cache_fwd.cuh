@@ -49,7 +49,6 @@ struct CacheFwdParams {
   int causal, window;
   float scale2;    // scale * log2(e)
   int no_split;    // segments are never cut: `part` is not used
-  int team;        // ... and a CTA's four warps share one, a CTA having one at most
   int* meta;       // [workers][2][8]: the segments a warp left a part of
   float* part;     // [workers][2][rows (D + 2)]
 };
@@ -58,12 +57,14 @@ struct CacheFwdParams {
 // `pieces - 1` workers behind it the next ones in their slots 0.  Beside each
 // part stand {first, pieces, first row of the sequence, its rows, row tile, head}.
 
-template <int D, int NT>
+// TEAM: a CTA has one whole segment at most, and its warps take the steps in turn.
+template <int D, int NT, bool TEAM_ = false>
 struct SplitCfg {
-  static constexpr int THREADS = 128, WARPS = 4;
-  static constexpr int WORKERS = 4;    // of a CTA: its warps
-  static constexpr int START = 2;      // what a segment's start costs, in steps
-  static constexpr int RUN_STEPS = 6;  // the fewest steps (starts included) that are worth a worker
+  static constexpr bool TEAM = TEAM_;
+  static constexpr int WARPS = TEAM ? 8 : 4, THREADS = 32 * WARPS;
+  static constexpr int WORKERS = TEAM ? 1 : WARPS;  // of a CTA: its warps, or itself
+  static constexpr int START = 2;                   // what a segment's start costs, in steps
+  static constexpr int RUN_STEPS = TEAM ? 1 : 6;    // the fewest steps (starts included) that are worth a worker
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
 #ifndef XNB
@@ -76,7 +77,7 @@ struct SplitCfg {
   // CTAs an SM, and ring stages: enough tiles in flight to cover the memory's
   // latency (an SM's share of 6.8 TB/s is 45 KB a microsecond) at the
   // registers that the accumulators leave
-  static constexpr int CTAS = NT == 1 ? XC : NT == 2 ? 3 : 2;
+  static constexpr int CTAS = TEAM ? 1 : NT == 1 ? XC : NT == 2 ? 3 : 2;
   static constexpr int STAGES = NT == 1 ? (D == 64 ? (2 * XS * XNB > 8 ? 8 / XNB : 2 * XS) : XS) : D == 64 ? 6 : NT == 2 ? 3 : 4;
   static_assert(STAGES * NB <= 8, "a nibble of state for each tile of the ring");
   static constexpr int STAGE = NB * 2 * TILE;
@@ -188,7 +189,7 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
 }
 template <class C>
 __device__ __forceinline__ int64_t seq_cost(const CacheFwdParams& p, const SeqWork& w) {
-  return static_cast<int64_t>(w.tiles) * p.cache.H * (p.team ? 1 : w.steps + C::START);
+  return static_cast<int64_t>(w.tiles) * p.cache.H * (C::TEAM ? 1 : w.steps + C::START);
 }
 
 // The runs of a CTA's workers: where each begins.  All threads take part.
@@ -219,11 +220,11 @@ __device__ __forceinline__ void schedule(const CacheFwdParams& p, Schedule<C>& s
     if (w < warp) incl += sh.scan[w];
     total += sh.scan[w];
   }
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * (p.team ? 1 : C::WORKERS);
-  chunk = max((total + workers - 1) / workers, p.team ? (int64_t)1 : (int64_t)C::RUN_STEPS);
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WORKERS;
+  chunk = max((total + workers - 1) / workers, (int64_t)C::RUN_STEPS);
 #pragma unroll 1
   for (int w = 0; w < C::WORKERS; ++w) {
-    const int64_t from = chunk * (p.team ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
+    const int64_t from = chunk * (static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
     if (from < total && from >= incl - mine && from < incl) {
       int64_t base = incl - mine;
       int b = b_lo;
@@ -254,13 +255,13 @@ struct Walk {
   __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
     b = seq;
     w = seq_work<C>(p, b);
-    const int64_t cost = p.team ? 1 : w.steps + C::START, seg = (at - base) / cost;
+    const int64_t cost = C::TEAM ? 1 : w.steps + C::START, seg = (at - base) / cost;
     start = base + seg * cost;
     tile = static_cast<int>(seg / p.cache.H);
     h = static_cast<int>(seg - static_cast<int64_t>(tile) * p.cache.H);
   }
   __device__ __forceinline__ void next(const CacheFwdParams& p) {
-    start += p.team ? 1 : w.steps + C::START;
+    start += C::TEAM ? 1 : w.steps + C::START;
     if (++h < p.cache.H) return;
     h = 0;
     if (++tile < w.tiles) return;
@@ -301,15 +302,14 @@ struct Walk {
 
 }  // namespace split
 
-// A segment that the CTA's four warps shared: their references, sums and
+// A segment that the CTA's warps shared: their references, sums and
 // outputs meet in shared memory, and each thread joins pieces of rows.
-template <int D, int NT>
+template <int D, int NT, class C>
 __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem,
-                                          float (&s_team)[SplitCfg<D, NT>::WARPS][SplitCfg<D, NT>::ROWS][2],
+                                          float (&s_team)[C::WARPS][C::ROWS][2],
                                           const float (&acc)[D / 16][NT][4], const float (&ref)[NT][2],
                                           const float (&room)[NT][2], const float (&sum)[NT][2], const CacheSeq& s,
                                           int h, int row0, int rows) {
-  using C = SplitCfg<D, NT>;
   static_assert(C::WARPS * C::ROWS * D * 4 <= C::WARPS * C::RING, "the rings hold the outputs");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   split::cp_wait<0>();
@@ -355,26 +355,27 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
   }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split_kernel(const CacheFwdParams p) {
+template <int D, int NT, bool TEAM>
+__global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D, NT, TEAM>::CTAS))
+    gdpa_cache_split_kernel(const CacheFwdParams p) {
   using namespace split;
-  using C = SplitCfg<D, NT>;
+  using C = SplitCfg<D, NT, TEAM>;
   constexpr int KS = C::KSTEPS, ND = D / 16;  // k-steps of S^T; 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Schedule<C> sh;
-  __shared__ float s_team[C::WARPS][C::ROWS][2];
+  __shared__ float s_team[C::TEAM ? C::WARPS : 1][C::TEAM ? C::ROWS : 1][2];
   __shared__ __align__(8) uint32_t s_sf[C::WARPS][C::STAGES][2 * C::NB];  // words that hold the scale codes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const CacheBatch& bt = p.batch;
-  const int worker = blockIdx.x * C::WARPS + warp;
+  const int worker = C::TEAM ? blockIdx.x : blockIdx.x * C::WARPS + warp;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up beside this
 
   if (lane == 0 && !p.no_split) p.meta[worker * 16 + 1] = p.meta[worker * 16 + 9] = 0;  // no parts yet
   int64_t total, chunk;
   schedule<C>(p, sh, total, chunk);
-  const int64_t at = chunk * (p.team ? blockIdx.x : worker), stop = min(total, at + chunk);
+  const int64_t at = chunk * worker, stop = min(total, at + chunk);
   if (at >= stop) return;
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
@@ -383,11 +384,12 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
   const int pmask = (1 << p.cache.lp) - 1;
   const int64_t sf_bytes = static_cast<int64_t>(p.cache.num_pages) * p.cache.H << (p.cache.lp - 4);
 
-  const int stride = p.team ? C::WARPS : 1, skip = p.team ? warp : 0;  // a team's warps take its steps in turn
+  constexpr int stride = C::TEAM ? C::WARPS : 1;
+  const int skip = C::TEAM ? warp : 0, self = C::TEAM ? 0 : warp;
 
   // ---- the copies: a walk that runs ahead of the one that computes
   Walk<C> ahead;
-  ahead.begin(p, sh.seq[warp], sh.base[warp], at);
+  ahead.begin(p, sh.seq[self], sh.base[self], at);
   Walk<C> now = ahead;
   int ahead_u = 0;
   bool ahead_more = false;
@@ -736,9 +738,9 @@ __global__ void __launch_bounds__(128, (SplitCfg<D, NT>::CTAS)) gdpa_cache_split
         }
       }
     }
-    if (p.team) {  // join the four warps' results in the rings' room
-      team_join<D, NT>(p, smem, s_team, acc, ref, room, sum, s, h, row0, rows);
-      break;  // a CTA has one segment
+    if constexpr (C::TEAM) {  // the warps' results meet in the rings' room
+      team_join<D, NT, C>(p, smem, s_team, acc, ref, room, sum, s, h, row0, rows);
+      return;  // the CTA's only one
     }
 
     // ---- the segment's result, or this run's part of it

@@ -46,6 +46,7 @@ namespace gdpa {
 template <int D_>
 struct TileCfg {
   static constexpr int D = D_;
+  static constexpr bool TEAM = false;
   static constexpr int THREADS = 640, WORKERS = 1;  // five warpgroups
   static constexpr int START = 3, RUN_STEPS = 8;
   static constexpr int HALF = 128, ROWS = 2 * HALF, SPAN = 64;
