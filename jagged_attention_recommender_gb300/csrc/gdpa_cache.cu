@@ -171,8 +171,10 @@ gdpa_status_t launch_append(const AppendParams& p, int64_t groups, int share, in
 template <class C>
 int prepare_launch(CacheFwdParams& p, void* workspace, int max_q, const Device& dev) {
   const int64_t keys = most_keys(p, max_q), segments = most_segments(p, C::ROWS);
-  p.no_split = C::TEAM || keys <= 512;  // one warp is done with so many before a second kernel had begun
-  const int64_t workers = C::TEAM ? segments : segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
+  // Whole segments need no second kernel: so few keys that one worker is done
+  // with them before that had begun, or enough segments for all workers.
+  p.no_split = C::TEAM || keys <= 128 || (keys <= 512 && segments >= 2 * (int64_t)dev.sms * C::CTAS * C::WORKERS);
+  const int64_t workers = p.no_split ? segments : segments * ((keys / C::SPAN + 1 + C::START) / C::RUN_STEPS + 1);
   const int ctas = static_cast<int>(
       std::min<int64_t>((workers + C::WORKERS - 1) / C::WORKERS, (int64_t)dev.sms * C::CTAS));
   p.meta = static_cast<int*>(workspace);
@@ -346,6 +348,7 @@ extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q
   p.lse = lse;
   p.Hq = Hq;
   p.G = Hq / cache->H;
+  p.inv_g = p.G == 1 ? 0 : static_cast<uint32_t>((((uint64_t)1 << 32) + p.G - 1) / p.G);
   p.causal = causal;
   p.window = window_tokens;
   p.scale2 = scale * 1.4426950408889634f;

@@ -46,11 +46,31 @@ struct CacheFwdParams {
   __nv_bfloat16* out;
   float* lse;
   int Hq, G;       // query heads, query heads of a key/value head
+  uint32_t inv_g;  // 2^32 / G rounded up (0 for G = 1)
   int causal, window;
   float scale2;    // scale * log2(e)
   int no_split;    // segments are never cut: `part` is not used
   int* meta;       // [workers][2][8]: the segments a warp left a part of
   float* part;     // [workers][2][rows (D + 2)]
+};
+
+// Query rows of a segment by token and head.  The division by G is a product
+// with 2^32 / G rounded up, which is exact below 2^32 / G, so the row of the
+// segment's start is divided once and only rows behind it take it.
+struct RowMap {
+  int tok0, rem0;  // the first row's token and head of the group
+  __device__ __forceinline__ void begin(const CacheFwdParams& p, int row0) {
+    tok0 = row0 / p.G;
+    rem0 = row0 - tok0 * p.G;
+  }
+  // Row r of the segment: its token of the sequence, and its head of the group.
+  __device__ __forceinline__ int token(const CacheFwdParams& p, int r) const {
+    const uint32_t x = rem0 + r;
+    return tok0 + static_cast<int>(p.inv_g ? __umulhi(x, p.inv_g) : x);
+  }
+  __device__ __forceinline__ int head(const CacheFwdParams& p, int r, int tok) const {
+    return rem0 + r - (tok - tok0) * p.G;
+  }
 };
 
 // Parts of a cut segment: worker `first` holds the first in its slot 1, the
@@ -64,7 +84,7 @@ struct SplitCfg {
   static constexpr int WARPS = TEAM ? 8 : 4, THREADS = 32 * WARPS;
   static constexpr int WORKERS = TEAM ? 1 : WARPS;  // of a CTA: its warps, or itself
   static constexpr int START = 2;                   // what a segment's start costs, in steps
-  static constexpr int RUN_STEPS = TEAM ? 1 : 6;    // the fewest steps (starts included) that are worth a worker
+  static constexpr int RUN_STEPS = 6;               // the fewest steps (starts included) that are worth a part
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
 #ifndef XNB
@@ -221,7 +241,7 @@ __device__ __forceinline__ void schedule(const CacheFwdParams& p, Schedule<C>& s
     total += sh.scan[w];
   }
   const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WORKERS;
-  chunk = max((total + workers - 1) / workers, (int64_t)C::RUN_STEPS);
+  chunk = max((total + workers - 1) / workers, p.no_split ? (int64_t)1 : (int64_t)C::RUN_STEPS);
 #pragma unroll 1
   for (int w = 0; w < C::WORKERS; ++w) {
     const int64_t from = chunk * (static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
@@ -247,6 +267,7 @@ struct Walk {
   int64_t start;  // of the present segment
   int b, h, tile;
   int row0;       // its first query row (of the sequence and key head)
+  RowMap map;
   int rows;
   int u0, u1;     // its steps that are in the run and hold visible keys
   int lo_min, hi_max;  // keys any of its rows sees: [lo_min, hi_max)
@@ -288,8 +309,9 @@ struct Walk {
     }
     row0 = tile * C::ROWS;
     rows = min(C::ROWS, s.n * p.G - row0);
-    const int pos0 = s.len - s.n + row0 / p.G;
-    const int pos1 = s.len - s.n + (row0 + rows - 1) / p.G;
+    map.begin(p, row0);
+    const int pos0 = s.len - s.n + map.tok0;
+    const int pos1 = s.len - s.n + map.token(p, rows - 1);
     lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
     hi_max = max(0, p.causal ? min(s.len, pos1 + 1) : s.len);
     lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
@@ -309,7 +331,7 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
                                           float (&s_team)[C::WARPS][C::ROWS][2],
                                           const float (&acc)[D / 16][NT][4], const float (&ref)[NT][2],
                                           const float (&room)[NT][2], const float (&sum)[NT][2], const CacheSeq& s,
-                                          int h, int row0, int rows) {
+                                          int h, const RowMap& map, int rows) {
   static_assert(C::WARPS * C::ROWS * D * 4 <= C::WARPS * C::RING, "the rings hold the outputs");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   split::cp_wait<0>();
@@ -345,8 +367,8 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
       o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
       o[4] += y.x * f, o[5] += y.y * f, o[6] += y.z * f, o[7] += y.w * f;
     }
-    const int rr = row0 + r, tok = rr / p.G;
-    const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + rr - tok * p.G;
+    const int tok = map.token(p, r);
+    const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + map.head(p, r, tok);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint4*>(p.out + at_row * D + d) =
         make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
@@ -480,7 +502,6 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
     if (!now.enter(p, at, stop)) continue;
     const CacheSeq s = now.w.s;
     const int h = now.h, rows = now.rows;
-    const int row0 = now.row0;
 
     // ---- query fragments, and what each column (query row) sees
     uint32_t qf[NT == 1 ? KS : 1][2];
@@ -492,8 +513,9 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
       float x[D / 4];
       float amax = 0.0f;
       if (r < rows) {
-        const int rr = row0 + r, i = rr / p.G;
-        const __nv_bfloat16* src = p.q + (s.first + i) * p.q_stride + (h * p.G + rr - i * p.G) * D + t * (D / 4);
+        const int tok = now.map.token(p, r);
+        const __nv_bfloat16* src =
+            p.q + (s.first + tok) * p.q_stride + (h * p.G + now.map.head(p, r, tok)) * D + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -531,7 +553,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
       for (int c = 0; c < 2; ++c) {
         const int col = nt * 8 + 2 * t + c;
         fac[nt][c] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * c);
-        const int pos = s.len - s.n + (row0 + col) / p.G;
+        const int pos = s.len - s.n + now.map.token(p, col);
         lo[nt][c] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         hi[nt][c] = col < rows ? (p.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
@@ -739,7 +761,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
       }
     }
     if constexpr (C::TEAM) {  // the warps' results meet in the rings' room
-      team_join<D, NT, C>(p, smem, s_team, acc, ref, room, sum, s, h, row0, rows);
+      team_join<D, NT, C>(p, smem, s_team, acc, ref, room, sum, s, h, now.map, rows);
       return;  // the CTA's only one
     }
 
@@ -765,8 +787,8 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         const float m = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
         if (r >= rows) continue;
         if (pieces == 1) {
-          const int rr = row0 + r, i = rr / p.G;
-          const int64_t at_row = static_cast<int64_t>(s.first + i) * p.Hq + h * p.G + rr - i * p.G;
+          const int tok = now.map.token(p, r);
+          const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + now.map.head(p, r, tok);
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           uint32_t o[ND];
 #pragma unroll
@@ -815,6 +837,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
     const int first = m[0], row_first = m[2], n = m[3], tile = m[4], h = m[5];
     const int member = blockIdx.x * WORKERS + (slot >> 1) - first;
     const int row0 = tile * ROWS, rows = min(ROWS, n * p.G - row0);
+    RowMap map;
+    map.begin(p, row0);
     const bool together = pieces > kJoinFew;
     const int j0 = together ? pieces * warp / kJoinWarps : 0, j1 = together ? pieces * (warp + 1) / kJoinWarps : pieces;
     // rows r with r pieces / rows == member
@@ -883,8 +907,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
           for (int e = 0; e < E; ++e) o[e] += s_part[w][lane * E + e] * f;
         }
       }
-      const int rr = row0 + r, i = rr / p.G;
-      const int64_t at_row = static_cast<int64_t>(row_first + i) * p.Hq + h * p.G + rr - i * p.G;
+      const int tok = map.token(p, r);
+      const int64_t at_row = static_cast<int64_t>(row_first + tok) * p.Hq + h * p.G + map.head(p, r, tok);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
       for (int e = 0; e < E; e += 2)

@@ -183,9 +183,8 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     const Target to = target<C>(p, w, chunk, blockIdx.x);
     const bool pair = w.rows > C::HALF;  // the halves hold different rows
     const int ri = pair ? half * C::HALF + r : r;
-    const int rr = w.row0 + ri;
     const bool valid = ri < w.rows;
-    const int in_seq = rr / p.G, head = w.h * p.G + rr - in_seq * p.G;
+    const int in_seq = w.map.token(p, ri), head = w.h * p.G + w.map.head(p, ri, in_seq);
     const int64_t tok = s.first + in_seq;
     const int64_t q_at = tok * p.q_stride + static_cast<int64_t>(head) * D;
     const int64_t out_row = tok * p.Hq + head;
