@@ -186,6 +186,13 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (r >> 1) * 128 + (((r ^ (r >> 1)) & 1) << 6) + ((c ^ ((r >> 1) & 2)) << 4);
 }
 
+// a / b of numbers that are nearly always below 2^32 (a 64-bit division takes
+// several times as long, and the first tile waits for some of these).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // A sequence's share of the work.
 struct SeqWork {
   CacheSeq s;
@@ -241,7 +248,7 @@ __device__ __forceinline__ void schedule(const CacheFwdParams& p, Schedule<C>& s
     total += sh.scan[w];
   }
   const int64_t workers = static_cast<int64_t>(gridDim.x) * C::WORKERS;
-  chunk = max((total + workers - 1) / workers, p.no_split ? (int64_t)1 : (int64_t)C::RUN_STEPS);
+  chunk = max(quotient(total + workers - 1, workers), p.no_split ? (int64_t)1 : (int64_t)C::RUN_STEPS);
 #pragma unroll 1
   for (int w = 0; w < C::WORKERS; ++w) {
     const int64_t from = chunk * (static_cast<int64_t>(blockIdx.x) * C::WORKERS + w);
@@ -276,9 +283,9 @@ struct Walk {
   __device__ __forceinline__ void begin(const CacheFwdParams& p, int seq, int64_t base, int64_t at) {
     b = seq;
     w = seq_work<C>(p, b);
-    const int64_t cost = C::TEAM ? 1 : w.steps + C::START, seg = (at - base) / cost;
+    const int64_t cost = C::TEAM ? 1 : w.steps + C::START, seg = quotient(at - base, cost);
     start = base + seg * cost;
-    tile = static_cast<int>(seg / p.cache.H);
+    tile = static_cast<int>(quotient(seg, p.cache.H));
     h = static_cast<int>(seg - static_cast<int64_t>(tile) * p.cache.H);
   }
   __device__ __forceinline__ void next(const CacheFwdParams& p) {
@@ -413,6 +420,16 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
   Walk<C> ahead;
   ahead.begin(p, sh.seq[self], sh.base[self], at);
   Walk<C> now = ahead;
+  if (now.enter(p, at, stop)) {  // the first segment's queries come while its first tiles are looked up
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (nt * 8 + g < now.rows) {
+        const int r = nt * 8 + g, tok = now.map.token(p, r);
+        const __nv_bfloat16* src =
+            p.q + (now.w.s.first + tok) * p.q_stride + (now.h * p.G + now.map.head(p, r, tok)) * D + t * (D / 4);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+      }
+  }
   int ahead_u = 0;
   bool ahead_more = false;
   // its next step: page of each tile, -1: nothing to read
@@ -767,8 +784,8 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
 
     // ---- the segment's result, or this run's part of it
     const int64_t unit0 = now.start + C::START;
-    const int first = static_cast<int>(unit0 / chunk);
-    const int pieces = p.no_split ? 1 : static_cast<int>((unit0 + now.w.steps - 1) / chunk) - first + 1;
+    const int first = p.no_split ? 0 : static_cast<int>(quotient(unit0, chunk));
+    const int pieces = p.no_split ? 1 : static_cast<int>(quotient(unit0 + now.w.steps - 1, chunk)) - first + 1;
     const int slot = first == worker ? 1 : 0;
     float* part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * C::ROWS * (D + 2);
     if (pieces > 1 && lane == 0) {
@@ -844,7 +861,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
     // rows r with r pieces / rows == member
     const int r0 = (member * rows + pieces - 1) / pieces, r1 = ((member + 1) * rows + pieces - 1) / pieces;
 #pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
+    for (int r = r0 + blockIdx.y; r < r1; r += gridDim.y) {  // segments of many rows have several blocks
       if (!together && task++ % kJoinWarps != warp) continue;
       float ref = -INFINITY, l = 0.0f, o[E] = {};
 #pragma unroll 1

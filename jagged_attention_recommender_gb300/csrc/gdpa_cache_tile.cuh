@@ -48,7 +48,7 @@ struct TileCfg {
   static constexpr int D = D_;
   static constexpr bool TEAM = false;
   static constexpr int THREADS = 640, WORKERS = 1;  // five warpgroups
-  static constexpr int START = 3, RUN_STEPS = 8;
+  static constexpr int START = 8, RUN_STEPS = 12;
   static constexpr int HALF = 128, ROWS = 2 * HALF, SPAN = 64;
   static constexpr int CTAS = 1;
   static constexpr int Q_CHUNK = HALF * 128, KV_CHUNK = SPAN * 128;  // 64 columns of a tile
@@ -151,8 +151,8 @@ template <class C>
 __device__ __forceinline__ Target target(const CacheFwdParams& p, const split::Walk<C>& w, int64_t chunk, int worker) {
   Target r;
   const int64_t unit0 = w.start + C::START;
-  const int first = static_cast<int>(unit0 / chunk);
-  r.pieces = p.no_split ? 1 : static_cast<int>((unit0 + w.w.steps - 1) / chunk) - first + 1;
+  const int first = p.no_split ? 0 : static_cast<int>(split::quotient(unit0, chunk));
+  r.pieces = p.no_split ? 1 : static_cast<int>(split::quotient(unit0 + w.w.steps - 1, chunk)) - first + 1;
   const int slot = first == worker ? 1 : 0;
   r.part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * C::ROWS * (C::D + 2);
   if (r.pieces > 1 && threadIdx.x == 0) {
@@ -246,93 +246,123 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         if (live) {
           const int kb = w.w.kbase + (w.u0 + i) * C::SPAN;
           const uint32_t s_addr = tmem + lane_off + C::TM_S + half * 128 + sb * 64;
-          uint32_t sr[64];
-          ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
           const float4 sk = *reinterpret_cast<const float4*>(&notes.k_scale[gi & 7]);
           const int e_now = notes.exponent[gi & 7];
           float f[4] = {fac * sk.x, fac * sk.y, fac * sk.z, fac * sk.w};
           const uint32_t gone = (sk.x < 0.0f) | (sk.y < 0.0f) << 1 | (sk.z < 0.0f) << 2 | (sk.w < 0.0f) << 3;  // blocks on no page
-          ptx::tmem_wait_ld_r64(sr);
-          float mx = -INFINITY;
           const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN || gone != 0 || !fold;
-          if (!edge) {
+          // Weights against the present reference, in one pass: nearly always
+          // no score exceeds it by 15 and nothing else has to move.
+          bool redo = edge || m == -INFINITY || (mine > 0 && e_now != exponent);
+          if (!__all_sync(0xffffffffu, redo)) {
+            uint32_t sr[64], pk[32];
+            ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            ptx::tmem_wait_ld_r64(sr);
+            const float neg = -m;
+            float mx[2] = {-INFINITY, -INFINITY};
+            uint64_t add[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float a = __uint_as_float(sr[16 * j]), c = __uint_as_float(sr[16 * j + 1]);
+            for (int u = 0; u < 32; ++u) {
+              const float a = fmaf(__uint_as_float(sr[2 * u]), f[u >> 3], neg);
+              const float c = fmaf(__uint_as_float(sr[2 * u + 1]), f[u >> 3], neg);
+              mx[u & 1] = ptx::max3(mx[u & 1], a, c);
+              const float x = ptx::ex2_approx(a), y = ptx::ex2_approx(c);
+              add[u & 1] = ptx::f2_add(add[u & 1], ptx::f2_pack(x, y));
+              pk[u] = split::pack_f16x2(x, y);
+            }
+            redo |= fmaxf(mx[0], mx[1]) > 15.0f;
+            if (!__any_sync(0xffffffffu, redo)) {
+              float x, y;
+              ptx::f2_unpack(ptx::f2_add(add[0], add[1]), x, y);
+              l += x + y;
+              ptx::tmem_st32(s_addr, pk);
+            }
+          }
+          if (__any_sync(0xffffffffu, redo)) {  // the largest score first (S is still there)
+            uint32_t sr[64];
+            ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            ptx::tmem_wait_ld_r64(sr);
+            float mx = -INFINITY;
+            if (!edge) {
 #pragma unroll
-              for (int u = 2; u < 16; u += 4) {
-                a = ptx::max3(a, __uint_as_float(sr[16 * j + u]), __uint_as_float(sr[16 * j + u + 1]));
-                if (u + 3 < 16) c = ptx::max3(c, __uint_as_float(sr[16 * j + u + 2]), __uint_as_float(sr[16 * j + u + 3]));
+              for (int j = 0; j < 4; ++j) {
+                float a = __uint_as_float(sr[16 * j]), c = __uint_as_float(sr[16 * j + 1]);
+#pragma unroll
+                for (int u = 2; u < 16; u += 4) {
+                  a = ptx::max3(a, __uint_as_float(sr[16 * j + u]), __uint_as_float(sr[16 * j + u + 1]));
+                  if (u + 3 < 16) c = ptx::max3(c, __uint_as_float(sr[16 * j + u + 2]), __uint_as_float(sr[16 * j + u + 3]));
+                }
+                mx = fmaxf(mx, fmaxf(a, c) * f[j]);
               }
-              mx = fmaxf(mx, fmaxf(a, c) * f[j]);
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int u = 0; u < 64; ++u) {
-              float x = __uint_as_float(sr[u]) * f[u >> 4];
-              const int key = kb + u;
-              if (key < lo || key >= hi || (gone >> (u >> 4) & 1)) x = -INFINITY;
-              sr[u] = __float_as_uint(x);
-              mx = fmaxf(mx, x);
-            }
+              for (int u = 0; u < 64; ++u) {
+                float x = __uint_as_float(sr[u]) * f[u >> 4];
+                const int key = kb + u;
+                if (key < lo || key >= hi || (gone >> (u >> 4) & 1)) x = -INFINITY;
+                sr[u] = __float_as_uint(x);
+                mx = fmaxf(mx, x);
+              }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = 1.0f;
-          }
-          // the reference moves when a score exceeds it by 15, to 7 below it;
-          // the output follows, once P V of the last tile is in (where nothing
-          // was added yet there is nothing to follow)
-          float alpha = 1.0f;
-          bool follow = false;
-          if (mx > m + 15.0f || m == -INFINITY) {
-            const float up = fmaxf(m, mx - 7.0f);
-            alpha = m == -INFINITY ? 0.0f : ptx::ex2_approx(m - up);
-            follow = mine > 0 && l != 0.0f;
-            l *= alpha;
-            m = up;
-          }
-          if (mine > 0 && e_now != exponent) {  // so it does V's exponent
-            alpha *= exponent - e_now < -126 ? 0.0f : sf_value(127 + exponent - e_now);
-            follow = l != 0.0f || follow;
-          }
-          exponent = e_now;
-          if (__any_sync(0xffffffffu, follow)) {
-            // S of this tile came after P V of this half's tile before the
-            // last (its P is in the same buffer), so that pv_done is in the
-            // phase waited for, or has left it
-            ok = ptx::mbar_wait(&B.pv_done[half], (ti - 1) & 1, limit, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after();
+              for (int j = 0; j < 4; ++j) f[j] = 1.0f;
+            }
+            // the reference moves when a score exceeds it by 15, to 7 below it;
+            // the output follows, once P V of the last tile is in (where nothing
+            // was added yet there is nothing to follow)
+            float alpha = 1.0f;
+            bool follow = false;
+            if (mx > m + 15.0f || m == -INFINITY) {
+              const float up = fmaxf(m, mx - 7.0f);
+              alpha = m == -INFINITY ? 0.0f : ptx::ex2_approx(m - up);
+              follow = mine > 0 && l != 0.0f;
+              l *= alpha;
+              m = up;
+            }
+            if (mine > 0 && e_now != exponent) {  // so it does V's exponent
+              alpha *= exponent - e_now < -126 ? 0.0f : sf_value(127 + exponent - e_now);
+              follow = l != 0.0f || follow;
+            }
+            exponent = e_now;
+            if (__any_sync(0xffffffffu, follow)) {
+              // S of this tile came after P V of this half's tile before the
+              // last (its P is in the same buffer), so that pv_done is in the
+              // phase waited for, or has left it
+              ok = ptx::mbar_wait(&B.pv_done[half], (ti - 1) & 1, limit, abort);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              ptx::tmem_ld16(o_addr + c, o);
-              ptx::tmem_wait_ld();
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld16(o_addr + c, o);
+                ptx::tmem_wait_ld();
 #pragma unroll
-              for (int u = 0; u < 16; ++u)
-                if (follow) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-              ptx::tmem_st16(o_addr + c, o);
+                for (int u = 0; u < 16; ++u)
+                  if (follow) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                ptx::tmem_st16(o_addr + c, o);
+              }
             }
-          }
-          const float neg = m == -INFINITY ? 0.0f : -m;
-          uint64_t add[2] = {0, 0};
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            uint64_t add[2] = {0, 0};
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint32_t pk[16];
+            for (int part = 0; part < 2; ++part) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const int v = 16 * part + u;
-              const float a = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v]), f[v >> 3], neg));
-              const float c = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v + 1]), f[v >> 3], neg));
-              add[u & 1] = ptx::f2_add(add[u & 1], ptx::f2_pack(a, c));
-              pk[u] = split::pack_f16x2(a, c);
+              for (int u = 0; u < 16; ++u) {
+                const int v = 16 * part + u;
+                const float a = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v]), f[v >> 3], neg));
+                const float c = ptx::ex2_approx(fmaf(__uint_as_float(sr[2 * v + 1]), f[v >> 3], neg));
+                add[u & 1] = ptx::f2_add(add[u & 1], ptx::f2_pack(a, c));
+                pk[u] = split::pack_f16x2(a, c);
+              }
+              ptx::tmem_st16(s_addr + 16 * part, pk);
             }
-            ptx::tmem_st16(s_addr + 16 * part, pk);
+            float x, y;
+            ptx::f2_unpack(ptx::f2_add(add[0], add[1]), x, y);
+            l += x + y;
           }
-          float x, y;
-          ptx::f2_unpack(ptx::f2_add(add[0], add[1]), x, y);
-          l += x + y;
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
