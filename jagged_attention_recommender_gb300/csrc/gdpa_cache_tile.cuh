@@ -713,13 +713,13 @@ struct Pending {
   int first[2];        // the half's first in this segment
 };
 template <int D>
-__device__ __forceinline__ bool issue_pv(Bars& B, uint8_t* sm, uint32_t tmem, const Pending& t,
+__device__ __forceinline__ bool issue_pv(Bars& B, uint64_t v_desc, uint32_t tmem, const Pending& t,
                                          unsigned long long limit) {
   using C = TileCfg<D>;
   const int vs = t.gi & 1;
   volatile int* abort = &B.abort;
   if (!ptx::mbar_wait(&B.v_full[vs], (t.gi >> 1) & 1, limit, abort)) return false;
-  const uint32_t v_base = ptx::smem_u32(sm + C::OFF_V + vs * C::KV_BYTES);
+  const uint64_t v = v_desc + vs * (C::KV_BYTES >> 4);
   constexpr uint32_t idesc = ptx::idesc_f16(128, D, 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -731,7 +731,7 @@ __device__ __forceinline__ bool issue_pv(Bars& B, uint8_t* sm, uint32_t tmem, co
     for (int kk = 0; kk < C::SPAN / 16; ++kk)
       // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
       ptx::mma_ts_elect(tmem + C::TM_O + h * 128, tmem + C::TM_S + h * 128 + sb * 64 + 8 * kk,
-                        ptx::sdesc_sw128(v_base + kk * 2048, C::KV_CHUNK, 1024), idesc, t.first[h] && kk == 0 ? 0u : 1u);
+                        v + (kk * 2048 >> 4), idesc, kk > 0 ? 1u : t.first[h] ? 0u : 1u);
     ptx::mma_commit_elect(&B.pv_done[h]);
   }
   ptx::mma_commit_elect(&B.v_free[vs]);
@@ -747,7 +747,12 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
   w.begin(p, sh.seq[0], sh.base[0], at);
   uint32_t gi = 0, seg = 0, ti[2] = {0, 0};
   bool ok = true;
-  const uint32_t q_base = ptx::smem_u32(sm);
+  // Descriptors of the first tiles: all others are a constant further on (the
+  // address field counts 16 bytes and has room).  This warp's instructions are
+  // a tile's critical path, so none of them is a descriptor's making.
+  const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
+  const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm + C::OFF_K), 16, 1024);
+  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm + C::OFF_V), C::KV_CHUNK, 1024);
   constexpr uint32_t idesc = ptx::idesc_f16(128, C::SPAN, 0);
 #pragma unroll 1
   for (; ok && w.more(p, stop); w.next(p)) {
@@ -764,7 +769,7 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
       ok = ptx::mbar_wait(&B.k_full[ks], (gi >> 1) & 1, limit, abort);
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t k_base = ptx::smem_u32(sm + C::OFF_K + ks * C::KV_BYTES);
+      const uint64_t k = k_desc + ks * (C::KV_BYTES >> 4);
       Pending now = {gi, pair ? 3 : 1 << (i & 1), {ti[0], ti[1]}, {i < (pair ? 1 : 2), i < (pair ? 1 : 2)}};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -773,19 +778,18 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           ptx::mma_ss_elect(tmem + C::TM_S + h * 128 + sb * 64,
-                            ptx::sdesc_sw128(q_base + h * C::Q_BYTES + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32, 16, 1024),
-                            ptx::sdesc_sw128(k_base + (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32, 16, 1024), idesc,
-                            kk > 0 ? 1u : 0u);
+                            q_desc + ((h * C::Q_BYTES + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32) >> 4),
+                            k + (((kk >> 2) * C::KV_CHUNK + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
         ptx::mma_commit_elect(&B.s_full[h][sb]);
         ++ti[h];
       }
       ptx::mma_commit_elect(&B.k_free[ks]);
-      if (pair ? i > 0 : i > 1) ok = issue_pv<D>(B, sm, tmem, pair ? last : older, limit);
+      if (pair ? i > 0 : i > 1) ok = issue_pv<D>(B, v_desc, tmem, pair ? last : older, limit);
       older = last;
       last = now;
     }
-    if (ok && !pair && steps > 1) ok = issue_pv<D>(B, sm, tmem, older, limit);
-    if (ok) ok = issue_pv<D>(B, sm, tmem, last, limit);
+    if (ok && !pair && steps > 1) ok = issue_pv<D>(B, v_desc, tmem, older, limit);
+    if (ok) ok = issue_pv<D>(B, v_desc, tmem, last, limit);
     ptx::mma_commit_elect(&B.o_full);
   }
   if (!ok && (threadIdx.x & 31) == 0) {
