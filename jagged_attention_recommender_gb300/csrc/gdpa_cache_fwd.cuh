@@ -34,6 +34,8 @@
 // keys: results do not depend on timing.
 #pragma once
 
+#include <type_traits>
+
 #include "gdpa_cache.cuh"
 
 namespace gdpa {
@@ -87,18 +89,13 @@ struct SplitCfg {
   static constexpr int RUN_STEPS = 6;               // the fewest steps (starts included) that are worth a part
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
-#ifndef XNB
-#define XNB 2
-#define XS (D == 64 ? 2 : 3)
-#define XC (D == 64 ? 3 : 2)
-#endif
-  static constexpr int NB = NT == 1 ? XNB : 1;     // 16-key tiles of a step
+  static constexpr int NB = NT == 1 ? 2 : 1;  // 16-key tiles of a step
   static constexpr int SPAN = NB * kCacheBlock;
   // CTAs an SM, and ring stages: enough tiles in flight to cover the memory's
   // latency (an SM's share of 6.8 TB/s is 45 KB a microsecond) at the
   // registers that the accumulators leave
-  static constexpr int CTAS = TEAM ? 1 : NT == 1 ? XC : NT == 2 ? 3 : 2;
-  static constexpr int STAGES = NT == 1 ? (D == 64 ? (2 * XS * XNB > 8 ? 8 / XNB : 2 * XS) : XS) : D == 64 ? 6 : NT == 2 ? 3 : 4;
+  static constexpr int CTAS = TEAM ? 1 : NT == 1 ? (D == 64 ? 3 : 2) : NT == 2 ? 3 : 2;
+  static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 6) : NT == 4 ? 4 : 3;
   static_assert(STAGES * NB <= 8, "a nibble of state for each tile of the ring");
   static constexpr int STAGE = NB * 2 * TILE;
   static constexpr int RING = STAGES * STAGE;      // of a warp
@@ -336,7 +333,7 @@ struct Walk {
 template <int D, int NT, class C>
 __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem,
                                           float (&s_team)[C::WARPS][C::ROWS][2],
-                                          const float (&acc)[D / 16][NT][4], const float (&ref)[NT][2],
+                                          const float (&acc)[D / 16][NT][4], float unit, const float (&ref)[NT][2],
                                           const float (&room)[NT][2], const float (&sum)[NT][2], const CacheSeq& s,
                                           int h, const RowMap& map, int rows) {
   static_assert(C::WARPS * C::ROWS * D * 4 <= C::WARPS * C::RING, "the rings hold the outputs");
@@ -357,7 +354,8 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
       float4* dst = reinterpret_cast<float4*>(merge + (warp * C::ROWS + r) * D + g * (D / 8));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        dst[i] = make_float4(acc[2 * i][nt][c], acc[2 * i][nt][c + 2], acc[2 * i + 1][nt][c], acc[2 * i + 1][nt][c + 2]);
+        dst[i] = make_float4(acc[2 * i][nt][c] * unit, acc[2 * i][nt][c + 2] * unit, acc[2 * i + 1][nt][c] * unit,
+                             acc[2 * i + 1][nt][c + 2] * unit);
     }
   __syncthreads();
   for (int i = tid; i < rows * (D / 8); i += C::THREADS) {
@@ -434,6 +432,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
   bool ahead_more = false;
   // its next step: page of each tile, -1: nothing to read
   int page_next[C::NB];
+  bool whole = false;  // all of the step is there, and in one page
   auto look = [&]() {
     while (!ahead_more || ahead_u >= ahead.u1) {
       if (ahead_more) ahead.next(p);
@@ -447,19 +446,21 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
     }
     const int kb = ahead.w.kbase + ahead_u * C::SPAN;
     const int32_t* table = bt.table + static_cast<int64_t>(ahead.b) * bt.max_pages;
+    whole = kb >= ahead.lo_min && kb <= ahead.hi_max - C::SPAN && (C::NB == 1 || p.cache.lp > 4);
+    if (whole) {
+      page_next[0] = __ldg(table + (kb >> p.cache.lp));
+      whole = static_cast<unsigned>(page_next[0]) < static_cast<unsigned>(p.cache.num_pages);
+      if (whole) return;
+    }
 #pragma unroll
     for (int n = 0; n < C::NB; ++n) {
       const int k = kb + n * kCacheBlock;
       page_next[n] = -1;
       if (k < ahead.hi_max && k + kCacheBlock > ahead.lo_min) {
-        if (n > 0 && p.cache.lp > 4 && page_next[0] >= 0) {  // a step lies in one page, unless pages are single tiles
-          page_next[n] = page_next[0];
-        } else {
-          page_next[n] = __ldg(table + (k >> p.cache.lp));
-          if (page_next[n] < 0 || page_next[n] >= p.cache.num_pages) {
-            if (lane == 0) atomicOr(bt.status, kStatusBadPlan);
-            page_next[n] = -1;
-          }
+        page_next[n] = __ldg(table + (k >> p.cache.lp));
+        if (page_next[n] < 0 || page_next[n] >= p.cache.num_pages) {
+          if (lane == 0) atomicOr(bt.status, kStatusBadPlan);
+          page_next[n] = -1;
         }
       }
     }
@@ -467,41 +468,57 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
   // A nibble for each tile of the ring: bit 0 the tile is there, bits 1-2
   // which byte of its words the scale codes are.
   uint32_t state = 0;
+  const uint32_t chunk_at = tile_at<D>(lane / (D / 16), lane % (D / 16));  // of this lane's first 16 bytes of a tile
   auto issue = [&](int stage) {
-    state &= ~(((1u << 4 * C::NB) - 1) << (stage * 4 * C::NB));
+    constexpr uint32_t nibbles = C::NB == 2 ? 0x11u : 1u;
+    state &= ~(15u * nibbles << (stage * 4 * C::NB));
     if (ahead_more) {
       const int kb = ahead.w.kbase + ahead_u * C::SPAN;
       const uint32_t dst = ring + stage * C::STAGE;
-#pragma unroll
-      for (int n = 0; n < C::NB; ++n) {
-        const int page = page_next[n], slot = (kb + n * kCacheBlock) & pmask;
-        const int valid = page >= 0 ? ahead.w.s.len - (kb + n * kCacheBlock) : 0;
-        const int64_t row = cache_row(p.cache, max(page, 0), ahead.h, slot);
+      if (whole) {
+        const int64_t row = cache_row(p.cache, page_next[0], ahead.h, kb & pmask);
         const uint8_t* ks = p.cache.k + row * D + lane * 16;
         const uint8_t* vs = p.cache.v + row * D + lane * 16;
-        const uint32_t kd = dst + n * 2 * C::TILE, vd = kd + C::TILE;
-        if (valid >= kCacheBlock) {
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n)
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
-            cp_async16(kd + tile_at<D>(r, c), ks + 512 * j, 16);
-            cp_async16(vd + tile_at<D>(r, c), vs + 512 * j, 16);
+            // 32 chunks further on: as many rows, and the same permutation
+            // (or another one, which is a constant too)
+            const uint32_t to = dst + n * 2 * C::TILE + (D == 128 ? (chunk_at ^ (j & 1) * 64) : chunk_at) + j * 512;
+            cp_async16(to, ks + (n * kCacheBlock * D + 512 * j), 16);
+            cp_async16(to + C::TILE, vs + (n * kCacheBlock * D + 512 * j), 16);
           }
-        } else {  // rows that are not stored: zeros
+        const int64_t block = row >> 4, word = block & ~(int64_t)3;
+        // (a step's second block is in the same word: its first one is even)
+        state |= (nibbles + (nibbles * (static_cast<uint32_t>(block & 3) << 1)) + (C::NB == 2 ? 0x20u : 0u))
+                 << (stage * C::NB * 4);
+        if (lane < 2 * C::NB)
+          cp_async4(sf_at + (stage * 2 * C::NB + lane) * 4, ((lane & 1) ? p.cache.v_sf : p.cache.k_sf) + word,
+                    static_cast<int>(min((int64_t)4, sf_bytes - word)));
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < C::NB; ++n) {
+          const int page = n == 0 ? page_next[0] : page_next[C::NB - 1], slot = (kb + n * kCacheBlock) & pmask;
+          const int valid = page >= 0 ? ahead.w.s.len - (kb + n * kCacheBlock) : 0;
+          const int64_t row = cache_row(p.cache, max(page, 0), ahead.h, slot);
+          const uint8_t* ks = p.cache.k + row * D + lane * 16;
+          const uint8_t* vs = p.cache.v + row * D + lane * 16;
+          const uint32_t kd = dst + n * 2 * C::TILE, vd = kd + C::TILE;
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
+          for (int j = 0; j < D / 32; ++j) {  // rows that are not stored: zeros
             const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
             const int bytes = r < valid ? 16 : 0;
             cp_async16(kd + tile_at<D>(r, c), ks + 512 * j, bytes);
             cp_async16(vd + tile_at<D>(r, c), vs + 512 * j, bytes);
           }
-        }
-        if (page >= 0) {
-          const int64_t block = row >> 4, word = block & ~(int64_t)3;
-          state |= (1u | static_cast<uint32_t>(block & 3) << 1) << ((stage * C::NB + n) * 4);
-          if (lane >> 1 == n)  // lanes 2n and 2n + 1: K's word and V's
-            cp_async4(sf_at + (stage * 2 * C::NB + lane) * 4, ((lane & 1) ? p.cache.v_sf : p.cache.k_sf) + word,
-                      static_cast<int>(min((int64_t)4, sf_bytes - word)));
+          if (page >= 0) {
+            const int64_t block = row >> 4, word = block & ~(int64_t)3;
+            state |= (1u | static_cast<uint32_t>(block & 3) << 1) << ((stage * C::NB + n) * 4);
+            if (lane >> 1 == n)  // lanes 2n and 2n + 1: K's word and V's
+              cp_async4(sf_at + (stage * 2 * C::NB + lane) * 4, ((lane & 1) ? p.cache.v_sf : p.cache.k_sf) + word,
+                        static_cast<int>(min((int64_t)4, sf_bytes - word)));
+          }
         }
       }
       ahead_u += stride;
@@ -582,6 +599,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
     // the softmax's reference of each column, and by how much a score may
     // exceed it (not at all while there is none)
     float ref[NT][2], room[NT][2], sum[NT][2];
+    int vexp = -1;  // the output is in units of 2^(vexp - 127)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -592,19 +610,10 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.0f;
     }
 
-#pragma unroll 1
-    for (int u = now.u0 + skip; u < now.u1; u += stride) {
-      cp_wait<C::STAGES - 2>();
-      __syncwarp();
-      issue(stage == 0 ? C::STAGES - 1 : stage - 1);
-      const uint32_t kt = ring + stage * C::STAGE;
-      const int cur = stage;
-      const uint32_t there = state >> (cur * 4 * C::NB);
-      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-      const uint32_t all = C::NB == 2 ? 0x11u : 1u;
-      if ((there & all) == 0) continue;
-      const int kb = now.w.kbase + u * C::SPAN;
-
+    // One step's products and softmax; EDGE: some of its keys are hidden from
+    // some of the rows, or a tile is not there.
+    auto compute = [&](auto edge_tag, const uint32_t kt, const int cur, const uint32_t there, const int kb) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
       // S^T = K Q^T: rows g and g + 8 are keys, columns 2t and 2t + 1 queries
       float st[C::NB][NT][4];
 #pragma unroll
@@ -637,24 +646,24 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         }
 
       // scores in units of log2, less the reference; hidden keys -inf; does
-      // one leave the range?
-      const bool edge = kb < lo_max || kb > hi_min - C::SPAN || (there & all) != all;
-      float sv[C::NB];
+      // one leave the range, or a scale of V the output's units?
+      int sv[C::NB];
       bool over = false;
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) {
         uint32_t kw, vw;
         lds64(sf_at + (cur * C::NB + n) * 8, kw, vw);
-        const bool here = there >> (4 * n) & 1;
+        const bool here = !EDGE || (there >> (4 * n) & 1);
         const int byte = (there >> (4 * n) & 6) * 4;
         const float sk = sf_value(here ? kw >> byte & 0xff : 127);
-        sv[n] = sf_value(here ? vw >> byte & 0xff : 127);
+        sv[n] = here ? vw >> byte & 0xff : max(vexp, 0);
+        over |= sv[n] > vexp;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float x = fmaf(st[n][nt][c], fac[nt][c & 1] * sk, -ref[nt][c & 1]);
-            if (edge) {
+            if (EDGE) {
               const int key = kb + n * kCacheBlock + g + (c & 2) * 4;
               if (key < lo[nt][c & 1] || key >= hi[nt][c & 1] || !here) x = -INFINITY;
             }
@@ -663,6 +672,15 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           }
       }
       if (__any_sync(0xffffffffu, over)) {
+        // V's units: one above the largest scale, so that they seldom move
+        int top_sv = sv[0];
+        if (C::NB == 2) top_sv = max(top_sv, sv[C::NB - 1]);
+        float turn = 1.0f;
+        if (top_sv > vexp) {
+          const int up = min(top_sv + 1, 254);
+          turn = vexp < 0 ? 0.0f : up - vexp > 126 ? 0.0f : sf_value(127 - (up - vexp));
+          vexp = up;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -673,23 +691,29 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const bool none = room[nt][c] == -INFINITY;
-            const float up = none ? (top == -INFINITY ? 0.0f : top - 7.0f) : fmaxf(top - 7.0f, 0.0f);
+            // (the column's reference stays unless a score of it has left the range)
+            const bool none = room[nt][c] == -INFINITY, move = top > room[nt][c];
+            const float up = !move ? 0.0f : none ? top - 7.0f : fmaxf(top - 7.0f, 0.0f);
             const float keep = none ? 0.0f : ptx::ex2_approx(-up);
-            if (top != -INFINITY) room[nt][c] = 15.0f;
+            if (move) room[nt][c] = 15.0f;
             ref[nt][c] += up;
             sum[nt][c] *= keep;
+            const float keep_o = keep * turn;
 #pragma unroll
             for (int n = 0; n < C::NB; ++n) st[n][nt][c] -= up, st[n][nt][c + 2] -= up;
 #pragma unroll
             for (int i2 = 0; i2 < ND; ++i2) {
-              acc[i2][nt][c] *= keep;
-              acc[i2][nt][c + 2] *= keep;
+              acc[i2][nt][c] *= keep_o;
+              acc[i2][nt][c + 2] *= keep_o;
             }
           }
       }
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) {
+        // a scale up to 2^6 below the units goes into the weights
+        const int below = vexp - sv[n];
+        const bool near = below <= 6;
+        const float unit = sf_value(127 - (near ? below : 0));
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -697,8 +721,8 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           const float p2 = ptx::ex2_approx(st[n][nt][2]), p3 = ptx::ex2_approx(st[n][nt][3]);
           sum[nt][0] += p0 + p2;
           sum[nt][1] += p1 + p3;
-          pb[nt][0] = transpose8x8(pack_f16x2(p0, p1));
-          pb[nt][1] = transpose8x8(pack_f16x2(p2, p3));
+          pb[nt][0] = transpose8x8(pack_f16x2(p0 * unit, p1 * unit));
+          pb[nt][1] = transpose8x8(pack_f16x2(p2 * unit, p3 * unit));
         }
 
         // O^T += V^T P^T: lane (g, t) holds D/8 coordinates of tokens 2t, 2t+1, 2t+8, 2t+9
@@ -719,8 +743,9 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         // At an edge a token may be hidden from some rows only, and 0 times a
         // NaN value is NaN: such a tile is added token by token to the rows
         // that see it.  Tokens hidden from all rows are cleared.
-        bool by_token = false;
-        if (edge) {
+        bool apart = !near;
+        int tokens = 1;  // products that a tile apart takes
+        if (EDGE) {
           bool nan = false;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -731,9 +756,9 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
               nan |= has_nan_code(v[j][w]);
             }
           }
-          by_token = __any_sync(0xffffffffu, nan);
+          if (__any_sync(0xffffffffu, nan)) apart = true, tokens = kCacheBlock;
         }
-        if (!by_token) {
+        if (!apart) {
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
@@ -742,24 +767,22 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
               const uint32_t x23 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
               const uint32_t a0 = codes_lo(x01), a1 = codes_hi(x01), a2 = codes_lo(x23), a3 = codes_hi(x23);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float o[4];
-                mma_f16_new(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[2 * w + half][nt][c] = fmaf(o[c], sv[n], acc[2 * w + half][nt][c]);
-              }
+              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
             }
         } else {
+          // what the weights do not hold of the scale, as a factor of the product
+          const float rest = near ? 1.0f : sf_value(127 - (below >> 1)) * sf_value(127 - (below - (below >> 1)));
 #pragma unroll 1
-          for (int k = 0; k < kCacheBlock; ++k) {
+          for (int k = 0; k < tokens; ++k) {
             const int key = kb + n * kCacheBlock + k;
+            const bool one = tokens > 1;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 uint32_t y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = 2 * t + (j & 1) + (j & 2) * 4 == k ? v[j][w] : 0;
+                for (int j = 0; j < 4; ++j) y[j] = !one || 2 * t + (j & 1) + (j & 2) * 4 == k ? v[j][w] : 0;
                 const uint32_t x01 = __byte_perm(y[0], y[1], half ? 0x7362 : 0x5140);
                 const uint32_t x23 = __byte_perm(y[2], y[3], half ? 0x7362 : 0x5140);
                 const uint32_t a0 = codes_lo(x01), a1 = codes_hi(x01), a2 = codes_lo(x23), a3 = codes_hi(x23);
@@ -769,16 +792,35 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
                   mma_f16_new(o, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
 #pragma unroll
                   for (int c = 0; c < 4; ++c)
-                    if (key >= lo[nt][c & 1] && key < hi[nt][c & 1])
-                      acc[2 * w + half][nt][c] = fmaf(o[c], sv[n], acc[2 * w + half][nt][c]);
+                    if (!one || (key >= lo[nt][c & 1] && key < hi[nt][c & 1]))
+                      acc[2 * w + half][nt][c] = fmaf(o[c], rest, acc[2 * w + half][nt][c]);
                 }
               }
           }
         }
       }
+    };
+
+#pragma unroll 1
+    for (int u = now.u0 + skip; u < now.u1; u += stride) {
+      cp_wait<C::STAGES - 2>();
+      __syncwarp();
+      issue(stage == 0 ? C::STAGES - 1 : stage - 1);
+      const uint32_t kt = ring + stage * C::STAGE;
+      const int cur = stage;
+      const uint32_t there = state >> (cur * 4 * C::NB);
+      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      constexpr uint32_t all = C::NB == 2 ? 0x11u : 1u;
+      const int kb = now.w.kbase + u * C::SPAN;
+      if (kb >= lo_max && kb <= hi_min - C::SPAN && (there & all) == all)
+        compute(std::false_type(), kt, cur, there, kb);
+      else if ((there & all) != 0)
+        compute(std::true_type(), kt, cur, there, kb);
     }
+    // the output in its own units
+    const float unit = vexp < 0 ? 0.0f : sf_value(vexp);
     if constexpr (C::TEAM) {  // the warps' results meet in the rings' room
-      team_join<D, NT, C>(p, smem, s_team, acc, ref, room, sum, s, h, now.map, rows);
+      team_join<D, NT, C>(p, smem, s_team, acc, unit, ref, room, sum, s, h, now.map, rows);
       return;  // the CTA's only one
     }
 
@@ -809,7 +851,8 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           uint32_t o[ND];
 #pragma unroll
-          for (int i = 0; i < ND; ++i) o[i] = ptx::pack_bf16x2(acc[i][nt][c] * inv, acc[i][nt][c + 2] * inv);
+          for (int i = 0; i < ND; ++i)
+            o[i] = ptx::pack_bf16x2(acc[i][nt][c] * inv * unit, acc[i][nt][c + 2] * inv * unit);
           uint4* dst = reinterpret_cast<uint4*>(p.out + at_row * D + g * (D / 8));
 #pragma unroll
           for (int i = 0; i < ND / 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -819,8 +862,8 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           float4* dst = reinterpret_cast<float4*>(part + 2 * C::ROWS + r * D + g * (D / 8));
 #pragma unroll
           for (int i = 0; i < ND / 2; ++i)
-            dst[i] = make_float4(acc[2 * i][nt][c], acc[2 * i][nt][c + 2], acc[2 * i + 1][nt][c],
-                                 acc[2 * i + 1][nt][c + 2]);
+            dst[i] = make_float4(acc[2 * i][nt][c] * unit, acc[2 * i][nt][c + 2] * unit, acc[2 * i + 1][nt][c] * unit,
+                                 acc[2 * i + 1][nt][c + 2] * unit);
         }
       }
   }
