@@ -192,7 +192,7 @@ gdpa_status_t launch_join(const CacheFwdParams& p, int ctas, cudaStream_t s) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (C::ROWS + 31) / 32);
+  cfg.gridDim = dim3(ctas, std::max(1, C::ROWS * C::WORKERS / 32));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cfg.attrs = &early;

@@ -85,8 +85,8 @@ struct SplitCfg {
   static constexpr bool TEAM = TEAM_;
   static constexpr int WARPS = TEAM ? 8 : 4, THREADS = 32 * WARPS;
   static constexpr int WORKERS = TEAM ? 1 : WARPS;  // of a CTA: its warps, or itself
-  static constexpr int START = 2;                   // what a segment's start costs, in steps
-  static constexpr int RUN_STEPS = 6;               // the fewest steps (starts included) that are worth a part
+  static constexpr int START = NT == 1 ? 2 : NT == 2 ? 5 : 10;  // what a segment's start and end cost, in steps
+  static constexpr int RUN_STEPS = START + 4;  // the fewest steps (starts included) that are worth a part
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
   static constexpr int NB = NT == 1 ? 2 : 1;  // 16-key tiles of a step
@@ -418,16 +418,6 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
   Walk<C> ahead;
   ahead.begin(p, sh.seq[self], sh.base[self], at);
   Walk<C> now = ahead;
-  if (now.enter(p, at, stop)) {  // the first segment's queries come while its first tiles are looked up
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (nt * 8 + g < now.rows) {
-        const int r = nt * 8 + g, tok = now.map.token(p, r);
-        const __nv_bfloat16* src =
-            p.q + (now.w.s.first + tok) * p.q_stride + (now.h * p.G + now.map.head(p, r, tok)) * D + t * (D / 4);
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
-      }
-  }
   int ahead_u = 0;
   bool ahead_more = false;
   // its next step: page of each tile, -1: nothing to read
@@ -442,7 +432,19 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         ahead_more = false;
         return;
       }
-      if (ahead.enter(p, at, stop)) ahead_u = ahead.u0 + skip; else ahead_u = ahead.u1 = 0;
+      if (!ahead.enter(p, at, stop)) {
+        ahead_u = ahead.u1 = 0;
+        continue;
+      }
+      ahead_u = ahead.u0 + skip;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)  // its queries come while its first tiles do
+        if (nt * 8 + g < ahead.rows) {
+          const int r = nt * 8 + g, tok = ahead.map.token(p, r);
+          const __nv_bfloat16* src = p.q + (ahead.w.s.first + tok) * p.q_stride +
+                                     (ahead.h * p.G + ahead.map.head(p, r, tok)) * D + t * (D / 4);
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+        }
     }
     const int kb = ahead.w.kbase + ahead_u * C::SPAN;
     const int32_t* table = bt.table + static_cast<int64_t>(ahead.b) * bt.max_pages;
@@ -872,108 +874,134 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
 // Joins the parts of cut segments.  A worker is a member of up to two of them
 // (the segment that its run begins inside, slot 0, and the one it ends inside,
 // slot 1), and the members of a segment share its rows evenly; a block stands
-// for the WORKERS workers of a CTA.  Up to kJoinFew parts: a warp takes a row.
-// More: the block's warps take a row together, each a run of the parts.  All that
-// is read of up to 8 parts is under way at once: what this kernel takes is the
-// latency of two dependent reads.
+// for the WORKERS workers of a CTA and its slots are shared out to its warps, a
+// row to D / 4 lanes.  A segment of more than kJoinFew parts: the block's warps
+// take a row together, each a run of the parts.  All that is read of up to 8
+// parts is under way at once: what this kernel takes is the latency of two
+// dependent reads.  (With all warps going through all slots, a warp a row, the
+// slots' own arithmetic was most of it: 27 us after 32 candidates of 128
+// samples, which takes 12 so.)
 constexpr int kJoinWarps = 8, kJoinFew = 8;
 
 template <int D, int ROWS, int WORKERS>
 __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(const CacheFwdParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_part[kJoinWarps][D + 2];
-  __shared__ int s_meta[2 * WORKERS][8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int LANES = D / 4, SUBS = 32 / LANES;  // lanes of a row, rows of a warp
+  constexpr int SLOTS = 2 * WORKERS, SHARE = kJoinWarps / SLOTS;
+  __shared__ float s_part[kJoinWarps * SUBS][D + 4];
+  __shared__ int s_meta[SLOTS][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LANES, li = lane % LANES;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
-  if (threadIdx.x < 16 * WORKERS)
-    s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 16 * WORKERS + threadIdx.x];
+  if (threadIdx.x < 8 * SLOTS)
+    s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 8 * SLOTS + threadIdx.x];
   __syncthreads();
-  int task = 0;  // rows so far, for the warps to take in turn
+
+  // Adds parts [j, j + cnt), cnt up to 8, of a row: four coordinates a lane.
+  auto add = [&](int first, int j, int cnt, int r, float& ref, float& l, float4& o) {
+    constexpr int step = 2 * ROWS * (D + 2);
+    const float* part = p.part + static_cast<int64_t>(first + j) * step;
+    const int skip = j == 0 ? ROWS * (D + 2) : 0;  // slot 1 for the first part, 0 for the others
+    const int i8 = li & 7;
+    float2 own = make_float2(-INFINITY, 0.0f);
+    if (i8 < cnt) own = *reinterpret_cast<const float2*>(part + i8 * step + (i8 == 0 ? skip : 0) + 2 * r);
+    const float* src = part + 2 * ROWS + r * D + li * 4;
+    float4 x[kJoinFew];
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < cnt) x[i] = *reinterpret_cast<const float4*>(src + i * step + (i == 0 ? skip : 0));
+    }
+    float top = fmaxf(ref, own.x);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float zero = top == -INFINITY ? 0.0f : top;
+    const float keep = ptx::ex2_approx(ref - zero), f = ptx::ex2_approx(own.x - zero);
+    float more = own.y * f;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) more += __shfl_xor_sync(0xffffffffu, more, d);
+    ref = top;
+    l = l * keep + more;
+    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i, 8);  // (0 times 0 behind the last part)
+      o.x = fmaf(x[i].x, w, o.x), o.y = fmaf(x[i].y, w, o.y), o.z = fmaf(x[i].z, w, o.z), o.w = fmaf(x[i].w, w, o.w);
+    }
+  };
+  auto store = [&](const RowMap& map, const int* m, int r, float ref, float l, const float4& o) {
+    const int tok = map.token(p, r);
+    const int64_t at_row = static_cast<int64_t>(m[2] + tok) * p.Hq + m[5] * p.G + map.head(p, r, tok);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2*>(p.out + at_row * D + li * 4) =
+        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && li == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  };
+  // m: {first worker, pieces, first row of the sequence, its rows, row tile, head}
+  auto share_of = [&](const int* m, int slot, RowMap& map, int& r0, int& r1) {
+    const int pieces = m[1], member = blockIdx.x * WORKERS + (slot >> 1) - m[0];
+    const int row0 = m[4] * ROWS, rows = min(ROWS, m[3] * p.G - row0);
+    map.begin(p, row0);
+    r0 = (member * rows + pieces - 1) / pieces;  // rows r with r pieces / rows == member
+    r1 = ((member + 1) * rows + pieces - 1) / pieces;
+  };
+
+  {
+    const int slot = warp % SLOTS;
+    const int* m = s_meta[slot];
+    if (m[1] > 0 && m[1] <= kJoinFew) {
+      RowMap map;
+      int r0, r1;
+      share_of(m, slot, map, r0, r1);
+      const int unit = blockIdx.y * SHARE + warp / SLOTS, units = gridDim.y * SHARE;
 #pragma unroll 1
-  for (int slot = 0; slot < 2 * WORKERS; ++slot) {
+      for (int rb = r0 + unit * SUBS; rb < r1; rb += units * SUBS) {
+        const int r = min(rb + sub, r1 - 1);
+        float ref = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        add(m[0], 0, m[1], r, ref, l, o);
+        if (rb + sub < r1) store(map, m, r, ref, l, o);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int slot = 0; slot < SLOTS; ++slot) {
     const int* m = s_meta[slot];
     const int pieces = m[1];
-    if (pieces == 0) continue;
-    const int first = m[0], row_first = m[2], n = m[3], tile = m[4], h = m[5];
-    const int member = blockIdx.x * WORKERS + (slot >> 1) - first;
-    const int row0 = tile * ROWS, rows = min(ROWS, n * p.G - row0);
+    if (pieces <= kJoinFew) continue;
     RowMap map;
-    map.begin(p, row0);
-    const bool together = pieces > kJoinFew;
-    const int j0 = together ? pieces * warp / kJoinWarps : 0, j1 = together ? pieces * (warp + 1) / kJoinWarps : pieces;
-    // rows r with r pieces / rows == member
-    const int r0 = (member * rows + pieces - 1) / pieces, r1 = ((member + 1) * rows + pieces - 1) / pieces;
+    int r0, r1;
+    share_of(m, slot, map, r0, r1);
+    constexpr int RUNS = kJoinWarps * SUBS;
+    const int run = warp * SUBS + sub;
+    const int j0 = static_cast<int>(static_cast<int64_t>(pieces) * run / RUNS);
+    const int j1 = static_cast<int>(static_cast<int64_t>(pieces) * (run + 1) / RUNS);
+    const int turns = (pieces + RUNS * kJoinFew - 1) / (RUNS * kJoinFew);  // all lanes take as many
 #pragma unroll 1
-    for (int r = r0 + blockIdx.y; r < r1; r += gridDim.y) {  // segments of many rows have several blocks
-      if (!together && task++ % kJoinWarps != warp) continue;
-      float ref = -INFINITY, l = 0.0f, o[E] = {};
+    for (int r = r0 + blockIdx.y; r < r1; r += gridDim.y) {
+      float ref = -INFINITY, l = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-      for (int j = j0; j < j1; j += kJoinFew) {
-        const int cnt = min(kJoinFew, j1 - j);
-        // slot 1 for the first part, 0 for the others
-        const float* part = p.part + (static_cast<int64_t>(first + j) * 2) * ROWS * (D + 2);
-        constexpr int step = 2 * ROWS * (D + 2);
-        const int skip = j == 0 ? ROWS * (D + 2) : 0;
-        float r2 = -INFINITY, l2 = 0.0f, x[kJoinFew][E];
-        if (lane < cnt) {
-          const float2 y = *reinterpret_cast<const float2*>(part + lane * step + (lane == 0 ? skip : 0) + 2 * r);
-          r2 = y.x;
-          l2 = y.y;
-        }
-        const float* src = part + 2 * ROWS + r * D + lane * E;
-#pragma unroll
-        for (int i = 0; i < kJoinFew; ++i)
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float2 y = make_float2(0.0f, 0.0f);
-            if (i < cnt) y = *reinterpret_cast<const float2*>(src + i * step + (i == 0 ? skip : 0) + e);
-            x[i][e] = y.x, x[i][e + 1] = y.y;
-          }
-        float top = fmaxf(ref, r2);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float zero = top == -INFINITY ? 0.0f : top;
-        const float keep = ptx::ex2_approx(ref - zero), f = ptx::ex2_approx(r2 - zero);
-        float add = l2 * f;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-        ref = top;
-        l = l * keep + add;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= keep;
-#pragma unroll
-        for (int i = 0; i < kJoinFew; ++i) {
-          const float w = __shfl_sync(0xffffffffu, f, i);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], w, o[e]);  // 0 * 0 behind the last part
-        }
+      for (int i = 0; i < turns; ++i) {
+        const int j = j0 + i * kJoinFew;
+        add(m[0], j, min(max(j1 - j, 0), kJoinFew), r, ref, l, o);
       }
-      if (together) {
-        __syncthreads();
+      __syncthreads();
+      *reinterpret_cast<float4*>(&s_part[run][li * 4]) = o;
+      if (li == 0) s_part[run][D] = ref, s_part[run][D + 1] = l;
+      __syncthreads();
+      if (warp != 0 || sub != 0) continue;
+      ref = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_part[warp][lane * E + e] = o[e];
-        if (lane == 0) s_part[warp][D] = ref, s_part[warp][D + 1] = l;
-        __syncthreads();
-        if (warp != 0) continue;
-        ref = -INFINITY;
-        for (int w = 0; w < kJoinWarps; ++w) ref = fmaxf(ref, s_part[w][D]);
-        l = 0.0f;
+      for (int w = 0; w < RUNS; ++w) ref = fmaxf(ref, s_part[w][D]);
+      l = 0.0f;
+      o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.0f;
-        for (int w = 0; w < kJoinWarps; ++w) {
-          const float f = ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref));
-          l += s_part[w][D + 1] * f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += s_part[w][lane * E + e] * f;
-        }
+      for (int w = 0; w < RUNS; ++w) {
+        const float f = ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref));
+        const float4 x = *reinterpret_cast<const float4*>(&s_part[w][li * 4]);
+        l += s_part[w][D + 1] * f;
+        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
       }
-      const int tok = map.token(p, r);
-      const int64_t at_row = static_cast<int64_t>(row_first + tok) * p.Hq + h * p.G + map.head(p, r, tok);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(p.out + at_row * D + lane * E + e) = ptx::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-      if (p.lse && lane == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+      store(map, m, r, ref, l, o);
     }
   }
 }
