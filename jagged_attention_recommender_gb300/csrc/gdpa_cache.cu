@@ -108,14 +108,26 @@ int64_t most_segments(const CacheFwdParams& p, int rows) {
   return ((int64_t)p.batch.T * p.G / rows + p.batch.B) * p.cache.H;
 }
 
-// The kernel for so many query rows of a key head: eights of rows of the one
-// for few rows, or 0: the one for many.  A segment costs the latter about 5 us
-// of an SM's time and 0.8 us (up to 128 rows; 1.4 us up to 256) for 64 keys; the
-// former about 0.2 us and 0.9 us for 32 rows and 64 keys.
+// The kernel for so many query rows of a key head: eights of rows in a tile of
+// the one for few rows, or 0: the one for many.  Measured (us, 48 sequences of
+// 500 to 6001 keys, 4 key heads, D = 128; D = 64 behind the stroke), in tiles
+// of 16, 24, 32 rows and by the kernel for many:
+//   24 rows  76 / 56   62 / 50   84 / 54   111 / 71
+//   32 rows  77 / 57   92 / 69   87 / 58   112 / 70
+//   48 rows  -  / 71   93 / 70  134 / 79   114 / 72
+//   64 rows 135 / 89  127 / 95  136 / 80   117 / 72
+// and for 96 sequences of up to 1500 keys (tiles of 16 rows, kernel for many):
+//   64 rows  88 / 60   109 / 72       96 rows  122 / 82   113 / 74
+// up to 700:
+//   96 rows  72 / 51    82 / 58      128 rows   90 / 62    85 / 59
+// Tiles of 32 rows at D = 128 do not fit the registers; at D = 64 they take 172
+// us for 32 candidates of 128 samples, where two of 16 take 202.
+template <int D>
 int split_columns(int64_t rows, int64_t keys) {
-  if (rows <= 16) return rows <= 8 ? 1 : 2;
-  const int64_t tiles = (rows + 31) / 32;
-  return tiles == 1 || tiles * keys <= 512 ? 4 : 0;
+  if (rows <= 24) return rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
+  if (rows <= 32) return D == 64 ? 4 : 2;
+  if (rows <= 48) return 3;
+  return rows <= 96 && (rows + 15) / 16 * keys <= 6144 ? 2 : 0;
 }
 
 // Bytes of meta data and parts for so many workers.
@@ -133,9 +145,9 @@ template <int D>
 int64_t workspace_bytes(const Device& dev, int max_q, int G) {
   const int64_t rows = (int64_t)max_q * G;
   if (rows <= 8) return workspace_of<SplitCfg<D, 1>>(dev, D);
-  if (rows <= 16) return workspace_of<SplitCfg<D, 2>>(dev, D);
-  const int64_t few = workspace_of<SplitCfg<D, 4>>(dev, D);
-  return rows <= 32 ? few : std::max(few, workspace_of<TileCfg<D>>(dev, D));
+  int64_t most = std::max(workspace_of<SplitCfg<D, 2>>(dev, D), workspace_of<SplitCfg<D, 3>>(dev, D));
+  if (D == 64) most = std::max(most, workspace_of<SplitCfg<64, 4>>(dev, D));
+  return rows <= 48 ? most : std::max(most, workspace_of<TileCfg<D>>(dev, D));
 }
 
 // Shared memory above 48 KB has to be asked for, once a device and kernel.
@@ -145,13 +157,20 @@ template <typename Kernel>
 gdpa_status_t allow_smem(Kernel kernel, int bytes, int min_regs, int device, std::mutex& mu, bool* done) {
   std::lock_guard<std::mutex> lock(mu);
   if (done[device]) return GDPA_OK;
+  // (as in current_device: the first call may load the kernel while a stream is captured)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return GDPA_ERR_CUDA;
-  if (fa.numRegs < min_regs) return GDPA_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return GDPA_ERR_CUDA;
-  done[device] = true;
-  return GDPA_OK;
+  gdpa_status_t st = GDPA_OK;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
+    st = GDPA_ERR_CUDA;
+  else if (fa.numRegs < min_regs)
+    st = GDPA_ERR_UNSUPPORTED;
+  else if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    st = GDPA_ERR_CUDA;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) st = GDPA_ERR_CUDA;
+  done[device] = st == GDPA_OK;
+  return st;
 }
 
 template <int D>
@@ -239,10 +258,13 @@ gdpa_status_t launch_tile(CacheFwdParams& p, void* workspace, int max_q, const D
 
 template <int D>
 gdpa_status_t launch_fwd(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
-  switch (split_columns((int64_t)max_q * p.G, most_keys(p, max_q))) {
+  switch (split_columns<D>((int64_t)max_q * p.G, most_keys(p, max_q))) {
     case 1: return launch_split<D, 1>(p, workspace, max_q, dev, s);
     case 2: return launch_split<D, 2>(p, workspace, max_q, dev, s);
-    case 4: return launch_split<D, 4>(p, workspace, max_q, dev, s);
+    case 3: return launch_split<D, 3>(p, workspace, max_q, dev, s);
+    case 4:
+      if constexpr (D == 64) return launch_split<D, 4>(p, workspace, max_q, dev, s);
+      return GDPA_ERR_UNSUPPORTED;
     default: return launch_tile<D>(p, workspace, max_q, dev, s);
   }
 }

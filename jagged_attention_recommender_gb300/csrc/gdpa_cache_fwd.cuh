@@ -85,7 +85,7 @@ struct SplitCfg {
   static constexpr bool TEAM = TEAM_;
   static constexpr int WARPS = TEAM ? 8 : 4, THREADS = 32 * WARPS;
   static constexpr int WORKERS = TEAM ? 1 : WARPS;  // of a CTA: its warps, or itself
-  static constexpr int START = NT == 1 ? 2 : NT == 2 ? 5 : 10;  // what a segment's start and end cost, in steps
+  static constexpr int START = NT == 1 ? 2 : NT == 2 ? 5 : NT == 3 ? 8 : 10;  // what a segment's start and end cost, in steps
   static constexpr int RUN_STEPS = START + 4;  // the fewest steps (starts included) that are worth a part
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
@@ -94,8 +94,8 @@ struct SplitCfg {
   // CTAs an SM, and ring stages: enough tiles in flight to cover the memory's
   // latency (an SM's share of 6.8 TB/s is 45 KB a microsecond) at the
   // registers that the accumulators leave
-  static constexpr int CTAS = TEAM ? 1 : NT == 1 ? (D == 64 ? 3 : 2) : NT == 2 ? 3 : 2;
-  static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 6) : NT == 4 ? 4 : 3;
+  static constexpr int CTAS = TEAM ? 1 : NT == 1 ? (D == 64 ? 3 : 2) : NT == 2 && D == 64 ? 3 : 2;
+  static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 6) : NT >= 2 ? 4 : 3;
   static_assert(STAGES * NB <= 8, "a nibble of state for each tile of the ring");
   static constexpr int STAGE = NB * 2 * TILE;
   static constexpr int RING = STAGES * STAGE;      // of a warp

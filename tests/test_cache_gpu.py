@@ -5,6 +5,9 @@ scales in these tests, so a read of one shows in the result."""
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -380,6 +383,33 @@ def test_fwd_many_rows_wide_value_scales(D, kind):
         check_fwd(x, d, True, window)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["grows", "drops", "jumps", "zeros", "steps"])
+@pytest.mark.parametrize("new,keys", [(1, 500), (1, 2600), (2, 700), (3, 500), (4, 2600)])
+def test_fwd_few_rows_wide_value_scales(D, kind, new, keys):
+    """The same for one token and for a few, in one CTA and cut into parts."""
+    x = ref.make(25, 16, 2, D, 32, [keys, 33], [new, 1], jitter=0)
+    j = np.arange(-(-keys // 16))
+    sf = {"grows": 60 + j % 100, "drops": 220 - j % 200, "jumps": 120 + 25 * (j % 4 == 1), "zeros": 120 * (j % 3 != 0),
+          "steps": 120 + 7 * (j // 4 % 2) - 8 * (j % 2)}[kind]
+    x.v_sf[x.table[0, :-(-keys // 32)].repeat(2)[:len(j)], :, j % 2] = sf[:, None]
+    for window in (0, 33):
+        d = Dev(x)
+        d.fwd(window=window)
+        check_fwd(x, d, True, window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [7, 8, 9, 16, 17, 24, 25, 32, 33, 48, 49, 64, 96, 97])
+@pytest.mark.parametrize("keys,causal", [(300, True), (900, False), (2600, True)])
+def test_fwd_row_counts(D, rows, keys, causal):
+    """Both sides of every number of rows at which another kernel or tile takes over, few keys and many."""
+    x = ref.make(26 + rows, 2, 2, D, 32, [keys, rows // 2, rows + 40], [rows, rows // 3, rows - 1])
+    d = Dev(x, pad=1)
+    d.fwd(causal)
+    check_fwd(x, d, causal, 0)
+
+
 @pytest.mark.parametrize("new,window,heads", [(6, 0, (4, 1)), (20, 0, (8, 2)), (150, 0, (4, 2)), (5, 9, (2, 2)),
                                               (150, 9, (8, 1))])
 def test_fwd_hidden_keys_never_count(new, window, heads):
@@ -559,3 +589,30 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for x, d in zip(xs, ds):
         check_fwd(x, d, True, 0)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """Nothing but the capture has run: modules, kernels and their settings are loaded inside it."""
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch
+from tests import cache_ref as ref
+from tests.test_cache_gpu import Dev, check_append, check_fwd, host, inv_freq, gdpa
+for new in ([1, 1], [3, 2], [90, 20]):
+    f = inv_freq(64)
+    x = ref.make(40, 8, 2, 64, 16, [300, 41], new, [300 - new[0], 41 - new[1]])
+    d = Dev(x, f)
+    ws = torch.empty(gdpa.gdpa_cache_workspace_size(d.cache, 8, max(new)), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d.append()
+        d.fwd(q=d.q_out, workspace=ws)
+    for _ in range(2):
+        g.replay()
+    check_append(x, d, f, False)
+    x.k_codes, x.k_sf, x.v_codes, x.v_sf = host(d.k_codes), host(d.k_sf), host(d.v_codes), host(d.v_sf)
+    check_fwd(x, d, True, 0, q=host(d.q_out))
+print("fine")
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stderr[-2000:]
