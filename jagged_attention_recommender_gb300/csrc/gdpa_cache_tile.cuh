@@ -28,7 +28,8 @@
 //                     every tile S -> P (over S in TMEM), and the output;
 //   warps 8-11        convert K tiles (128-byte swizzle, two stages);
 //   warps 12-15       convert V tiles;
-//   warp 16           issues the MMAs, S ahead of P V;
+//   warp 16           issues the MMAs of S;
+//   warp 18           issues those of P V;
 //   warp 17           finds pages and scales, and brings codes to shared memory
 //                     by bulk copies, RAWS tiles ahead.
 // (Conversion by the warps that also looked up pages and copied, one tile ahead
@@ -97,10 +98,10 @@ namespace tile {
 struct Bars {
   uint64_t raw_full[8], raw_free[8];
   uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2];  // of a half (and S buffer)
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a half and S buffer
   uint64_t o_full;                                  // after a segment's last P V
   uint64_t x_full, x_free;                          // the second half's result is there, is read
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -119,7 +120,7 @@ struct __align__(16) RawNote {
 struct Notes {
   RawNote raw[8];
   // For the softmax of tile i, in a ring of eight: the refill of an entry waits
-  // for S(i + 6), which waits for P(i + 3) at least.
+  // for S(i + 6), which waits for P V of tile i + 2 of this half at least.
   float4 k_scale[8];
   int exponent[8];
   // Segments of this CTA, in a ring: some tile takes the plain form.  Entries
@@ -349,10 +350,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
             }
             exponent = e_now;
             if (__any_sync(0xffffffffu, follow)) {
-              // S of this tile came after P V of this half's tile before the
-              // last (its P is in the same buffer), so that pv_done is in the
-              // phase waited for, or has left it
-              ok = ptx::mbar_wait(&B.pv_done[half], (ti - 1) & 1, limit, abort);
+              ok = ptx::mbar_wait(&B.pv_done[half][(ti - 1) & 1], ((ti - 1) >> 1) & 1, limit, abort);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               ptx::tc_fence_after();
@@ -728,42 +726,12 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
 }
 
 // ------------------------------------------------------------------ MMA
-// P V of tile gi, for each half that has it.
-struct Pending {
-  uint32_t gi;
-  int halves;          // bits
-  uint32_t ti[2];      // the halves' tile numbers
-  int first[2];        // the half's first in this segment
-};
+// S = Q K^T of every tile, up to two tiles of a half ahead of its softmax.  A
+// buffer of S holds P of the tile that used it last, until P V of that one is
+// done.
 template <int D>
-__device__ __forceinline__ bool issue_pv(Bars& B, uint64_t v_desc, uint32_t tmem, const Pending& t,
-                                         unsigned long long limit) {
-  using C = TileCfg<D>;
-  const int vs = t.gi & 1;
-  volatile int* abort = &B.abort;
-  if (!ptx::mbar_wait(&B.v_full[vs], (t.gi >> 1) & 1, limit, abort)) return false;
-  const uint64_t v = v_desc + vs * (C::KV_BYTES >> 4);
-  constexpr uint32_t idesc = ptx::idesc_f16(128, D, 1);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!(t.halves >> h & 1)) continue;
-    const uint32_t sb = t.ti[h] & 1;
-    if (!ptx::mbar_wait(&B.p_full[h][sb], (t.ti[h] >> 1) & 1, limit, abort)) return false;
-    ptx::tc_fence_after();
-#pragma unroll
-    for (int kk = 0; kk < C::SPAN / 16; ++kk)
-      // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
-      ptx::mma_ts_elect(tmem + C::TM_O + h * 128, tmem + C::TM_S + h * 128 + sb * 64 + 8 * kk,
-                        v + (kk * 2048 >> 4), idesc, kk > 0 ? 1u : t.first[h] ? 0u : 1u);
-    ptx::mma_commit_elect(&B.pv_done[h]);
-  }
-  ptx::mma_commit_elect(&B.v_free[vs]);
-  return true;
-}
-
-template <int D>
-__device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t tmem,
-                        const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, unsigned long long limit) {
+__device__ void run_scores(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t tmem,
+                           const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, unsigned long long limit) {
   using C = TileCfg<D>;
   volatile int* abort = &B.abort;
   split::Walk<C> w;
@@ -771,11 +739,9 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
   uint32_t gi = 0, seg = 0, ti[2] = {0, 0};
   bool ok = true;
   // Descriptors of the first tiles: all others are a constant further on (the
-  // address field counts 16 bytes and has room).  This warp's instructions are
-  // a tile's critical path, so none of them is a descriptor's making.
+  // address field counts 16 bytes and has room).
   const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm + C::OFF_K), 16, 1024);
-  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm + C::OFF_V), C::KV_CHUNK, 1024);
   constexpr uint32_t idesc = ptx::idesc_f16(128, C::SPAN, 0);
 #pragma unroll 1
   for (; ok && w.more(p, stop); w.next(p)) {
@@ -783,21 +749,19 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
     ok = ptx::mbar_wait(&B.q_full, seg++ & 1, limit, abort);
     const int steps = w.u1 - w.u0;
     const bool pair = w.rows > C::HALF;
-    // P V follows S by a tile, or by two where the halves take turns (each
-    // half's softmax then always finds its next S)
-    Pending last = {0, 0, {0, 0}, {0, 0}}, older = last;
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++gi) {
       const int ks = gi & 1;
       ok = ptx::mbar_wait(&B.k_full[ks], (gi >> 1) & 1, limit, abort);
       if (!ok) break;
-      ptx::tc_fence_after();
       const uint64_t k = k_desc + ks * (C::KV_BYTES >> 4);
-      Pending now = {gi, pair ? 3 : 1 << (i & 1), {ti[0], ti[1]}, {i < (pair ? 1 : 2), i < (pair ? 1 : 2)}};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!(now.halves >> h & 1)) continue;
+        if (!pair && (i & 1) != h) continue;
         const uint32_t sb = ti[h] & 1;
+        ok = ok && ptx::mbar_wait(&B.pv_done[h][sb], ((ti[h] >> 1) & 1) ^ 1, limit, abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           ptx::mma_ss_elect(tmem + C::TM_S + h * 128 + sb * 64,
@@ -807,22 +771,68 @@ __device__ void run_mma(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t 
         ++ti[h];
       }
       ptx::mma_commit_elect(&B.k_free[ks]);
-      if (pair ? i > 0 : i > 1) ok = issue_pv<D>(B, v_desc, tmem, pair ? last : older, limit);
-      older = last;
-      last = now;
     }
-    if (ok && !pair && steps > 1) ok = issue_pv<D>(B, v_desc, tmem, older, limit);
-    if (ok) ok = issue_pv<D>(B, v_desc, tmem, last, limit);
-    ptx::mma_commit_elect(&B.o_full);
   }
   if (!ok && (threadIdx.x & 31) == 0) {
     *abort = 1;
     atomicOr(p.batch.status, kStatusMma);
   }
   // every MMA this warp issued is complete once this commit lands
-  ptx::mma_commit_elect(&B.drain);
+  ptx::mma_commit_elect(&B.drain[0]);
   const int never = 0;
-  ptx::mbar_wait(&B.drain, 0, 100000000ull, &never);
+  ptx::mbar_wait(&B.drain[0], 0, 100000000ull, &never);
+}
+
+// O += P V of every tile.
+template <int D>
+__device__ void run_values(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t tmem,
+                           const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, unsigned long long limit) {
+  using C = TileCfg<D>;
+  volatile int* abort = &B.abort;
+  split::Walk<C> w;
+  w.begin(p, sh.seq[0], sh.base[0], at);
+  uint32_t gi = 0, ti[2] = {0, 0};
+  bool ok = true;
+  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm + C::OFF_V), C::KV_CHUNK, 1024);
+  constexpr uint32_t idesc = ptx::idesc_f16(128, D, 1);
+#pragma unroll 1
+  for (; ok && w.more(p, stop); w.next(p)) {
+    if (!w.enter(p, at, stop) || w.u1 <= w.u0) continue;
+    const int steps = w.u1 - w.u0;
+    const bool pair = w.rows > C::HALF;
+#pragma unroll 1
+    for (int i = 0; ok && i < steps; ++i, ++gi) {
+      const int vs = gi & 1;
+      ok = ptx::mbar_wait(&B.v_full[vs], (gi >> 1) & 1, limit, abort);
+      if (!ok) break;
+      const uint64_t v = v_desc + vs * (C::KV_BYTES >> 4);
+      const bool first = i < (pair ? 1 : 2);  // a half's first in this segment
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!pair && (i & 1) != h) continue;
+        const uint32_t sb = ti[h] & 1;
+        ok = ok && ptx::mbar_wait(&B.p_full[h][sb], (ti[h] >> 1) & 1, limit, abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < C::SPAN / 16; ++kk)
+          // V is MN-major: 16 keys = two 8-row groups 1024 B apart; 64-column chunks KV_CHUNK apart
+          ptx::mma_ts_elect(tmem + C::TM_O + h * 128, tmem + C::TM_S + h * 128 + sb * 64 + 8 * kk,
+                            v + (kk * 2048 >> 4), idesc, kk > 0 ? 1u : first ? 0u : 1u);
+        ptx::mma_commit_elect(&B.pv_done[h][sb]);
+        ++ti[h];
+      }
+      ptx::mma_commit_elect(&B.v_free[vs]);
+    }
+    ptx::mma_commit_elect(&B.o_full);
+  }
+  if (!ok && (threadIdx.x & 31) == 0) {
+    *abort = 1;
+    atomicOr(p.batch.status, kStatusMma);
+  }
+  ptx::mma_commit_elect(&B.drain[1]);
+  const int never = 0;
+  ptx::mbar_wait(&B.drain[1], 0, 100000000ull, &never);
 }
 
 }  // namespace tile
@@ -864,13 +874,13 @@ __global__ void __launch_bounds__(640, 1) gdpa_cache_tile_kernel(const CacheFwdP
       for (int h = 0; h < 2; ++h) {
         ptx::mbar_init(&B.s_full[h][i], 1);
         ptx::mbar_init(&B.p_full[h][i], 128);
+        ptx::mbar_init(&B.pv_done[h][i], 1);
       }
-      ptx::mbar_init(&B.pv_done[i], 1);
+      ptx::mbar_init(&B.drain[i], 1);
     }
     ptx::mbar_init(&B.o_full, 1);
     ptx::mbar_init(&B.x_full, 128);
     ptx::mbar_init(&B.x_free, 128);
-    ptx::mbar_init(&B.drain, 1);
     B.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -898,7 +908,8 @@ __global__ void __launch_bounds__(640, 1) gdpa_cache_tile_kernel(const CacheFwdP
       tile::run_convert<D, true>(p, sm, B, notes, limit);
   } else {
     ptx::regs_dec<C::REGS_ISSUE>();
-    if (warp == 16) tile::run_mma<D>(p, sm, B, tmem, sh, at, stop, limit);
+    if (warp == 16) tile::run_scores<D>(p, sm, B, tmem, sh, at, stop, limit);
+    if (warp == 18) tile::run_values<D>(p, sm, B, tmem, sh, at, stop, limit);
     if (warp == 17) tile::run_copies<D>(p, sm, B, notes, sh, at, stop, limit);
   }
   __syncwarp();
