@@ -426,7 +426,8 @@ typedef enum {
  *
  *   k_codes, v_codes  device uint8 [num_pages, H, page_tokens, D]  OCP e4m3
  *   k_sf, v_sf        device uint8 [num_pages, H, page_tokens/16]  OCP E8M0
- *   value = e4m3(code) * 2^(sf - 127), one scale for 16 tokens of one head
+ *   value = e4m3(code) * 2^(sf - 127), one scale for 16 tokens of one head; a
+ *   scale is at most 254 (gdpa_cache_append never writes more than 247)
  *
  * Token t of sequence b lies in page page_table[b, t / page_tokens] at slot
  * t % page_tokens.  H is the number of key/value heads, D 64 or 128,

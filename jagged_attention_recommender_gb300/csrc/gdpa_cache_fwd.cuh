@@ -10,23 +10,31 @@
 // by a power of two into [-2, 2) and becomes fp16 (exact down to 2^-17 of its
 // largest element, below that off by 2^-25 of it); products are summed in fp32.
 // The scale of a block of 16 tokens is the scale of a whole 16-key tile: K's
-// multiplies the tile's scores, V's the tile's product as it is added to the
-// output, in fp32, so no block's precision depends on another's.  Weights are
+// multiplies the tile's scores.  The output is in units of 2^E, E one above the
+// largest scale of V so far; a scale up to 2^6 below goes into the weights (in
+// fp32, before their rounding to fp16) and the tile's product is summed in place,
+// one further below multiplies the tile's product in fp32: no block's precision
+// depends on another's within fp32's range.  Weights are
 // 2^(x - r) with a reference r 7 below the running maximum when it was last
 // moved, and r only moves when a score exceeds it by 15: weights stay below
-// 2^15 (fp16 holds 65504), those down to 2^-21 of the maximum keep 11 bits,
-// and nothing above 2^-31 of it is lost.  The row sum takes the weights before
+// 2^15 (fp16 holds 65504), those down to 2^-21 of the maximum (2^-15 with a
+// scale 2^6 below) keep 11 bits, and nothing above 2^-31 (2^-25) of it is lost.  The row sum takes the weights before
 // their rounding to fp16.
 //
-// Bound: memory, 2 D bytes a key and head, with the instruction issue close
-// behind (the codes' conversions and byte shuffles).
+// Bound: memory, 2 D bytes a key and head, with the latency of a warp's own
+// instructions close behind (conversions, byte shuffles, products).  Measured:
+// one token of 64 histories of 100 to 8192 keys, 32 query and 8 key heads of 128,
+// 98 us (5.6 TB/s); of 512 histories of up to 1023 keys, 8 and 8 heads of 64, 75 us
+// (3.6 TB/s; the start and the join are 12 us of it); 32
+// rows of 128 samples, 8 and 8 heads of 64, 172 us.
 //
 // Work split.  A segment is (sequence, up to 8 NT query rows of one key head);
 // a step is SPAN keys of it.  The steps of all segments are counted from the
 // lengths on the device, and every warp takes an equal run of them (a segment's
-// start is counted as kStart steps more), so a batch of any raggedness, or one
+// start is counted as START steps more), so a batch of any raggedness, or one
 // very long sequence, loads all SMs alike and nothing is planned on the host.
-// Warps never wait for one another.  Each owns a ring of stages in shared
+// Warps never wait for one another (but where the eight warps of a CTA share one
+// short segment: TEAM).  Each owns a ring of stages in shared
 // memory that its own asynchronous copies fill, STAGES - 1 steps ahead and
 // across the ends of segments (rows that are not stored are zero-filled).  A
 // segment that lies in several warps' runs leaves its parts (reference, sum,
@@ -79,13 +87,18 @@ struct RowMap {
 // `pieces - 1` workers behind it the next ones in their slots 0.  Beside each
 // part stand {first, pieces, first row of the sequence, its rows, row tile, head}.
 
-// TEAM: a CTA has one whole segment at most, and its warps take the steps in turn.
+// TEAM: a CTA has one whole segment at most, and its warps take the steps in turn:
+// one token over 201 keys takes 9.4 us of a call so and 14.3 as cut parts.
 template <int D, int NT, bool TEAM_ = false>
 struct SplitCfg {
   static constexpr bool TEAM = TEAM_;
   static constexpr int WARPS = TEAM ? 8 : 4, THREADS = 32 * WARPS;
   static constexpr int WORKERS = TEAM ? 1 : WARPS;  // of a CTA: its warps, or itself
-  static constexpr int START = NT == 1 ? 2 : NT == 2 ? 5 : NT == 3 ? 8 : 10;  // what a segment's start and end cost, in steps
+  // What a segment's start and end cost, in steps: about 16 000 cycles of 1 600
+  // with 32 rows, 5 000 of 2 200 with 8.  (2 for all left warps with many short
+  // segments working when others were done: 232 us for 32 rows of 128 samples,
+  // 190 so; 7 took 200 and 20 took 197.)
+  static constexpr int START = NT == 1 ? 2 : NT == 2 ? 5 : NT == 3 ? 8 : 10;
   static constexpr int RUN_STEPS = START + 4;  // the fewest steps (starts included) that are worth a part
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE = 16 * D;  // bytes of a tile of K or of V
@@ -93,7 +106,10 @@ struct SplitCfg {
   static constexpr int SPAN = NB * kCacheBlock;
   // CTAs an SM, and ring stages: enough tiles in flight to cover the memory's
   // latency (an SM's share of 6.8 TB/s is 45 KB a microsecond) at the
-  // registers that the accumulators leave
+  // registers that the accumulators leave.  Two tiles a step: 64 histories take
+  // 98 us so, 114 with one (512 short ones 75 and 86).  D = 64 with 8 rows: 75 us
+  // on three CTAs, 96 on two, 80 on four of three stages.  With 16 rows at D = 128:
+  // 53 us on two CTAs, 63 on three (registers); at D = 64 42 on three, 43 on two.
   static constexpr int CTAS = TEAM ? 1 : NT == 1 ? (D == 64 ? 3 : 2) : NT == 2 && D == 64 ? 3 : 2;
   static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 6) : NT >= 2 ? 4 : 3;
   static_assert(STAGES * NB <= 8, "a nibble of state for each tile of the ring");

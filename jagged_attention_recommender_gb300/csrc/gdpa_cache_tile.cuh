@@ -13,9 +13,12 @@
 // by 15, and rounded to fp16, as in the kernel for few rows.  Sums stay in fp32;
 // the row sum takes the weights before their rounding.
 //
-// Bound: the instruction issue (softmax and conversions), the tensor core and
-// the special-function unit (512 cycles each of a 128 x 64 tile at D = 128)
-// close behind.
+// Bound: the chain of hand-overs between the roles.  The tensor core and the
+// special-function unit each need about 1050 cycles for 256 rows and 64 keys at
+// D = 128 and a step takes about 2000: 258 us (746 TFLOP/s) for 2321 rows of
+// prompts behind 2100 to 8192 keys, 32 query and 8 key heads of 128.  With a
+// softmax that only hands over 194 us are left, with an eighth of S's and a
+// quarter of P V's MMAs as well 157.
 //
 // Work split.  Segments (sequence, 256 rows, key head) and runs as in the
 // kernel for few rows, a CTA being the worker and 64 keys a step; a cut
@@ -29,11 +32,13 @@
 //   warps 8-11        convert K tiles (128-byte swizzle, two stages);
 //   warps 12-15       convert V tiles;
 //   warp 16           issues the MMAs of S;
-//   warp 18           issues those of P V;
+//   warp 18           issues those of P V (one warp for both was the longest
+//                     of all chains: 297 us);
 //   warp 17           finds pages and scales, and brings codes to shared memory
 //                     by bulk copies, RAWS tiles ahead.
 // (Conversion by the warps that also looked up pages and copied, one tile ahead
-// and two CTAs of 128 rows an SM, took 435 us where this takes TIME_PROMPTS.)
+// and two CTAs of 128 rows an SM, took 435 us.  Results written by way of shared
+// memory, whole lines at a time, took 8 us more than a row a thread.)
 //
 // A value that is NaN must not reach rows that do not see its token, and 0
 // times NaN is NaN: a segment with a NaN value in a tile that some row sees
