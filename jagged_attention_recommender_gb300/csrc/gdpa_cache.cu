@@ -112,14 +112,14 @@ int64_t most_segments(const CacheFwdParams& p, int rows) {
 // the one for few rows, or 0: the one for many.  Measured (us, 48 sequences of
 // 500 to 6001 keys, 4 key heads, D = 128; D = 64 behind the stroke), in tiles
 // of 16, 24, 32 rows and by the kernel for many:
-//   24 rows  76 / 56   62 / 50   84 / 54   111 / 71
-//   32 rows  77 / 57   92 / 69   87 / 58   112 / 70
-//   48 rows  -  / 71   93 / 70  134 / 79   114 / 72
-//   64 rows 135 / 89  127 / 95  136 / 80   117 / 72
-// and for 96 sequences of up to 1500 keys (tiles of 16 rows, kernel for many):
-//   64 rows  88 / 60   109 / 72       96 rows  122 / 82   113 / 74
-// up to 700:
-//   96 rows  72 / 51    82 / 58      128 rows   90 / 62    85 / 59
+//   24 rows  76 / 56   62 / 50   84 / 54   102 / 66
+//   32 rows  78 / 57   92 / 69   87 / 58   101 / 66
+//   48 rows 107 / 72   93 / 70  134 / 79   105 / 72
+//   64 rows 135 / 90  127 / 95  136 / 80   107 / 72
+// for 96 sequences of up to 1500 keys, in tiles of 16 and by the kernel for many,
+//   64 rows  89 / 60   100 / 68       96 rows  123 / 82   103 / 70
+// and of up to 700
+//   96 rows  72 / 51    75 / 55      128 rows   91 / 62    76 / 55
 // Tiles of 32 rows at D = 128 do not fit the registers; at D = 64 they take 172
 // us for 32 candidates of 128 samples, where two of 16 take 202.
 template <int D>

@@ -77,7 +77,10 @@ struct TileCfg {
   static constexpr int D = D_;
   static constexpr bool TEAM = false;
   static constexpr int THREADS = 640, WORKERS = 1;  // five warpgroups
-  static constexpr int START = 8, RUN_STEPS = 12;
+  // What a segment's start and end cost, in steps (48 sequences of 500 to 6001
+  // keys, 128 rows: 111 us with 16 at D = 128, 120 with 8; 76 with 8 at D = 64, 82
+  // with 16), and the fewest that are worth a part.
+  static constexpr int START = D == 128 ? 16 : 8, RUN_STEPS = START + 4;
   static constexpr int HALF = 128, ROWS = 2 * HALF, SPAN = 64;
   static constexpr int CTAS = 1;
   static constexpr int Q_CHUNK = HALF * 128, KV_CHUNK = SPAN * 128;  // 64 columns of a tile
