@@ -38,7 +38,7 @@
 // memory that its own asynchronous copies fill, STAGES - 1 steps ahead and
 // across the ends of segments (rows that are not stored are zero-filled).  A
 // segment that lies in several warps' runs leaves its parts (reference, sum,
-// output) in the workspace and the second kernel joins them in the order of the
+// mean) in the workspace and the second kernel joins them in the order of the
 // keys: results do not depend on timing.
 #pragma once
 
@@ -367,11 +367,12 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const int r = nt * 8 + 2 * t + c;
       if (g == 0) s_team[warp][r][0] = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c], s_team[warp][r][1] = l;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // means: they are as large as values, sums may not be held
       float4* dst = reinterpret_cast<float4*>(merge + (warp * C::ROWS + r) * D + g * (D / 8));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        dst[i] = make_float4(acc[2 * i][nt][c] * unit, acc[2 * i][nt][c + 2] * unit, acc[2 * i + 1][nt][c] * unit,
-                             acc[2 * i + 1][nt][c + 2] * unit);
+        dst[i] = make_float4(acc[2 * i][nt][c] * inv * unit, acc[2 * i][nt][c + 2] * inv * unit,
+                             acc[2 * i + 1][nt][c] * inv * unit, acc[2 * i + 1][nt][c + 2] * inv * unit);
     }
   __syncthreads();
   for (int i = tid; i < rows * (D / 8); i += C::THREADS) {
@@ -380,9 +381,12 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, s_team[w][r][0]);
 #pragma unroll
+    for (int w = 0; w < C::WARPS; ++w)
+      l += s_team[w][r][1] * ptx::ex2_approx(s_team[w][r][0] - (top == -INFINITY ? 0.0f : top));
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-      const float f = ptx::ex2_approx(s_team[w][r][0] - (top == -INFINITY ? 0.0f : top));
-      l += s_team[w][r][1] * f;
+      const float f = s_team[w][r][1] * ptx::ex2_approx(s_team[w][r][0] - (top == -INFINITY ? 0.0f : top)) * inv;
       const float4* src = reinterpret_cast<const float4*>(merge + (w * C::ROWS + r) * D + d);
       const float4 x = src[0], y = src[1];
       o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
@@ -390,10 +394,9 @@ __device__ __forceinline__ void team_join(const CacheFwdParams& p, uint8_t* smem
     }
     const int tok = map.token(p, r);
     const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + map.head(p, r, tok);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint4*>(p.out + at_row * D + d) =
-        make_uint4(ptx::pack_bf16x2(o[0] * inv, o[1] * inv), ptx::pack_bf16x2(o[2] * inv, o[3] * inv),
-                   ptx::pack_bf16x2(o[4] * inv, o[5] * inv), ptx::pack_bf16x2(o[6] * inv, o[7] * inv));
+        make_uint4(ptx::pack_bf16x2(o[0], o[1]), ptx::pack_bf16x2(o[2], o[3]), ptx::pack_bf16x2(o[4], o[5]),
+                   ptx::pack_bf16x2(o[6], o[7]));
     if (p.lse && d == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
   }
 }
@@ -690,12 +693,16 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           }
       }
       if (__any_sync(0xffffffffu, over)) {
-        // V's units: one above the largest scale, so that they seldom move
+        // V's units: one above the largest scale, so that they seldom move.  At
+        // an edge a row may see nothing of a block that lies far above, and what
+        // it has summed must not vanish in that block's units: there they stay up
+        // to 2^90 behind (edges behind a row's last key are three steps at most).
         int top_sv = sv[0];
         if (C::NB == 2) top_sv = max(top_sv, sv[C::NB - 1]);
         float turn = 1.0f;
         if (top_sv > vexp) {
-          const int up = min(top_sv + 1, 254);
+          int up = min(top_sv + 1, 254);
+          if (EDGE && vexp >= 0 && top_sv - vexp > 40) up = max(vexp, top_sv - 90);
           turn = vexp < 0 ? 0.0f : up - vexp > 126 ? 0.0f : sf_value(127 - (up - vexp));
           vexp = up;
         }
@@ -730,7 +737,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
       for (int n = 0; n < C::NB; ++n) {
         // a scale up to 2^6 below the units goes into the weights
         const int below = vexp - sv[n];
-        const bool near = below <= 6;
+        const bool near = below >= 0 && below <= 6;
         const float unit = sf_value(127 - (near ? below : 0));
         uint32_t pb[NT][2];
 #pragma unroll
@@ -789,7 +796,9 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
             }
         } else {
           // what the weights do not hold of the scale, as a factor of the product
-          const float rest = near ? 1.0f : sf_value(127 - (below >> 1)) * sf_value(127 - (below - (below >> 1)));
+          const float rest = near        ? 1.0f
+                             : below < 0 ? sf_value(127 - below)
+                                         : sf_value(127 - (below >> 1)) * sf_value(127 - (below - (below >> 1)));
 #pragma unroll 1
           for (int k = 0; k < tokens; ++k) {
             const int key = kb + n * kCacheBlock + k;
@@ -863,10 +872,10 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         const int r = nt * 8 + 2 * t + c;
         const float m = room[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
         if (r >= rows) continue;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (pieces == 1) {
           const int tok = now.map.token(p, r);
           const int64_t at_row = static_cast<int64_t>(s.first + tok) * p.Hq + h * p.G + now.map.head(p, r, tok);
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           uint32_t o[ND];
 #pragma unroll
           for (int i = 0; i < ND; ++i)
@@ -879,9 +888,9 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
           if (g == 0) part[2 * r] = m, part[2 * r + 1] = l;
           float4* dst = reinterpret_cast<float4*>(part + 2 * C::ROWS + r * D + g * (D / 8));
 #pragma unroll
-          for (int i = 0; i < ND / 2; ++i)
-            dst[i] = make_float4(acc[2 * i][nt][c] * unit, acc[2 * i][nt][c + 2] * unit, acc[2 * i + 1][nt][c] * unit,
-                                 acc[2 * i + 1][nt][c + 2] * unit);
+          for (int i = 0; i < ND / 2; ++i)  // means, as large as values: their sums may not be held
+            dst[i] = make_float4(acc[2 * i][nt][c] * inv * unit, acc[2 * i][nt][c + 2] * inv * unit,
+                                 acc[2 * i + 1][nt][c] * inv * unit, acc[2 * i + 1][nt][c + 2] * inv * unit);
         }
       }
   }
@@ -911,7 +920,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
     s_meta[threadIdx.x >> 3][threadIdx.x & 7] = p.meta[blockIdx.x * 8 * SLOTS + threadIdx.x];
   __syncthreads();
 
-  // Adds parts [j, j + cnt), cnt up to 8, of a row: four coordinates a lane.
+  // Adds parts [j, j + cnt), cnt up to 8, of a row: four coordinates a lane.  A
+  // part is a reference, a sum and the mean of the values; so is the result.
   auto add = [&](int first, int j, int cnt, int r, float& ref, float& l, float4& o) {
     constexpr int step = 2 * ROWS * (D + 2);
     const float* part = p.part + static_cast<int64_t>(first + j) * step;
@@ -935,20 +945,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1) more += __shfl_xor_sync(0xffffffffu, more, d);
     ref = top;
-    l = l * keep + more;
-    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+    const float all = l * keep + more, inv = all == 0.0f ? 0.0f : 1.0f / all, stay = l * keep * inv;
+    const float share = own.y * f * inv;
+    l = all;
+    o.x *= stay, o.y *= stay, o.z *= stay, o.w *= stay;
 #pragma unroll
     for (int i = 0; i < kJoinFew; ++i) {
-      const float w = __shfl_sync(0xffffffffu, f, i, 8);  // (0 times 0 behind the last part)
+      const float w = __shfl_sync(0xffffffffu, share, i, 8);  // (0 times 0 behind the last part)
       o.x = fmaf(x[i].x, w, o.x), o.y = fmaf(x[i].y, w, o.y), o.z = fmaf(x[i].z, w, o.z), o.w = fmaf(x[i].w, w, o.w);
     }
   };
   auto store = [&](const RowMap& map, const int* m, int r, float ref, float l, const float4& o) {
     const int tok = map.token(p, r);
     const int64_t at_row = static_cast<int64_t>(m[2] + tok) * p.Hq + m[5] * p.G + map.head(p, r, tok);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(p.out + at_row * D + li * 4) =
-        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(ptx::pack_bf16x2(o.x, o.y), ptx::pack_bf16x2(o.z, o.w));
     if (p.lse && li == 0) p.lse[at_row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
   };
   // m: {first worker, pieces, first row of the sequence, its rows, row tile, head}
@@ -1011,10 +1022,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) gdpa_cache_join_kernel(con
       l = 0.0f;
       o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
+      for (int w = 0; w < RUNS; ++w) l += s_part[w][D + 1] * ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref));
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
       for (int w = 0; w < RUNS; ++w) {
-        const float f = ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref));
+        const float f = s_part[w][D + 1] * ptx::ex2_approx(s_part[w][D] - (ref == -INFINITY ? 0.0f : ref)) * inv;
         const float4 x = *reinterpret_cast<const float4*>(&s_part[w][li * 4]);
-        l += s_part[w][D + 1] * f;
         o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
       }
       store(map, m, r, ref, l, o);

@@ -138,7 +138,7 @@ struct Notes {
 };
 
 // One row of a segment over keys [j0, j1), one warp, D / 32 coordinates a lane:
-// the plain form, for segments that the tensor core cannot take.
+// the plain form, for segments that the tensor core cannot take.  o: the mean.
 template <int D>
 __device__ __noinline__ void attend_row(const CacheFwdParams& p, int b, int h, int64_t q_at, int j0, int j1,
                                         float& top, float& total, float* o) {
@@ -165,9 +165,11 @@ __device__ __noinline__ void attend_row(const CacheFwdParams& p, int b, int h, i
     const float up = fmaxf(m, x), zero = up == -INFINITY ? 0.0f : up;
     const float keep = ptx::ex2_approx(m - zero), w = ptx::ex2_approx(x - zero);
     const float sv = sf_value(p.cache.v_sf[row >> 4]);
-    l = l * keep + w;
+    const float all = l * keep + w, inv = all == 0.0f ? 0.0f : 1.0f / all;
+    const float stay = l * keep * inv, add = w * inv;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * (e4m3_to_float(p.cache.v[at + e]) * sv);
+    for (int e = 0; e < E; ++e) o[e] = o[e] * stay + add * (e4m3_to_float(p.cache.v[at + e]) * sv);
+    l = all;
     m = up;
   }
   top = m;
@@ -419,12 +421,11 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         const int64_t row_q = __shfl_sync(0xffffffffu, q_at, row), row_o = __shfl_sync(0xffffffffu, out_row, row);
         attend_row<D>(p, w.b, w.h, row_q, max(k0, __shfl_sync(0xffffffffu, lo, row)),
                       min(k1, __shfl_sync(0xffffffffu, hi, row)), top, total, o);
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         const int at_row = (ri & ~31) + row;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           if (to.pieces == 1)
-            p.out[row_o * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
+            p.out[row_o * D + lane * E + e] = __float2bfloat16_rn(o[e]);
           else
             to.part[2 * C::ROWS + at_row * D + lane * E + e] = o[e];
         }
@@ -437,9 +438,11 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
       }
       continue;
     }
-    // this half's output is in units of 2^exponent
-    float unit = sf_value(min(max(127 + exponent, 0), 254));
-    float other = 0.0f;  // weight of the second half's output
+    // this half's output is in units of 2^exponent; its weight makes it a mean
+    // (as large as values: their sums may not be held)
+    const float unit = sf_value(min(max(127 + exponent, 0), 254));
+    float own = l == 0.0f ? 0.0f : 1.0f / l;
+    float other = 0.0f;  // weight of the second half's mean
     const uint32_t x_row = ptx::smem_u32(sm) + r * D * 4;
     if (!pair && steps > 0) {
       if (half == 1) {  // hand over: reference, sum, output
@@ -454,7 +457,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
               uint32_t y[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                y[e] = l == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[4 * u + e]) * unit);
+                y[e] = l == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[4 * u + e]) * own * unit);
               ptx::st_shared_v4(x_row + (((c / 4 + u) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
             }
           }
@@ -473,16 +476,15 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
       if (live) {
         const float m2 = *const_cast<volatile float*>(&notes.x_ref[r]), l2 = *const_cast<volatile float*>(&notes.x_sum[r]);
         const float top = fmaxf(m, m2), zero = top == -INFINITY ? 0.0f : top;
-        const float f1 = ptx::ex2_approx(m - zero);
-        other = l2 == 0.0f ? 0.0f : ptx::ex2_approx(m2 - zero);
-        unit *= f1;
-        if (l == 0.0f) unit = 0.0f;
-        l = l * f1 + l2 * other;
+        const float f1 = ptx::ex2_approx(m - zero), f2 = l2 == 0.0f ? 0.0f : ptx::ex2_approx(m2 - zero);
+        const float all = l * f1 + l2 * f2, inv = all == 0.0f ? 0.0f : 1.0f / all;
+        own = l == 0.0f ? 0.0f : f1 * inv;
+        other = l2 * f2 * inv;
+        l = all;
         m = top;
       }
     }
     if (live) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -492,7 +494,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         }
 #pragma unroll
         for (int u = 0; u < 32; ++u)  // (where this half saw nothing its output may be anything)
-          o[u] = mine == 0 || unit == 0.0f || l == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[u]) * unit);
+          o[u] = mine == 0 || own == 0.0f ? 0 : __float_as_uint(__uint_as_float(o[u]) * own * unit);
         if (other != 0.0f) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
@@ -511,7 +513,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv, __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+              y[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]), __uint_as_float(o[8 * u + 2 * e + 1]));
             dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
@@ -605,17 +607,21 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
         }
         const bool first = t == 0 && u == w.u0;
         const int tile_top = __shfl_sync(0xffffffffu, top, 4 * t);
+        const int kb = w.w.kbase + (u + t) * C::SPAN;
+        const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN;
+        // At an edge a row may see nothing of a block far above the units, and
+        // what it has summed must not vanish in that block's (five such tiles at
+        // most lie behind a row's last key): the plain form.
+        const bool above = edge && !first && exponent > -1000 && tile_top > exponent + 24;
         if (first || tile_top > exponent + 7) exponent = tile_top;  // -1000: nothing is there yet
         const int up = ev - exponent;  // at most 7
-        const uint32_t low = __ballot_sync(0xffffffffu, there && up < -15) >> (4 * t) & 15;
+        const uint32_t low = above ? have : __ballot_sync(0xffffffffu, there && up < -15) >> (4 * t) & 15;
         RawNote& n = notes.raw[slot];
         if (mine == t) {
           n.k_scale[j] = there ? sf_value(sk) : -1.0f;
           n.v_mul[j] = !there ? 0 : up < -14 ? 0x00010001u << max(up + 24, 0) : static_cast<uint32_t>(up + 15) * 0x04000400u;
         }
         if (lane == 0) {
-          const int kb = w.w.kbase + (u + t) * C::SPAN;
-          const bool edge = kb < w.lo_max || kb > w.hi_min - C::SPAN;
           n.state = 1 | (first ? 2 : 0) | (edge ? 4 : 0) | (!edge && have == 15 && low == 0 ? 8 : 0);
           n.exponent = exponent;
           n.kb = kb, n.lo = w.lo_min, n.hi = w.hi_max;

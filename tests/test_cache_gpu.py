@@ -616,3 +616,106 @@ print("fine")
 """ % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ calls that programs make and the tests above do not
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 5, 40])
+def test_two_sequences_share_a_prefix(D, new):
+    """The same page numbers twice in the table: both read them, neither writes."""
+    x = ref.make(41, 8, 2, D, 16, [new + 300, new + 200], [new, new])
+    x.table[1, :10] = x.table[0, :10]
+    d = Dev(x)
+    d.fwd()
+    check_fwd(x, d, True, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", [(2, (8, 2)), (6, (4, 1)), (24, (2, 1)), (90, (4, 2)), (130, (2, 2))])
+def test_same_inputs_same_bits_with_more_rows(D, new, heads):
+    x = ref.make(42, *heads, D, 64, [4000, 500, new], [new, new // 2, new])
+    d = Dev(x)
+    d.fwd()
+    first = d.out.clone(), d.lse.clone()
+    for _ in range(3):
+        d.out.fill_(7), d.lse.fill_(7)
+        d.fwd()
+        assert torch.equal(first[0], d.out) and torch.equal(first[1], d.lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", [(2, (4, 1)), (3, (8, 1)), (12, (4, 1)), (30, (1, 1)), (130, (2, 1))])
+@pytest.mark.parametrize("sf", [230, 254])
+def test_fwd_a_huge_value_hidden_from_all_but_the_last_row(D, new, heads, sf):
+    """The last token alone in its block, of a scale far above the others: it decides the last row and leaves no trace
+    in the others."""
+    for keys in (497, 2593):
+        x = ref.make(43, *heads, D, 32, [keys], [new], jitter=1)
+        block = (keys - 1) // 16
+        x.v_sf[x.table[0, block // 2], :, block % 2] = sf
+        codes = x.v_codes[x.table[0, block // 2], :, (keys - 1) % 32]
+        x.v_codes[x.table[0, block // 2], :, (keys - 1) % 32] = codes & 0x87  # below 2^-5: finite in the result
+        d = Dev(x)
+        d.fwd()
+        check_fwd(x, d, True, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", [(1, (4, 1)), (3, (8, 1)), (12, (4, 1)), (40, (2, 1)), (130, (2, 1))])
+@pytest.mark.parametrize("sf", [3, 246])
+def test_fwd_largest_and_smallest_values(D, new, heads, sf):
+    """Values up to 448 2^119 (a sum of two is not finite in fp32) and from 2^-133 on."""
+    for keys in (497, 2593):
+        x = ref.make(48, *heads, D, 32, [keys], [new], jitter=1)
+        x.v_sf[x.v_sf != 255] = sf
+        d = Dev(x)
+        d.fwd()
+        check_fwd(x, d, True, 0)
+        x.v_sf[x.table[0, 3], :, 0] = 200 - sf // 2  # blocks far apart as well: many rows take the plain form
+        d = Dev(x)
+        d.fwd()
+        check_fwd(x, d, True, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", [(3, (2, 1)), (3, (5, 1)), (6, (4, 1)), (28, (1, 1)), (48, (1, 1)), (140, (1, 1))])
+def test_fwd_a_nan_value_stays_with_the_rows_that_see_it(D, new, heads):
+    for keys in (299, 2603):
+        x = ref.make(44, *heads, D, 32, [keys], [new])
+        at = keys - max(1, new // 2)
+        page, slot = x.table[0, at // 32], at % 32
+        was = x.v_codes[page, :, slot, 9].copy()
+        x.v_codes[page, :, slot, 9] = 0x7F
+        d = Dev(x)
+        d.fwd()
+        x.v_codes[page, :, slot, 9] = was
+        got = host(d.out)
+        ro = ref.attend(x, True, 0, 1 / math.sqrt(D))
+        tol, _ = ref.attend_bounds(x, *ro)
+        for i in range(new):
+            sees = at < ref.seen(keys, new, i, True, 0)[1]
+            ok = np.abs(got[i] - ro[0][i]) <= tol[i]
+            assert np.delete(ok, 9, -1).all(), (keys, i)
+            assert np.isnan(got[i, :, 9]).all() if sees else ok[:, 9].all(), (keys, i)
+
+
+def test_two_graphs_take_turns_with_one_workspace():
+    xs = [ref.make(45 + i, 16, 2, 128, 64, [3000 + 500 * i, 70], [n, 1]) for i, n in enumerate((1, 12))]
+    ds = [Dev(x) for x in xs]
+    size = max(gdpa.gdpa_cache_workspace_size(d.cache, 16, 12) for d in ds)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for d in ds:
+        d.fwd(workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.fwd(workspace=ws)
+        graphs.append(g)
+    for d in ds:
+        d.out.fill_(7), d.lse.fill_(7)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    for x, d in zip(xs, ds):
+        check_fwd(x, d, True, 0)
