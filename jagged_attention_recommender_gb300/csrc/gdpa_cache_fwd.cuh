@@ -18,15 +18,15 @@
 // 2^(x - r) with a reference r 7 below the running maximum when it was last
 // moved, and r only moves when a score exceeds it by 15: weights stay below
 // 2^15 (fp16 holds 65504), those down to 2^-21 of the maximum (2^-15 with a
-// scale 2^6 below) keep 11 bits, and nothing above 2^-31 (2^-25) of it is lost.  The row sum takes the weights before
-// their rounding to fp16.
+// scale 2^6 below) keep 11 bits, and nothing above 2^-31 (2^-25) of it is lost.
+// The row sum takes the weights before their rounding to fp16.
 //
 // Bound: memory, 2 D bytes a key and head, with the latency of a warp's own
 // instructions close behind (conversions, byte shuffles, products).  Measured:
 // one token of 64 histories of 100 to 8192 keys, 32 query and 8 key heads of 128,
 // 98 us (5.6 TB/s); of 512 histories of up to 1023 keys, 8 and 8 heads of 64, 75 us
-// (3.6 TB/s; the start and the join are 12 us of it); 32
-// rows of 128 samples, 8 and 8 heads of 64, 172 us.
+// (3.6 TB/s; the start and the join are 12 us of it); 32 rows of 128 samples, 8
+// and 8 heads of 64, 172 us.
 //
 // Work split.  A segment is (sequence, up to 8 NT query rows of one key head);
 // a step is SPAN keys of it.  The steps of all segments are counted from the
