@@ -354,14 +354,17 @@ def _device() -> int:
     return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
 
 
-def _at(where, device, dtype, t):
-    """The address of a tensor of type ``dtype`` on ``device``; another one is refused (addresses and None pass)."""
+def _at(where, device, dtype, t, strided=False):
+    """The address of a tensor of type ``dtype`` on ``device``, contiguous unless it comes with a stride; another one
+    is refused (addresses and None pass)."""
     if t is None or t.__class__ is int:
         return t
     if t.dtype is not _dtypes[dtype]:
         raise TypeError("%s: %s wanted, got %s" % (where, dtype, t.dtype))
     if t.get_device() != device:
         raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
+    if not strided and not t.is_contiguous():
+        raise ValueError("%s: a contiguous tensor wanted, got strides %r" % (where, t.stride()))
     return t.data_ptr()
 
 
@@ -392,8 +395,8 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
     ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
     d, where = _device(), "gdpa_cache_append"
     _check(lib().gdpa_cache_append(
-        cache.addr, _at(where, d, "bfloat16", q), q_stride, _at(where, d, "bfloat16", k), k_stride,
-        _at(where, d, "bfloat16", v), v_stride, _at(where, d, "int32", offsets), _at(where, d, "int32", kv_lens),
+        cache.addr, _at(where, d, "bfloat16", q, True), q_stride, _at(where, d, "bfloat16", k, True), k_stride,
+        _at(where, d, "bfloat16", v, True), v_stride, _at(where, d, "int32", offsets), _at(where, d, "int32", kv_lens),
         _at(where, d, "int32", page_table), T, B, Hq, max_pages, _at(where, d, "bfloat16", q_out),
         _stream_on(d) if stream is None else _stream(stream)), where)
 
@@ -407,7 +410,7 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
     _check(lib().gdpa_cache_fwd(
-        cache.addr, _at(where, d, "bfloat16", q), q_stride, _at(where, d, "int32", offsets),
+        cache.addr, _at(where, d, "bfloat16", q, True), q_stride, _at(where, d, "int32", offsets),
         _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, max_q, causal,
         window_tokens, scale, _at(where, d, "bfloat16", out), _at(where, d, "float32", lse),
         _at(where, d, "uint8", workspace), workspace_bytes, _stream_on(d) if stream is None else _stream(stream)), where)

@@ -719,3 +719,13 @@ def test_two_graphs_take_turns_with_one_workspace():
             g.replay()
     for x, d in zip(xs, ds):
         check_fwd(x, d, True, 0)
+
+
+def test_a_slice_of_a_wider_table_is_refused():
+    x = ref.make(49, 8, 2, 64, 16, [100, 50], [1, 1])
+    d = Dev(x)
+    d.table = torch.nn.functional.pad(d.table, (0, 3))[:, :d.table.shape[1]]
+    with pytest.raises(ValueError, match="contiguous"):
+        d.fwd()
+    with pytest.raises(ValueError, match="contiguous"):
+        d.append()
