@@ -7,12 +7,11 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "gdpa_cache_index.h"
 #include "gdpa_fwd_common.cuh"
 #include "gdpa_internal.h"
 
 namespace gdpa {
-
-constexpr int kCacheBlock = 16;  // tokens that share a scale, per head
 
 struct CacheView {
   uint8_t* k;
@@ -84,20 +83,10 @@ __device__ __forceinline__ int find_sequence_warp(const int32_t* __restrict__ of
   return lo;
 }
 
-// Sequence b's rows and length.  ok = 0 (and the launch is flagged) when its
-// offsets do not describe rows of the tensors or its length does not fit the
-// page table.
-struct CacheSeq {
-  int first, n, len, ok;
-};
+// Sequence b's rows and length (an invalid one flags the launch).
 __device__ __forceinline__ CacheSeq load_sequence(const CacheBatch& c, int lp, int b) {
-  CacheSeq s;
-  s.first = __ldg(c.offsets + b);
-  const int end = __ldg(c.offsets + b + 1);
-  s.len = __ldg(c.kv_lens + b);
-  s.n = end - s.first;
-  s.ok = s.first >= 0 && end >= s.first && end <= c.T && s.len >= 0 &&
-         s.len <= (static_cast<int64_t>(c.max_pages) << lp);
+  const CacheSeq s = cache_sequence(__ldg(c.offsets + b), __ldg(c.offsets + b + 1), __ldg(c.kv_lens + b), c.T,
+                                    static_cast<int64_t>(c.max_pages) << lp);
   if (!s.ok) atomicOr(c.status, kStatusBadPlan);
   return s;
 }

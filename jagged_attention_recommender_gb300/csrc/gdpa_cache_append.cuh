@@ -228,14 +228,13 @@ __global__ void __launch_bounds__(kAppendThreads, 3) gdpa_cache_append_kernel(co
     if (lane < rows_per_cta && r < bt.T) {
       if (b == b0 + 32) b = find_sequence(bt.offsets, bt.B, r);  // many empty sequences
       if (b < bt.B) {
-        const CacheSeq s = load_sequence(bt, p.cache.lp, b);
-        const int pos = s.len - s.n + (r - s.first);
-        if (s.ok && s.len < s.n) atomicOr(bt.status, kStatusBadPlan);
-        if (s.ok && s.len >= s.n && r >= s.first && (r == s.first || (pos & 15) == 0)) {
+        const OwnedRows rows = owned_rows(load_sequence(bt, p.cache.lp, b), r);
+        if (rows.bad) atomicOr(bt.status, kStatusBadPlan);
+        if (rows.cnt > 0) {
           o.row = r;
-          o.pos = pos;
-          o.cnt = min(kCacheBlock - (pos & 15), s.first + s.n - r);
-          o.page = load_page(p.cache, bt, b, pos);
+          o.pos = rows.pos;
+          o.cnt = rows.cnt;
+          o.page = load_page(p.cache, bt, b, rows.pos);
         }
       }
     }
@@ -247,7 +246,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) gdpa_cache_append_kernel(co
     }
     o.tab = tab - o.cnt;
     // Blocks of one group never overlap, so that their rows fit the table;
-    // offsets that decrease can make them, and are caught here.
+    // offsets that decrease can make them, and are caught here (no count is
+    // negative, so a place in the table never is).
     if (o.cnt > 0 && tab > rows_per_cta + kCacheBlock - 1) {
       o.cnt = 0;
       atomicOr(bt.status, kStatusBadPlan);
