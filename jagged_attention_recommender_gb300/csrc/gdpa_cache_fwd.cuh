@@ -221,7 +221,7 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int b) {
   w.steps = 0;
   w.tiles = 0;
   if (!w.s.ok || w.s.n == 0) return w;
-  if (p.window > 0) w.kbase = max(0, w.s.len - w.s.n - p.window + 1) & ~(C::SPAN - 1);
+  w.kbase = first_key(w.s.len - w.s.n, p.window) & ~(C::SPAN - 1);
   // (a length may be as large as 2^31 - 16)
   w.steps = static_cast<int>((static_cast<unsigned>(max(w.s.len - w.kbase, 1)) + C::SPAN - 1) / C::SPAN);
   w.tiles = static_cast<int>((static_cast<unsigned>(w.s.n) * p.G + C::ROWS - 1) / C::ROWS);  // T G is below 2^31
@@ -332,9 +332,9 @@ struct Walk {
     map.begin(p, row0);
     const int pos0 = s.len - s.n + map.tok0;
     const int pos1 = s.len - s.n + map.token(p, rows - 1);
-    lo_min = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+    lo_min = first_key(pos0, p.window);
     hi_max = max(0, p.causal ? min(s.len, pos1 + 1) : s.len);
-    lo_max = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
+    lo_max = first_key(pos1, p.window);
     hi_min = max(0, p.causal ? min(s.len, pos0 + 1) : s.len);
     u0 = max(u0, (lo_min - w.kbase) / C::SPAN);
     u1 = hi_max > w.kbase ? min(u1, (hi_max - 1 - w.kbase) / C::SPAN + 1) : u0;
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
         const int col = nt * 8 + 2 * t + c;
         fac[nt][c] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * c);
         const int pos = s.len - s.n + now.map.token(p, col);
-        lo[nt][c] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+        lo[nt][c] = first_key(pos, p.window);
         hi[nt][c] = col < rows ? (p.causal ? min(s.len, pos + 1) : s.len) : 0;
       }
     }

@@ -48,4 +48,9 @@ GDPA_HD OwnedRows owned_rows(const CacheSeq& s, int r) {
   return o;
 }
 
+// The first key that the row at position `pos` (negative in front of the first
+// token) sees through a window of `window` tokens, 0 for none.  (pos - window
+// alone can lie below -2^31.)
+GDPA_HD int first_key(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
 }  // namespace gdpa

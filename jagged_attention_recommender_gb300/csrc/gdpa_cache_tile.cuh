@@ -224,7 +224,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     const int64_t out_row = tok * p.Hq + head;
     const int pos = s.len - s.n + in_seq;
     // keys this row sees: [lo, hi)
-    const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    const int lo = first_key(pos, p.window);
     const int hi = valid ? max(0, p.causal ? min(s.len, pos + 1) : s.len) : 0;
     const int steps = w.u1 - w.u0;
     const bool live = (ri & ~31) < w.rows;  // a warp without rows keeps the barriers' protocol

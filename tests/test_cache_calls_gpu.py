@@ -38,3 +38,17 @@ def test_append_with_decreasing_offsets_stays_inside():
     d = Dev(x, inv_freq(D))
     d.append()
     check_append(x, d, inv_freq(D), False)
+
+
+FEW_MANY = [(4, 1), (64, 2)]  # six rows of one: the kernel for few rows (24) and for many (192)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", FEW_MANY)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30, 7, 6])
+def test_a_window_of_any_size_with_more_rows_than_tokens(D, heads, window):
+    """Rows in front of the first token have negative positions: a window near 2^31 in front of them is still one."""
+    x = ref.make(62, *heads, D, 16, [2, 3, 40], [5, 6, 4])
+    d = Dev(x, pad=1)
+    d.fwd(window=window)
+    check_fwd(x, d, True, window)

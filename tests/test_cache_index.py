@@ -59,6 +59,8 @@ extern "C" int owners(const int* off, const int* lens, int T, int B, long long m
   }
   return found;
 }
+
+extern "C" int first(int pos, int window) { return first_key(pos, window); }
 """
 
 
@@ -135,3 +137,10 @@ def test_right_offsets_give_every_row_to_one_owner(host, seed, rows):
         times[r:r + cnt] += 1
         assert pos == lens[b] - new[b] + r - off[b]
     assert (times[:off[-1]] == 1).all() and (times[off[-1]:] == 0).all()
+
+
+def test_a_window_s_first_key(host):
+    ends = [-2 ** 31 + 256, -2 ** 31 + 300, -5, -1, 0, 1, 2, 6, 7, 2 ** 20, 2 ** 31 - 17]
+    for pos in ends:
+        for window in (0, 1, 2, 6, 7, 8, 2 ** 20, 2 ** 31 - 4, 2 ** 31 - 1):
+            assert host.first(pos, window) == (max(0, pos - window + 1) if window else 0), (pos, window)
