@@ -368,6 +368,44 @@ def _at(where, device, dtype, t, strided=False):
     return t.data_ptr()
 
 
+def _rows_at(where, device, cache, t, stride, T, heads=0):
+    """The address of bf16 rows ``stride`` apart, T of them or more, each of ``heads`` heads (0: the cache's) of D
+    elements side by side; a tensor laid out in another way is refused."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not _dtypes["bfloat16"] or t.get_device() != device:
+        return _at(where, device, "bfloat16", t, True)
+    heads, D, st = heads or cache.H, cache.D, t.stride()
+    if st == (stride, D, 1):
+        n, h, d = t.shape
+        if h == heads and d == D and n >= T:
+            return t.data_ptr()
+    if T <= 0:
+        return t.data_ptr()
+    shape = t.shape
+    dims = [(n, s) for n, s in zip(shape, st) if n != 1]  # the stride of a single element says nothing
+    rows = 0
+    if dims and dims[-1][1] == 1:
+        if dims[-1][0] == D and heads == 1:
+            rows, dims = 1, dims[:-1]
+        elif dims[-1][0] == D and len(dims) > 1 and dims[-2] == (heads, D):
+            rows, dims = 1, dims[:-2]
+        elif dims[-1][0] == D and len(dims) == 2 and dims[0][1] == D and stride == heads * D:
+            rows, dims = dims[0][0] // heads, []  # all heads of all rows one behind the other
+        elif dims[-1][0] >= heads * D:  # rows not cut into heads, or one behind the other
+            rows = 1 + ((dims[-1][0] - heads * D) // stride if len(dims) == 1 and stride > 0 else 0)
+            dims = dims[:-1]
+    step = stride
+    for n, s in reversed(dims):
+        if s != step:
+            rows = 0
+        rows, step = rows * n, step * n
+    if rows < T:
+        raise ValueError("%s: %d rows of %d heads of %d side by side wanted, %d elements apart, got shape %r, strides %r"
+                         % (where, T, heads, D, stride, tuple(shape), st))
+    return t.data_ptr()
+
+
 class KvCache:
     """A gdpa_cache_t over the caller's tensors, which it keeps alive: codes uint8 ``[num_pages, H, page_tokens, D]``
     (e4m3), scales uint8 ``[num_pages, H, page_tokens // 16]`` (E8M0), ``inv_freq`` host float64 ``[rot_dim // 2]``
@@ -382,6 +420,7 @@ class KvCache:
         device = _device()
         at = [_at("KvCache", device, "uint8", t) for t in (k_codes, v_codes, k_sf, v_sf)]
         self.tensors = (k_codes, v_codes, k_sf, v_sf)
+        self.H, self.D = H, D
         self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
         n = 0 if self.inv_freq is None else self.inv_freq.size
         self.desc = _CacheDesc(*at, pages, tokens, H, D,
@@ -395,9 +434,10 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
     ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
     d, where = _device(), "gdpa_cache_append"
     _check(lib().gdpa_cache_append(
-        cache.addr, _at(where, d, "bfloat16", q, True), q_stride, _at(where, d, "bfloat16", k, True), k_stride,
-        _at(where, d, "bfloat16", v, True), v_stride, _at(where, d, "int32", offsets), _at(where, d, "int32", kv_lens),
-        _at(where, d, "int32", page_table), T, B, Hq, max_pages, _at(where, d, "bfloat16", q_out),
+        cache.addr, _rows_at(where, d, cache, q, q_stride, T, Hq), q_stride,
+        _rows_at(where, d, cache, k, k_stride, T), k_stride,
+        _rows_at(where, d, cache, v, v_stride, T), v_stride, _at(where, d, "int32", offsets),
+        _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, _at(where, d, "bfloat16", q_out),
         _stream_on(d) if stream is None else _stream(stream)), where)
 
 
@@ -410,7 +450,7 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
     _check(lib().gdpa_cache_fwd(
-        cache.addr, _at(where, d, "bfloat16", q, True), q_stride, _at(where, d, "int32", offsets),
+        cache.addr, _rows_at(where, d, cache, q, q_stride, T, Hq), q_stride, _at(where, d, "int32", offsets),
         _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, max_q, causal,
         window_tokens, scale, _at(where, d, "bfloat16", out), _at(where, d, "float32", lse),
         _at(where, d, "uint8", workspace), workspace_bytes, _stream_on(d) if stream is None else _stream(stream)), where)
