@@ -354,9 +354,9 @@ def _device() -> int:
     return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
 
 
-def _at(where, device, dtype, t, strided=False):
-    """The address of a tensor of type ``dtype`` on ``device``, contiguous unless it comes with a stride; another one
-    is refused (addresses and None pass)."""
+def _at(where, device, dtype, t, least=0, cache=None, strided=False):
+    """The address of a tensor of type ``dtype`` on ``device``, of ``least`` elements (heads of ``cache``) or more,
+    contiguous unless it comes with a stride; another one is refused (addresses and None pass)."""
     if t is None or t.__class__ is int:
         return t
     if t.dtype is not _dtypes[dtype]:
@@ -365,7 +365,19 @@ def _at(where, device, dtype, t, strided=False):
         raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
     if not strided and not t.is_contiguous():
         raise ValueError("%s: a contiguous tensor wanted, got strides %r" % (where, t.stride()))
+    if cache is not None:
+        least *= cache.D
+    if t.numel() < least:
+        raise ValueError("%s: a %s tensor of %d elements or more wanted, got shape %r" % (where, dtype, least, tuple(t.shape)))
     return t.data_ptr()
+
+
+def _table_at(where, device, t, B, max_pages):
+    """The address of a page table whose rows are ``max_pages`` entries."""
+    at = _at(where, device, "int32", t, B * max_pages)
+    if B > 1 and t.__class__ is not int and t is not None and t.dim() > 1 and t.shape[-1] != max_pages:
+        raise ValueError("%s: a page table of %d entries a row wanted, got shape %r" % (where, max_pages, tuple(t.shape)))
+    return at
 
 
 def _rows_at(where, device, cache, t, stride, T, heads=0):
@@ -374,7 +386,7 @@ def _rows_at(where, device, cache, t, stride, T, heads=0):
     if t is None or t.__class__ is int:
         return t
     if t.dtype is not _dtypes["bfloat16"] or t.get_device() != device:
-        return _at(where, device, "bfloat16", t, True)
+        return _at(where, device, "bfloat16", t, strided=True)
     heads, D, st = heads or cache.H, cache.D, t.stride()
     if st == (stride, D, 1):
         n, h, d = t.shape
@@ -433,11 +445,13 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
     """Stores the new tokens' ``k`` and ``v`` in the cache (``k`` rotated by position) and the rotated ``q`` in
     ``q_out``.  ``kv_lens``: tokens of each sequence after this call.  Strides of rows in elements."""
     d, where = _device(), "gdpa_cache_append"
+    n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
     _check(lib().gdpa_cache_append(
-        cache.addr, _rows_at(where, d, cache, q, q_stride, T, Hq), q_stride,
-        _rows_at(where, d, cache, k, k_stride, T), k_stride,
-        _rows_at(where, d, cache, v, v_stride, T), v_stride, _at(where, d, "int32", offsets),
-        _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, _at(where, d, "bfloat16", q_out),
+        cache.addr, _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
+        _rows_at(where, d, cache, k, k_stride, n), k_stride, _rows_at(where, d, cache, v, v_stride, n), v_stride,
+        _at(where, d, "int32", offsets, b + 1), _at(where, d, "int32", kv_lens, b),
+        _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages,
+        _at(where, d, "bfloat16", q_out, 0 if q is None else n * Hq, cache),
         _stream_on(d) if stream is None else _stream(stream)), where)
 
 
@@ -449,11 +463,13 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     d, where = _device(), "gdpa_cache_fwd"
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
+    n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
     _check(lib().gdpa_cache_fwd(
-        cache.addr, _rows_at(where, d, cache, q, q_stride, T, Hq), q_stride, _at(where, d, "int32", offsets),
-        _at(where, d, "int32", kv_lens), _at(where, d, "int32", page_table), T, B, Hq, max_pages, max_q, causal,
-        window_tokens, scale, _at(where, d, "bfloat16", out), _at(where, d, "float32", lse),
-        _at(where, d, "uint8", workspace), workspace_bytes, _stream_on(d) if stream is None else _stream(stream)), where)
+        cache.addr, _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride, _at(where, d, "int32", offsets, b + 1),
+        _at(where, d, "int32", kv_lens, b), _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages, max_q,
+        causal, window_tokens, scale, _at(where, d, "bfloat16", out, n * Hq, cache),
+        _at(where, d, "float32", lse, n * Hq), _at(where, d, "uint8", workspace, workspace_bytes), workspace_bytes,
+        _stream_on(d) if stream is None else _stream(stream)), where)
 
 
 def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:

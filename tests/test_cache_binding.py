@@ -130,3 +130,35 @@ def test_layouts_that_it_would_misread(calls, i):
         with pytest.raises(ValueError, match="rows of"):
             append(**{name: t, name + "_stride": stride})
     assert calls.append == calls.fwd == 0
+
+
+def test_tensors_that_are_too_small_for_the_call(calls):
+    short = dict(offsets=i32(B), kv_lens=i32(B - 1), page_table=i32(B - 1, WIDTH))
+    for name, t in short.items():
+        for call in (append, fwd):
+            with pytest.raises(ValueError, match="elements or more"):
+                call(**{name: t})
+    with pytest.raises(ValueError, match="elements or more"):
+        append(q_out=bf(T, HQ - 1, D))
+    for kw in (dict(out=bf(T - 1, HQ, D)), dict(lse=torch.zeros(T, HQ - 1)), dict(workspace_bytes=65)):
+        with pytest.raises(ValueError, match="elements or more"):
+            fwd(**kw)
+    for call in (append, fwd):  # rows wider or narrower than max_pages: another sequence's pages would be read
+        for width in (WIDTH - 1, WIDTH + 2):
+            with pytest.raises(ValueError, match="entries a row|elements or more"):
+                call(page_table=i32(2 * B, width))
+    assert calls.append == calls.fwd == 0
+
+
+def test_tensors_with_room_to_spare(calls):
+    more = dict(offsets=i32(B + 9), kv_lens=i32(B + 8), page_table=i32(B + 8, WIDTH))
+    append(q_out=bf(T + 2, HQ, D), **more)
+    append(page_table=i32(B * WIDTH))
+    append(q=None, q_stride=0, q_out=bf(0))
+    fwd(out=bf(T + 2, HQ, D), lse=torch.zeros(T + 2, HQ), **more)
+    fwd(lse=None, workspace_bytes=60)
+    fwd(page_table=i32(1, WIDTH + 3), B=1)  # one sequence: its row may be wider
+    for kw in (dict(T=0), dict(B=0)):  # nothing to do
+        append(offsets=i32(0), kv_lens=i32(0), page_table=i32(0), q_out=bf(0), **kw)
+        fwd(offsets=i32(0), kv_lens=i32(0), page_table=i32(0), out=bf(0), lse=torch.zeros(0), **kw)
+    assert calls.append == 5 and calls.fwd == 5
