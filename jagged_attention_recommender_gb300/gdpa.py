@@ -342,16 +342,18 @@ def gdpa_wait_selftest(timeout_ms: int, stream=None):
 
 _torch = None
 _dtypes = None
+_cuda = False  # whether torch has found a CUDA device
 
 
 def _device() -> int:
     """The current CUDA device (-2: there is none)."""
-    global _torch, _dtypes
+    global _torch, _dtypes, _cuda
     if _torch is None:
         import torch
         _dtypes = {n: getattr(torch, n) for n in ("bfloat16", "int32", "float32", "uint8")}
         _torch = torch
-    return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
+    _cuda = _cuda or _torch.cuda.is_available()
+    return _torch.cuda.current_device() if _cuda else -2
 
 
 def _at(where, device, dtype, t, least=0, cache=None, strided=False):
