@@ -382,6 +382,13 @@ def _table_at(where, device, t, B, max_pages):
     return at
 
 
+def _cache_at(where, device, cache):
+    """The address of the cache's descriptor; a cache on another device than the current one is refused."""
+    if getattr(cache, "device", device) != device:
+        raise ValueError("%s: the cache is on cuda:%d, not on the current CUDA device" % (where, cache.device))
+    return cache.addr
+
+
 def _rows_at(where, device, cache, t, stride, T, heads=0):
     """The address of bf16 rows ``stride`` apart, T of them or more, each of ``heads`` heads (0: the cache's) of D
     elements side by side; a tensor laid out in another way is refused."""
@@ -434,7 +441,7 @@ class KvCache:
         device = _device()
         at = [_at("KvCache", device, "uint8", t) for t in (k_codes, v_codes, k_sf, v_sf)]
         self.tensors = (k_codes, v_codes, k_sf, v_sf)
-        self.H, self.D = H, D
+        self.H, self.D, self.device = H, D, device
         self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
         n = 0 if self.inv_freq is None else self.inv_freq.size
         self.desc = _CacheDesc(*at, pages, tokens, H, D,
@@ -449,7 +456,7 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
     d, where = _device(), "gdpa_cache_append"
     n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
     _check(lib().gdpa_cache_append(
-        cache.addr, _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
+        _cache_at(where, d, cache), _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
         _rows_at(where, d, cache, k, k_stride, n), k_stride, _rows_at(where, d, cache, v, v_stride, n), v_stride,
         _at(where, d, "int32", offsets, b + 1), _at(where, d, "int32", kv_lens, b),
         _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages,
@@ -467,9 +474,10 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.numel()
     n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
     _check(lib().gdpa_cache_fwd(
-        cache.addr, _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride, _at(where, d, "int32", offsets, b + 1),
-        _at(where, d, "int32", kv_lens, b), _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages, max_q,
-        causal, window_tokens, scale, _at(where, d, "bfloat16", out, n * Hq, cache),
+        _cache_at(where, d, cache), _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
+        _at(where, d, "int32", offsets, b + 1), _at(where, d, "int32", kv_lens, b),
+        _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages, max_q, causal, window_tokens, scale,
+        _at(where, d, "bfloat16", out, n * Hq, cache),
         _at(where, d, "float32", lse, n * Hq), _at(where, d, "uint8", workspace, workspace_bytes), workspace_bytes,
         _stream_on(d) if stream is None else _stream(stream)), where)
 

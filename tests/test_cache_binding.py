@@ -162,3 +162,16 @@ def test_tensors_with_room_to_spare(calls):
         append(offsets=i32(0), kv_lens=i32(0), page_table=i32(0), q_out=bf(0), **kw)
         fwd(offsets=i32(0), kv_lens=i32(0), page_table=i32(0), out=bf(0), lse=torch.zeros(0), **kw)
     assert calls.append == 5 and calls.fwd == 5
+
+
+def test_a_cache_on_another_device_than_the_current_one(calls, monkeypatch):
+    """Codes of one device must not be read by a launch on another, whatever the other tensors are."""
+    c = cache()
+    bare = dict(q=1 << 20, k=1 << 20, v=1 << 20, offsets=1 << 20, kv_lens=1 << 20, page_table=1 << 20, q_stride=HQ * D)
+    monkeypatch.setattr(gdpa, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        append(cache=c, q_out=1 << 20, k_stride=H * D, v_stride=H * D, **bare)
+    del bare["k"], bare["v"]
+    with pytest.raises(ValueError, match="current CUDA device"):
+        fwd(cache=c, out=1 << 20, lse=None, workspace=1 << 20, workspace_bytes=64, **bare)
+    assert calls.append == calls.fwd == 0
