@@ -484,7 +484,8 @@ typedef struct {
  * finite becomes the NaN code.
  *
  * Strides are in elements, multiples of 8, and at least H * D (Hq * D); q, k,
- * v and q_out 16-byte aligned.  Two sequences may share pages that both only
+ * v and q_out 16-byte aligned.  T is below 2^31 - 256, B below 2^31 - 4097,
+ * max_pages * page_tokens below 2^31.  Two sequences may share pages that both only
  * read; a block into which both append has undefined contents.
  *
  * Asynchronous on `stream`, one kernel, no allocation, no host read of device

@@ -73,7 +73,8 @@ gdpa_status_t check_rows(const void* p, int64_t stride, int64_t H, int64_t D) {
 
 gdpa_status_t check_batch(const gdpa_cache_t* c, int64_t T, int B, int max_pages) {
   if (T < 0 || B < 0 || max_pages < 0) return GDPA_ERR_INVALID_ARG;
-  if (T >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
+  // Rows and sequences are counted in 32 bits, up to a warp's or a block's stretch past the last one.
+  if (T >= ((int64_t)1 << 31) - 256 || B >= INT32_MAX - 4096) return GDPA_ERR_UNSUPPORTED;
   if ((int64_t)max_pages * c->page_tokens >= (int64_t)1 << 31) return GDPA_ERR_UNSUPPORTED;
   return GDPA_OK;
 }
