@@ -103,6 +103,12 @@ struct TileCfg {
 
 namespace tile {
 
+// What the roles of a CTA tell one another while they wait.
+struct Watch {
+  int abort;  // a wait has given up
+  int turns;  // steps of the plain form that warps have taken
+};
+
 struct Bars {
   uint64_t raw_full[8], raw_free[8];
   uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2];
@@ -111,8 +117,30 @@ struct Bars {
   uint64_t x_full, x_free;                          // the second half's result is there, is read
   uint64_t drain[2];
   uint32_t tmem;
-  int abort;
+  Watch watch;
 };
+
+// ptx::mbar_wait for the roles of a CTA.  A segment in the plain form takes
+// hundreds of times as long as its tiles, and every role may wait for it: the
+// limit is on the time in which no warp gets on with it.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile Watch* watch) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = ptx::global_timer_ns();
+  int turns = watch->turns;
+  while (true) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (watch->abort) return false;
+    const uint64_t now = ptx::global_timer_ns();
+    const int at = watch->turns;
+    if (at != turns) {
+      turns = at;
+      t0 = now;
+    } else if (now - t0 > limit_ns) {
+      return false;
+    }
+  }
+}
 
 // Beside the codes of a tile, in their ring.
 struct __align__(16) RawNote {
@@ -138,10 +166,11 @@ struct Notes {
 };
 
 // One row of a segment over keys [j0, j1), one warp, D / 32 coordinates a lane:
-// the plain form, for segments that the tensor core cannot take.  o: the mean.
+// the plain form, for segments that the tensor core cannot take.  o: the mean;
+// turns: where it shows that it gets on (every 64 keys).
 template <int D>
 __device__ __noinline__ void attend_row(const CacheFwdParams& p, int b, int h, int64_t q_at, int j0, int j1,
-                                        float& top, float& total, float* o) {
+                                        float& top, float& total, float* o, int* turns) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float q[E], m = -INFINITY, l = 0.0f;
@@ -152,6 +181,7 @@ __device__ __noinline__ void attend_row(const CacheFwdParams& p, int b, int h, i
   }
 #pragma unroll 1
   for (int j = j0; j < j1; ++j) {
+    if (((j - j0) & 63) == 0 && lane == 0) atomicAdd(turns, 1);
     const int page = load_page(p.cache, p.batch, b, j);
     if (page < 0) continue;
     const int slot = j & ((1 << p.cache.lp) - 1);
@@ -205,7 +235,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
   const int lane = threadIdx.x & 31, half = threadIdx.x >> 7, r = threadIdx.x & 127, quarter = r >> 5;
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t o_addr = tmem + lane_off + C::TM_O + half * 128;
-  volatile int* abort = &B.abort;
+  volatile Watch* watch = &B.watch;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
   uint32_t gi = 0, ti = 0, seg = 0, xs = 0;  // tiles of the CTA, of this half; segments with tiles; exchanges
@@ -233,7 +263,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     bool plain = false;
     if (steps > 0) {
       if (exchanged) {  // Q's room held the last segment's exchange
-        ok = ptx::mbar_wait(&B.x_free, (xs - 1) & 1, limit, abort);
+        ok = wait(&B.x_free, (xs - 1) & 1, limit, watch);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         exchanged = false;
@@ -273,7 +303,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
       for (int i = 0; i < steps; ++i, ++gi) {
         if (!pair && (i & 1) != half) continue;
         const int sb = ti & 1;
-        ok = ptx::mbar_wait(&B.s_full[half][sb], (ti >> 1) & 1, limit, abort);
+        ok = wait(&B.s_full[half][sb], (ti >> 1) & 1, limit, watch);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -360,7 +390,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
             }
             exponent = e_now;
             if (__any_sync(0xffffffffu, follow)) {
-              ok = ptx::mbar_wait(&B.pv_done[half][(ti - 1) & 1], ((ti - 1) >> 1) & 1, limit, abort);
+              ok = wait(&B.pv_done[half][(ti - 1) & 1], ((ti - 1) >> 1) & 1, limit, watch);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               ptx::tc_fence_after();
@@ -402,7 +432,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         ++mine;
       }
       if (!ok) break;
-      ok = ptx::mbar_wait(&B.o_full, seg & 1, limit, abort);
+      ok = wait(&B.o_full, seg & 1, limit, watch);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -420,7 +450,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         float top, total, o[E];
         const int64_t row_q = __shfl_sync(0xffffffffu, q_at, row), row_o = __shfl_sync(0xffffffffu, out_row, row);
         attend_row<D>(p, w.b, w.h, row_q, max(k0, __shfl_sync(0xffffffffu, lo, row)),
-                      min(k1, __shfl_sync(0xffffffffu, hi, row)), top, total, o);
+                      min(k1, __shfl_sync(0xffffffffu, hi, row)), top, total, o, &B.watch.turns);
         const int at_row = (ri & ~31) + row;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -470,7 +500,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
         ++xs;
         continue;
       }
-      ok = ptx::mbar_wait(&B.x_full, xs & 1, limit, abort);
+      ok = wait(&B.x_full, xs & 1, limit, watch);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (live) {
@@ -537,7 +567,7 @@ __device__ void run_softmax(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     ptx::tc_fence_before();  // O has been read when the next segment's P allows its first product
   }
   if (!ok && lane == 0) {
-    *abort = 1;
+    watch->abort = 1;
     atomicOr(p.batch.status, kStatusActivation);
   }
 }
@@ -551,7 +581,7 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
   // Eight tiles at a time: a lane looks after one block of one of them, so that
   // the latency of page and scales is met once for all.
   const int lane = threadIdx.x & 31, mine = lane >> 2, j = lane & 3;
-  volatile int* abort = &B.abort;
+  volatile Watch* watch = &B.watch;
   const int pmask = (1 << p.cache.lp) - 1;
   const uint32_t raw = ptx::smem_u32(sm + C::OFF_RAW) + j * kCacheBlock * D;
   split::Walk<C> w;
@@ -593,7 +623,7 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
 #pragma unroll 1
       for (int t = 0; t < cnt; ++t) {
         const int slot = gi % C::RAWS;
-        ok = ptx::mbar_wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, abort);
+        ok = wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, watch);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++gi;
@@ -634,7 +664,7 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
   }
   if (ok) {  // the last entry: no tile
     const int slot = gi % C::RAWS;
-    ok = ptx::mbar_wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, abort);
+    ok = wait(&B.raw_free[slot], ((gi / C::RAWS) & 1) ^ 1, limit, watch);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       ++gi;
@@ -645,7 +675,7 @@ __device__ void run_copies(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes&
     }
   }
   if (!ok && lane == 0) {
-    *abort = 1;
+    watch->abort = 1;
     atomicOr(p.batch.status, kStatusProducer);
   }
   // no copy may land after the CTA has ended
@@ -664,21 +694,21 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
   constexpr int NI = C::SPAN / RPI;         // ... and how often for a tile
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const int c = tid % CPR, r0 = tid / CPR;
-  volatile int* abort = &B.abort;
+  volatile Watch* watch = &B.watch;
   const int swap = c >> 2 & 1;
   uint32_t seg = 0xffffffffu;  // the segment's number
   bool ok = true;
 #pragma unroll 1
   for (uint32_t gi = 0;; ++gi) {
     const int slot = gi % C::RAWS, st = gi & 1;
-    ok = ptx::mbar_wait(&B.raw_full[slot], (gi / C::RAWS) & 1, limit, abort);
+    ok = wait(&B.raw_full[slot], (gi / C::RAWS) & 1, limit, watch);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const RawNote& n = notes.raw[slot];
     const uint32_t state = *const_cast<volatile const uint32_t*>(&n.state);
     if (!(state & 1)) break;
     seg += state >> 1 & 1;
-    ok = ptx::mbar_wait(V ? &B.v_free[st] : &B.k_free[st], ((gi >> 1) & 1) ^ 1, limit, abort);
+    ok = wait(V ? &B.v_free[st] : &B.k_free[st], ((gi >> 1) & 1) ^ 1, limit, watch);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const uint32_t from = ptx::smem_u32(sm + C::OFF_RAW) + slot * 2 * C::RAW + (V ? C::RAW : 0) + tid * 16;
@@ -734,7 +764,7 @@ __device__ void run_convert(const CacheFwdParams& p, uint8_t* sm, Bars& B, Notes
     ptx::mbar_arrive(&B.raw_free[slot]);
   }
   if (!ok && lane == 0) {
-    *abort = 1;
+    watch->abort = 1;
     atomicOr(p.batch.status, kStatusProducer);
   }
 }
@@ -747,7 +777,7 @@ template <int D>
 __device__ void run_scores(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t tmem,
                            const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, unsigned long long limit) {
   using C = TileCfg<D>;
-  volatile int* abort = &B.abort;
+  volatile Watch* watch = &B.watch;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
   uint32_t gi = 0, seg = 0, ti[2] = {0, 0};
@@ -760,20 +790,20 @@ __device__ void run_scores(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32
 #pragma unroll 1
   for (; ok && w.more(p, stop); w.next(p)) {
     if (!w.enter(p, at, stop) || w.u1 <= w.u0) continue;
-    ok = ptx::mbar_wait(&B.q_full, seg++ & 1, limit, abort);
+    ok = wait(&B.q_full, seg++ & 1, limit, watch);
     const int steps = w.u1 - w.u0;
     const bool pair = w.rows > C::HALF;
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++gi) {
       const int ks = gi & 1;
-      ok = ptx::mbar_wait(&B.k_full[ks], (gi >> 1) & 1, limit, abort);
+      ok = wait(&B.k_full[ks], (gi >> 1) & 1, limit, watch);
       if (!ok) break;
       const uint64_t k = k_desc + ks * (C::KV_BYTES >> 4);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!pair && (i & 1) != h) continue;
         const uint32_t sb = ti[h] & 1;
-        ok = ok && ptx::mbar_wait(&B.pv_done[h][sb], ((ti[h] >> 1) & 1) ^ 1, limit, abort);
+        ok = ok && wait(&B.pv_done[h][sb], ((ti[h] >> 1) & 1) ^ 1, limit, watch);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -788,7 +818,7 @@ __device__ void run_scores(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32
     }
   }
   if (!ok && (threadIdx.x & 31) == 0) {
-    *abort = 1;
+    watch->abort = 1;
     atomicOr(p.batch.status, kStatusMma);
   }
   // every MMA this warp issued is complete once this commit lands
@@ -802,7 +832,7 @@ template <int D>
 __device__ void run_values(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32_t tmem,
                            const split::Schedule<TileCfg<D>>& sh, int64_t at, int64_t stop, unsigned long long limit) {
   using C = TileCfg<D>;
-  volatile int* abort = &B.abort;
+  volatile Watch* watch = &B.watch;
   split::Walk<C> w;
   w.begin(p, sh.seq[0], sh.base[0], at);
   uint32_t gi = 0, ti[2] = {0, 0};
@@ -817,7 +847,7 @@ __device__ void run_values(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32
 #pragma unroll 1
     for (int i = 0; ok && i < steps; ++i, ++gi) {
       const int vs = gi & 1;
-      ok = ptx::mbar_wait(&B.v_full[vs], (gi >> 1) & 1, limit, abort);
+      ok = wait(&B.v_full[vs], (gi >> 1) & 1, limit, watch);
       if (!ok) break;
       const uint64_t v = v_desc + vs * (C::KV_BYTES >> 4);
       const bool first = i < (pair ? 1 : 2);  // a half's first in this segment
@@ -825,7 +855,7 @@ __device__ void run_values(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32
       for (int h = 0; h < 2; ++h) {
         if (!pair && (i & 1) != h) continue;
         const uint32_t sb = ti[h] & 1;
-        ok = ok && ptx::mbar_wait(&B.p_full[h][sb], (ti[h] >> 1) & 1, limit, abort);
+        ok = ok && wait(&B.p_full[h][sb], (ti[h] >> 1) & 1, limit, watch);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -841,7 +871,7 @@ __device__ void run_values(const CacheFwdParams& p, uint8_t* sm, Bars& B, uint32
     ptx::mma_commit_elect(&B.o_full);
   }
   if (!ok && (threadIdx.x & 31) == 0) {
-    *abort = 1;
+    watch->abort = 1;
     atomicOr(p.batch.status, kStatusMma);
   }
   ptx::mma_commit_elect(&B.drain[1]);
@@ -895,7 +925,7 @@ __global__ void __launch_bounds__(640, 1) gdpa_cache_tile_kernel(const CacheFwdP
     ptx::mbar_init(&B.o_full, 1);
     ptx::mbar_init(&B.x_full, 128);
     ptx::mbar_init(&B.x_free, 128);
-    B.abort = 0;
+    B.watch.abort = B.watch.turns = 0;
     ptx::fence_mbar_init();
   }
   if (tid < 8) notes.plain[tid] = 0;

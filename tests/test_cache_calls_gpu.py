@@ -2,6 +2,10 @@
 values at the ends of what the documentation allows."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -52,3 +56,40 @@ def test_a_window_of_any_size_with_more_rows_than_tokens(D, heads, window):
     d = Dev(x, pad=1)
     d.fwd(window=window)
     check_fwd(x, d, True, window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_plain_form_may_take_longer_than_a_wait_may(D):
+    """Every segment has a block of V far below the others and takes the plain form (about 50 ms a segment here), in
+    front of another segment of the same run: with a wait limit of 5 ms the roles that wait for it must not give up.
+    In a process of its own, for the limit."""
+    code = """
+import sys; sys.path.insert(0, %r)
+import math
+import os
+import subprocess
+import sys
+
+import numpy as np
+from tests import cache_ref as ref
+from tests.test_cache_gpu import Dev, gdpa, host
+B, new, n, D = 160, 40, 2000, %d
+x = ref.make(72, 4, 1, D, 64, [n], [new], jitter=1)
+x.v_sf[x.table[0, 5], :, 1] = 60
+ro = ref.attend(x, True, 0, float(np.float32(1 / math.sqrt(D))))
+tol, tl = ref.attend_bounds(x, *ro)
+# the same sequence many times over (its pages are only read)
+x.table, x.lens, x.new = np.repeat(x.table, B, 0), [n] * B, [new] * B
+x.offsets = (np.arange(B + 1) * new).astype(np.int32)
+x.q, x.k, x.v = (np.tile(a, (B, 1, 1)) for a in (x.q, x.k, x.v))
+d = Dev(x)
+d.fwd()
+status = gdpa.gdpa_device_status()
+assert status == gdpa.GDPA_OK, status
+got, lse = host(d.out).reshape(B, new, 4, D), host(d.lse).reshape(B, new, 4)
+assert (np.abs(got - ro[0]) <= tol).all() and (np.abs(lse - ro[1]) <= tl).all()
+print("fine")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), D)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, GDPA_WAIT_TIMEOUT_MS="5"))
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stderr[-2000:]
