@@ -694,15 +694,16 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
       }
       if (__any_sync(0xffffffffu, over)) {
         // V's units: one above the largest scale, so that they seldom move.  At
-        // an edge a row may see nothing of a block that lies far above, and what
-        // it has summed must not vanish in that block's units: there they stay up
-        // to 2^90 behind (edges behind a row's last key are three steps at most).
+        // an edge a row may see nothing of a block that lies far above: what it
+        // has summed, or will sum, must not vanish in that block's units.  There
+        // they stay up to 2^90 behind (edges are three steps at most, at either
+        // end of a row's keys, so that the sums stay finite).
         int top_sv = sv[0];
         if (C::NB == 2) top_sv = max(top_sv, sv[C::NB - 1]);
         float turn = 1.0f;
         if (top_sv > vexp) {
           int up = min(top_sv + 1, 254);
-          if (EDGE && vexp >= 0 && top_sv - vexp > 40) up = max(vexp, top_sv - 90);
+          if (EDGE && (up > 140 || (vexp >= 0 && top_sv - vexp > 40))) up = max(vexp < 0 ? 100 : vexp, top_sv - 90);
           turn = vexp < 0 ? 0.0f : up - vexp > 126 ? 0.0f : sf_value(127 - (up - vexp));
           vexp = up;
         }

@@ -93,3 +93,24 @@ print("fine")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, GDPA_WAIT_TIMEOUT_MS="5"))
     assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", [(2, (4, 1)), (3, (8, 1)), (12, (4, 1)), (30, (1, 1)), (70, (2, 1)), (130, (2, 1))])
+@pytest.mark.parametrize("sf,rest", [(254, 120), (254, 100), (247, 70), (254, 60), (247, 40)])
+def test_a_huge_value_that_only_the_first_row_s_window_holds(D, new, heads, sf, rest):
+    """The last key of its block that any row sees, far above all others: it decides the first row and leaves no trace
+    in the next ones."""
+    window = 100
+    for keys in (497, 2593):
+        x = ref.make(71, *heads, D, 32, [keys], [new], jitter=1)
+        at = keys - new - window + 1
+        x.v_sf[x.v_sf != 255] = rest
+        page, slot = x.table[0, at // 32], at % 32
+        x.v_sf[page, :, slot // 16] = sf
+        block = x.v_codes[page, :, slot // 16 * 16:slot // 16 * 16 + 16]
+        block[:, :slot % 16 + 1] = block[:, :slot % 16 + 1] & 0x87 | 1  # from 2^-9 to 2^-6: finite in the result
+        block[:, slot % 16 + 1:] = 0
+        d = Dev(x)
+        d.fwd(window=window)
+        check_fwd(x, d, True, window)
