@@ -473,8 +473,9 @@ typedef struct {
  *               read, and q_out keeps what it held there
  *
  * A pair (x, y) at position p turns by p * inv_freq: (x cos - y sin, y cos + x
- * sin).  The angle is exact to 2^-32 turns at every position (a 64-bit
- * fraction of a turn, times p, modulo 1), sine and cosine are fp32.
+ * sin).  The angle is right to 2^-32 turns at every position (a 64-bit fraction
+ * of a turn, times p, modulo 1) and then rounded to fp32 (2^-26 turns at most);
+ * sine, cosine and the rotated pair are fp32.
  *
  * Quantisation: for the tokens that this call adds to a block of 16 and one
  * head, A = the largest finite magnitude; e = the smallest integer >= -127

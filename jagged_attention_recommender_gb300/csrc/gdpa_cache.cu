@@ -88,16 +88,6 @@ CacheView view(const gdpa_cache_t* c) {
                    c->H};
 }
 
-// f / 2 pi modulo 1 as a 64-bit fraction.
-unsigned long long turn_fraction(double f) {
-  double t = f * 0.15915494309189535;  // 1 / 2 pi
-  t -= std::floor(t);
-  if (t >= 1.0) t = 0.0;
-  const double hi = std::floor(t * 4294967296.0);
-  const double lo = std::floor((t * 4294967296.0 - hi) * 4294967296.0);
-  return (static_cast<unsigned long long>(hi) << 32) + static_cast<unsigned long long>(lo);
-}
-
 // Keys a segment can have, as far as the host knows.
 int64_t most_keys(const CacheFwdParams& p, int max_q) {
   const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;

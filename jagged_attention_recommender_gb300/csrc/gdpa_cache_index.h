@@ -1,7 +1,9 @@
-// gdpa_cache_index.h -- the paged cache's index arithmetic, free of CUDA: the
-// kernels compile it for the device, the tests as plain C++ for the host.
+// gdpa_cache_index.h -- the paged cache's index arithmetic and the launch's
+// angles, free of CUDA: the kernels compile it for the device, the tests as
+// plain C++ for the host.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -52,5 +54,24 @@ GDPA_HD OwnedRows owned_rows(const CacheSeq& s, int r) {
 // token) sees through a window of `window` tokens, 0 for none.  (pos - window
 // alone can lie below -2^31.)
 GDPA_HD int first_key(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
+// x modulo 1 in units of 2^-64, rounded (the difference is exact: x and its
+// floor are multiples of x's last bit).
+inline uint64_t fraction64(double x) {
+  const double a = std::fabs(x), y = (a - std::floor(a)) * 4294967296.0, top = std::floor(y);
+  const uint64_t u = (static_cast<uint64_t>(top) << 32) + static_cast<uint64_t>(std::nearbyint((y - top) * 4294967296.0));
+  return x < 0 ? ~u + 1 : u;
+}
+
+// f / 2 pi modulo 1 in units of 2^-64, off by one of them at most (|f| below
+// 2^40): 1 / 2 pi is a sum of two doubles, and the first product's rounding error
+// is added.  A position times this, modulo 2^64, is the angle to 2^-32 turns at
+// every position below 2^31; a single product's error of 2^-56 grows to 2^-25.
+inline uint64_t turn_fraction(double f) {
+  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;  // 1 / 2 pi
+  const volatile double product = f * kHigh;  // rounded here (never part of a fused product)
+  const double p = product;
+  return fraction64(p) + fraction64(std::fma(f, kHigh, -p) + f * kLow);
+}
 
 }  // namespace gdpa

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import fractions
 import os
 import shutil
 import subprocess
@@ -60,6 +61,7 @@ extern "C" int owners(const int* off, const int* lens, int T, int B, long long m
   return found;
 }
 
+extern "C" unsigned long long turn(double f) { return turn_fraction(f); }
 extern "C" int first(int pos, int window) { return first_key(pos, window); }
 """
 
@@ -72,7 +74,9 @@ def host(tmp_path_factory):
     src.write_text(HOST)
     subprocess.check_call([cxx, "-std=c++17", "-O1", "-fwrapv", "-Wall", "-Werror", "-shared", "-fPIC", "-I", gbuild.CSRC,
                            str(src), "-o", str(so)])
-    return ctypes.CDLL(str(so))
+    lib = ctypes.CDLL(str(so))
+    lib.turn.argtypes, lib.turn.restype = [ctypes.c_double], ctypes.c_uint64
+    return lib
 
 
 def owners(host, off, lens, T, most, rows):
@@ -144,3 +148,34 @@ def test_a_window_s_first_key(host):
     for pos in ends:
         for window in (0, 1, 2, 6, 7, 8, 2 ** 20, 2 ** 31 - 4, 2 ** 31 - 1):
             assert host.first(pos, window) == (max(0, pos - window + 1) if window else 0), (pos, window)
+
+
+def two_pi(digits=60):
+    """2 pi as a fraction, by Machin's formula in whole numbers."""
+    def arctan_of_one_over(n):
+        term = total = 10 ** (digits + 10) // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+    return fractions.Fraction(8 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239)), 10 ** (digits + 10))
+
+
+def test_fractions_of_a_turn(host):
+    """Off by one unit of 2^-64 at most, so that an angle is right to 2^-32 turns (and the unit below it) wherever a
+    position lies."""
+    circle = two_pi()
+    freqs = list(10000.0 ** (-np.arange(0, 128, 2) / 128)) + list(5e5 ** (-np.arange(0, 64, 2) / 64))
+    freqs += [0.0, 5e-324, 1e-300, 2.0 ** -70, 1e-12, 1.0, np.pi, 2 * np.pi, 100.0, 12345.678, 2.0 ** 30, 1e11]
+    for f in freqs:
+        for x in (f, -f):
+            exact = fractions.Fraction(x) / circle
+            got = host.turn(x)
+            units = (fractions.Fraction(got) - exact * 2 ** 64) % 2 ** 64
+            assert min(units, 2 ** 64 - units) <= 1, (x, float(units))
+            for pos in (1, 131071, 2 ** 24 + 1, 2 ** 31 - 17):
+                angle = (pos * got % 2 ** 64 >> 32) / fractions.Fraction(2 ** 32)
+                off = (angle - exact * pos) % 1
+                assert min(off, 1 - off) <= fractions.Fraction(3, 2) / 2 ** 32, (x, pos)
