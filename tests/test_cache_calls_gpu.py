@@ -2,6 +2,8 @@
 values at the ends of what the documentation allows."""
 from __future__ import annotations
 
+import dataclasses
+import math
 import os
 import subprocess
 import sys
@@ -66,6 +68,8 @@ def test_the_plain_form_may_take_longer_than_a_wait_may(D):
     code = """
 import sys; sys.path.insert(0, %r)
 import math
+import dataclasses
+import math
 import os
 import subprocess
 import sys
@@ -114,3 +118,91 @@ def test_a_huge_value_that_only_the_first_row_s_window_holds(D, new, heads, sf, 
         d = Dev(x)
         d.fwd(window=window)
         check_fwd(x, d, True, window)
+
+
+def attend_kept(x, causal, window, scale):
+    """ref.attend over the keys whose page the cache has."""
+    pages = x.k_codes.shape[0]
+    bad = (x.table < 0) | (x.table >= pages)
+    y = dataclasses.replace(x, table=np.where(bad, 0, x.table))
+    G = x.Hq // x.H
+    out, lse, big = np.zeros((x.T, x.Hq, x.D)), np.full((x.T, x.Hq), -np.inf), np.zeros((x.T, x.Hq))
+    mag = np.zeros_like(out)
+    for b, (n, new) in enumerate(zip(x.lens, x.new)):
+        k, v = ref.gather(y, b, x.k_codes, x.k_sf), ref.gather(y, b, x.v_codes, x.v_sf)
+        there = ~bad[b, np.arange(n) // x.P]
+        for i in range(new):
+            j0, j1 = ref.seen(n, new, i, causal, window)
+            j = np.arange(j0, max(j0, j1))
+            j = j[there[j]]
+            if not len(j):
+                continue
+            r = x.offsets[b] + i
+            for h in range(x.H):
+                qq, kk, vv = x.q[r, h * G:(h + 1) * G], k[j, h], v[j, h]
+                s = scale * (qq @ kk.T)
+                m = s.max(-1, keepdims=True)
+                p = np.exp(s - m)
+                l = p.sum(-1, keepdims=True)
+                at = np.s_[r, h * G:(h + 1) * G]
+                out[at], mag[at], lse[at] = p @ vv / l, p @ np.abs(vv) / l, (np.log(l) + m)[:, 0]
+                big[at] = (abs(scale) * (np.abs(qq) @ np.abs(kk).T)).max(-1)
+    return out, lse, mag, big
+
+
+def check_kept(x, d, causal, window, skipped=()):
+    """The rows of all sequences but the skipped ones, which keep what the outputs held."""
+    ro = attend_kept(x, causal, window, float(np.float32(1 / math.sqrt(x.D))))
+    tol, tl = ref.attend_bounds(x, *ro)
+    got, lse = host(d.out), host(d.lse)
+    rows = np.zeros(d.T, bool)
+    for b in range(len(x.lens)):
+        if b not in skipped:
+            rows[x.offsets[b]:x.offsets[b + 1]] = True
+    assert (got[~rows] == 7).all() and (lse[~rows] == 7).all()
+    rows = rows[:x.T]
+    bad = ~(np.abs(got[:x.T] - ro[0]) <= tol)[rows]
+    assert not bad.any(), (np.argwhere(bad)[:5], got[:x.T][rows][bad][:5], ro[0][rows][bad][:5])
+    none = np.isneginf(ro[1])[rows]
+    np.testing.assert_array_equal(np.isneginf(lse[:x.T][rows]), none)
+    assert (none | (np.abs(np.where(none, 0, lse[:x.T][rows]) - np.where(none, 0, ro[1][rows])) <= tl[rows])).all()
+
+
+ROWS = [(1, (1, 1)), (3, (8, 1)), (6, (4, 1)), (12, (4, 1)), (65, (2, 1)), (70, (4, 1))]  # every tile and kernel
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", ROWS)
+@pytest.mark.parametrize("keys", [300, 2603])
+@pytest.mark.parametrize("P,causal,window", [(16, True, 0), (32, True, 77), (128, False, 0)])
+def test_keys_on_a_page_out_of_range_are_not_seen(D, new, heads, keys, P, causal, window):
+    """Bad entries first, in the middle, last, several and all of them; with and without a block of V so far below the
+    others that many rows take the plain form."""
+    for low in (False, True):
+        x = ref.make(70, *heads, D, P, [keys, 55], [new, 2], jitter=1)
+        if low:
+            x.v_sf[x.table[0, 130 // P], :, 130 % P // 16] = 60
+        n = -(-keys // P)
+        spans = [ref.seen(keys, new, i, causal, window) for i in (0, new - 1)]
+        for bad in ([0], [n // 2], [n - 1], [0, 1, n - 2], list(range(n))):
+            y = dataclasses.replace(x, table=x.table.copy())
+            y.table[0, bad] = [[-1, -2 ** 31, x.k_codes.shape[0], 2 ** 31 - 1][i % 4] for i in range(len(bad))]
+            d = Dev(y, pad=1)
+            d.fwd(causal, window)
+            read = any(j0 < (b + 1) * P and b * P < j1 for b in bad for j0, j1 in spans)
+            assert gdpa.gdpa_device_status() == (gdpa.GDPA_ERR_INVALID_ARG if read else gdpa.GDPA_OK), bad
+            check_kept(y, d, causal, window)
+
+
+@pytest.mark.parametrize("new,heads", ROWS)
+@pytest.mark.parametrize("spoil", ["long", "negative", "offsets"])
+def test_other_sequences_are_right_beside_a_spoilt_one(new, heads, spoil):
+    x = ref.make(73, *heads, 64, 32, [90, 2203, 41], [new, 1, new])
+    d = Dev(x, pad=2)
+    if spoil == "offsets":  # of the last sequence: past the rows there are
+        d.offsets[3] = d.T + 1
+    else:
+        d.lens[1] = x.table.shape[1] * 32 + 1 if spoil == "long" else -5
+    d.fwd()
+    assert gdpa.gdpa_device_status() == gdpa.GDPA_ERR_INVALID_ARG
+    check_kept(x, d, True, 0, skipped=[2 if spoil == "offsets" else 1])
