@@ -521,7 +521,7 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
 #pragma unroll 1
         for (int n = 0; n < C::NB; ++n) {
           const int page = n == 0 ? page_next[0] : page_next[C::NB - 1], slot = (kb + n * kCacheBlock) & pmask;
-          const int valid = page >= 0 ? ahead.w.s.len - (kb + n * kCacheBlock) : 0;
+          const int valid = ahead.w.s.len - (kb + n * kCacheBlock);
           const int64_t row = cache_row(p.cache, max(page, 0), ahead.h, slot);
           const uint8_t* ks = p.cache.k + row * D + lane * 16;
           const uint8_t* vs = p.cache.v + row * D + lane * 16;
@@ -529,9 +529,15 @@ __global__ void __launch_bounds__((SplitCfg<D, NT, TEAM>::THREADS), (SplitCfg<D,
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {  // rows that are not stored: zeros
             const int idx = lane + 32 * j, r = idx / (D / 16), c = idx % (D / 16);
+            const uint32_t to = tile_at<D>(r, c);
+            if (page < 0) {  // (no address stands for them: a cache may have no page at all)
+              ptx::st_shared_v4(kd + to, 0, 0, 0, 0);
+              ptx::st_shared_v4(vd + to, 0, 0, 0, 0);
+              continue;
+            }
             const int bytes = r < valid ? 16 : 0;
-            cp_async16(kd + tile_at<D>(r, c), ks + 512 * j, bytes);
-            cp_async16(vd + tile_at<D>(r, c), vs + 512 * j, bytes);
+            cp_async16(kd + to, ks + 512 * j, bytes);
+            cp_async16(vd + to, vs + 512 * j, bytes);
           }
           if (page >= 0) {
             const int64_t block = row >> 4, word = block & ~(int64_t)3;

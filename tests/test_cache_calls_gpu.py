@@ -206,3 +206,38 @@ def test_other_sequences_are_right_beside_a_spoilt_one(new, heads, spoil):
     d.fwd()
     assert gdpa.gdpa_device_status() == gdpa.GDPA_ERR_INVALID_ARG
     check_kept(x, d, True, 0, skipped=[2 if spoil == "offsets" else 1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,heads", ROWS)
+def test_a_cache_without_pages(D, new, heads):
+    """Nothing is stored and nothing can be: rows see nothing, and lengths above zero are reported."""
+    for lens, status in (([0, 0], gdpa.GDPA_OK), ([new + 40, 0], gdpa.GDPA_ERR_INVALID_ARG)):
+        x = ref.make(74, *heads, D, 32, [0, 0], [new, 1], spare=0)
+        x.lens, x.table = lens, np.full((2, 5), -1, np.int32)
+        d = Dev(x, inv_freq(D), pad=1)
+        assert d.k_codes.numel() == 0
+        d.fwd()
+        assert gdpa.gdpa_device_status() == status
+        assert (host(d.out)[:x.T] == 0).all() and np.isneginf(host(d.lse)[:x.T]).all()
+        assert (host(d.out)[x.T:] == 7).all() and (host(d.lse)[x.T:] == 7).all()
+    x.lens = [new, 1]  # an append keeps nothing, and rotates the queries
+    d = Dev(x, inv_freq(D))
+    d.append()
+    assert gdpa.gdpa_device_status() == gdpa.GDPA_ERR_INVALID_ARG
+    q = np.concatenate([ref.rotate(x.q[:new], np.arange(new), inv_freq(D), False), x.q[new:]])
+    slack = 2.0 ** -21 * np.sqrt(2) * np.linalg.norm(x.q, axis=-1, keepdims=True)
+    assert (np.abs(host(d.q_out) - q) <= 2.0 ** -8 * np.abs(q) + slack).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [(300, 1), (1000, 2), (600, 600), (1023, 341)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_many_heads(D, heads, new):
+    """Groups of more heads than a tile has rows, and more key heads than a CTA has tiles."""
+    x = ref.make(75, *heads, D, 16, [70, new], [new, new], jitter=1)
+    d = Dev(x)
+    d.fwd()
+    check_fwd(x, d, True, 0)
+    d.append()  # (unrotated: so many blocks hold some whose scale a rotation's rounding decides)
+    check_append(x, d, None, False)
