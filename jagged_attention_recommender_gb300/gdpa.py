@@ -129,12 +129,6 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream or None
 
 
-def _stream_on(device: int) -> int | None:
-    """The address of the current stream of ``device``."""
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object is made where torch offers that
-    return (raw(device) if raw else _torch.cuda.current_stream(device).cuda_stream) or None
-
-
 def _check(code: int, where: str):
     if code != GDPA_OK:
         raise GdpaError(code, where)
@@ -341,45 +335,56 @@ def gdpa_wait_selftest(timeout_ms: int, stream=None):
 
 
 _torch = None
-_dtypes = None
+_bf16 = _i32_t = _f32 = _u8 = None  # torch's types
 _cuda = False  # whether torch has found a CUDA device
+_raw_stream = None  # the address of a device's current stream
 
 
 def _device() -> int:
     """The current CUDA device (-2: there is none)."""
-    global _torch, _dtypes, _cuda
+    global _torch, _bf16, _i32_t, _f32, _u8, _cuda, _raw_stream
     if _torch is None:
         import torch
-        _dtypes = {n: getattr(torch, n) for n in ("bfloat16", "int32", "float32", "uint8")}
+        _bf16, _i32_t, _f32, _u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+        # (no Stream object is made where torch offers that)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         _torch = torch
     _cuda = _cuda or _torch.cuda.is_available()
     return _torch.cuda.current_device() if _cuda else -2
 
 
-def _at(where, device, dtype, t, least=0, cache=None, strided=False):
-    """The address of a tensor of type ``dtype`` on ``device``, of ``least`` elements (heads of ``cache``) or more,
-    contiguous unless it comes with a stride; another one is refused (addresses and None pass)."""
+def _at(where, device, dtype, t, least=0):
+    """The address of a contiguous tensor of type ``dtype`` on ``device``, of ``least`` elements or more; another one is
+    refused (addresses and None pass)."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype is not _dtypes[dtype]:
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.numel() >= least:
+        return t.data_ptr()
+    _kind(where, device, dtype, t)
+    if not t.is_contiguous():
+        raise ValueError("%s: a contiguous tensor wanted, got strides %r" % (where, t.stride()))
+    raise ValueError("%s: a %s tensor of %d elements or more wanted, got shape %r" % (where, dtype, least, tuple(t.shape)))
+
+
+def _kind(where, device, dtype, t):
+    if t.dtype is not dtype:
         raise TypeError("%s: %s wanted, got %s" % (where, dtype, t.dtype))
     if t.get_device() != device:
         raise ValueError("%s: tensor on %s, not on the current CUDA device" % (where, t.device))
-    if not strided and not t.is_contiguous():
-        raise ValueError("%s: a contiguous tensor wanted, got strides %r" % (where, t.stride()))
-    if cache is not None:
-        least *= cache.D
-    if t.numel() < least:
-        raise ValueError("%s: a %s tensor of %d elements or more wanted, got shape %r" % (where, dtype, least, tuple(t.shape)))
-    return t.data_ptr()
 
 
 def _table_at(where, device, t, B, max_pages):
     """The address of a page table whose rows are ``max_pages`` entries."""
-    at = _at(where, device, "int32", t, B * max_pages)
+    at = _at(where, device, _i32_t, t, B * max_pages)
     if B > 1 and t.__class__ is not int and t is not None and t.dim() > 1 and t.shape[-1] != max_pages:
         raise ValueError("%s: a page table of %d entries a row wanted, got shape %r" % (where, max_pages, tuple(t.shape)))
     return at
+
+
+def _heads_at(where, device, cache, t, rows):
+    """The address of ``rows`` or more contiguous heads of D bf16."""
+    return t if t is None or t.__class__ is int else _at(where, device, _bf16, t, rows * cache.D)
 
 
 def _cache_at(where, device, cache):
@@ -394,8 +399,8 @@ def _rows_at(where, device, cache, t, stride, T, heads=0):
     elements side by side; a tensor laid out in another way is refused."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype is not _dtypes["bfloat16"] or t.get_device() != device:
-        return _at(where, device, "bfloat16", t, strided=True)
+    if t.dtype is not _bf16 or t.get_device() != device:
+        _kind(where, device, _bf16, t)
     heads, D, st = heads or cache.H, cache.D, t.stride()
     if st == (stride, D, 1):
         n, h, d = t.shape
@@ -439,7 +444,7 @@ class KvCache:
             if tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("KvCache: %s must be contiguous %r, got %r" % (name, shape, tuple(t.shape)))
         device = _device()
-        at = [_at("KvCache", device, "uint8", t) for t in (k_codes, v_codes, k_sf, v_sf)]
+        at = [_at("KvCache", device, _u8, t) for t in (k_codes, v_codes, k_sf, v_sf)]
         self.tensors = (k_codes, v_codes, k_sf, v_sf)
         self.H, self.D, self.device = H, D, device
         self.inv_freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
@@ -458,10 +463,10 @@ def gdpa_cache_append(cache: KvCache, q, q_stride, k, k_stride, v, v_stride, off
     _check(lib().gdpa_cache_append(
         _cache_at(where, d, cache), _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
         _rows_at(where, d, cache, k, k_stride, n), k_stride, _rows_at(where, d, cache, v, v_stride, n), v_stride,
-        _at(where, d, "int32", offsets, b + 1), _at(where, d, "int32", kv_lens, b),
+        _at(where, d, _i32_t, offsets, b + 1), _at(where, d, _i32_t, kv_lens, b),
         _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages,
-        _at(where, d, "bfloat16", q_out, 0 if q is None else n * Hq, cache),
-        _stream_on(d) if stream is None else _stream(stream)), where)
+        _heads_at(where, d, cache, q_out, 0 if q is None else n * Hq),
+        (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
 
 
 def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
@@ -475,11 +480,11 @@ def gdpa_cache_fwd(cache: KvCache, q, q_stride, offsets, kv_lens, page_table, T,
     n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
     _check(lib().gdpa_cache_fwd(
         _cache_at(where, d, cache), _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
-        _at(where, d, "int32", offsets, b + 1), _at(where, d, "int32", kv_lens, b),
+        _at(where, d, _i32_t, offsets, b + 1), _at(where, d, _i32_t, kv_lens, b),
         _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages, max_q, causal, window_tokens, scale,
-        _at(where, d, "bfloat16", out, n * Hq, cache),
-        _at(where, d, "float32", lse, n * Hq), _at(where, d, "uint8", workspace, workspace_bytes), workspace_bytes,
-        _stream_on(d) if stream is None else _stream(stream)), where)
+        _heads_at(where, d, cache, out, n * Hq),
+        _at(where, d, _f32, lse, n * Hq), _at(where, d, _u8, workspace, workspace_bytes), workspace_bytes,
+        (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
 
 
 def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:
