@@ -510,7 +510,19 @@ gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_
  *               j > L - n + i - W as well
  *   causal = 0: all L keys (window_tokens must be 0)
  * A row that sees no key gives 0, and -inf in lse.  Keys that a row does not
- * see never influence it, whatever they hold (infinite and NaN values included).
+ * see never influence it, whatever they hold (NaN codes included; beside hidden
+ * values above 2^100 a row's own below 2^-80 may lose bits).
+ *
+ * Scores, softmax statistics, sums and lse are fp32; a score that fp32 does not
+ * hold may make its row NaN.  Rounded to fewer bits are
+ *   q        to fp16 after a division by the row's largest power of two:
+ *            elements down to 2^-17 of the largest are exact, smaller ones are
+ *            off by 2^-25 of it
+ *   weights  exp(s - m) to fp16: 2^-11 of themselves down to 2^-15 of the row's
+ *            largest, fewer bits below, and zero below 2^-25
+ *   out      to bf16
+ * Blocks of V that a row sees should have scales less than 2^100 apart: what
+ * smaller ones add may be lost.
  *
  *   q      device bf16, row t at q + t * q_stride (elements): [Hq, D]
  *   out    device bf16 [T, Hq, D] contiguous; rows from offsets[B] on keep
@@ -519,7 +531,10 @@ gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_
  *   offsets, kv_lens, page_table, max_pages, T, B  as gdpa_cache_append; the
  *          cache must already hold the kv_lens[b] tokens
  *   max_q  the most rows any sequence has, as far as the caller knows: it
- *          picks the kernel; sequences with more rows are still computed
+ *          picks the kernel, one for the whole batch; sequences with more rows
+ *          are still computed.  max_pages is taken for the longest sequence in
+ *          that choice: a table much wider than the sequences costs short ones
+ *          a second kernel (about 7 us)
  *   workspace  device memory, 16-byte aligned, of at least
  *          gdpa_cache_workspace_size() bytes, the caller's.  It holds nothing
  *          between calls; calls (or captured graphs) that may run at the same
@@ -531,6 +546,11 @@ gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void* q, int64_
  * be captured).  Offsets, lengths or page numbers out of range are handled as
  * in gdpa_cache_append: keys on a page out of range are not seen.  A workspace
  * that is too small returns GDPA_ERR_NO_MEMORY.
+ *
+ * With many rows (max_q * Hq / H above 48, and few keys aside 96) a sequence and
+ * head whose blocks of V have scales 2^16 or more apart, zeros aside, or a NaN
+ * value that some rows see and others do not, is computed row by row: right, but
+ * about 1400 times as slow.
  */
 gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q, int64_t q_stride, const int32_t* offsets,
                              const int32_t* kv_lens, const int32_t* page_table, int64_t T, int B, int Hq,

@@ -229,7 +229,7 @@ gdpa_status_t launch_split_as(CacheFwdParams& p, void* workspace, int max_q, con
 
 // A second kernel costs a call about 5 us: up to 2048 keys the eight warps of a
 // CTA are done with a whole segment sooner, if every segment has an SM (one token
-// over 201 keys: 9.4 us, cut into parts 14.3).
+// over 201 keys, 50 calls in a graph: 6.3 us a call, cut into parts 13.7).
 template <int D, int NT>
 gdpa_status_t launch_split(CacheFwdParams& p, void* workspace, int max_q, const Device& dev, cudaStream_t s) {
   const bool team = most_keys(p, max_q) <= 2048 && most_segments(p, 8 * NT) <= dev.sms;
@@ -302,14 +302,16 @@ extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void
   for (int i = 0; i < 64; ++i) p.freq[i] = i < p.rot / 2 ? turn_fraction(cache->inv_freq[i]) : 0;
   // Rows of a CTA: 16 where sequences bring several tokens (a scale block's
   // worth); for single tokens as few as keep its eight warps busy (256 tokens of
-  // 32 query and 8 key heads of 128: 8.9 us, with 16 rows 16.4).
+  // 32 query and 8 key heads of 128, 50 calls in a graph: 6.4 us a call, with 16
+  // rows 13.8).
   const int items = cache->D / 16;
   const int64_t row_tasks = 2 * ((int64_t)cache->H * items + 127) / 128 + ((int64_t)p.Hq * items + 127) / 128;
   int rows = 16;
   while (T <= 4 * (int64_t)B && rows > 1 && rows * row_tasks > kAppendThreads / 32) rows >>= 1;
   const int64_t groups = (T + rows - 1) / rows;
   // Few groups: several CTAs share the tasks of one (each finds its rows and
-  // angles again; the same 256 tokens take 10.9 us without).
+  // angles again).  A piece of 64 tokens of such heads takes 9.8 us so and 24.6
+  // without, one of 1000 13.1 and 25.0; from 4000 tokens on there is none to spare.
   const int64_t spare = (int64_t)dev.sms * 3 / groups, useful = (rows * row_tasks + 7) / 8;
   const int share = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(spare, useful)));
   const int smem = (rows + kCacheBlock - 1) * (p.rot / 2) * (int)sizeof(float2) + kAppendThreads / 32 * 4096;

@@ -88,7 +88,7 @@ struct RowMap {
 // part stand {first, pieces, first row of the sequence, its rows, row tile, head}.
 
 // TEAM: a CTA has one whole segment at most, and its warps take the steps in turn:
-// one token over 201 keys takes 9.4 us of a call so and 14.3 as cut parts.
+// one token over 201 keys takes 6.3 us on the device so and 13.7 as cut parts.
 template <int D, int NT, bool TEAM_ = false>
 struct SplitCfg {
   static constexpr bool TEAM = TEAM_;

@@ -8,15 +8,17 @@
 // scores.  V is multiplied by its block's scale over 2^E, E the largest scale's
 // exponent so far (raised when a block exceeds it by 7, the output following):
 // exact while a block is less than 2^15 below it, and a block of other than
-// zeros further below sends its segment to the plain form.  Weights are 2^(x - r)
+// zeros further below sends its segment to the plain form: row by row, a warp
+// each, 1400 times as slow (2321 prompt rows with one such block: 360 ms).  Weights are 2^(x - r)
 // with a reference r 7 below the running maximum, moved when a score exceeds it
 // by 15, and rounded to fp16, as in the kernel for few rows.  Sums stay in fp32;
 // the row sum takes the weights before their rounding.
 //
 // Bound: the chain of hand-overs between the roles.  The tensor core and the
 // special-function unit each need about 1050 cycles for 256 rows and 64 keys at
-// D = 128 and a step takes about 2000: 258 us (746 TFLOP/s) for 2321 rows of
-// prompts behind 2100 to 8192 keys, 32 query and 8 key heads of 128.  With a
+// D = 128 and a step takes about 2000: 258 to 277 us on different boards (746 to
+// 695 TFLOP/s) for 2321 rows of prompts behind 2100 to 8192 keys, 32 query and 8
+// key heads of 128.  With a
 // softmax that only hands over 194 us are left, with an eighth of S's and a
 // quarter of P V's MMAs as well 157.
 //
