@@ -5,9 +5,10 @@
 // F = f / 2 pi as a 64-bit fraction of a turn, p F modulo 2^64 IS theta
 // modulo one turn, with an error of p 2^-64 turns: one integer product, no
 // argument reduction and no 64-bit floating point at any position.  The top 32
-// bits, rounded to fp32's 24 (2^-26 turns at most), go to sincospif.  A block of 16 tokens of one head has one scale 2^e,
-// e the smallest integer with amax <= 448 2^e, so from the bits of amax
-// (exponent field E, mantissa M): e + 127 = E - 8 + (M > 0.75 2^23).
+// bits, rounded to fp32's 24 (2^-26 turns at most), go to sincospif.  A block
+// of 16 tokens of one head has one scale 2^e, e the smallest integer with
+// amax <= 448 2^e, so from the bits of amax (exponent field E, mantissa M):
+// e + 127 = E - 8 + (M > 0.75 2^23).
 //
 // Bound: memory.  Per new token Hq D 4 bytes (queries in and out) and
 // H D (4 + 2) (keys and values in, codes out) against about 3 flops an element.

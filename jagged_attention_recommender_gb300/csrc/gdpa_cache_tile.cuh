@@ -9,10 +9,10 @@
 // exponent so far (raised when a block exceeds it by 7, the output following):
 // exact while a block is less than 2^15 below it, and a block of other than
 // zeros further below sends its segment to the plain form: row by row, a warp
-// each, 1400 times as slow (2321 prompt rows with one such block: 360 ms).  Weights are 2^(x - r)
-// with a reference r 7 below the running maximum, moved when a score exceeds it
-// by 15, and rounded to fp16, as in the kernel for few rows.  Sums stay in fp32;
-// the row sum takes the weights before their rounding.
+// each, 1400 times as slow (2321 prompt rows with one such block: 360 ms).
+// Weights are 2^(x - r) with a reference r 7 below the running maximum, moved when
+// a score exceeds it by 15, and rounded to fp16, as in the kernel for few rows.
+// Sums stay in fp32; the row sum takes the weights before their rounding.
 //
 // Bound: the chain of hand-overs between the roles.  The tensor core and the
 // special-function unit each need about 1050 cycles for 256 rows and 64 keys at

@@ -1,4 +1,4 @@
-"""What the paged cache's Python binding refuses: tensors that the library would misread.  On the CPU: the binding is told
+"""What the paged cache's Python binding refuses: tensors that the library would misread.  On the CPU: it is told
 that host memory is the current device, and the C calls are replaced by one that only counts."""
 from __future__ import annotations
 

@@ -241,3 +241,21 @@ def test_many_heads(D, heads, new):
     check_fwd(x, d, True, 0)
     d.append()  # (unrotated: so many blocks hold some whose scale a rotation's rounding decides)
     check_append(x, d, None, False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_calls_for_many_and_few_rows_at_once(D):
+    """Four streams with a workspace each, two of them with the kernel for many rows."""
+    xs = [ref.make(90 + i, 8, 2, D, 64, [3000, 100 * i + 99, 700], [n, 30, 99]) for i, n in enumerate((90, 1, 140, 6))]
+    ds = [Dev(x) for x in xs]
+    hints = (140, 1, 140, 6)
+    spaces = [torch.empty(gdpa.gdpa_cache_workspace_size(d.cache, 8, n), dtype=torch.uint8, device="cuda")
+              for d, n in zip(ds, hints)]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, w, s, n in zip(ds, spaces, streams, hints):
+            d.fwd(workspace=w, stream=s, max_q=n)
+    torch.cuda.synchronize()
+    for x, d in zip(xs, ds):
+        check_fwd(x, d, True, 0)
