@@ -561,6 +561,152 @@ gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q, int64_t q
  * heads and max_q rows a sequence. */
 gdpa_status_t gdpa_cache_workspace_size(const gdpa_cache_t* cache, int Hq, int max_q, int64_t* bytes);
 
+/* How gdpa_rope_freqs stretches the positions of a context longer than the trained one. */
+typedef enum {
+  GDPA_ROPE_SCALE_NONE = 0,   /* f_i = base^(-2 i / rot_dim) */
+  GDPA_ROPE_SCALE_LINEAR = 1, /* f_i / factor */
+  GDPA_ROPE_SCALE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base: the first pair
+                                 keeps its frequency, the last one's is divided by factor */
+  GDPA_ROPE_SCALE_RAMP = 3    /* by wave length: f_i where a pair turns `fast` times or more over the trained
+                                 context, f_i / factor where it turns `slow` times or less, a linear ramp of
+                                 the pair's index between; magnitude 0.1 ln(factor) + 1 */
+} gdpa_rope_scaling_t;
+
+/*
+ * gdpa_rope_freqs -- fills inv_freq (HOST double [rot_dim / 2], radians per
+ * position of each rotated pair) and *magnitude, for gdpa_rope and, as
+ * gdpa_cache_t's inv_freq, for gdpa_cache_append (which has no magnitude:
+ * multiply the attention's scale by its square instead where whole heads turn).
+ * rot_dim: a multiple of 16 up to 128; base > 1; factor >= 1 (ignored without
+ * scaling); trained, fast, slow: the ramp's only, trained > 0, fast > slow > 0.
+ * The ramp begins at the pair of index floor(i(fast)) and ends at that of index
+ * ceil(i(slow)), i(turns) = rot_dim ln(trained / (2 pi turns)) / (2 ln base),
+ * limited to [0, rot_dim - 1].  All in 64 bits, on the host; needs no GPU.
+ */
+gdpa_status_t gdpa_rope_freqs(int rot_dim, double base, int scaling, double factor, int64_t trained, double fast,
+                              double slow, double* inv_freq, float* magnitude);
+
+/*
+ * gdpa_rope -- rotates rows of a jagged batch by their positions, or (inverse =
+ * 1) returns the gradient of that: the same magnitude, the opposite turn.
+ *
+ *   x   device bf16, row t at x + t * x_stride (elements): [H, D]
+ *   y   device bf16, row t at y + t * y_stride: [H, D]; may be x itself with
+ *       the same stride, and must not overlap x otherwise
+ *   offsets    device int32 [B+1], offsets[0] = 0, non-decreasing: rows
+ *              [offsets[b], offsets[b+1]) are those of sequence b
+ *   first      device int32 [B]: the position of each sequence's first row (NULL:
+ *              0); row i of sequence b has position first[b] + i.  (After an
+ *              eviction a new token's position is no longer its cache's length:
+ *              rotate it here and append it to a cache without rotation.)
+ *   T          rows of x and y; rows from offsets[B] on are padding: not read,
+ *              and y keeps what it held there
+ *   inv_freq   HOST double [rot_dim / 2], radians per position, read during the
+ *              call; may be NULL with rot_dim 0
+ *   rot_dim    how many leading coordinates of a head turn, a multiple of 16 up to
+ *              D; the others are copied
+ *   magnitude  what the turned coordinates are multiplied by
+ *
+ * A pair (x, y) at position p turns by a = p * inv_freq:
+ *   inverse = 0:  magnitude (x cos a - y sin a, y cos a + x sin a)
+ *   inverse = 1:  magnitude (x cos a + y sin a, y cos a - x sin a)
+ * rope_style (gdpa_rope_style_t) says which coordinates are a pair.  Queries and
+ * keys that lie side by side in a fused projection's rows are turned by one call
+ * (H: the heads of both).  The angle is as exact as gdpa_cache_append's; sine,
+ * cosine and the rotated pair are fp32, rounded once to bf16.
+ *
+ * D is 64 or 128.  Strides are multiples of 8 and at least H * D; x and y
+ * 16-byte aligned.  T is below 2^31 - 256, B below 2^31 - 4097.  Asynchronous
+ * on `stream`, one kernel, no allocation, no host read of device data (may be
+ * captured; a replay reads offsets and first anew).  Offsets out of range never make
+ * it read or write outside the buffers: the rows of a sequence that begins
+ * below 0 or ends behind T are skipped and gdpa_device_status() returns
+ * GDPA_ERR_INVALID_ARG (where offsets decrease, which sequence a row counts to is
+ * undefined).
+ */
+gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_t* offsets, const int32_t* first, int64_t T, int B,
+                        int H, int D, const double* inv_freq, int rot_dim, int rope_style, float magnitude, int inverse,
+                        void* y, int64_t y_stride, void* stream);
+
+/*
+ * gdpa_cache_weights -- how much attention weight each stored key has received:
+ * adds what the rows of this call give it, for gdpa_cache_evict to choose by.
+ *
+ *   weights[j] = (j < L - n ? decay * weights_in[j] : 0) + sum p_ij
+ *   p_ij = exp(scale <q_i, k_j> - lse_i)
+ *
+ * for every key j < L of a sequence with n > 0 rows and L = kv_lens[b] tokens, over
+ * the rows i of the sequence that see key j (as in gdpa_cache_fwd: causal,
+ * window_tokens) and the query heads that read its key head.  The last n keys, the
+ * rows' own, begin at 0, so a new page needs no clearing.  Sequences without rows
+ * keep their weights.
+ *
+ *   weights     device fp32 [num_pages, H, page_tokens], in the cache's pages;
+ *               16-byte aligned
+ *   weights_in  the same layout, or NULL (all zero: what this call gives alone); may
+ *               be weights itself, and must not overlap it otherwise
+ *   decay       finite, >= 0; 1 sums over all calls, less lets old weight fade
+ *   lse         device fp32 [T, Hq] from gdpa_cache_fwd on the same rows.  A row of
+ *               -inf saw no key and gives nothing.  (The last rows of a prompt may
+ *               stand for all of it; the keys in front of them count as earlier ones
+ *               then, so weights_in is NULL, or holds something for them)
+ *   q, q_stride, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
+ *   window_tokens, scale  as gdpa_cache_fwd
+ *
+ * Scores, weights and their sums are fp32, summed in an order that does not depend
+ * on timing.  Keys that a row does not see take nothing from it, whatever it
+ * holds; a NaN in a row or its lse goes to the keys that it sees, one in a key to that key.
+ * With few rows (max_q * Hq / H up to 48) queries are rounded as in
+ * gdpa_cache_fwd; with more they are taken as they are.
+ *
+ * A page that two sequences of the call share has undefined weights.
+ * Asynchronous on `stream`, no allocation, no workspace, no host read of device data (may
+ * be captured).  Offsets, lengths or page numbers out of range are handled as in
+ * gdpa_cache_fwd: nothing is written outside the buffers, and
+ * gdpa_device_status() returns GDPA_ERR_INVALID_ARG.
+ */
+gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const void* q, int64_t q_stride, const float* lse,
+                                 const int32_t* offsets, const int32_t* kv_lens, const int32_t* page_table, int64_t T,
+                                 int B, int Hq, int max_pages, int max_q, int causal, int window_tokens, float scale,
+                                 float decay, const float* weights_in, float* weights, void* stream);
+
+/*
+ * gdpa_cache_evict -- cuts each sequence to its `budget` most attended tokens,
+ * every head by its own weights, and stores what is kept in other pages.
+ *
+ * Of a sequence of L = kv_lens[b] tokens each head keeps K = min(L, budget): the
+ * first `sink` and the last `recent` ones always, and of the others those with
+ * the largest weights, equal ones by the lower place (a NaN counts as less than
+ * any number).  They keep their order: the i-th kept token goes to page
+ * new_table[b, i / page_tokens], slot i % page_tokens, with its codes of K and
+ * V and its weight.  16 tokens of a new block take the largest of their scales,
+ * and codes from smaller ones are rounded to it: e4m3(code * 2^(e - e_new)), to
+ * nearest even.
+ *
+ *   weights    device fp32 [num_pages, H, page_tokens] (gdpa_cache_weights), read
+ *              in the old pages and written in the new ones; 16-byte aligned
+ *   kv_lens    device int32 [B];  page_table  device int32 [B, max_pages]
+ *   budget     >= 1;  sink, recent  >= 0, sink + recent <= budget
+ *   new_table  device int32 [B, new_max_pages]: new_max_pages * page_tokens at
+ *              least budget or max_pages * page_tokens, whichever is less.  No page
+ *              in it may appear in page_table or twice (pages of page_table may be shared:
+ *              they are only read, and the caller frees them afterwards)
+ *   kept       device int32 [B, H, budget]: the old place of each kept token,
+ *              ascending; entries from K on keep what they held
+ *   new_lens   device int32 [B]: K; must not overlap kv_lens
+ *
+ * The cache's codes and scales are read in the old pages and written in the new
+ * ones.  max_pages * page_tokens is below 2^31.  Asynchronous on `stream`, no allocation, no
+ * workspace, no host read of device data (may be captured).  A sequence whose
+ * length does not fit the table is skipped, with new_lens 0; tokens on an old page
+ * out of range count as NaN and leave the new slot as it was, as does a new page
+ * out of range; gdpa_device_status() then returns GDPA_ERR_INVALID_ARG.
+ */
+gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weights, const int32_t* kv_lens,
+                               const int32_t* page_table, int B, int max_pages, int budget, int sink, int recent,
+                               const int32_t* new_table, int new_max_pages, int32_t* kept, int32_t* new_lens,
+                               void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* gdpa_status_string(int status);
 

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libgdpa.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["gdpa_kernels.cu", "gdpa_bwd.cu", "gdpa_api.cu", "gdpa_plan.cpp", "gdpa_noalloc.cu", "gdpa_cache.cu"]
+SOURCES = ["gdpa_kernels.cu", "gdpa_bwd.cu", "gdpa_api.cu", "gdpa_plan.cpp", "gdpa_noalloc.cu", "gdpa_cache.cu",
+           "gdpa_cache_weights.cu", "gdpa_cache_evict.cu", "gdpa_rope.cu"]
 
 
 def _nvcc() -> str:

@@ -47,7 +47,7 @@ struct AppendParams {
 constexpr int kAppendThreads = 256;
 
 // cos, sin of position pos times fraction F of a turn.
-__device__ __forceinline__ float2 rope_angle(unsigned long long F, int pos) {
+__device__ __forceinline__ float2 rope_angle(unsigned long long F, int64_t pos) {
   const int turn = static_cast<int>((static_cast<unsigned long long>(pos) * F) >> 32);  // [-1/2, 1/2) turns, 2^-32 units
   float s, c;
   sincospif(static_cast<float>(turn) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns

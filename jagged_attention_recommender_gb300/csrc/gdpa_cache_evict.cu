@@ -1,0 +1,59 @@
+// gdpa_cache_evict.cu -- the C ABI of the cache's eviction (gdpa_cache_evict;
+// declared in include/gdpa.h): argument checks and launches.  Nothing here
+// allocates, synchronises or reads device data.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gdpa_cache_evict.cuh"
+#include "gdpa_cache_host.h"
+
+using namespace gdpa;
+
+extern "C" gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weights, const int32_t* kv_lens,
+                                          const int32_t* page_table, int B, int max_pages, int budget, int sink,
+                                          int recent, const int32_t* new_table, int new_max_pages, int32_t* kept,
+                                          int32_t* new_lens, void* stream) {
+  gdpa_status_t st = check_cache(cache);
+  if (st != GDPA_OK) return st;
+  if ((st = check_batch(cache, 0, B, max_pages)) != GDPA_OK) return st;
+  if (budget <= 0 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget || new_max_pages < 0)
+    return GDPA_ERR_INVALID_ARG;
+  if (B == 0) return GDPA_OK;
+  const int64_t most = (int64_t)max_pages * cache->page_tokens, room = (int64_t)new_max_pages * cache->page_tokens;
+  if (max_pages == 0 || room < std::min<int64_t>(budget, most)) return GDPA_ERR_INVALID_ARG;
+  if (!weights || !aligned(weights, 16) || !kv_lens || !page_table || !new_table || !kept || !new_lens)
+    return GDPA_ERR_INVALID_ARG;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(kv_lens), c = reinterpret_cast<uintptr_t>(new_lens), n = 4 * (uintptr_t)B;
+  if (a < c + n && c < a + n) return GDPA_ERR_INVALID_ARG;
+  Device dev;
+  if ((st = current_device(&dev)) != GDPA_OK) return st;
+  EvictParams p;
+  p.cache = view(cache);
+  p.weights = weights;
+  p.kv_lens = kv_lens;
+  p.table = page_table;
+  p.new_table = new_table;
+  p.kept = kept;
+  p.new_lens = new_lens;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.new_max_pages = new_max_pages;
+  p.budget = budget;
+  p.most = static_cast<int>(std::min<int64_t>(budget, most));
+  p.sink = sink;
+  p.recent = recent;
+  p.status = dev.status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t heads = (int64_t)B * cache->H;
+  gdpa_cache_choose_kernel<<<static_cast<unsigned>(std::min<int64_t>(heads, 1 << 20)), kChooseThreads, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return GDPA_ERR_CUDA;
+  const int64_t tasks = heads * (((int64_t)p.most + kCacheBlock - 1) / kCacheBlock);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((tasks + 7) / 8, 1 << 20));
+  if (cache->D == 128)
+    gdpa_cache_move_kernel<128><<<blocks, 256, 0, s>>>(p);
+  else
+    gdpa_cache_move_kernel<64><<<blocks, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}

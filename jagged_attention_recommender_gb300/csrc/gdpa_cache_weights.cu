@@ -1,0 +1,65 @@
+// gdpa_cache_weights.cu -- the C ABI of the weight that stored keys receive
+// (gdpa_cache_weights; declared in include/gdpa.h): argument checks and
+// launches.  Nothing here allocates, synchronises or reads device data.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gdpa_cache_host.h"
+#include "gdpa_cache_weights.cuh"
+
+namespace gdpa {
+namespace {
+
+template <int D>
+gdpa_status_t launch_weights(const CacheWeightsParams& p, cudaStream_t s) {
+  const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((keys + 127) / 128, 1 << 20)),
+                  static_cast<unsigned>(std::min<int64_t>((int64_t)p.batch.B * p.cache.H, 65535)));
+  gdpa_cache_weights_kernel<D><<<grid, 128, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace gdpa
+
+using namespace gdpa;
+
+extern "C" gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const void* q, int64_t q_stride,
+                                            const float* lse, const int32_t* offsets, const int32_t* kv_lens,
+                                            const int32_t* page_table, int64_t T, int B, int Hq, int max_pages,
+                                            int max_q, int causal, int window_tokens, float scale, float decay,
+                                            const float* weights_in, float* weights, void* stream) {
+  gdpa_status_t st = check_cache(cache);
+  if (st != GDPA_OK) return st;
+  if ((st = check_batch(cache, T, B, max_pages)) != GDPA_OK) return st;
+  if (Hq <= 0 || Hq % cache->H || max_q <= 0 || window_tokens < 0 || (causal != 0 && causal != 1) ||
+      (window_tokens > 0 && !causal) || !std::isfinite(scale) || !std::isfinite(decay) || decay < 0)
+    return GDPA_ERR_INVALID_ARG;
+  if ((int64_t)Hq * cache->D > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
+  if (T * (Hq / cache->H) >= ((int64_t)1 << 31) - 256) return GDPA_ERR_UNSUPPORTED;  // query rows of a key head
+  if (T == 0 || B == 0) return GDPA_OK;
+  if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
+  if (!lse || !aligned(lse, 4) || !offsets || !kv_lens || !page_table || max_pages == 0) return GDPA_ERR_INVALID_ARG;
+  if (!weights || !aligned(weights, 16) || !aligned(weights_in, 16)) return GDPA_ERR_INVALID_ARG;
+  Device dev;
+  if ((st = current_device(&dev)) != GDPA_OK) return st;
+  CacheWeightsParams p;
+  p.cache = view(cache);
+  p.batch = CacheBatch{offsets, kv_lens, page_table, static_cast<int>(T), B, max_pages, dev.status};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.lse = lse;
+  p.w_in = weights_in;
+  p.w = weights;
+  p.Hq = Hq;
+  p.G = Hq / cache->H;
+  p.causal = causal;
+  p.window = window_tokens;
+  p.scale2 = scale * 1.4426950408889634f;
+  p.decay = decay;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->D == 128 ? launch_weights<128>(p, s) : launch_weights<64>(p, s);
+}

@@ -25,6 +25,11 @@ GDPA_ROUTE_ALU = 1
 GDPA_ROPE_HALF = 0
 GDPA_ROPE_INTERLEAVED = 1
 
+GDPA_ROPE_SCALE_NONE = 0
+GDPA_ROPE_SCALE_LINEAR = 1
+GDPA_ROPE_SCALE_BASE = 2
+GDPA_ROPE_SCALE_RAMP = 3
+
 GDPA_OK = 0
 GDPA_ERR_INVALID_ARG = 1
 GDPA_ERR_UNSUPPORTED = 2
@@ -36,7 +41,8 @@ GDPA_ERR_NO_MEMORY = 5
 EXPORTS = ("gdpa_fwd", "gdpa_fwd_async", "gdpa_fwd_lse", "gdpa_fwd_sliding", "gdpa_fwd_mx", "gdpa_fwd_mxfp8", "gdpa_bwd", "gdpa_bwd_sliding", "gdpa_fwd_noalloc", "gdpa_plan_create", "gdpa_plan_create_sliding", "gdpa_fwd_planned", "gdpa_plan_destroy", "gdpa_plan_num_items",
            "gdpa_plan_num_ctas", "gdpa_fwd_host", "gdpa_plan_enumerate", "gdpa_act_eval", "gdpa_set_act_route",
            "gdpa_get_act_route", "gdpa_device_status", "gdpa_wait_selftest", "gdpa_status_string", "gdpa_version",
-           "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size")
+           "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size", "gdpa_cache_weights", "gdpa_cache_evict",
+           "gdpa_rope", "gdpa_rope_freqs")
 
 
 class GdpaError(RuntimeError):
@@ -98,13 +104,19 @@ def lib() -> ctypes.CDLL:
     L.gdpa_cache_append.argtypes = [P, P, I64, P, I64, P, I64, P, P, P, I64, I, I, I, P, P]
     L.gdpa_cache_fwd.argtypes = [P, P, I64, P, P, P, I64, I, I, I, I, I, I, F, P, P, P, I64, P]
     L.gdpa_cache_workspace_size.argtypes = [P, I, I, ctypes.POINTER(I64)]
+    D = ctypes.c_double
+    L.gdpa_cache_weights.argtypes = [P, P, I64, P, P, P, P, I64, I, I, I, I, I, I, F, F, P, P, P]
+    L.gdpa_cache_evict.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, P]
+    L.gdpa_rope.argtypes = [P, I64, P, P, I64, I, I, I, P, I, I, F, I, P, I64, P]
+    L.gdpa_rope_freqs.argtypes = [I, D, I, D, I64, D, D, P, P]
     L.gdpa_status_string.argtypes = [I]
     L.gdpa_status_string.restype = ctypes.c_char_p
     L.gdpa_version.argtypes = []
     L.gdpa_version.restype = ctypes.c_char_p
     for name in ("gdpa_fwd", "gdpa_fwd_async", "gdpa_fwd_lse", "gdpa_fwd_sliding", "gdpa_fwd_mxfp8", "gdpa_bwd", "gdpa_bwd_sliding", "gdpa_fwd_noalloc", "gdpa_plan_create", "gdpa_plan_create_sliding", "gdpa_fwd_planned", "gdpa_plan_num_ctas", "gdpa_fwd_host",
                  "gdpa_plan_enumerate", "gdpa_act_eval", "gdpa_set_act_route", "gdpa_device_status", "gdpa_wait_selftest",
-                 "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size"):
+                 "gdpa_cache_append", "gdpa_cache_fwd", "gdpa_cache_workspace_size", "gdpa_cache_weights",
+                 "gdpa_cache_evict", "gdpa_rope", "gdpa_rope_freqs"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -395,8 +407,8 @@ def _cache_at(where, device, cache):
 
 
 def _rows_at(where, device, cache, t, stride, T, heads=0):
-    """The address of bf16 rows ``stride`` apart, T of them or more, each of ``heads`` heads (0: the cache's) of D
-    elements side by side; a tensor laid out in another way is refused."""
+    """The address of bf16 rows ``stride`` apart, T of them or more, each of ``heads`` heads (0: the cache's) of
+    cache.D elements side by side; a tensor laid out in another way is refused."""
     if t is None or t.__class__ is int:
         return t
     if t.dtype is not _bf16 or t.get_device() != device:
@@ -493,3 +505,69 @@ def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:
     _check(lib().gdpa_cache_workspace_size(cache.addr, int(Hq), int(max_q), ctypes.byref(n)),
            "gdpa_cache_workspace_size")
     return n.value
+
+
+def _weights_at(where, device, cache, t):
+    """The address of one fp32 weight for every slot and head of the cache."""
+    pages, H, tokens = cache.desc.num_pages, cache.H, cache.desc.page_tokens
+    return _at(where, device, _f32, t, pages * H * tokens)
+
+
+def gdpa_cache_weights(cache: KvCache, q, q_stride, lse, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
+                       window_tokens, scale, decay, weights_in, weights, stream=None):
+    """Adds to ``weights`` (fp32 ``[num_pages, H, page_tokens]``) the attention weight that the rows ``q`` give each
+    stored key; ``lse`` is gdpa_cache_fwd's.  ``weights_in``: the earlier weights (``weights`` itself, or None)."""
+    d, where = _device(), "gdpa_cache_weights"
+    n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
+    _check(lib().gdpa_cache_weights(
+        _cache_at(where, d, cache), _rows_at(where, d, cache, q, q_stride, n, Hq), q_stride,
+        _at(where, d, _f32, lse, n * Hq), _at(where, d, _i32_t, offsets, b + 1), _at(where, d, _i32_t, kv_lens, b),
+        _table_at(where, d, page_table, b, max_pages), T, B, Hq, max_pages, max_q, causal, window_tokens, scale, decay,
+        _weights_at(where, d, cache, weights_in), _weights_at(where, d, cache, weights),
+        (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
+
+
+def gdpa_cache_evict(cache: KvCache, weights, kv_lens, page_table, B, max_pages, budget, sink, recent, new_table,
+                     new_max_pages, kept, new_lens, stream=None):
+    """Cuts each sequence to ``budget`` tokens, every head by its own ``weights``, and stores what is kept in the pages
+    of ``new_table``.  ``kept``: int32 ``[B, H, budget]``, ``new_lens``: int32 ``[B]``."""
+    d, where = _device(), "gdpa_cache_evict"
+    b = B if B > 0 else 0
+    _check(lib().gdpa_cache_evict(
+        _cache_at(where, d, cache), _weights_at(where, d, cache, weights), _at(where, d, _i32_t, kv_lens, b),
+        _table_at(where, d, page_table, b, max_pages), B, max_pages, budget, sink, recent,
+        _table_at(where, d, new_table, b, new_max_pages), new_max_pages,
+        _at(where, d, _i32_t, kept, b * cache.H * max(budget, 0)), _at(where, d, _i32_t, new_lens, b),
+        (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
+
+
+class _Heads:
+    """What _rows_at asks of a cache, for rows that belong to none."""
+
+    def __init__(self, H, D):
+        self.H, self.D = H, D
+
+
+def gdpa_rope(x, x_stride, offsets, first, T, B, H, D, inv_freq, rope_style, magnitude, inverse, y, y_stride, stream=None):
+    """``y``: the rows ``x`` of a jagged batch turned by their positions (``inverse``: the gradient of that).
+    ``inv_freq``: host float64, radians per position of each pair (None: nothing turns); ``first``: int32 ``[B]``, the
+    position of each sequence's first row (None: 0)."""
+    d, where = _device(), "gdpa_rope"
+    n, b = (T, B) if T > 0 and B > 0 else (0, -1)  # a call with nothing to do wants nothing of its tensors
+    f = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
+    heads = _Heads(H, D)
+    _check(lib().gdpa_rope(
+        _rows_at(where, d, heads, x, x_stride, n), x_stride, _at(where, d, _i32_t, offsets, b + 1),
+        _at(where, d, _i32_t, first, b), T, B, H, D, None if f is None or f.size == 0 else f.ctypes.data,
+        0 if f is None else 2 * f.size, int(rope_style), magnitude, int(inverse),
+        _rows_at(where, d, heads, y, y_stride, n), y_stride,
+        (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
+
+
+def gdpa_rope_freqs(rot_dim, base=10000.0, scaling=GDPA_ROPE_SCALE_NONE, factor=1.0, trained=0, fast=32.0, slow=1.0):
+    """(inv_freq float64 ``[rot_dim // 2]``, magnitude) of a context stretched by ``factor`` (``scaling``:
+    GDPA_ROPE_SCALE_...)."""
+    f, m = np.empty(max(int(rot_dim), 0) // 2, np.float64), ctypes.c_float(0)
+    _check(lib().gdpa_rope_freqs(int(rot_dim), float(base), int(scaling), float(factor), int(trained), float(fast),
+                                 float(slow), f.ctypes.data, ctypes.byref(m)), "gdpa_rope_freqs")
+    return f, m.value
