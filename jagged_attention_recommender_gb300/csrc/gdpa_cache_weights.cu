@@ -14,12 +14,35 @@ namespace gdpa {
 namespace {
 
 template <int D>
-gdpa_status_t launch_weights(const CacheWeightsParams& p, cudaStream_t s) {
+gdpa_status_t launch_simple(const CacheWeightsParams& p, cudaStream_t s) {
   const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((keys + 127) / 128, 1 << 20)),
                   static_cast<unsigned>(std::min<int64_t>((int64_t)p.batch.B * p.cache.H, 65535)));
   gdpa_cache_weights_kernel<D><<<grid, 128, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <int D, int NT>
+gdpa_status_t launch_split(const CacheWeightsParams& p, const Device& dev, cudaStream_t s) {
+  using C = WeightCfg<D, NT>;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  const gdpa_status_t st = allow_smem(gdpa_cache_weights_split_kernel<D, NT>, C::SMEM, 0, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
+  const int64_t work = (int64_t)p.batch.B * p.cache.H * ((keys + C::SPAN - 1) / C::SPAN + C::START);
+  const int ctas = static_cast<int>(std::min<int64_t>((work + C::WARPS - 1) / C::WARPS, (int64_t)dev.sms * C::CTAS));
+  gdpa_cache_weights_split_kernel<D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <int D>
+gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
+  const int64_t rows = (int64_t)max_q * p.G;
+  if (rows <= 8) return launch_split<D, 1>(p, dev, s);
+  if (rows <= 24) return launch_split<D, 3>(p, dev, s);
+  if (rows <= 48) return launch_split<D, 6>(p, dev, s);
+  return launch_simple<D>(p, s);
 }
 
 }  // namespace
@@ -58,8 +81,9 @@ extern "C" gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const voi
   p.G = Hq / cache->H;
   p.causal = causal;
   p.window = window_tokens;
-  p.scale2 = scale * 1.4426950408889634f;
+  p.scale2 = scale * kLog2e;
   p.decay = decay;
+  p.keep = weights_in == weights && decay == 1.0f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cache->D == 128 ? launch_weights<128>(p, s) : launch_weights<64>(p, s);
+  return cache->D == 128 ? launch_weights<128>(p, max_q, dev, s) : launch_weights<64>(p, max_q, dev, s);
 }
