@@ -9,18 +9,16 @@
 
 #include "gdpa_cache_host.h"
 #include "gdpa_cache_weights.cuh"
+#include "gdpa_cache_weights_tile.cuh"
 
 namespace gdpa {
-namespace {
 
-template <int D>
-gdpa_status_t launch_simple(const CacheWeightsParams& p, cudaStream_t s) {
-  const int64_t keys = (int64_t)p.batch.max_pages << p.cache.lp;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((keys + 127) / 128, 1 << 20)),
-                  static_cast<unsigned>(std::min<int64_t>((int64_t)p.batch.B * p.cache.H, 65535)));
-  gdpa_cache_weights_kernel<D><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
-}
+// gdpa_kernels.cu: a view [rows, H, D] of bf16 rows `stride` elements apart, boxes
+// of 64 columns, box_heads heads and box_rows rows with the 128-byte swizzle.
+gdpa_status_t encode_heads_3d(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int64_t stride, int box_heads,
+                              int box_rows);
+
+namespace {
 
 template <int D, int NT>
 gdpa_status_t launch_split(const CacheWeightsParams& p, const Device& dev, cudaStream_t s) {
@@ -37,12 +35,34 @@ gdpa_status_t launch_split(const CacheWeightsParams& p, const Device& dev, cudaS
 }
 
 template <int D>
+gdpa_status_t launch_tile(const CacheWeightsParams& w, int max_q, const Device& dev, cudaStream_t s) {
+  using C = WeightTileCfg<D>;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  gdpa_status_t st = allow_smem(gdpa_cache_weights_tile_kernel<D>, C::SMEM, 0, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  WeightTileParams p;
+  p.w = w;
+  p.heads = std::min(w.G, C::COLS);
+  p.tokens = C::COLS / p.heads;
+  p.parts = (w.G + p.heads - 1) / p.heads;
+  p.group = p.parts == 1 && max_q <= p.tokens ? 4 : 1;
+  p.limit = bounded_wait_ns();
+  if ((st = encode_heads_3d(&p.tm_q, w.q, w.batch.T, w.Hq, D, w.q_stride, p.heads, p.tokens)) != GDPA_OK) return st;
+  const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp, items = (keys + 255) / 256;
+  const int64_t groups = (int64_t)w.batch.B * w.cache.H * ((items + p.group - 1) / p.group);
+  const int ctas = static_cast<int>(std::min<int64_t>(groups, dev.sms));
+  gdpa_cache_weights_tile_kernel<D><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <int D>
 gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
   const int64_t rows = (int64_t)max_q * p.G;
   if (rows <= 8) return launch_split<D, 1>(p, dev, s);
   if (rows <= 24) return launch_split<D, 3>(p, dev, s);
   if (rows <= 48) return launch_split<D, 6>(p, dev, s);
-  return launch_simple<D>(p, s);
+  return launch_tile<D>(p, max_q, dev, s);
 }
 
 }  // namespace

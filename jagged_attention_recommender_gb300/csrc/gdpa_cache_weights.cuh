@@ -55,40 +55,6 @@ __device__ __forceinline__ RowSpan rows_of_key(const CacheSeq& s, int j, int cau
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) gdpa_cache_weights_kernel(const __grid_constant__ CacheWeightsParams p) {
-  const CacheBatch& bt = p.batch;
-  const int64_t heads = static_cast<int64_t>(bt.B) * p.cache.H;
-  for (int64_t bh = blockIdx.y; bh < heads; bh += gridDim.y) {
-    const int b = static_cast<int>(bh / p.cache.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * p.cache.H);
-    const CacheSeq s = load_sequence(bt, p.cache.lp, b);
-    if (!s.ok || s.n == 0) continue;
-    for (int64_t j64 = blockIdx.x * 128ll + threadIdx.x; j64 < s.len; j64 += gridDim.x * 128ll) {
-      const int j = static_cast<int>(j64);
-      const int page = load_page(p.cache, bt, b, j);
-      if (page < 0) continue;
-      const int64_t row = cache_row(p.cache, page, h, j & ((1 << p.cache.lp) - 1));
-      float k[D];
-      const uint8_t* codes = p.cache.k + row * D;
-      for (int d = 0; d < D; ++d) k[d] = e4m3_to_float(codes[d]);
-      const float f = sf_value(p.cache.k_sf[row >> 4]) * p.scale2;
-      float sum = p.w_in && j < s.len - s.n ? p.decay * p.w_in[row] : 0.0f;
-      const RowSpan rows = rows_of_key(s, j, p.causal, p.window);
-      for (int i = rows.lo; i < rows.hi; ++i) {
-        for (int g = 0; g < p.G; ++g) {
-          const int head = h * p.G + g;
-          const float lse = __ldg(p.lse + static_cast<int64_t>(s.first + i) * p.Hq + head);
-          const __nv_bfloat16* q = p.q + (s.first + i) * p.q_stride + head * D;
-          float x = 0.0f;
-          for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), k[d], x);
-          if (lse != -INFINITY) sum += ptx::ex2_approx(x * f - lse * 1.4426950408889634f);
-        }
-      }
-      p.w[row] = sum;
-    }
-  }
-}
-
 // NT: row tiles of 8 whose fragments a warp keeps (sequences with more rows make
 // them anew at every step).
 template <int D, int NT_>

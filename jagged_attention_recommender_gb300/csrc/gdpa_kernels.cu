@@ -248,6 +248,20 @@ __global__ void wait_selftest_kernel(int* status, unsigned long long limit_ns) {
 }  // namespace
 
 // Shared with the backward launcher (gdpa_bwd.cu).
+gdpa_status_t encode_heads_3d(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int64_t stride, int box_heads,
+                              int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return GDPA_ERR_CUDA;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
 gdpa_status_t encode_rows_2d(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int box_rows) {
   return encode_rows(m, base, rows, H, D, box_rows);
 }
