@@ -46,7 +46,10 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, int max_q, const Device& 
   p.heads = std::min(w.G, C::COLS);
   p.tokens = C::COLS / p.heads;
   p.parts = (w.G + p.heads - 1) / p.heads;
-  p.group = p.parts == 1 && max_q <= p.tokens ? 4 : 1;
+  const bool single = p.parts == 1 && max_q <= p.tokens;  // the rows of a sequence fit one chunk
+  p.group = single ? 4 : 1;
+  p.ks = single ? 3 : 2;
+  p.qs = C::STAGES - p.ks;
   p.limit = bounded_wait_ns();
   if ((st = encode_heads_3d(&p.tm_q, w.q, w.batch.T, w.Hq, D, w.q_stride, p.heads, p.tokens)) != GDPA_OK) return st;
   const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp, items = (keys + 255) / 256;

@@ -14,10 +14,14 @@
 // columns (tokens times heads of the group); sequences whose rows fit one
 // chunk keep the chunk instead and pass p.group items.  CTAs take every
 // gridDim.x-th group of items.  Roles:
-//   warps 0-3, 4-7  the sums of the item's first and second 128 keys, a key a thread
-//   warps 8-11      convert K (128-byte swizzle, four tiles)
-//   warp 12         issues the MMAs
-//   warp 13         brings the queries by TMA, their logsumexp and last keys
+//   warps 0-15   the sums, a key a thread: warpgroups 0 and 2 those of the item's
+//                first 128 keys, 1 and 3 of its second, each every other chunk
+//   warps 16-19  bring codes, scales and earlier weights by their own
+//                asynchronous copies, RAWS tiles ahead, and convert K (128-byte
+//                swizzle)
+//   warp 20      issues the MMAs
+//   warp 21      brings the queries by TMA
+//   warp 22      notes their logsumexp and the last keys they see
 #pragma once
 
 #include "gdpa_cache_append.cuh"
@@ -45,17 +49,23 @@ struct WeightTileParams {
   int heads, tokens;  // of a chunk: heads * tokens <= 128 (heads: G, or 128 of more)
   int parts;          // chunks that the heads of a group make
   int group;          // items of a group
+  int ks, qs;         // stages of K and of Q: ks + qs = WeightTileCfg::STAGES
   unsigned long long limit;
 };
 
 template <int D_>
 struct WeightTileCfg {
-  static constexpr int D = D_, THREADS = 448, KEYS = 128, COLS = 128;
+  static constexpr int D = D_, THREADS = 736, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
-  static constexpr int KS = 4, QS = 2;             // stages of K and of Q
-  static constexpr int OFF_Q = KS * TILE, OFF_NOTES = OFF_Q + QS * TILE;
-  static constexpr int USED = OFF_NOTES + KS * 512 + QS * 1024;
+  // Stages of K and Q together.  Where chunks pass the keys two are K's and three
+  // Q's: a chunk's way from L2 takes longer than its products.  Where tiles pass
+  // the queries three are K's.
+  static constexpr int STAGES = 5, MOST_KS = 3, MOST_QS = 3, NS = 4;  // NS: of a chunk's notes
+  static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
+  static constexpr int OFF_RAW = STAGES * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
+  static constexpr int KEY_NOTES = 2048;           // of each key: its row, its scale, its earlier weight
+  static constexpr int USED = OFF_NOTES + (RAWS + MOST_KS) * KEY_NOTES + NS * 1024 + 1024;
   static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;  // one CTA an SM (all of its TMEM)
   static constexpr uint32_t TM_COLS = 512;         // S of two tiles, two buffers each
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -64,57 +74,107 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t k_full[4], k_free[4], q_full[2], q_free[2], s_full[2][2], s_free[2][2], drain;
+  uint64_t k_full[3], k_free[3], q_full[3], q_free[3], n_full[4], n_free[4];
+  uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
 };
 
-struct Notes {
-  float* factor;  // [KS][128]: of each key's scores, in units of log2
-  float* lse;     // [QS][128]: minus each column's logsumexp, in units of log2
-  int* last;      // [QS][128]: the last key that each column sees, -1 for none
+// A place in a ring of stages, and the parity of its present turn.
+struct Ring {
+  uint32_t at = 0, turn = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++at == stages) at = 0, turn ^= 1;
+  }
 };
 
-// Groups of items of one CTA, in order.
-struct Walk {
-  CacheSeq s;
-  int64_t idx;  // among the sequence's groups
-  int b, h, kbase, pairs, groups;
-  int pair, pair_end;
-  bool single;  // its rows fit one chunk
+// What goes with a tile of keys: where each one's weight is (-1: nowhere), and
+//   on its way (word, old)  the word with its scale's code, its earlier weight
+//   converted (factor, old) the factor of its scores in units of log2, the weight
+struct KeyNotes {
+  int64_t row[128];
+  union {
+    uint32_t word[128];
+    float factor[128];
+  };
+  float old[128];
+};
 
+struct Notes {
+  KeyNotes* raw;  // [RAWS]
+  KeyNotes* key;  // [KS]
+  float* lse;     // [NS][128]: minus each column's logsumexp, in units of log2
+  int* last;      // [NS][128]: the last key that each column sees, -1 for none
+  float* half;    // [2][128]: sums on their way from one warpgroup to the other
+};
+
+// Groups of items of one CTA, in order, by a whole warp: its lanes hold 32
+// sequences, so that the next group is found without a load.
+struct Walk {
+  int64_t upto;     // groups of the sequences up to this lane's
+  CacheSeq lane_s;  // this lane's sequence
+  int64_t idx;      // the present group, counted from the first lane's sequence
+  int base;         // that sequence
+  bool back;
+  // the present group
+  CacheSeq s;
+  int b, h, kbase, pair, pair_end;
+  bool single;      // its rows fit one chunk
+
+  __device__ __forceinline__ int first_stored(const WeightTileParams& p, const CacheSeq& q) const {
+    return p.w.keep ? min(first_key(q.len - q.n, p.w.window), q.len) & ~255 : 0;
+  }
+  __device__ __forceinline__ int pairs_of(const WeightTileParams& p, const CacheSeq& q) const {
+    return static_cast<int>((static_cast<unsigned>(q.len - first_stored(p, q)) + 255) >> 8);
+  }
   __device__ __forceinline__ void load(const WeightTileParams& p) {
-    const CacheWeightsParams& w = p.w;
-    s = load_sequence(w.batch, w.cache.lp, b);
-    pairs = groups = kbase = 0;
-    single = false;
-    if (!s.ok || s.n == 0 || s.len == 0) return;
-    if (w.keep) kbase = min(first_key(s.len - s.n, w.window), s.len) & ~255;
-    pairs = static_cast<int>((static_cast<unsigned>(s.len - kbase) + 255) >> 8);
-    groups = (pairs + p.group - 1) / p.group;
-    single = p.parts == 1 && s.n <= p.tokens;
+    const int lane = threadIdx.x & 31;
+    lane_s = CacheSeq{0, 0, 0, 0};
+    if (base + lane < p.w.batch.B) lane_s = load_sequence(p.w.batch, p.w.cache.lp, base + lane);
+    upto = 0;
+    if (lane_s.ok && lane_s.n > 0 && lane_s.len > 0)
+      upto = static_cast<int64_t>((pairs_of(p, lane_s) + p.group - 1) / p.group) * p.w.cache.H;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
   }
   __device__ __forceinline__ bool settle(const WeightTileParams& p) {
     while (true) {
-      const int64_t all = static_cast<int64_t>(groups) * p.w.cache.H;
+      const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
       if (idx < all) break;
       idx -= all;
-      if (++b >= p.w.batch.B) return false;
+      if (p.w.batch.B - base <= 32) return false;
+      base += 32;
       load(p);
     }
-    h = static_cast<int>(idx / groups);
-    pair = static_cast<int>(idx - static_cast<int64_t>(h) * groups) * p.group;
+    const int at = __popc(__ballot_sync(0xffffffffu, upto <= idx));
+    const int64_t before = __shfl_sync(0xffffffffu, upto, max(at - 1, 0));
+    s.first = __shfl_sync(0xffffffffu, lane_s.first, at);
+    s.n = __shfl_sync(0xffffffffu, lane_s.n, at);
+    s.len = __shfl_sync(0xffffffffu, lane_s.len, at);
+    s.ok = 1;
+    b = base + at;
+    const int64_t i = idx - (at > 0 ? before : 0);
+    const int pairs = pairs_of(p, s), groups = (pairs + p.group - 1) / p.group;
+    h = static_cast<int>(i / groups);
+    pair = static_cast<int>(i - static_cast<int64_t>(h) * groups) * p.group;
     pair_end = min(pairs, pair + p.group);
+    kbase = first_stored(p, s);
+    single = p.parts == 1 && s.n <= p.tokens;
     return true;
   }
   __device__ __forceinline__ bool begin(const WeightTileParams& p) {
-    b = 0;
+    base = 0;
+    back = false;
     idx = blockIdx.x;
     load(p);
     return settle(p);
   }
   __device__ __forceinline__ bool next(const WeightTileParams& p) {
-    idx += gridDim.x;
+    back = !back;  // there and back: neighbours' costs are alike
+    idx += 2 * static_cast<int64_t>(back ? gridDim.x - 1 - blockIdx.x : blockIdx.x) + 1;
     return settle(p);
   }
 };
@@ -146,12 +206,15 @@ template <int D>
 __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes, uint32_t tmem) {
   using C = WeightTileCfg<D>;
   const CacheWeightsParams& w = p.w;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = warp >> 2;  // m: this warpgroup's tile of an item
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int m = warp >> 2 & 1;        // this warpgroup's tile of an item ...
+  const uint32_t turn = warp >> 3;    // ... and buffer of S
   const int key_in = (warp & 3) * 32 + lane;
-  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * 256;
+  const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * 256 + turn * 128;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  uint32_t ki = 0, qi = 0, si = 0;  // tiles of K, chunks and tiles of S so far
+  Ring k, n;                 // of tiles of K and chunks' notes
+  uint32_t si = 0, xi = 0;   // tiles of S, and sums in two halves, so far
   bool ok = true;
   Walk walk;
   for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
@@ -161,61 +224,65 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
     for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
       const Item it = item_of(p, walk, pair);
       const bool mine = m < it.tiles;
-      const int k0 = it.k0 + m * 128;
-      const bool stored = mine && s.len - k0 > key_in;
-      const int key = k0 + key_in;
-      // where the key's weight is, and what it was
+      const int k0 = it.k0 + m * 128, key = k0 + key_in;
       int64_t row = -1;
-      float old = 0.0f;
-      if (stored) {
-        const int page = load_page(w.cache, w.batch, walk.b, key);
-        if (page >= 0) {
-          row = cache_row(w.cache, page, walk.h, key & pmask);
-          if (w.w_in && key < s.len - s.n) old = w.decay * w.w_in[row];
+      float old = 0.0f, factor = 0.0f;
+      if (it.chunks == 0) {  // no row sees these keys: earlier weights alone
+        if (mine && turn == 0 && s.len - k0 > key_in) {
+          const int page = load_page(w.cache, w.batch, walk.b, key);
+          if (page >= 0) {
+            row = cache_row(w.cache, page, walk.h, key & pmask);
+            w.w[row] = w.w_in && key < s.len - s.n ? w.decay * w.w_in[row] : 0.0f;
+          }
         }
+        __syncwarp();
+        continue;
       }
-      __syncwarp();
-      float factor = 0.0f;
-      if (it.chunks > 0 && mine) {
-        const uint32_t k = ki + m;
-        ok = ptx::mbar_wait(&B.k_full[k % C::KS], k / C::KS & 1, p.limit, abort);
+      if (m == 1 && mine) k.next(p.ks);  // the first tile is the others'
+      if (mine) {
+        ok = ptx::mbar_wait(&B.k_full[k.at], k.turn, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        factor = notes.factor[k % C::KS * 128 + key_in];
+        row = notes.key[k.at].row[key_in];
+        factor = notes.key[k.at].factor[key_in];
+        old = notes.key[k.at].old[key_in];
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&B.k_free[k % C::KS]);
+        if (lane == 0) ptx::mbar_arrive(&B.k_free[k.at]);
       }
-      if (it.chunks > 0) ki += it.tiles;
+      k.next(p.ks);
+      if (m == 0 && it.tiles == 2) k.next(p.ks);
       const uint64_t f2 = ptx::f2_splat(factor);
       uint64_t sum[2] = {0, 0};
       float edge_sum = 0.0f;
       const int k_last = k0 + min(127, s.len - 1 - k0);
+      const bool writes = it.chunks == 1 ? (si & 1) == turn : turn == 0;
 #pragma unroll 1
       for (int c = 0; c < it.chunks; ++c) {
-        const uint32_t qs = qi % C::QS;
-        if (!held) ok = ptx::mbar_wait(&B.q_full[qs], qi / C::QS & 1, p.limit, abort);
+        const bool due = mine && (si & 1) == turn;
+        if (!held) ok = ptx::mbar_wait(&B.n_full[n.at], n.turn, p.limit, abort);
         held = walk.single;
-        if (ok && mine) ok = ptx::mbar_wait(&B.s_full[m][si & 1], si >> 1 & 1, p.limit, abort);
+        if (ok && due) ok = ptx::mbar_wait(&B.s_full[m][turn], si >> 1 & 1, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (mine) {
+        if (due) {
           ptx::tc_fence_after();
-          const int n = (chunk_columns(p, it, c) + 31) >> 5;
-          const float* lse = notes.lse + qs * 128;
-          const int* last = notes.last + qs * 128;
+          const int blocks = (chunk_columns(p, it, c) + 31) >> 5;
+          const float* lse = notes.lse + n.at * 128;
+          const int* last = notes.last + n.at * 128;
 #pragma unroll 1
-          for (int q = 0; q < n; ++q) {
+          for (int q = 0; q < blocks; ++q) {
             uint32_t r[32];
-            ptx::tmem_ld32(lanes + (si & 1) * 128 + q * 32, r);
+            ptx::tmem_ld32(from + q * 32, r);
+            const int end0 = last[q * 32], end1 = last[q * 32 + 31];  // tokens, and so last keys, ascend
+            const bool all = end0 >= k_last && end1 >= end0 && (w.window == 0 || end1 - w.window < k0);
             ptx::tmem_wait_ld_r32(r);
-            if (q == n - 1) {  // the buffer is read
+            if (q == blocks - 1) {  // the buffer is read
               ptx::tc_fence_before();
               __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(&B.s_free[m][si & 1]);
+              if (lane == 0) ptx::mbar_arrive(&B.s_free[m][turn]);
               __syncwarp();
             }
-            const int end0 = last[q * 32], end1 = last[q * 32 + 31];  // tokens, and so last keys, ascend
-            if (end0 >= k_last && end1 >= end0 && (w.window == 0 || end1 - w.window < k0)) {
+            if (all) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const ulonglong2 l = reinterpret_cast<const ulonglong2*>(lse + q * 32)[i];
@@ -237,33 +304,51 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
             }
             __syncwarp();
           }
-          ++si;
         }
+        if (mine) ++si;
         if (!walk.single) {
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&B.q_free[qs]);
-          ++qi;
+          if (lane == 0) ptx::mbar_arrive(&B.n_free[n.at]);
+          n.next(C::NS);
         }
       }
       if (!ok) break;
-      if (row >= 0) {
-        float a, b, c, d;
-        ptx::f2_unpack(sum[0], a, b);
-        ptx::f2_unpack(sum[1], c, d);
-        w.w[row] = old + (((a + b) + (c + d)) + edge_sum);
+      if (!mine) continue;
+      float a, b, c, d;
+      ptx::f2_unpack(sum[0], a, b);
+      ptx::f2_unpack(sum[1], c, d);
+      float total = ((a + b) + (c + d)) + edge_sum;
+      if (it.chunks > 1) {  // both warpgroups have a part
+        if (turn == 1) {
+          ok = ptx::mbar_wait(&B.x_free[m], (xi & 1) ^ 1, p.limit, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          notes.half[m * 128 + key_in] = total;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&B.x_full[m]);
+        } else {
+          ok = ptx::mbar_wait(&B.x_full[m], xi & 1, p.limit, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          total += notes.half[m * 128 + key_in];
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&B.x_free[m]);
+        }
+        ++xi;
       }
+      if (writes && row >= 0) w.w[row] = old + total;
       __syncwarp();
     }
     if (!ok) break;
     if (walk.single) {
-      if (!held) {  // (its keys saw no row: the chunk came all the same)
-        ok = ptx::mbar_wait(&B.q_full[qi % C::QS], qi / C::QS & 1, p.limit, abort);
+      if (!held) {  // (its keys saw no row: the notes came all the same)
+        ok = ptx::mbar_wait(&B.n_full[n.at], n.turn, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&B.q_free[qi % C::QS]);
-      ++qi;
+      if (lane == 0) ptx::mbar_arrive(&B.n_free[n.at]);
+      n.next(C::NS);
     }
   }
   if (!ok && lane == 0) {
@@ -279,89 +364,209 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& h
   hi = ptx::pack_bf16x2(b.x, b.y);
 }
 
+// The tiles of K that a CTA needs, in order.
+struct TileWalk {
+  Walk walk;
+  Item it;
+  int pair, m;
+  __device__ __forceinline__ bool settle(const WeightTileParams& p) {  // to a tile at or behind `pair`
+    while (true) {
+      for (; pair < walk.pair_end; ++pair) {
+        it = item_of(p, walk, pair);
+        if (it.chunks > 0) return true;
+      }
+      if (!walk.next(p)) return false;
+      pair = walk.pair;
+    }
+  }
+  __device__ __forceinline__ bool begin(const WeightTileParams& p) {
+    m = 0;
+    if (!walk.begin(p)) return false;
+    pair = walk.pair;
+    return settle(p);
+  }
+  __device__ __forceinline__ bool next(const WeightTileParams& p) {
+    if (++m < it.tiles) return true;
+    m = 0;
+    ++pair;
+    return settle(p);
+  }
+};
+
 template <int D>
 __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
   using C = WeightTileCfg<D>;
   constexpr int CPR = D / 16, ROWS = 128 / CPR, N = 128 / ROWS;  // chunks of a key; keys of a pass; passes
   const CacheWeightsParams& w = p.w;
-  const int tid = threadIdx.x - 256, lane = tid & 31;
+  const int tid = threadIdx.x - 512, lane = tid & 31;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
+  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
   const int r0 = tid / CPR, c = tid % CPR;  // its row in a pass, and 16 coordinates
+  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW + tid * 16;  // a thread converts what it copied
   // 16-byte chunks 2c and 2c + 1 of a row, 64 columns a sub-tile
   const uint32_t base = ptx::smem_u32(sm) + (c >> 2) * C::SUB;
-  uint32_t ki = 0;
+  uint32_t ri = 0, ki = 0;  // tiles brought, and converted
+  Ring in, out, k;          // of codes brought, codes converted, tiles of K
   bool ok = true;
-  Walk walk;
-  for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
-#pragma unroll 1
-    for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
-      const Item it = item_of(p, walk, pair);
-      if (it.chunks == 0) continue;
-#pragma unroll 1
-      for (int m = 0; m < it.tiles; ++m, ++ki) {
-        const int k0 = it.k0 + m * 128;
-        int page = -1;  // lane i: of the tile's i-th block of 16
-        if (lane < 8 && walk.s.len - k0 > lane * 16) page = load_page(w.cache, w.batch, walk.b, k0 + lane * 16);
-        __syncwarp();
-        uint4 x[N];
+  TileWalk tiles;
+  bool more = tiles.begin(p);
+  while (true) {
+    while (more && ri - ki < C::RAWS) {
+      const Walk& at = tiles.walk;
+      const int k0 = tiles.it.k0 + tiles.m * 128, valid = at.s.len - k0;
+      const uint32_t rs = in.at;
+      KeyNotes& note = notes.raw[rs];
+      int page = -1;  // lane i: of the tile's i-th block of 16
+      if (lane < 8 && valid > lane * 16) page = load_page(w.cache, w.batch, at.b, k0 + lane * 16);
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = r0 + i * ROWS, pg = __shfl_sync(0xffffffffu, page, r >> 4);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (pg >= 0)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(
-                w.cache.k + cache_row(w.cache, pg, walk.h, (k0 + r) & pmask) * D + c * 16));
-        }
-        const int pg = __shfl_sync(0xffffffffu, page, tid >> 4);
-        const float f =
-            pg >= 0 ? sf_value(__ldg(w.cache.k_sf + cache_sf(w.cache, pg, walk.h, (k0 + tid) & pmask))) * w.scale2 : 0.0f;
-        const uint32_t ks = ki % C::KS;
-        ok = ptx::mbar_wait(&B.k_free[ks], (ki / C::KS & 1) ^ 1, p.limit, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        notes.factor[ks * 128 + tid] = f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = r0 + i * ROWS;
-          const uint32_t at = base + ks * C::TILE + r * 128, j = 2 * c & 7;
-          uint32_t a[8];
-          codes_bf16(x[i].x, a[0], a[1]);
-          codes_bf16(x[i].y, a[2], a[3]);
-          codes_bf16(x[i].z, a[4], a[5]);
-          codes_bf16(x[i].w, a[6], a[7]);
-          ptx::st_shared_v4(at + ((j ^ (r & 7)) << 4), a[0], a[1], a[2], a[3]);
-          ptx::st_shared_v4(at + (((j + 1) ^ (r & 7)) << 4), a[4], a[5], a[6], a[7]);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&B.k_full[ks]);
+      for (int i = 0; i < N; ++i) {  // (what is not there keeps what it held: no other key's score depends on it)
+        const int r = r0 + i * ROWS, pg = __shfl_sync(0xffffffffu, page, r >> 4);
+        if (pg >= 0)
+          split::cp_async16(raw + rs * C::RAW + i * 2048,
+                            w.cache.k + cache_row(w.cache, pg, at.h, (k0 + r) & pmask) * D + c * 16, 16);
       }
+      const int pg = __shfl_sync(0xffffffffu, page, tid >> 4);
+      const int64_t row = cache_row(w.cache, max(pg, 0), at.h, (k0 + tid) & pmask);
+      note.row[tid] = pg >= 0 && tid < valid ? row : -1;
+      if (pg >= 0) {
+        const int64_t word = (row >> 4) & ~(int64_t)3;
+        split::cp_async4(ptx::smem_u32(&note.word[tid]), w.cache.k_sf + word,
+                         static_cast<int>(min((int64_t)4, sf_bytes - word)));
+      }
+      // the rows' own keys have no earlier weight
+      if (pg >= 0 && w.w_in && tid < valid && k0 + tid < at.s.len - at.s.n)
+        split::cp_async4(ptx::smem_u32(&note.old[tid]), w.w_in + row, 4);
+      else
+        note.old[tid] = 0.0f;
+      split::cp_commit();
+      ++ri;
+      in.next(C::RAWS);
+      more = tiles.next(p);
     }
+    if (ri == ki) break;
+    const uint32_t ks = k.at, rs = out.at;
+    ok = ptx::mbar_wait(&B.k_free[ks], k.turn ^ 1, p.limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    if (more)
+      split::cp_wait<C::RAWS - 1>();
+    else
+      split::cp_wait<0>();
+    const KeyNotes& from = notes.raw[rs];
+    KeyNotes& to = notes.key[ks];
+    const int64_t row = from.row[tid];
+    to.row[tid] = row;
+    to.factor[tid] = sf_value(from.word[tid] >> static_cast<int>((row >> 4) & 3) * 8 & 0xff) * w.scale2;
+    to.old[tid] = w.decay * from.old[tid];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = r0 + i * ROWS;
+      const uint32_t at = base + ks * C::TILE + r * 128, j = 2 * c & 7;
+      uint32_t x[4], a[8];
+      split::lds128(raw + rs * C::RAW + i * 2048, x);
+      codes_bf16(x[0], a[0], a[1]);
+      codes_bf16(x[1], a[2], a[3]);
+      codes_bf16(x[2], a[4], a[5]);
+      codes_bf16(x[3], a[6], a[7]);
+      ptx::st_shared_v4(at + ((j ^ (r & 7)) << 4), a[0], a[1], a[2], a[3]);
+      ptx::st_shared_v4(at + (((j + 1) ^ (r & 7)) << 4), a[4], a[5], a[6], a[7]);
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive(&B.k_full[ks]);
+    ++ki;
+    k.next(p.ks);
+    out.next(C::RAWS);
   }
+  split::cp_wait<0>();
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusProducer);
   }
 }
 
+// f(item, chunk) for every chunk of this CTA, in order, until it returns false.
+template <class F>
+__device__ __forceinline__ bool each_chunk(const WeightTileParams& p, const F& f) {
+  Walk walk;
+  for (bool more = walk.begin(p); more; more = walk.next(p)) {
+    if (walk.single) {
+      const Item it = {0, 0, 0, walk.s.n, 1};
+      if (!f(walk, it, 0)) return false;
+      continue;
+    }
+    for (int pair = walk.pair; pair < walk.pair_end; ++pair) {
+      const Item it = item_of(p, walk, pair);
+#pragma unroll 1
+      for (int c = 0; c < it.chunks; ++c)
+        if (!f(walk, it, c)) return false;
+    }
+  }
+  return true;
+}
+
+// A chunk's first token, and which part of its tokens' heads it is.
+__device__ __forceinline__ void chunk_at(const WeightTileParams& p, const Item& it, int c, int& tok, int& part) {
+  part = p.parts == 1 ? 0 : c % p.parts;
+  tok = it.lo + (p.parts == 1 ? c : c / p.parts) * p.tokens;
+}
+
 template <int D>
-__device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
+__device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
+  using C = WeightTileCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const volatile int* abort = &B.abort;
+  const uint32_t bytes = static_cast<uint32_t>(p.heads) * p.tokens * D * 2;
+  const uint32_t to = ptx::smem_u32(sm) + p.ks * C::TILE;
+  Ring q;
+  uint32_t count = 0;
+  const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
+    int tok, part;
+    chunk_at(p, it, c, tok, part);
+    const bool fine = ptx::mbar_wait(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
+    if (!__all_sync(0xffffffffu, fine)) return false;
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(&B.q_full[q.at], bytes);
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d)
+        ptx::tma_load_3d(to + q.at * C::TILE + d * C::SUB, &p.tm_q, &B.q_full[q.at], d * 64,
+                         walk.h * p.w.G + part * p.heads, walk.s.first + tok);
+    }
+    __syncwarp();
+    q.next(p.qs);
+    ++count;
+    return true;
+  });
+  if (!ok && lane == 0) {
+    B.abort = 1;
+    atomicOr(p.w.batch.status, kStatusProducer);
+  }
+  // no copy may land behind the CTA's end: the last turn of every stage
+  for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(p.qs)); ++i) {
+    const int never = 0;
+    if (q.at == 0) q.turn ^= 1;
+    q.at = (q.at == 0 ? p.qs : q.at) - 1;
+    ptx::mbar_wait(&B.q_full[q.at], q.turn, 100000000ull, &never);
+  }
+}
+
+template <int D>
+__device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes) {
   using C = WeightTileCfg<D>;
   const CacheWeightsParams& w = p.w;
   const int lane = threadIdx.x & 31;
   const volatile int* abort = &B.abort;
-  const uint32_t bytes = static_cast<uint32_t>(p.heads) * p.tokens * D * 2;
   int tok_of[4], head_of[4];  // of this lane's four columns in a chunk
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     tok_of[i] = (lane * 4 + i) / p.heads;
     head_of[i] = lane * 4 + i - tok_of[i] * p.heads;
   }
-  uint32_t qi = 0;
-  bool ok = true;
-  auto bring = [&](const Walk& walk, const Item& it, int c) {
-    const CacheSeq& s = walk.s;
-    const int part = p.parts == 1 ? 0 : c % p.parts, tok0 = it.lo + (p.parts == 1 ? c : c / p.parts) * p.tokens;
+  Ring n;
+  const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
+    int tok0, part;
+    chunk_at(p, it, c, tok0, part);
     float lse[4];
     int last[4];
 #pragma unroll
@@ -370,49 +575,22 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B, con
       lse[i] = INFINITY;
       last[i] = -1;
       if (tok_of[i] < p.tokens && tok < it.hi && head < w.G) {
-        const float x = __ldg(w.lse + static_cast<int64_t>(s.first + tok) * w.Hq + walk.h * w.G + head);
+        const float x = __ldg(w.lse + static_cast<int64_t>(walk.s.first + tok) * w.Hq + walk.h * w.G + head);
         lse[i] = x == -INFINITY ? INFINITY : x * kLog2e;
-        last[i] = w.causal ? s.len - s.n + tok : s.len - 1;
+        last[i] = w.causal ? walk.s.len - walk.s.n + tok : walk.s.len - 1;
       }
     }
-    const uint32_t qs = qi % C::QS;
-    ok = ptx::mbar_wait(&B.q_free[qs], (qi / C::QS & 1) ^ 1, p.limit, abort);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
-    if (lane == 0) {
-      ptx::mbar_arrive_expect_tx(&B.q_full[qs], bytes);
-#pragma unroll
-      for (int d = 0; d < D / 64; ++d)
-        ptx::tma_load_3d(ptx::smem_u32(sm) + C::OFF_Q + qs * C::TILE + d * C::SUB, &p.tm_q, &B.q_full[qs], d * 64,
-                         walk.h * w.G + part * p.heads, s.first + tok0);
-    }
-    __syncwarp();
-    reinterpret_cast<float4*>(notes.lse + qs * 128)[lane] = make_float4(-lse[0], -lse[1], -lse[2], -lse[3]);
-    reinterpret_cast<int4*>(notes.last + qs * 128)[lane] = make_int4(last[0], last[1], last[2], last[3]);
-    ptx::mbar_arrive(&B.q_full[qs]);
-    ++qi;
-  };
-  Walk walk;
-  for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
-    if (walk.single) {
-      const Item it = {0, 0, 0, walk.s.n, 1};
-      bring(walk, it, 0);
-      continue;
-    }
-    for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
-      const Item it = item_of(p, walk, pair);
-#pragma unroll 1
-      for (int c = 0; c < it.chunks && ok; ++c) bring(walk, it, c);
-    }
-  }
+    const bool fine = ptx::mbar_wait(&B.n_free[n.at], n.turn ^ 1, p.limit, abort);
+    if (!__all_sync(0xffffffffu, fine)) return false;
+    reinterpret_cast<float4*>(notes.lse + n.at * 128)[lane] = make_float4(-lse[0], -lse[1], -lse[2], -lse[3]);
+    reinterpret_cast<int4*>(notes.last + n.at * 128)[lane] = make_int4(last[0], last[1], last[2], last[3]);
+    ptx::mbar_arrive(&B.n_full[n.at]);
+    n.next(C::NS);
+    return true;
+  });
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusProducer);
-  }
-  // no copy may land behind the CTA's end
-  for (uint32_t i = qi > C::QS ? qi - C::QS : 0; i < qi; ++i) {
-    const int never = 0;
-    ptx::mbar_wait(&B.q_full[i % C::QS], i / C::QS & 1, 100000000ull, &never);
   }
 }
 
@@ -421,8 +599,9 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
   using C = WeightTileCfg<D>;
   const volatile int* abort = &B.abort;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
-  const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm) + C::OFF_Q, 16, 1024);
-  uint32_t ki = 0, qi = 0, si[2] = {0, 0};
+  const uint64_t q_desc = k_desc + p.ks * (C::TILE >> 4);
+  Ring k, q;
+  uint32_t si[2] = {0, 0};
   bool ok = true;
   Walk walk;
   for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
@@ -430,50 +609,53 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
 #pragma unroll 1
     for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
       const Item it = item_of(p, walk, pair);
+      Ring second = k;
+      second.next(p.ks);
 #pragma unroll 1
-      for (int c = 0; c < it.chunks && ok; ++c) {
-        const uint32_t qs = qi % C::QS;
-        if (!held) ok = ptx::mbar_wait(&B.q_full[qs], qi / C::QS & 1, p.limit, abort);
+      for (int c = 0; c < it.chunks; ++c) {
+        if (!held) ok = ptx::mbar_wait(&B.q_full[q.at], q.turn, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         held = walk.single;
         const uint32_t idesc = ptx::idesc_bf16(128, (chunk_columns(p, it, c) + 15) & ~15, 0);
-        const uint64_t q = q_desc + qs * (C::TILE >> 4);
+        const uint64_t b = q_desc + q.at * (C::TILE >> 4);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          if (m >= it.tiles || !ok) break;
-          const uint32_t k = ki + m, ks = k % C::KS, sb = si[m] & 1;
-          if (c == 0) ok = ptx::mbar_wait(&B.k_full[ks], k / C::KS & 1, p.limit, abort);
+          if (m >= it.tiles) break;
+          const Ring at = m ? second : k;
+          const uint32_t sb = si[m] & 1;
+          if (c == 0) ok = ptx::mbar_wait(&B.k_full[at.at], at.turn, p.limit, abort);
           ok = ok && ptx::mbar_wait(&B.s_free[m][sb], (si[m] >> 1 & 1) ^ 1, p.limit, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint64_t a = k_desc + ks * (C::TILE >> 4);
+          const uint64_t a = k_desc + at.at * (C::TILE >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::SUB + (kk & 3) * 32) >> 4;
-            ptx::mma_ss_elect(tmem + m * 256 + sb * 128, a + off, q + off, idesc, kk > 0 ? 1u : 0u);
+            ptx::mma_ss_elect(tmem + m * 256 + sb * 128, a + off, b + off, idesc, kk > 0 ? 1u : 0u);
           }
           ptx::mma_commit_elect(&B.s_full[m][sb]);
+          if (c == it.chunks - 1) ptx::mma_commit_elect(&B.k_free[at.at]);
           ++si[m];
         }
         if (!ok) break;
         if (!walk.single) {
-          ptx::mma_commit_elect(&B.q_free[qs]);
-          ++qi;
+          ptx::mma_commit_elect(&B.q_free[q.at]);
+          q.next(p.qs);
         }
       }
-      if (it.chunks > 0 && ok) {
-        for (int m = 0; m < it.tiles; ++m) ptx::mma_commit_elect(&B.k_free[(ki + m) % C::KS]);
-        ki += it.tiles;
+      if (it.chunks > 0) {
+        k.next(p.ks);
+        if (it.tiles == 2) k.next(p.ks);
       }
     }
     if (walk.single && ok) {
-      if (!held) ok = ptx::mbar_wait(&B.q_full[qi % C::QS], qi / C::QS & 1, p.limit, abort);
+      if (!held) ok = ptx::mbar_wait(&B.q_full[q.at], q.turn, p.limit, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      ptx::mma_commit_elect(&B.q_free[qi % C::QS]);
-      ++qi;
+      ptx::mma_commit_elect(&B.q_free[q.at]);
+      q.next(p.qs);
     }
   }
   if (!ok && (threadIdx.x & 31) == 0) {
@@ -497,20 +679,26 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   __shared__ wtile::Bars B;
   uint8_t* const sm = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   wtile::Notes notes;
-  notes.factor = reinterpret_cast<float*>(sm + C::OFF_NOTES);
-  notes.lse = notes.factor + C::KS * 128;
-  notes.last = reinterpret_cast<int*>(notes.lse + C::QS * 128);
+  static_assert(sizeof(wtile::KeyNotes) == C::KEY_NOTES, "notes");
+  notes.raw = reinterpret_cast<wtile::KeyNotes*>(sm + C::OFF_NOTES);
+  notes.key = notes.raw + C::RAWS;
+  notes.lse = reinterpret_cast<float*>(notes.key + C::MOST_KS);
+  notes.last = reinterpret_cast<int*>(notes.lse + C::NS * 128);
+  notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 4);
-    for (int i = 0; i < C::QS; ++i) ptx::mbar_init(&B.q_full[i], 1 + 32), ptx::mbar_init(&B.q_free[i], 1 + 8);
-    for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < C::MOST_KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 8);
+    for (int i = 0; i < C::MOST_QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
+    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 16);
+    for (int m = 0; m < 2; ++m) {
       for (int i = 0; i < 2; ++i) ptx::mbar_init(&B.s_full[m][i], 1), ptx::mbar_init(&B.s_free[m][i], 4);
+      ptx::mbar_init(&B.x_full[m], 4), ptx::mbar_init(&B.x_free[m], 4);
+    }
     ptx::mbar_init(&B.drain, 1);
     B.abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     ptx::tmem_alloc(&B.tmem, C::TM_COLS);
     ptx::tmem_relinquish();
   }
@@ -518,19 +706,21 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = B.tmem;
-  if (warp < 8)
+  if (warp < 16)
     wtile::run_sums<D>(p, B, notes, tmem);
-  else if (warp < 12)
+  else if (warp < 20)
     wtile::run_convert<D>(p, sm, B, notes);
-  else if (warp == 12)
+  else if (warp == 20)
     wtile::run_mma<D>(p, sm, B, tmem);
+  else if (warp == 21)
+    wtile::run_queries<D>(p, sm, B);
   else
-    wtile::run_queries<D>(p, sm, B, notes);
+    wtile::run_notes<D>(p, B, notes);
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 12) ptx::tmem_dealloc(tmem, C::TM_COLS);
+  if (warp == 20) ptx::tmem_dealloc(tmem, C::TM_COLS);
 }
 
 }  // namespace gdpa
