@@ -13,7 +13,7 @@
 //
 // Bound: memory, D bytes a key and head, and 8 of its weight.
 //
-// Work split.  A step is 32 keys of one sequence and head.  The steps of all
+// Work split.  A step is 4 KB of codes (32 or 64 keys) of one sequence and head.  The steps of all
 // sequences are counted from the lengths on the device, and every warp takes an
 // equal run of them, so a batch of any raggedness or one long history loads all
 // SMs alike.  A warp's own asynchronous copies bring codes, scales and
@@ -60,17 +60,18 @@ __device__ __forceinline__ RowSpan rows_of_key(const CacheSeq& s, int j, int cau
 template <int D, int NT_>
 struct WeightCfg {
   static constexpr int NT = NT_, WARPS = 4, THREADS = 32 * WARPS;
-  static constexpr int SPAN = 2 * kCacheBlock;
+  static constexpr int SPAN = 4096 / D, TILES = SPAN / kCacheBlock;
   static constexpr int START = 2;  // what a sequence and head's start costs, in steps
   static constexpr int KSTEPS = D / 16;
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int STAGES = 3;
   static constexpr int TILE = kCacheBlock * D;
-  static constexpr int W_AT = 2 * TILE, SF_AT = W_AT + SPAN * 4, STAGE = SF_AT + 16;  // of a stage: codes, weights, scales
+  // of a stage: codes, earlier weights, words with scales, pages
+  static constexpr int W_AT = 4096, SF_AT = W_AT + SPAN * 4, PAGE_AT = SF_AT + 16, STAGE = PAGE_AT + 16;
   static constexpr int QFRAG = NT * KSTEPS * 32 * 8;  // a warp's query fragments ...
   static constexpr int ROWS_AT = QFRAG;               // ... and what it knows of their rows
   static constexpr int WARP = STAGES * STAGE + QFRAG + NT * 8 * 16;
   static constexpr int SMEM = WARPS * WARP;
-  static constexpr int CTAS = NT == 1 ? (D == 128 ? 3 : 4) : NT == 3 ? (D == 128 ? 2 : 3) : 2;
+  static constexpr int CTAS = NT == 1 || (NT == 3 && D == 64) ? 3 : 2;
   static_assert(STAGE % 16 == 0 && WARP % 16 == 0, "16-byte copies");
 };
 
@@ -111,6 +112,7 @@ __device__ __forceinline__ void weight_schedule(const CacheWeightsParams& p, Wei
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
   int64_t mine = 0;
+#pragma unroll 4
   for (int b = b_lo; b < b_hi; ++b) mine += weight_cost<C>(p, weight_seq<C>(p, b));
   int64_t incl = mine;
 #pragma unroll
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
     gdpa_cache_weights_split_kernel(const __grid_constant__ CacheWeightsParams p) {
   using namespace split;
   using C = WeightCfg<D, NT>;
-  constexpr int KS = C::KSTEPS;
+  constexpr int KS = C::KSTEPS, SPAN = C::SPAN;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ WeightSchedule<C> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
   uint2* const qfrag = reinterpret_cast<uint2*>(mine + C::STAGES * C::STAGE);
   WeightRow* const row_of = reinterpret_cast<WeightRow*>(mine + C::STAGES * C::STAGE + C::ROWS_AT);
   const int pmask = (1 << p.cache.lp) - 1;
+  const bool one = (1 << p.cache.lp) >= SPAN;  // a step lies in one page
   const int64_t sf_bytes = static_cast<int64_t>(p.cache.num_pages) * p.cache.H << (p.cache.lp - 4);
 
   WeightWalk<C> ahead, now;
@@ -221,51 +224,64 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
   now = ahead;
   bool left = more;
 
-  // Pages of a step's two tiles (-1: none, flagged).
-  auto pages = [&](const WeightWalk<C>& k, int (&page)[2]) {
-    const int key = k.w.kbase + k.u * C::SPAN;
-    const int32_t* table = bt.table + static_cast<int64_t>(k.b) * bt.max_pages;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      page[n] = -1;
-      if (key + n * kCacheBlock >= k.w.s.len) continue;
-      const int x = __ldg(table + ((key + n * kCacheBlock) >> p.cache.lp));
-      if (x >= 0 && x < p.cache.num_pages)
-        page[n] = x;
-      else if (lane == 0)
-        atomicOr(bt.status, kStatusBadPlan);
-    }
+  // The page of a step's tile (lanes from 0 on), or of all of it; -1 where there is none (flagged if there should be).
+  auto page_of = [&](const WeightWalk<C>& k) {
+    const int key = k.w.kbase + k.u * SPAN, off = one ? 0 : lane * kCacheBlock;
+    if (off >= SPAN || k.w.s.len - key <= off) return -1;
+    const int x = __ldg(bt.table + static_cast<int64_t>(k.b) * bt.max_pages + ((key + off) >> p.cache.lp));
+    if (x >= 0 && x < p.cache.num_pages) return x;
+    atomicOr(bt.status, kStatusBadPlan);
+    return -1;
   };
-  // A step's copies: tiles that a row may see, their scales, earlier weights.
-  int page_next[2];
+  // A step's copies: what a row may see, scales, earlier weights.
+  int page_next = -1;
+  const uint32_t chunk_to = tile_at<D>(lane / (D / 16), lane % (D / 16));  // of this lane's first 16 bytes of a tile
   auto issue = [&](int stage) {
     if (more) {
-      const int key = ahead.w.kbase + ahead.u * C::SPAN;
+      const int key = ahead.w.kbase + ahead.u * SPAN;
       const uint32_t dst = ring + stage * C::STAGE;
+      if (lane < 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + C::PAGE_AT + lane * 4), "r"(page_next) : "memory");
+      if (one) {
+        if (page_next >= 0) {
+          const int64_t row = cache_row(p.cache, page_next, ahead.h, key & pmask);
+          if (key + SPAN > ahead.w.see) {
+            const uint8_t* src = p.cache.k + row * D + lane * 16;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int k0 = key + n * kCacheBlock;
-        if (page_next[n] < 0) continue;
-        const int64_t row = cache_row(p.cache, page_next[n], ahead.h, k0 & pmask);
-        if (k0 + kCacheBlock > ahead.w.see) {
-          const uint8_t* src = p.cache.k + row * D + lane * 16;
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            const int idx = lane + 32 * j;
-            cp_async16(dst + n * C::TILE + tile_at<D>(idx / (D / 16), idx % (D / 16)), src + 512 * j, 16);
+            for (int j = 0; j < 8; ++j)
+              // 32 chunks further on: as many rows, and the same permutation (or another one, a constant too)
+              cp_async16(dst + (D == 128 ? (chunk_to ^ (j & 1) * 64) : chunk_to) + j * 512, src + 512 * j, 16);
+            const int64_t word = (row >> 4) & ~(int64_t)3;
+            if (lane == 0)
+              cp_async4(dst + C::SF_AT, p.cache.k_sf + word, static_cast<int>(min((int64_t)4, sf_bytes - word)));
           }
-          const int64_t word = (row >> 4) & ~(int64_t)3;
-          if (lane == 0)
-            cp_async4(dst + C::SF_AT + n * 4, p.cache.k_sf + word, static_cast<int>(min((int64_t)4, sf_bytes - word)));
+          if (p.w_in && lane < SPAN / 4) cp_async16(dst + C::W_AT + lane * 16, p.w_in + row + lane * 4, 16);
         }
-        if (p.w_in && lane < 4) cp_async16(dst + C::W_AT + n * 64 + lane * 16, p.w_in + row + lane * 4, 16);
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < C::TILES; ++n) {
+          const int k0 = key + n * kCacheBlock, page = __shfl_sync(0xffffffffu, page_next, n);
+          if (page < 0) continue;
+          const int64_t row = cache_row(p.cache, page, ahead.h, k0 & pmask);
+          if (k0 + kCacheBlock > ahead.w.see) {
+            const uint8_t* src = p.cache.k + row * D + lane * 16;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              const int idx = lane + 32 * j;
+              cp_async16(dst + n * C::TILE + tile_at<D>(idx / (D / 16), idx % (D / 16)), src + 512 * j, 16);
+            }
+            const int64_t word = (row >> 4) & ~(int64_t)3;
+            if (lane == 0)
+              cp_async4(dst + C::SF_AT + n * 4, p.cache.k_sf + word, static_cast<int>(min((int64_t)4, sf_bytes - word)));
+          }
+          if (p.w_in && lane < 4) cp_async16(dst + C::W_AT + n * 64 + lane * 16, p.w_in + row + lane * 4, 16);
+        }
       }
       more = ahead.next(p, at, stop);
-      if (more) pages(ahead, page_next);
+      if (more) page_next = page_of(ahead);
     }
     cp_commit();
   };
-  if (more) pages(ahead, page_next);
+  if (more) page_next = page_of(ahead);
 #pragma unroll 1
   for (int i = 0; i < C::STAGES - 1; ++i) issue(i);
 
@@ -324,112 +340,123 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
 #pragma unroll 1
   while (left) {
     const CacheSeq& s = now.w.s;
-    const int key0 = now.w.kbase + now.u * C::SPAN;
+    const int key0 = now.w.kbase + now.u * SPAN;
     const bool many = static_cast<int64_t>(s.n) * p.G > 8 * NT;
     if (now.b != at_b || now.h != at_h) {
       at_b = now.b, at_h = now.h;
       if (!many) rows = load_rows(0);
-      const int pos0 = s.len - s.n;
       lo_max = first_key(s.len - 1, p.window);  // keys that all rows see: [lo_max, hi_min)
-      hi_min = p.causal ? max(0, pos0 + 1) : s.len;
+      hi_min = p.causal ? max(0, s.len - s.n + 1) : s.len;
     }
     issue(stage == 0 ? C::STAGES - 1 : stage - 1);
     cp_wait<C::STAGES - 1>();
     __syncwarp();
     const uint32_t st = ring + stage * C::STAGE;
-    int page[2];
-    pages(now, page);
+    int page[4];
+    uint32_t sf_word[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(page[0]), "=r"(page[1]), "=r"(page[2]), "=r"(page[3])
+                 : "r"(st + C::PAGE_AT));
+    lds128(st + C::SF_AT, sf_word);
+    const bool seen = key0 + SPAN > now.w.see;
+    const bool edge = key0 < lo_max || key0 > hi_min - SPAN;
 
-    float sum[2][2] = {};
-    if (key0 + C::SPAN > now.w.see) {
-      uint32_t a[2][KS][4];
-      float sk[2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+    for (int half = 0; half < C::TILES / 2; ++half) {
+      const int k0 = key0 + half * 2 * kCacheBlock;
+      float sum[2][2] = {};
+      if (seen) {
+        uint32_t a[2][KS][4];
+        float sk[2];
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          uint32_t ka[4], kc[4];
-          const int c = D == 128 ? 2 * t + j : t;
-          lds128(st + n * C::TILE + tile_at<D>(g, c), ka);
-          lds128(st + n * C::TILE + tile_at<D>(g + 8, c), kc);
+        for (int n = 0; n < 2; ++n) {
+          const int tile = 2 * half + n;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            a[n][4 * j + w][0] = codes_lo(ka[w]), a[n][4 * j + w][2] = codes_hi(ka[w]);
-            a[n][4 * j + w][1] = codes_lo(kc[w]), a[n][4 * j + w][3] = codes_hi(kc[w]);
-          }
-        }
-        const int64_t block = cache_row(p.cache, max(page[n], 0), now.h, (key0 + n * kCacheBlock) & pmask) >> 4;
-        uint32_t word;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(st + C::SF_AT + n * 4));
-        sk[n] = sf_value(word >> static_cast<int>(block & 3) * 8 & 0xff);
-      }
-      const bool edge = key0 < lo_max || key0 + C::SPAN > hi_min;
-      auto tile = [&](auto edge_tag, int nt) {
-        constexpr bool EDGE = decltype(edge_tag)::value;
-        float x[2][4];
+          for (int j = 0; j < D / 64; ++j) {
+            uint32_t ka[4], kc[4];
+            const int c = D == 128 ? 2 * t + j : t;
+            lds128(st + tile * C::TILE + tile_at<D>(g, c), ka);
+            lds128(st + tile * C::TILE + tile_at<D>(g + 8, c), kc);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint2 q = qfrag[(nt * KS + k) * 32 + lane];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            if (k == 0)
-              mma_f16_new(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
-            else
-              mma_f16(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const WeightRow wr = row_of[nt * 8 + 2 * t + c];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float f = wr.fac * sk[n];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float e = ptx::ex2_approx(fmaf(x[n][2 * i + c], f, -wr.lse));
-              if (EDGE) {
-                const int key = key0 + n * kCacheBlock + 8 * i + g;
-                if (key < wr.lo || key >= wr.hi) e = 0.0f;
-              }
-              sum[n][i] += e;
+            for (int w = 0; w < 4; ++w) {
+              a[n][4 * j + w][0] = codes_lo(ka[w]), a[n][4 * j + w][2] = codes_hi(ka[w]);
+              a[n][4 * j + w][1] = codes_lo(kc[w]), a[n][4 * j + w][3] = codes_hi(kc[w]);
             }
           }
+          // the scale's place in its word: the low bits of its index
+          const int pg = one ? page[0] : page[tile], key = k0 + n * kCacheBlock;
+          const uint32_t block = (static_cast<uint32_t>(pg) * p.cache.H + now.h << (p.cache.lp - 4)) + ((key & pmask) >> 4);
+          sk[n] = sf_value((one ? sf_word[0] : sf_word[tile]) >> (block & 3) * 8 & 0xff);
         }
-      };
-      auto tiles = [&](int count) {
-        if (edge) {
+        auto tile = [&](auto edge_tag, int nt) {
+          constexpr bool EDGE = decltype(edge_tag)::value;
+          float x[2][4];
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const uint2 q = qfrag[(nt * KS + k) * 32 + lane];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              if (k == 0)
+                mma_f16_new(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
+              else
+                mma_f16(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const WeightRow wr = row_of[nt * 8 + 2 * t + c];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float f = wr.fac * sk[n];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float e = ptx::ex2_approx(fmaf(x[n][2 * i + c], f, -wr.lse));
+                if (EDGE) {
+                  const int key = k0 + n * kCacheBlock + 8 * i + g;
+                  if (key < wr.lo || key >= wr.hi) e = 0.0f;
+                }
+                sum[n][i] += e;
+              }
+            }
+          }
+        };
+        auto tiles = [&](int count) {
+          if (edge) {
 #pragma unroll 1
-          for (int nt = 0; nt * 8 < count; ++nt) tile(std::true_type{}, nt);
+            for (int nt = 0; nt * 8 < count; ++nt) tile(std::true_type{}, nt);
+          } else if (NT == 1) {
+            tile(std::false_type{}, 0);
+          } else {
+#pragma unroll 2
+            for (int nt = 0; nt * 8 < count; ++nt) tile(std::false_type{}, nt);
+          }
+        };
+        if (!many) {
+          tiles(rows);
         } else {
 #pragma unroll 1
-          for (int nt = 0; nt * 8 < count; ++nt) tile(std::false_type{}, nt);
+          for (int64_t r = 0; r < static_cast<int64_t>(s.n) * p.G; r += 8 * NT) tiles(load_rows(static_cast<int>(r)));
         }
-      };
-      if (!many) {
-        tiles(rows);
-      } else {
-#pragma unroll 1
-        for (int64_t r = 0; r < static_cast<int64_t>(s.n) * p.G; r += 8 * NT) tiles(load_rows(static_cast<int>(r)));
-      }
-    }
-    // a quad's lanes hold the same two rows of each tile: one key a lane
+        // a quad's lanes hold the same two rows of each tile: one key a lane
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sum[n][i] += __shfl_xor_sync(0xffffffffu, sum[n][i], 1);
-        sum[n][i] += __shfl_xor_sync(0xffffffffu, sum[n][i], 2);
+          for (int i = 0; i < 2; ++i) {
+            sum[n][i] += __shfl_xor_sync(0xffffffffu, sum[n][i], 1);
+            sum[n][i] += __shfl_xor_sync(0xffffffffu, sum[n][i], 2);
+          }
       }
-    const int off = (t >> 1) * kCacheBlock + (t & 1) * 8 + g, key = key0 + off;
-    float w = t == 0 ? sum[0][0] : t == 1 ? sum[0][1] : t == 2 ? sum[1][0] : sum[1][1];
-    const int pg = t < 2 ? page[0] : page[1];
-    if (pg >= 0 && key < s.len) {
-      if (p.w_in && key < s.len - s.n) {
-        float old;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(st + C::W_AT + off * 4));
-        w = fmaf(p.decay, old, w);
+      const int off = (t >> 1) * kCacheBlock + (t & 1) * 8 + g, key = k0 + off;
+      float w = t == 0 ? sum[0][0] : t == 1 ? sum[0][1] : t == 2 ? sum[1][0] : sum[1][1];
+      const int pg = one ? page[0] : t < 2 ? page[2 * half] : page[2 * half + 1];
+      if (pg >= 0 && s.len - k0 > off) {
+        if (p.w_in && key < s.len - s.n) {
+          float old;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(st + C::W_AT + (half * 32 + off) * 4));
+          w = fmaf(p.decay, old, w);
+        }
+        p.w[cache_row(p.cache, pg, now.h, key & pmask)] = w;
       }
-      p.w[cache_row(p.cache, pg, now.h, key & pmask)] = w;
     }
     __syncwarp();
     left = now.next(p, at, stop);

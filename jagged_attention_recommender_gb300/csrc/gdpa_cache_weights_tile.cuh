@@ -238,19 +238,23 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
         __syncwarp();
         continue;
       }
-      if (m == 1 && mine) k.next(p.ks);  // the first tile is the others'
-      if (mine) {
+      // (every warp sees every tile arrive: one that skipped some could take a
+      // later turn of a stage for the one it waits for)
+#pragma unroll 1
+      for (int j = 0; j < it.tiles; ++j) {
         ok = ptx::mbar_wait(&B.k_full[k.at], k.turn, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        row = notes.key[k.at].row[key_in];
-        factor = notes.key[k.at].factor[key_in];
-        old = notes.key[k.at].old[key_in];
+        if (j == m) {
+          row = notes.key[k.at].row[key_in];
+          factor = notes.key[k.at].factor[key_in];
+          old = notes.key[k.at].old[key_in];
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&B.k_free[k.at]);
+        k.next(p.ks);
       }
-      k.next(p.ks);
-      if (m == 0 && it.tiles == 2) k.next(p.ks);
+      if (!ok) break;
       const uint64_t f2 = ptx::f2_splat(factor);
       uint64_t sum[2] = {0, 0};
       float edge_sum = 0.0f;
@@ -411,15 +415,20 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   bool ok = true;
   TileWalk tiles;
   bool more = tiles.begin(p);
+  // lane i: the page of the tile's i-th block of 16 keys
+  auto page_of = [&]() {
+    const int k0 = tiles.it.k0 + tiles.m * 128;
+    if (lane >= 8 || tiles.walk.s.len - k0 <= lane * 16) return -1;
+    return load_page(w.cache, w.batch, tiles.walk.b, k0 + lane * 16);
+  };
+  int page = more ? page_of() : -1;  // (looked up a tile ahead)
+  __syncwarp();
   while (true) {
     while (more && ri - ki < C::RAWS) {
       const Walk& at = tiles.walk;
       const int k0 = tiles.it.k0 + tiles.m * 128, valid = at.s.len - k0;
       const uint32_t rs = in.at;
       KeyNotes& note = notes.raw[rs];
-      int page = -1;  // lane i: of the tile's i-th block of 16
-      if (lane < 8 && valid > lane * 16) page = load_page(w.cache, w.batch, at.b, k0 + lane * 16);
-      __syncwarp();
 #pragma unroll
       for (int i = 0; i < N; ++i) {  // (what is not there keeps what it held: no other key's score depends on it)
         const int r = r0 + i * ROWS, pg = __shfl_sync(0xffffffffu, page, r >> 4);
@@ -444,6 +453,8 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
       ++ri;
       in.next(C::RAWS);
       more = tiles.next(p);
+      if (more) page = page_of();
+      __syncwarp();
     }
     if (ri == ki) break;
     const uint32_t ks = k.at, rs = out.at;
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::MOST_KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 8);
+    for (int i = 0; i < C::MOST_KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 16);
     for (int i = 0; i < C::MOST_QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
     for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 16);
     for (int m = 0; m < 2; ++m) {

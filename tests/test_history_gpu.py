@@ -183,6 +183,17 @@ def test_weights_match_the_formula(case, causal, window):
     check_weights(x, causal, window, decay=[1.0, 0.75][case % 2], in_place=bool(case % 3 == 0), stride=case % 4)
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("hint", [1, 20, 40, 200])
+def test_weights_of_many_sequences(D, P, hint):
+    """More sequences than a warp has lanes, most of them shorter than a tile, whichever kernel the hint picks."""
+    rng = np.random.default_rng(D)
+    B = 150
+    lens = [int(n) for n in rng.choice([0, 1, 20, 127, 128, 129, 200, 300, 700], B)]
+    x = ref.make(14, 4, 4, D, P, lens, [int(n) for n in rng.choice([0, 1, 1, 2], B)])
+    check_weights(x, 1, 0, max_q=hint)
+
+
 @pytest.mark.parametrize("new", [[1, 1], [9, 1], [64, 80]])
 def test_weights_without_earlier_ones(new):
     x = ref.make(5, 8, 2, 64, 32, [90, 400], new)
