@@ -9,6 +9,7 @@
 
 #include "gdpa_cache_host.h"
 #include "gdpa_cache_weights.cuh"
+#include "gdpa_cache_weights_pass.cuh"
 #include "gdpa_cache_weights_tile.cuh"
 
 namespace gdpa {
@@ -60,11 +61,32 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, int max_q, const Device& 
 }
 
 template <int D>
+gdpa_status_t launch_pass(const CacheWeightsParams& w, const Device& dev, cudaStream_t s) {
+  using C = WeightPassCfg<D>;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  const gdpa_status_t st = allow_smem(gdpa_cache_weights_pass_kernel<D>, C::SMEM, 0, dev.id, mu, done);
+  if (st != GDPA_OK) return st;
+  WeightPassParams p;
+  p.w = w;
+  p.heads = std::min(w.G, C::COLS);
+  p.tokens = C::COLS / p.heads;
+  p.parts = (w.G + p.heads - 1) / p.heads;
+  p.limit = bounded_wait_ns();
+  const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp;
+  const int64_t tiles = (int64_t)w.batch.B * w.cache.H * ((keys + 127) / 128);
+  const int ctas = static_cast<int>(std::min<int64_t>(tiles, dev.sms));
+  gdpa_cache_weights_pass_kernel<D><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <int D>
 gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
   const int64_t rows = (int64_t)max_q * p.G;
   if (rows <= 8) return launch_split<D, 1>(p, dev, s);
   if (rows <= 24) return launch_split<D, 3>(p, dev, s);
   if (rows <= 48) return launch_split<D, 6>(p, dev, s);
+  if (p.G <= 128 && max_q <= 128 / p.G) return launch_pass<D>(p, dev, s);
   return launch_tile<D>(p, max_q, dev, s);
 }
 
