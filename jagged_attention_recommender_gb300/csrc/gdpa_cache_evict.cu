@@ -47,13 +47,35 @@ extern "C" gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weig
   p.status = dev.status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t heads = (int64_t)B * cache->H;
-  gdpa_cache_choose_kernel<<<static_cast<unsigned>(std::min<int64_t>(heads, 1 << 20)), kChooseThreads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return GDPA_ERR_CUDA;
+  // CTAs of a sequence and head: one, or where those are few as many as fill the SMs with 2048 tokens each.
+  int ctas = 1;
+  while (ctas < 8 && heads * ctas * 2 <= dev.sms && most / (ctas * 2) >= 2048) ctas *= 2;
+  const int64_t part = ((most + ctas - 1) / ctas + 3) & ~(int64_t)3;
+  const int slots = part <= kMostKeys ? static_cast<int>(part) : 0;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  if ((st = allow_smem(gdpa_cache_choose_kernel, kMostKeys * 4, 0, dev.id, mu, done)) != GDPA_OK) return st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(heads, 1 << 20) * ctas));
+  cfg.blockDim = dim3(kChooseThreads);
+  cfg.dynamicSmemBytes = slots * 4;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, gdpa_cache_choose_kernel, p, slots) != cudaSuccess) return GDPA_ERR_CUDA;
   const int64_t tasks = heads * (((int64_t)p.most + kCacheBlock - 1) / kCacheBlock);
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((tasks + 7) / 8, 1 << 20));
-  if (cache->D == 128)
-    gdpa_cache_move_kernel<128><<<blocks, 256, 0, s>>>(p);
-  else
-    gdpa_cache_move_kernel<64><<<blocks, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+  // Its blocks are placed while the last of the first kernel's CTAs finish, and wait there.
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  const cudaError_t e = cache->D == 128 ? cudaLaunchKernelEx(&cfg, gdpa_cache_move_kernel<128>, p)
+                                        : cudaLaunchKernelEx(&cfg, gdpa_cache_move_kernel<64>, p);
+  return e == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }

@@ -358,6 +358,8 @@ def evict_batch(seed, H, D, P, lens, budget, jitter=3):
     (1, 128, 1024, [3000, 1025], 1500, 5, 7),
     (2, 64, 32, [5000], 17, 0, 1),
     (5, 64, 32, [90, 91, 92], 1000, 10, 10),               # all stay
+    (2, 64, 64, [20001, 300], 1200, 2, 40),                # several CTAs a head
+    (1, 64, 1024, [400003], 333, 5, 1),                    # more keys than their shared memory holds
 ])
 def test_evict_matches_the_definition(H, D, P, lens, budget, sink, recent):
     x, w = evict_batch(budget, H, D, P, lens, budget)
