@@ -95,120 +95,125 @@ __global__ void __launch_bounds__(kChooseThreads) gdpa_cache_choose_kernel(const
       for (int64_t j = rank * kChooseThreads + tid; j < keep; j += ctas * kChooseThreads) kept[j] = static_cast<int>(j);
       continue;
     }
-    // this CTA's tokens [j0, j1), a multiple of 4 but for the last one, and this warp's [w0, w1)
+    // this CTA's tokens: n from j0 on (a multiple of 4 each, but for the last one's)
     const int per = static_cast<int>((static_cast<int64_t>(len) + ctas - 1) / ctas + 3) & ~3;
-    const int j0 = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(per) * rank));
-    const int j1 = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(j0) + per));
-    const int part = ((j1 - j0 + kChooseWarps - 1) / kChooseWarps + 31) & ~31;
-    const int w0 = min(j1 - j0, part * warp) + j0, w1 = min(j1 - w0, part) + w0;
+    const int j0 = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(per) * rank)), n = min(len - j0, per);
     const bool held = per <= slots;
+    // The first and last ones stay in any case: they count as larger than any
+    // number, so that the `keep` largest of all are what stays (sink + recent <=
+    // budget).  The others are [free0, free1) of this CTA's.
+    const int free0 = max(min(p.sink - j0, n), 0), free1 = max(min(len - p.recent - j0, n), 0);
     const int32_t* const table = p.table + static_cast<int64_t>(b) * p.max_pages;
-    auto load4 = [&](int j, uint32_t (&k)[4]) {  // j a multiple of 4: one page
-      const int page = __ldg(table + (j >> p.cache.lp));
-      k[0] = k[1] = k[2] = k[3] = 0;
+    const float* const weights = p.weights + (static_cast<int64_t>(h) << p.cache.lp);
+    const int64_t page_weights = static_cast<int64_t>(p.cache.H) << p.cache.lp;
+    auto load4 = [&](int i) {  // i a multiple of 4: one page
+      const int j = j0 + i, page = __ldg(table + (j >> p.cache.lp));
+      uint4 k = make_uint4(0, 0, 0, 0);
       if (page >= 0 && page < p.cache.num_pages) {
-        const float4 w = *reinterpret_cast<const float4*>(
-            p.weights + cache_row(p.cache, page, h, j & ((1 << p.cache.lp) - 1)));
-        k[0] = weight_key(w.x), k[1] = weight_key(w.y), k[2] = weight_key(w.z), k[3] = weight_key(w.w);
+        const float4 w = *reinterpret_cast<const float4*>(weights + page * page_weights + (j & ((1 << p.cache.lp) - 1)));
+        k = make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
       } else {
         atomicOr(p.status, kStatusBadPlan);
       }
+      if (i < free0 || i + 3 >= free1) {
+        if (i < free0 || i >= free1) k.x = 0xffffffffu;
+        if (i + 1 < free0 || i + 1 >= free1) k.y = 0xffffffffu;
+        if (i + 2 < free0 || i + 2 >= free1) k.z = 0xffffffffu;
+        if (i + 3 < free0 || i + 3 >= free1) k.w = 0xffffffffu;
+      }
+      return k;
     };
+    auto keys4 = [&](int i) { return held ? *reinterpret_cast<const uint4*>(keys + i) : load4(i); };
     for (int i = tid; i < 1024; i += kChooseThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
-    // sink + recent <= budget < len: the tokens between them compete for `need` places
-    const int lo = p.sink, hi = len - p.recent;
-    int need = keep - p.sink - p.recent;
-    const bool any = need > 0;  // (none of them stays otherwise)
-    uint32_t prefix = 0;
-    if (any) {
-      // the first digit's histogram while the keys come
+    // the first digit's histogram while the keys come
 #pragma unroll 4
-      for (int64_t j = j0 + 4 * tid; j < j1; j += 4 * kChooseThreads) {
-        uint32_t k[4];
-        load4(static_cast<int>(j), k);
-        if (held) *reinterpret_cast<uint4*>(keys + (j - j0)) = make_uint4(k[0], k[1], k[2], k[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j + i >= lo && j + i < hi && j + i < j1) atomicAdd(&sh.hist[0][k[i] >> 24], 1);
-      }
+    for (int i = 4 * tid; i < n; i += 4 * kChooseThreads) {
+      const uint4 k = load4(i);
+      if (held) *reinterpret_cast<uint4*>(keys + i) = k;
+      atomicAdd(&sh.hist[0][k.x >> 24], 1);
+      if (i + 1 < n) atomicAdd(&sh.hist[0][k.y >> 24], 1);
+      if (i + 2 < n) atomicAdd(&sh.hist[0][k.z >> 24], 1);
+      if (i + 3 < n) atomicAdd(&sh.hist[0][k.w >> 24], 1);
+    }
+    uint32_t prefix = 0;  // the digits so far of the least key that stays
+    int need = keep;      // how many of those that equal them do
 #pragma unroll 1
-      for (int d = 0; d < 4; ++d) {
-        const int shift = 24 - 8 * d;
-        if (d > 0) {
-          const uint32_t mask = 0xffffffffu << (shift + 8);
-          for (int64_t j = j0 + 4 * tid; j < j1; j += 4 * kChooseThreads) {
-            uint32_t k[4];
-            if (held) {
-              const uint4 u = *reinterpret_cast<const uint4*>(keys + (j - j0));
-              k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
-            } else {
-              load4(static_cast<int>(j), k);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((k[i] & mask) == prefix && j + i >= lo && j + i < hi && j + i < j1)
-                atomicAdd(&sh.hist[d][k[i] >> shift & 255], 1);
-          }
+    for (int d = 0; d < 4; ++d) {
+      const int shift = 24 - 8 * d;
+      if (d > 0) {
+        const uint32_t mask = 0xffffffffu << (shift + 8);
+        auto count = [&](uint32_t k) {
+          if (((k ^ prefix) & mask) == 0) atomicAdd(&sh.hist[d][k >> shift & 255], 1);
+        };
+#pragma unroll 2
+        for (int i = 4 * tid; i < n; i += 4 * kChooseThreads) {
+          const uint4 k = keys4(i);
+          count(k.x);
+          if (i + 1 < n) count(k.y);
+          if (i + 2 < n) count(k.z);
+          if (i + 3 < n) count(k.w);
         }
-        meet();
-        if (tid < 256) {
-          int n = 0;
-          for (int r = 0; r < ctas; ++r) n += ctas > 1 ? *cluster.map_shared_rank(&sh.hist[d][tid], r) : sh.hist[d][tid];
-          sh.total[tid] = n;
-        }
-        __syncthreads();
-        if (warp == 0) {  // lane i: digits 255 - 8 i down to 248 - 8 i
-          int n[8], mine = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mine += n[i] = sh.total[255 - 8 * lane - i];
-          int before = mine;
-#pragma unroll
-          for (int s = 1; s < 32; s <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, before, s);
-            if (lane >= s) before += x;
-          }
-          const int at = __ffs(__ballot_sync(0xffffffffu, before >= need)) - 1;
-          if (lane == at) {
-            before -= mine;
-            int i = 0;
-            while (i < 7 && before + n[i] < need) before += n[i++];
-            sh.digit = 255 - 8 * lane - i;
-            sh.need = need - before;
-          }
-        }
-        __syncthreads();
-        prefix |= sh.digit << shift;
-        need = sh.need;  // how many of those that equal the key so far stay
       }
+      meet();
+      if (tid < 256) {
+        int c = sh.hist[d][tid];
+        if (ctas > 1) {
+          c = 0;
+          for (int r = 0; r < ctas; ++r) c += *cluster.map_shared_rank(&sh.hist[d][tid], r);
+        }
+        sh.total[tid] = c;
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane i: digits 255 - 8 i down to 248 - 8 i
+        int c[8], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += c[i] = sh.total[255 - 8 * lane - i];
+        int before = mine;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, before, s);
+          if (lane >= s) before += x;
+        }
+        const int at = __ffs(__ballot_sync(0xffffffffu, before >= need)) - 1;
+        if (lane == at) {
+          before -= mine;
+          int i = 0;
+#pragma unroll
+          for (int u = 0; u < 7; ++u)
+            if (i == u && before + c[u] < need) before += c[u], ++i;
+          sh.digit = 255 - 8 * lane - i;
+          sh.need = need - before;
+        }
+      }
+      __syncthreads();
+      prefix |= sh.digit << shift;
+      need = sh.need;
     }
-    // what stays whatever its place, and what equals the least key
-    auto stays = [&](int j, bool& above, bool& same) {
-      above = j < w1 && (j < lo || j >= hi);
-      same = false;
-      if (any && j < w1 && !above) {
-        uint32_t k[4];
-        uint32_t key;
-        if (held) {
-          key = keys[j - j0];
-        } else {
-          load4(j & ~3, k);
-          key = (j & 2) ? ((j & 1) ? k[3] : k[2]) : ((j & 1) ? k[1] : k[0]);
-        }
-        above = key > prefix;
-        same = key == prefix;
-      }
+    // Each warp counts what is above the key and what equals it in its part of
+    // the tokens, 4 a lane at a time; then it knows its places.
+    const int part = ((n + kChooseWarps - 1) / kChooseWarps + 127) & ~127, w0 = min(n, part * warp), w1 = min(n, w0 + part);
+    auto flags = [&](int i) {  // of 4 tokens: bits 0-3 above, 16-19 equal
+      if (i >= w1) return 0;
+      const uint4 k = keys4(i);
+      int f = (k.x > prefix) | (k.y > prefix) << 1 | (k.z > prefix) << 2 | (k.w > prefix) << 3 | (k.x == prefix) << 16 |
+              (k.y == prefix) << 17 | (k.z == prefix) << 18 | (k.w == prefix) << 19;
+      if (i + 4 > w1) f &= ((1 << (w1 - i)) - 1) * 0x10001;
+      return f;
     };
-    int n_above = 0, n_same = 0;
-    for (int64_t j = w0; j < w1; j += 32) {
-      bool above, same;
-      stays(static_cast<int>(j) + lane, above, same);
-      n_above += __popc(__ballot_sync(0xffffffffu, above));
-      n_same += __popc(__ballot_sync(0xffffffffu, same));
+    auto counts = [](int f) { return __popc(f & 0xffff) | __popc(f >> 16) << 16; };
+    int mine_above = 0, mine_same = 0;
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+      const int c = counts(flags(i));
+      mine_above += c & 0xffff;
+      mine_same += c >> 16;
     }
-    if (lane == 0) sh.above[warp] = n_above, sh.same[warp] = n_same;
+    mine_above = __reduce_add_sync(0xffffffffu, mine_above);
+    mine_same = __reduce_add_sync(0xffffffffu, mine_same);
+    if (lane == 0) sh.above[warp] = mine_above, sh.same[warp] = mine_same;
     __syncthreads();
     int out = 0, equal = 0, all_above = 0, all_same = 0;
+#pragma unroll
     for (int w = 0; w < kChooseWarps; ++w) {
       if (w < warp) out += sh.above[w], equal += sh.same[w];
       all_above += sh.above[w], all_same += sh.same[w];
@@ -221,17 +226,27 @@ __global__ void __launch_bounds__(kChooseThreads) gdpa_cache_choose_kernel(const
         equal += *cluster.map_shared_rank(&sh.cta_same, r);
       }
     }
-    out += min(equal, need);  // (need counts places among equals by now; 0 if nothing competes)
-    for (int64_t j = w0; j < w1; j += 32) {
-      bool above, same;
-      stays(static_cast<int>(j) + lane, above, same);
-      const unsigned eq = __ballot_sync(0xffffffffu, same), before = (1u << lane) - 1;
-      const bool take = above || (same && equal + __popc(eq & before) < need);
-      const unsigned taken = __ballot_sync(0xffffffffu, take);
-      const int at = out + __popc(taken & before);
-      if (take && at < keep) kept[at] = static_cast<int>(j) + lane;
-      out += __popc(taken);
-      equal += __popc(eq);
+    // `out` counts what is above; of the equal ones the first `need` stay
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      const int i = i0 + 4 * lane, f = flags(i), mine = counts(f);
+      int incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += x;
+      }
+      const int all = __shfl_sync(0xffffffffu, incl, 31);
+      int above = out + ((incl - mine) & 0xffff), same = equal + ((incl - mine) >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is_above = f >> e & 1, is_same = f >> (16 + e) & 1;
+        const int at = above + min(same, need);
+        if ((is_above || (is_same && same < need)) && at < keep) kept[at] = j0 + i + e;
+        above += is_above;
+        same += is_same;
+      }
+      out += all & 0xffff;
+      equal += all >> 16;
     }
     meet();  // others may still read this CTA's counts
   }
