@@ -67,13 +67,12 @@ extern "C" gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weig
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, gdpa_cache_choose_kernel, p, slots) != cudaSuccess) return GDPA_ERR_CUDA;
-  const int64_t tasks = heads * (((int64_t)p.most + kCacheBlock - 1) / kCacheBlock);
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((tasks + 7) / 8, 1 << 20));
   // Its blocks are placed while the last of the first kernel's CTAs finish, and wait there.
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(256);
+  constexpr int tokens = kMoveWarps * kMoveTokens;
+  cfg.gridDim = dim3(static_cast<unsigned>(((int64_t)p.most + tokens - 1) / tokens), static_cast<unsigned>(std::min<int64_t>(heads, 65535)));
+  cfg.blockDim = dim3(32 * kMoveWarps);
   cfg.dynamicSmemBytes = 0;
   const cudaError_t e = cache->D == 128 ? cudaLaunchKernelEx(&cfg, gdpa_cache_move_kernel<128>, p)
                                         : cudaLaunchKernelEx(&cfg, gdpa_cache_move_kernel<64>, p);

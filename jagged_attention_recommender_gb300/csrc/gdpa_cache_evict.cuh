@@ -65,12 +65,12 @@ struct ChooseShared {
   int above[kChooseWarps], same[kChooseWarps];  // each warp's tokens that stay, and those that equal the least key that does
   int cta_above, cta_same;
   uint32_t digit;
-  int need;
+  int need, of;  // of the `of` tokens with these digits `need` stay
 };
 
 // One sequence and head by a cluster of CTAs, each with an equal part of its
 // tokens (a warp with an equal part of those).  `slots`: keys that `keys` holds.
-__global__ void __launch_bounds__(kChooseThreads) gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
+__global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];
   __shared__ ChooseShared sh;
@@ -184,11 +184,17 @@ __global__ void __launch_bounds__(kChooseThreads) gdpa_cache_choose_kernel(const
             if (i == u && before + c[u] < need) before += c[u], ++i;
           sh.digit = 255 - 8 * lane - i;
           sh.need = need - before;
+          sh.of = sh.total[255 - 8 * lane - i];
         }
       }
       __syncthreads();
       prefix |= sh.digit << shift;
       need = sh.need;
+      if (need == sh.of && prefix > 0) {  // all of them stay: the lower digits do not matter
+        prefix -= 1;
+        need = 0;
+        break;
+      }
     }
     // Each warp counts what is above the key and what equals it in its part of
     // the tokens, 4 a lane at a time; then it knows its places.
@@ -252,53 +258,65 @@ __global__ void __launch_bounds__(kChooseThreads) gdpa_cache_choose_kernel(const
   }
 }
 
-// 16 codes from scale `from` to the larger scale `to`.
-__device__ __forceinline__ uint4 rescale16(uint4 x, int from, int to) {
-  if (from == to) return x;
-  const float f = sf_value(127 - min(to - from, 126));
+// 16 codes to a scale 2^down as large.
+__device__ __forceinline__ uint4 rescale16(uint4 x, int down) {
+  if (down == 0) return x;
+  const float f = sf_value(127 - min(down, 126));
   return make_uint4(rescale4(x.x, f), rescale4(x.y, f), rescale4(x.z, f), rescale4(x.w, f));
 }
 
+constexpr int kMoveWarps = 8, kMoveTokens = 32;  // of a CTA; of a warp
+
 template <int D>
-__global__ void __launch_bounds__(256) gdpa_cache_move_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int LPT = D / 16, TPS = 32 / LPT;  // lanes of a token, tokens of a step
+__global__ void __launch_bounds__(32 * kMoveWarps) gdpa_cache_move_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int LPT = D / 16, TPS = 32 / LPT, STEPS = kMoveTokens / TPS;  // lanes of a token, tokens of a step
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what is kept has been chosen
   const int lane = threadIdx.x & 31, H = p.cache.H;
-  const int64_t blocks = (static_cast<int64_t>(p.most) + kCacheBlock - 1) / kCacheBlock;
-  const int64_t tasks = blocks * p.B * H, step = gridDim.x * 8ll;
-  for (int64_t task = blockIdx.x * 8ll + (threadIdx.x >> 5); task < tasks; task += step) {
-    const int64_t bh = task / blocks;
-    const int i0 = static_cast<int>(task - bh * blocks) * kCacheBlock;
+  const int i0 = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveTokens;
+  const int64_t heads = static_cast<int64_t>(p.B) * H;
+  for (int64_t bh = blockIdx.y; bh < heads; bh += gridDim.y) {
     const int b = static_cast<int>(bh / H), h = static_cast<int>(bh - static_cast<int64_t>(b) * H);
-    const int keep = min(evict_len(p, b), p.budget), cnt = min(keep - i0, kCacheBlock);
-    if (cnt <= 0) continue;
-    const int64_t to = token_row(p, p.new_table, p.new_max_pages, b, h, i0);
-    if (to < 0) continue;
-    // lanes 0..15 and 16..31 hold the tokens' old rows
-    const int t = lane & 15;
-    int64_t from = -1;
-    if (t < cnt) from = token_row(p, p.table, p.max_pages, b, h, p.kept[bh * p.budget + i0 + t]);
-    int sf = -1;  // of K in the lower lanes, of V in the upper ones
-    if (from >= 0) sf = __ldg((lane < 16 ? p.cache.k_sf : p.cache.v_sf) + (from >> 4));
-    if (lane < 16 && from >= 0) p.weights[to + t] = p.weights[from];
-    int top = sf;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (t == 0 && top >= 0) (lane < 16 ? p.cache.k_sf : p.cache.v_sf)[to >> 4] = static_cast<uint8_t>(top);
+    const int keep = min(evict_len(p, b), p.budget);
+    if (i0 >= keep) continue;
+    // each lane's token: its old row and its new one, -1 where there is none
+    int64_t from = -1, to = -1;
+    if (i0 + lane < keep) {
+      from = token_row(p, p.table, p.max_pages, b, h, p.kept[bh * p.budget + i0 + lane]);
+      to = token_row(p, p.new_table, p.new_max_pages, b, h, i0 + lane);
+      if (to < 0) from = -1;
+    }
+    __syncwarp();
+    int sf[2] = {-1, -1};
+    float w = 0.0f;
+    if (from >= 0) {
+      sf[0] = __ldg(p.cache.k_sf + (from >> 4));
+      sf[1] = __ldg(p.cache.v_sf + (from >> 4));
+      w = p.weights[from];
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const uint8_t* const codes = which ? p.cache.v : p.cache.k;
-      uint8_t* const dst = which ? p.cache.v : p.cache.k;
-      const int most = __shfl_sync(0xffffffffu, top, 16 * which);
+      uint8_t* const codes = (which ? p.cache.v : p.cache.k) + lane % LPT * 16;
+      uint4 x[STEPS];
 #pragma unroll
-      for (int u = 0; u < kCacheBlock; u += TPS) {
-        const int tok = u + lane / LPT;
-        const int64_t src = __shfl_sync(0xffffffffu, from, tok);
-        const int old = __shfl_sync(0xffffffffu, sf, 16 * which + tok);
-        if (tok < cnt && src >= 0) {
-          const uint4 x = *reinterpret_cast<const uint4*>(codes + src * D + lane % LPT * 16);
-          *reinterpret_cast<uint4*>(dst + (to + tok) * D + lane % LPT * 16) = rescale16(x, old, most);
-        }
+      for (int u = 0; u < STEPS; ++u) {
+        const int64_t src = __shfl_sync(0xffffffffu, from, u * TPS + lane / LPT);
+        if (src >= 0) x[u] = *reinterpret_cast<const uint4*>(codes + src * D);
+      }
+      // the largest scale of a new block: of 16 lanes
+      int top = sf[which];
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (which == 0 && from >= 0) p.weights[to] = w;
+      if ((lane & 15) == 0 && to >= 0 && top >= 0)
+        (which ? p.cache.v_sf : p.cache.k_sf)[to >> 4] = static_cast<uint8_t>(top);
+      const int below = top - sf[which];  // by how much a token's codes shrink
+      const bool any = __any_sync(0xffffffffu, from >= 0 && below != 0);
+#pragma unroll
+      for (int u = 0; u < STEPS; ++u) {
+        const int tok = u * TPS + lane / LPT;
+        const int64_t src = __shfl_sync(0xffffffffu, from, tok), dst = __shfl_sync(0xffffffffu, to, tok);
+        const int down = any ? __shfl_sync(0xffffffffu, below, tok) : 0;
+        if (src >= 0) *reinterpret_cast<uint4*>(codes + dst * D) = rescale16(x[u], down);
       }
     }
   }
