@@ -56,13 +56,13 @@ __device__ __forceinline__ int64_t token_row(const EvictParams& p, const int32_t
   return -1;
 }
 
-constexpr int kChooseThreads = 512, kChooseWarps = kChooseThreads / 32;
 constexpr int kMostKeys = 40960;  // keys that a CTA keeps in shared memory
 
+template <int WARPS>
 struct ChooseShared {
   int hist[4][256];  // of each digit, this CTA's
   int total[256];    // the cluster's
-  int above[kChooseWarps], same[kChooseWarps];  // each warp's tokens that stay, and those that equal the least key that does
+  int above[WARPS], same[WARPS];  // each warp's tokens that stay, and those that equal the least key that does
   int cta_above, cta_same;
   uint32_t digit;
   int need, of;  // of the `of` tokens with these digits `need` stay
@@ -70,10 +70,12 @@ struct ChooseShared {
 
 // One sequence and head by a cluster of CTAs, each with an equal part of its
 // tokens (a warp with an equal part of those).  `slots`: keys that `keys` holds.
-__global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];
-  __shared__ ChooseShared sh;
+  constexpr int WARPS = THREADS / 32;
+  __shared__ ChooseShared<WARPS> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(co
     if (keep <= 0) continue;
     int32_t* const kept = p.kept + bh * p.budget;
     if (keep == len) {
-      for (int64_t j = rank * kChooseThreads + tid; j < keep; j += ctas * kChooseThreads) kept[j] = static_cast<int>(j);
+      for (int64_t j = rank * THREADS + tid; j < keep; j += ctas * THREADS) kept[j] = static_cast<int>(j);
       continue;
     }
     // this CTA's tokens: n from j0 on (a multiple of 4 each, but for the last one's)
@@ -124,11 +126,11 @@ __global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(co
       return k;
     };
     auto keys4 = [&](int i) { return held ? *reinterpret_cast<const uint4*>(keys + i) : load4(i); };
-    for (int i = tid; i < 1024; i += kChooseThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = tid; i < 1024; i += THREADS) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
     // the first digit's histogram while the keys come
 #pragma unroll 4
-    for (int i = 4 * tid; i < n; i += 4 * kChooseThreads) {
+    for (int i = 4 * tid; i < n; i += 4 * THREADS) {
       const uint4 k = load4(i);
       if (held) *reinterpret_cast<uint4*>(keys + i) = k;
       atomicAdd(&sh.hist[0][k.x >> 24], 1);
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(co
           if (((k ^ prefix) & mask) == 0) atomicAdd(&sh.hist[d][k >> shift & 255], 1);
         };
 #pragma unroll 2
-        for (int i = 4 * tid; i < n; i += 4 * kChooseThreads) {
+        for (int i = 4 * tid; i < n; i += 4 * THREADS) {
           const uint4 k = keys4(i);
           count(k.x);
           if (i + 1 < n) count(k.y);
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(co
     }
     // Each warp counts what is above the key and what equals it in its part of
     // the tokens, 4 a lane at a time; then it knows its places.
-    const int part = ((n + kChooseWarps - 1) / kChooseWarps + 127) & ~127, w0 = min(n, part * warp), w1 = min(n, w0 + part);
+    const int part = ((n + WARPS - 1) / WARPS + 127) & ~127, w0 = min(n, part * warp), w1 = min(n, w0 + part);
     auto flags = [&](int i) {  // of 4 tokens: bits 0-3 above, 16-19 equal
       if (i >= w1) return 0;
       const uint4 k = keys4(i);
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kChooseThreads, 3) gdpa_cache_choose_kernel(co
     __syncthreads();
     int out = 0, equal = 0, all_above = 0, all_same = 0;
 #pragma unroll
-    for (int w = 0; w < kChooseWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) out += sh.above[w], equal += sh.same[w];
       all_above += sh.above[w], all_same += sh.same[w];
     }
