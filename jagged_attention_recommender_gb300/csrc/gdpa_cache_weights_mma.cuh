@@ -1,0 +1,57 @@
+// gdpa_cache_weights_mma.cuh -- what the two kernels of the stored keys' weight
+// on the 5th-generation tensor cores share.
+#pragma once
+
+#include "gdpa_cache_tile.cuh"
+#include "gdpa_cache_weights.cuh"
+
+namespace gdpa {
+
+namespace ptx {
+
+// 3-D tiled bulk tensor load global -> shared, completion counted in bytes on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Arrives on `bar` once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// tcgen05.wait::ld that also "writes" r[0..15]: uses of those registers cannot be
+// scheduled above the wait.
+__device__ __forceinline__ void tmem_wait_ld_r16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// mbar_wait for roles that are far ahead: a warp that waits sleeps between its
+// looks, so that it takes no issue slots from those that compute.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    __nanosleep(100);
+    if (mbar_test_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
+}  // namespace ptx
+
+// A place in a ring of stages, and the parity of its present turn.
+struct StageRing {
+  uint32_t at = 0, turn = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++at == stages) at = 0, turn ^= 1;
+  }
+};
+
+}  // namespace gdpa

@@ -25,27 +25,9 @@
 // queries converted anew for every tile.
 #pragma once
 
-#include "gdpa_cache_tile.cuh"
-#include "gdpa_cache_weights.cuh"
+#include "gdpa_cache_weights_mma.cuh"
 
 namespace gdpa {
-
-namespace ptx {
-
-// Arrives on `bar` once this thread's asynchronous copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// tcgen05.wait::ld that also "writes" r[0..15]: uses of those registers cannot be
-// scheduled above the wait.
-__device__ __forceinline__ void tmem_wait_ld_r16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
-}  // namespace ptx
 
 struct WeightPassParams {
   CacheWeightsParams w;
@@ -91,14 +73,6 @@ struct alignas(16) KeyNotes {
 struct ColumnNotes {
   float factor[128], lse[128];
   int last[128];
-};
-
-// A place in a ring of stages, and the parity of its present turn.
-struct Ring {
-  uint32_t at = 0, turn = 0;
-  __device__ __forceinline__ void next(uint32_t stages) {
-    if (++at == stages) at = 0, turn ^= 1;
-  }
 };
 
 // First key that any row of a sequence sees, and its tiles.
@@ -247,7 +221,7 @@ __device__ void run_sums(const WeightPassParams& p, const Run& run, Bars& B, con
   const int key_in = (warp & 3) * 32 + lane;
   const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + mine * 128;
   const volatile int* abort = &B.abort;
-  Ring n, q;         // of this warpgroup's notes (two of the eight stages), of chunks
+  StageRing n, q;         // of this warpgroup's notes (two of the eight stages), of chunks
   uint32_t count = 0, s_turn = 0;
   bool ok = true;
   Walk walk;
@@ -374,7 +348,7 @@ __device__ void run_convert(const WeightPassParams& p, const Run& run, uint8_t* 
   // 16-byte chunks 2c and 2c + 1 of a row, 64 columns a sub-tile (a pass's rows are 8 or 16 or 32: r & 7 is r0's)
   const uint32_t j = 2 * c & 7, base = ptx::smem_u32(sm) + (c >> 2) * C::SUB + r0 * 128;
   const uint32_t to0 = base + ((j ^ (r0 & 7)) << 4), to1 = base + (((j + 1) ^ (r0 & 7)) << 4);
-  Ring in, k;
+  StageRing in, k;
   bool ok = true;
   Walk walk;
   for (bool more = walk.begin(p, run); more && ok; more = walk.next(p)) {
@@ -420,12 +394,12 @@ __device__ void run_queries(const WeightPassParams& p, const Run& run, uint8_t* 
   const volatile int* abort = &B.abort;
   const int r0 = tid / LPR, c = tid % LPR;
   const uint32_t base = ptx::smem_u32(sm) + C::OFF_Q + (c >> 3) * C::SUB;
-  Ring q;
+  StageRing q;
   bool ok = true;
   auto bring = [&](const Walk& walk, int chunk) {
     const CacheSeq& s = walk.s;
     const Chunk k = chunk_of(p, walk, chunk);
-    ok = ptx::mbar_wait(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
+    ok = ptx::mbar_wait_idle(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return;
     ColumnNotes& col = columns[q.at];
@@ -491,7 +465,7 @@ __device__ void run_copies(const WeightPassParams& p, const Run& run, uint8_t* s
   const int pmask = (1 << w.cache.lp) - 1;
   const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
   const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW + lane * 16 * D;
-  Ring in, n;
+  StageRing in, n;
   uint32_t count = 0;
   bool ok = true;
   Walk walk;
@@ -566,7 +540,7 @@ __device__ void run_mma(const WeightPassParams& p, const Run& run, uint8_t* sm, 
   const volatile int* abort = &B.abort;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
   const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm) + C::OFF_Q, 16, 1024);
-  Ring k, q;
+  StageRing k, q;
   uint32_t count = 0, s_turns = 0;  // s_turns: a bit for each buffer
   bool ok = true;
   Walk walk;

@@ -25,23 +25,9 @@
 #pragma once
 
 #include "gdpa_cache_append.cuh"
-#include "gdpa_cache_tile.cuh"
-#include "gdpa_cache_weights.cuh"
+#include "gdpa_cache_weights_mma.cuh"
 
 namespace gdpa {
-
-namespace ptx {
-
-// 3-D tiled bulk tensor load global -> shared, completion counted in bytes on `bar`.
-__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          smem_dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-}  // namespace ptx
 
 struct WeightTileParams {
   CUtensorMap tm_q;  // [T, Hq, D] bf16, boxes of 64 x heads x tokens, 128-byte swizzle
@@ -78,14 +64,6 @@ struct Bars {
   uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
-};
-
-// A place in a ring of stages, and the parity of its present turn.
-struct Ring {
-  uint32_t at = 0, turn = 0;
-  __device__ __forceinline__ void next(uint32_t stages) {
-    if (++at == stages) at = 0, turn ^= 1;
-  }
 };
 
 // What goes with a tile of keys: where each one's weight is (-1: nowhere), and
@@ -213,7 +191,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
   const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * 256 + turn * 128;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  Ring k, n;                 // of tiles of K and chunks' notes
+  StageRing k, n;                 // of tiles of K and chunks' notes
   uint32_t si = 0, xi = 0;   // tiles of S, and sums in two halves, so far
   bool ok = true;
   Walk walk;
@@ -411,7 +389,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   // 16-byte chunks 2c and 2c + 1 of a row, 64 columns a sub-tile
   const uint32_t base = ptx::smem_u32(sm) + (c >> 2) * C::SUB;
   uint32_t ri = 0, ki = 0;  // tiles brought, and converted
-  Ring in, out, k;          // of codes brought, codes converted, tiles of K
+  StageRing in, out, k;          // of codes brought, codes converted, tiles of K
   bool ok = true;
   TileWalk tiles;
   bool more = tiles.begin(p);
@@ -458,7 +436,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
     }
     if (ri == ki) break;
     const uint32_t ks = k.at, rs = out.at;
-    ok = ptx::mbar_wait(&B.k_free[ks], k.turn ^ 1, p.limit, abort);
+    ok = ptx::mbar_wait_idle(&B.k_free[ks], k.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     if (more)
@@ -530,12 +508,12 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
   const volatile int* abort = &B.abort;
   const uint32_t bytes = static_cast<uint32_t>(p.heads) * p.tokens * D * 2;
   const uint32_t to = ptx::smem_u32(sm) + p.ks * C::TILE;
-  Ring q;
+  StageRing q;
   uint32_t count = 0;
   const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
     int tok, part;
     chunk_at(p, it, c, tok, part);
-    const bool fine = ptx::mbar_wait(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
+    const bool fine = ptx::mbar_wait_idle(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
     if (!__all_sync(0xffffffffu, fine)) return false;
     if (lane == 0) {
       ptx::mbar_arrive_expect_tx(&B.q_full[q.at], bytes);
@@ -574,7 +552,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
     tok_of[i] = (lane * 4 + i) / p.heads;
     head_of[i] = lane * 4 + i - tok_of[i] * p.heads;
   }
-  Ring n;
+  StageRing n;
   const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
     int tok0, part;
     chunk_at(p, it, c, tok0, part);
@@ -591,7 +569,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
         last[i] = w.causal ? walk.s.len - walk.s.n + tok : walk.s.len - 1;
       }
     }
-    const bool fine = ptx::mbar_wait(&B.n_free[n.at], n.turn ^ 1, p.limit, abort);
+    const bool fine = ptx::mbar_wait_idle(&B.n_free[n.at], n.turn ^ 1, p.limit, abort);
     if (!__all_sync(0xffffffffu, fine)) return false;
     reinterpret_cast<float4*>(notes.lse + n.at * 128)[lane] = make_float4(-lse[0], -lse[1], -lse[2], -lse[3]);
     reinterpret_cast<int4*>(notes.last + n.at * 128)[lane] = make_int4(last[0], last[1], last[2], last[3]);
@@ -611,7 +589,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
   const volatile int* abort = &B.abort;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
   const uint64_t q_desc = k_desc + p.ks * (C::TILE >> 4);
-  Ring k, q;
+  StageRing k, q;
   uint32_t si[2] = {0, 0};
   bool ok = true;
   Walk walk;
@@ -620,7 +598,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
 #pragma unroll 1
     for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
       const Item it = item_of(p, walk, pair);
-      Ring second = k;
+      StageRing second = k;
       second.next(p.ks);
 #pragma unroll 1
       for (int c = 0; c < it.chunks; ++c) {
@@ -633,7 +611,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (m >= it.tiles) break;
-          const Ring at = m ? second : k;
+          const StageRing at = m ? second : k;
           const uint32_t sb = si[m] & 1;
           if (c == 0) ok = ptx::mbar_wait(&B.k_full[at.at], at.turn, p.limit, abort);
           ok = ok && ptx::mbar_wait(&B.s_free[m][sb], (si[m] >> 1 & 1) ^ 1, p.limit, abort);
