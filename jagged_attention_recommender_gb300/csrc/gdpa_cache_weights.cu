@@ -36,7 +36,7 @@ gdpa_status_t launch_split(const CacheWeightsParams& p, const Device& dev, cudaS
 }
 
 template <int D>
-gdpa_status_t launch_tile(const CacheWeightsParams& w, int max_q, const Device& dev, cudaStream_t s) {
+gdpa_status_t launch_tile(const CacheWeightsParams& w, const Device& dev, cudaStream_t s) {
   using C = WeightTileCfg<D>;
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
@@ -47,15 +47,10 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, int max_q, const Device& 
   p.heads = std::min(w.G, C::COLS);
   p.tokens = C::COLS / p.heads;
   p.parts = (w.G + p.heads - 1) / p.heads;
-  const bool single = p.parts == 1 && max_q <= p.tokens;  // the rows of a sequence fit one chunk
-  p.group = single ? 4 : 1;
-  p.ks = single ? 3 : 2;
-  p.qs = C::STAGES - p.ks;
   p.limit = bounded_wait_ns();
   if ((st = encode_heads_3d(&p.tm_q, w.q, w.batch.T, w.Hq, D, w.q_stride, p.heads, p.tokens)) != GDPA_OK) return st;
   const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp, items = (keys + 255) / 256;
-  const int64_t groups = (int64_t)w.batch.B * w.cache.H * ((items + p.group - 1) / p.group);
-  const int ctas = static_cast<int>(std::min<int64_t>(groups, dev.sms));
+  const int ctas = static_cast<int>(std::min<int64_t>((int64_t)w.batch.B * w.cache.H * items, dev.sms));
   gdpa_cache_weights_tile_kernel<D><<<ctas, C::THREADS, C::SMEM, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
@@ -87,7 +82,7 @@ gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Devic
   if (rows <= 24) return launch_split<D, 3>(p, dev, s);
   if (rows <= 48) return launch_split<D, 6>(p, dev, s);
   if (p.G <= 128 && max_q <= 128 / p.G) return launch_pass<D>(p, dev, s);
-  return launch_tile<D>(p, max_q, dev, s);
+  return launch_tile<D>(p, dev, s);
 }
 
 }  // namespace

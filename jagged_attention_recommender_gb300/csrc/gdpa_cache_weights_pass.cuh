@@ -271,8 +271,7 @@ __device__ void run_sums(const WeightPassParams& p, const Run& run, Bars& B, con
 #pragma unroll 1
           for (int i = 0; i < blocks; ++i) {
             uint32_t r[16];
-            ptx::tmem_ld16(from + i * 16, r);
-            ptx::tmem_wait_ld_r16(r);
+            ptx::tmem_read16(from + i * 16, r);
             if (i == blocks - 1) {  // the buffer is read
               ptx::tc_fence_before();
               __syncwarp();

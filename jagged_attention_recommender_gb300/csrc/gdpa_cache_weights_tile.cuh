@@ -11,9 +11,8 @@
 //
 // Work split.  An item is 256 keys of a sequence and head, converted once and kept
 // in shared memory while all rows that see any of them pass in chunks of 128
-// columns (tokens times heads of the group); sequences whose rows fit one
-// chunk keep the chunk instead and pass p.group items.  CTAs take every
-// gridDim.x-th group of items.  Roles:
+// columns (tokens times heads of the group).  CTAs take items there and back over
+// the grid.  Roles:
 //   warps 0-15   the sums, a key a thread: warpgroups 0 and 2 those of the item's
 //                first 128 keys, 1 and 3 of its second, each every other chunk
 //   warps 16-19  bring codes, scales and earlier weights by their own
@@ -34,8 +33,6 @@ struct WeightTileParams {
   CacheWeightsParams w;
   int heads, tokens;  // of a chunk: heads * tokens <= 128 (heads: G, or 128 of more)
   int parts;          // chunks that the heads of a group make
-  int group;          // items of a group
-  int ks, qs;         // stages of K and of Q: ks + qs = WeightTileCfg::STAGES
   unsigned long long limit;
 };
 
@@ -44,14 +41,11 @@ struct WeightTileCfg {
   static constexpr int D = D_, THREADS = 736, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
-  // Stages of K and Q together.  Where chunks pass the keys two are K's and three
-  // Q's: a chunk's way from L2 takes longer than its products.  Where tiles pass
-  // the queries three are K's.
-  static constexpr int STAGES = 5, MOST_KS = 3, MOST_QS = 3, NS = 4;  // NS: of a chunk's notes
+  static constexpr int KS = 2, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
   static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
-  static constexpr int OFF_RAW = STAGES * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
+  static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
   static constexpr int KEY_NOTES = 2048;           // of each key: its row, its scale, its earlier weight
-  static constexpr int USED = OFF_NOTES + (RAWS + MOST_KS) * KEY_NOTES + NS * 1024 + 1024;
+  static constexpr int USED = OFF_NOTES + (RAWS + KS) * KEY_NOTES + NS * 1024 + 1024;
   static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;  // one CTA an SM (all of its TMEM)
   static constexpr uint32_t TM_COLS = 512;         // S of two tiles, two buffers each
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -60,7 +54,7 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t k_full[3], k_free[3], q_full[3], q_free[3], n_full[4], n_free[4];
+  uint64_t k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
   uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
@@ -86,23 +80,29 @@ struct Notes {
   float* half;    // [2][128]: sums on their way from one warpgroup to the other
 };
 
-// Groups of items of one CTA, in order, by a whole warp: its lanes hold 32
-// sequences, so that the next group is found without a load.
+// An item: its first key, its tiles, and the tokens [lo, hi) whose rows see any of
+// it, in chunks.
+struct Item {
+  int k0, tiles, lo, hi, chunks;
+};
+
+// The items of one CTA, in order, by a whole warp: its lanes hold 32 sequences, so
+// that the next item is found without a load.
 struct Walk {
-  int64_t upto;     // groups of the sequences up to this lane's
+  int64_t upto;     // items of the sequences up to this lane's
   CacheSeq lane_s;  // this lane's sequence
-  int64_t idx;      // the present group, counted from the first lane's sequence
+  int64_t idx;      // the present item, counted from the first lane's sequence
   int base;         // that sequence
   bool back;
-  // the present group
+  // the present item
   CacheSeq s;
-  int b, h, kbase, pair, pair_end;
-  bool single;      // its rows fit one chunk
+  int b, h;
+  Item it;
 
   __device__ __forceinline__ int first_stored(const WeightTileParams& p, const CacheSeq& q) const {
     return p.w.keep ? min(first_key(q.len - q.n, p.w.window), q.len) & ~255 : 0;
   }
-  __device__ __forceinline__ int pairs_of(const WeightTileParams& p, const CacheSeq& q) const {
+  __device__ __forceinline__ int items_of(const WeightTileParams& p, const CacheSeq& q) const {
     return static_cast<int>((static_cast<unsigned>(q.len - first_stored(p, q)) + 255) >> 8);
   }
   __device__ __forceinline__ void load(const WeightTileParams& p) {
@@ -110,8 +110,7 @@ struct Walk {
     lane_s = CacheSeq{0, 0, 0, 0};
     if (base + lane < p.w.batch.B) lane_s = load_sequence(p.w.batch, p.w.cache.lp, base + lane);
     upto = 0;
-    if (lane_s.ok && lane_s.n > 0 && lane_s.len > 0)
-      upto = static_cast<int64_t>((pairs_of(p, lane_s) + p.group - 1) / p.group) * p.w.cache.H;
+    if (lane_s.ok && lane_s.n > 0 && lane_s.len > 0) upto = static_cast<int64_t>(items_of(p, lane_s)) * p.w.cache.H;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
@@ -135,12 +134,14 @@ struct Walk {
     s.ok = 1;
     b = base + at;
     const int64_t i = idx - (at > 0 ? before : 0);
-    const int pairs = pairs_of(p, s), groups = (pairs + p.group - 1) / p.group;
-    h = static_cast<int>(i / groups);
-    pair = static_cast<int>(i - static_cast<int64_t>(h) * groups) * p.group;
-    pair_end = min(pairs, pair + p.group);
-    kbase = first_stored(p, s);
-    single = p.parts == 1 && s.n <= p.tokens;
+    const int items = items_of(p, s);
+    h = static_cast<int>(split::quotient(i, items));
+    it.k0 = first_stored(p, s) + (static_cast<int>(i - static_cast<int64_t>(h) * items) << 8);
+    it.tiles = s.len - it.k0 > 128 ? 2 : 1;
+    const int last = it.k0 + min(255, s.len - 1 - it.k0);
+    it.lo = rows_of_key(s, it.k0, p.w.causal, p.w.window).lo;
+    it.hi = rows_of_key(s, last, p.w.causal, p.w.window).hi;
+    it.chunks = it.hi > it.lo ? (it.hi - it.lo + p.tokens - 1) / p.tokens * p.parts : 0;
     return true;
   }
   __device__ __forceinline__ bool begin(const WeightTileParams& p) {
@@ -157,23 +158,6 @@ struct Walk {
   }
 };
 
-// An item: its first key, its tiles, and the tokens [lo, hi) whose rows see any of it, in chunks.
-struct Item {
-  int k0, tiles, lo, hi, chunks;
-};
-__device__ __forceinline__ Item item_of(const WeightTileParams& p, const Walk& w, int pair) {
-  Item it;
-  it.k0 = w.kbase + (pair << 8);
-  it.tiles = w.s.len - it.k0 > 128 ? 2 : 1;
-  const int last = it.k0 + min(255, w.s.len - 1 - it.k0);
-  it.lo = rows_of_key(w.s, it.k0, p.w.causal, p.w.window).lo;
-  it.hi = rows_of_key(w.s, last, p.w.causal, p.w.window).hi;
-  it.chunks = 0;
-  if (it.hi <= it.lo) return it;
-  if (w.single) it.lo = 0, it.hi = w.s.n;
-  it.chunks = (it.hi - it.lo + p.tokens - 1) / p.tokens * p.parts;
-  return it;
-}
 // Columns of chunk c, to the last one that is a row.
 __device__ __forceinline__ int chunk_columns(const WeightTileParams& p, const Item& it, int c) {
   const int part = p.parts == 1 ? 0 : c % p.parts, tok = it.lo + (p.parts == 1 ? c : c / p.parts) * p.tokens;
@@ -186,152 +170,141 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
   const CacheWeightsParams& w = p.w;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int m = warp >> 2 & 1;        // this warpgroup's tile of an item ...
-  const uint32_t turn = warp >> 3;    // ... and buffer of S
+  const uint32_t turn = warp >> 3;    // ... and its chunks, of every two: their notes and buffer of S
   const int key_in = (warp & 3) * 32 + lane;
   const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * 256 + turn * 128;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  StageRing k, n;                 // of tiles of K and chunks' notes
-  uint32_t si = 0, xi = 0;   // tiles of S, and sums in two halves, so far
+  StageRing k, n;                      // of tiles of K, of this warpgroup's notes (two of the four stages)
+  uint32_t ci = 0, s_turn = 0, xi = 0;  // chunks, turns of S's buffer, and sums in two halves, so far
   bool ok = true;
   Walk walk;
   for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
     const CacheSeq& s = walk.s;
-    bool held = false;  // this group's only chunk is there
-#pragma unroll 1
-    for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
-      const Item it = item_of(p, walk, pair);
-      const bool mine = m < it.tiles;
-      const int k0 = it.k0 + m * 128, key = k0 + key_in;
-      int64_t row = -1;
-      float old = 0.0f, factor = 0.0f;
-      if (it.chunks == 0) {  // no row sees these keys: earlier weights alone
-        if (mine && turn == 0 && s.len - k0 > key_in) {
-          const int page = load_page(w.cache, w.batch, walk.b, key);
-          if (page >= 0) {
-            row = cache_row(w.cache, page, walk.h, key & pmask);
-            w.w[row] = w.w_in && key < s.len - s.n ? w.decay * w.w_in[row] : 0.0f;
-          }
+    const Item it = walk.it;
+    const bool mine = m < it.tiles;
+    const int k0 = it.k0 + m * 128, key = k0 + key_in;
+    if (it.chunks == 0) {  // no row sees these keys: earlier weights alone
+      if (mine && turn == 0 && s.len - k0 > key_in) {
+        const int page = load_page(w.cache, w.batch, walk.b, key);
+        if (page >= 0) {
+          const int64_t row = cache_row(w.cache, page, walk.h, key & pmask);
+          w.w[row] = w.w_in && key < s.len - s.n ? w.decay * w.w_in[row] : 0.0f;
         }
-        __syncwarp();
-        continue;
       }
-      // (every warp sees every tile arrive: one that skipped some could take a
-      // later turn of a stage for the one it waits for)
+      __syncwarp();
+      continue;
+    }
+    // (every warp sees every tile arrive: one that skipped some could take a
+    // later turn of a stage for the one it waits for)
+    int64_t row = -1;
+    float old = 0.0f, factor = 0.0f;
 #pragma unroll 1
-      for (int j = 0; j < it.tiles; ++j) {
-        ok = ptx::mbar_wait(&B.k_full[k.at], k.turn, p.limit, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (j == m) {
-          row = notes.key[k.at].row[key_in];
-          factor = notes.key[k.at].factor[key_in];
-          old = notes.key[k.at].old[key_in];
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&B.k_free[k.at]);
-        k.next(p.ks);
-      }
+    for (int j = 0; j < it.tiles; ++j) {
+      ok = ptx::mbar_wait(&B.k_full[k.at], k.turn, p.limit, abort);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint64_t f2 = ptx::f2_splat(factor);
-      uint64_t sum[2] = {0, 0};
-      float edge_sum = 0.0f;
-      const int k_last = k0 + min(127, s.len - 1 - k0);
-      const bool writes = it.chunks == 1 ? (si & 1) == turn : turn == 0;
+      if (j == m) {
+        row = notes.key[k.at].row[key_in];
+        factor = notes.key[k.at].factor[key_in];
+        old = notes.key[k.at].old[key_in];
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&B.k_free[k.at]);
+      k.next(C::KS);
+    }
+    if (!ok) break;
+    const uint64_t f2 = ptx::f2_splat(factor);
+    uint64_t sum[2] = {0, 0};
+    const int k_last = k0 + min(127, s.len - 1 - k0);
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c) {
-        const bool due = mine && (si & 1) == turn;
-        if (!held) ok = ptx::mbar_wait(&B.n_full[n.at], n.turn, p.limit, abort);
-        held = walk.single;
-        if (ok && due) ok = ptx::mbar_wait(&B.s_full[m][turn], si >> 1 & 1, p.limit, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (due) {
-          ptx::tc_fence_after();
-          const int blocks = (chunk_columns(p, it, c) + 31) >> 5;
-          const float* lse = notes.lse + n.at * 128;
-          const int* last = notes.last + n.at * 128;
+    for (int c = (ci ^ turn) & 1; c < it.chunks; c += 2) {
+      const uint32_t stage = n.at * 2 + turn;
+      ok = ptx::mbar_wait(&B.n_full[stage], n.turn, p.limit, abort);
+      if (ok && mine) ok = ptx::mbar_wait(&B.s_full[m][turn], s_turn, p.limit, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (mine) {
+        s_turn ^= 1;
+        ptx::tc_fence_after();
+        const int columns = chunk_columns(p, it, c), blocks = (columns + 31) >> 5;
+        const float* lse = notes.lse + stage * 128;
+        const int* last = notes.last + stage * 128;
+        // whether all columns are rows that see all of these keys (tokens, and so last keys, ascend)
+        const int end0 = last[0], end1 = last[columns - 1];
+        const bool all = columns == p.heads * p.tokens && end0 >= k_last && (w.window == 0 || end1 - w.window < k0);
+        auto tile = [&](auto all_tag) {
 #pragma unroll 1
-          for (int q = 0; q < blocks; ++q) {
+          for (int i = 0; i < blocks; ++i) {
             uint32_t r[32];
-            ptx::tmem_ld32(from + q * 32, r);
-            const int end0 = last[q * 32], end1 = last[q * 32 + 31];  // tokens, and so last keys, ascend
-            const bool all = end0 >= k_last && end1 >= end0 && (w.window == 0 || end1 - w.window < k0);
-            ptx::tmem_wait_ld_r32(r);
-            if (q == blocks - 1) {  // the buffer is read
+            ptx::tmem_read32(from + i * 32, r);
+            if (i == blocks - 1) {  // the buffer is read
               ptx::tc_fence_before();
               __syncwarp();
               if (lane == 0) ptx::mbar_arrive(&B.s_free[m][turn]);
               __syncwarp();
             }
-            if (all) {
+            const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(lse + i * 32);
+            const int4* e4 = reinterpret_cast<const int4*>(last + i * 32);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const ulonglong2 l = reinterpret_cast<const ulonglong2*>(lse + q * 32)[i];
-                const uint64_t x = ptx::f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
-                const uint64_t y = ptx::f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                float a, b, e, d;
-                ptx::f2_unpack(ptx::f2_fma(x, f2, l.x), a, b);
-                ptx::f2_unpack(ptx::f2_fma(y, f2, l.y), e, d);
-                sum[0] = ptx::f2_add(sum[0], ptx::f2_pack(ptx::ex2_approx(a), ptx::ex2_approx(b)));
-                sum[1] = ptx::f2_add(sum[1], ptx::f2_pack(ptx::ex2_approx(e), ptx::ex2_approx(d)));
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 l = l4[j];
+              const uint64_t x = ptx::f2_pack(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+              const uint64_t y = ptx::f2_pack(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+              float a, b, d, e;
+              ptx::f2_unpack(ptx::f2_fma(x, f2, l.x), a, b);
+              ptx::f2_unpack(ptx::f2_fma(y, f2, l.y), d, e);
+              a = ptx::ex2_approx(a), b = ptx::ex2_approx(b), d = ptx::ex2_approx(d), e = ptx::ex2_approx(e);
+              if (!decltype(all_tag)::value) {
+                const int4 end = e4[j];
+                const int width = w.window > 0 ? w.window : 0x7fffffff;  // (key > end - window; none: always)
+                if (key > end.x || key <= end.x - width) a = 0.0f;
+                if (key > end.y || key <= end.y - width) b = 0.0f;
+                if (key > end.z || key <= end.z - width) d = 0.0f;
+                if (key > end.w || key <= end.w - width) e = 0.0f;
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int end = last[q * 32 + i];
-                const float e = ptx::ex2_approx(fmaf(__uint_as_float(r[i]), factor, lse[q * 32 + i]));
-                if (key <= end && (w.window == 0 || key > end - w.window)) edge_sum += e;
-              }
+              sum[0] = ptx::f2_add(sum[0], ptx::f2_pack(a, b));
+              sum[1] = ptx::f2_add(sum[1], ptx::f2_pack(d, e));
             }
-            __syncwarp();
           }
-        }
-        if (mine) ++si;
-        if (!walk.single) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&B.n_free[n.at]);
-          n.next(C::NS);
-        }
+        };
+        if (all)
+          tile(std::true_type{});
+        else
+          tile(std::false_type{});
       }
-      if (!ok) break;
-      if (!mine) continue;
-      float a, b, c, d;
-      ptx::f2_unpack(sum[0], a, b);
-      ptx::f2_unpack(sum[1], c, d);
-      float total = ((a + b) + (c + d)) + edge_sum;
-      if (it.chunks > 1) {  // both warpgroups have a part
-        if (turn == 1) {
-          ok = ptx::mbar_wait(&B.x_free[m], (xi & 1) ^ 1, p.limit, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          notes.half[m * 128 + key_in] = total;
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&B.x_full[m]);
-        } else {
-          ok = ptx::mbar_wait(&B.x_full[m], xi & 1, p.limit, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          total += notes.half[m * 128 + key_in];
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&B.x_free[m]);
-        }
-        ++xi;
-      }
-      if (writes && row >= 0) w.w[row] = old + total;
       __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&B.n_free[stage]);
+      n.next(2);
     }
     if (!ok) break;
-    if (walk.single) {
-      if (!held) {  // (its keys saw no row: the notes came all the same)
-        ok = ptx::mbar_wait(&B.n_full[n.at], n.turn, p.limit, abort);
+    const bool writes = it.chunks == 1 ? (ci & 1) == turn : turn == 0;
+    ci += it.chunks;
+    if (!mine) continue;
+    float a, b, c, d;
+    ptx::f2_unpack(sum[0], a, b);
+    ptx::f2_unpack(sum[1], c, d);
+    float total = (a + b) + (c + d);
+    if (it.chunks > 1) {  // both warpgroups have a part
+      if (turn == 1) {
+        ok = ptx::mbar_wait(&B.x_free[m], (xi & 1) ^ 1, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        notes.half[m * 128 + key_in] = total;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&B.x_full[m]);
+      } else {
+        ok = ptx::mbar_wait(&B.x_full[m], xi & 1, p.limit, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        total += notes.half[m * 128 + key_in];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&B.x_free[m]);
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&B.n_free[n.at]);
-      n.next(C::NS);
+      ++xi;
     }
+    if (writes && row >= 0) w.w[row] = old + total;
+    __syncwarp();
   }
   if (!ok && lane == 0) {
     B.abort = 1;
@@ -349,29 +322,16 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& h
 // The tiles of K that a CTA needs, in order.
 struct TileWalk {
   Walk walk;
-  Item it;
-  int pair, m;
-  __device__ __forceinline__ bool settle(const WeightTileParams& p) {  // to a tile at or behind `pair`
-    while (true) {
-      for (; pair < walk.pair_end; ++pair) {
-        it = item_of(p, walk, pair);
-        if (it.chunks > 0) return true;
-      }
-      if (!walk.next(p)) return false;
-      pair = walk.pair;
-    }
-  }
-  __device__ __forceinline__ bool begin(const WeightTileParams& p) {
+  int m;
+  __device__ __forceinline__ bool settle(const WeightTileParams& p, bool more) {
     m = 0;
-    if (!walk.begin(p)) return false;
-    pair = walk.pair;
-    return settle(p);
+    while (more && walk.it.chunks == 0) more = walk.next(p);
+    return more;
   }
+  __device__ __forceinline__ bool begin(const WeightTileParams& p) { return settle(p, walk.begin(p)); }
   __device__ __forceinline__ bool next(const WeightTileParams& p) {
-    if (++m < it.tiles) return true;
-    m = 0;
-    ++pair;
-    return settle(p);
+    if (++m < walk.it.tiles) return true;
+    return settle(p, walk.next(p));
   }
 };
 
@@ -395,7 +355,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   bool more = tiles.begin(p);
   // lane i: the page of the tile's i-th block of 16 keys
   auto page_of = [&]() {
-    const int k0 = tiles.it.k0 + tiles.m * 128;
+    const int k0 = tiles.walk.it.k0 + tiles.m * 128;
     if (lane >= 8 || tiles.walk.s.len - k0 <= lane * 16) return -1;
     return load_page(w.cache, w.batch, tiles.walk.b, k0 + lane * 16);
   };
@@ -404,7 +364,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   while (true) {
     while (more && ri - ki < C::RAWS) {
       const Walk& at = tiles.walk;
-      const int k0 = tiles.it.k0 + tiles.m * 128, valid = at.s.len - k0;
+      const int k0 = tiles.walk.it.k0 + tiles.m * 128, valid = at.s.len - k0;
       const uint32_t rs = in.at;
       KeyNotes& note = notes.raw[rs];
 #pragma unroll
@@ -465,7 +425,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
     ptx::fence_proxy_async_smem();
     ptx::mbar_arrive(&B.k_full[ks]);
     ++ki;
-    k.next(p.ks);
+    k.next(C::KS);
     out.next(C::RAWS);
   }
   split::cp_wait<0>();
@@ -475,22 +435,14 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   }
 }
 
-// f(item, chunk) for every chunk of this CTA, in order, until it returns false.
+// f(walk, chunk) for every chunk of this CTA, in order, until it returns false.
 template <class F>
 __device__ __forceinline__ bool each_chunk(const WeightTileParams& p, const F& f) {
   Walk walk;
   for (bool more = walk.begin(p); more; more = walk.next(p)) {
-    if (walk.single) {
-      const Item it = {0, 0, 0, walk.s.n, 1};
-      if (!f(walk, it, 0)) return false;
-      continue;
-    }
-    for (int pair = walk.pair; pair < walk.pair_end; ++pair) {
-      const Item it = item_of(p, walk, pair);
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c)
-        if (!f(walk, it, c)) return false;
-    }
+    for (int c = 0; c < walk.it.chunks; ++c)
+      if (!f(walk, c)) return false;
   }
   return true;
 }
@@ -507,12 +459,12 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
   const int lane = threadIdx.x & 31;
   const volatile int* abort = &B.abort;
   const uint32_t bytes = static_cast<uint32_t>(p.heads) * p.tokens * D * 2;
-  const uint32_t to = ptx::smem_u32(sm) + p.ks * C::TILE;
+  const uint32_t to = ptx::smem_u32(sm) + C::OFF_Q;
   StageRing q;
   uint32_t count = 0;
-  const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
+  const bool ok = each_chunk(p, [&](const Walk& walk, int c) {
     int tok, part;
-    chunk_at(p, it, c, tok, part);
+    chunk_at(p, walk.it, c, tok, part);
     const bool fine = ptx::mbar_wait_idle(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
     if (!__all_sync(0xffffffffu, fine)) return false;
     if (lane == 0) {
@@ -523,7 +475,7 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
                          walk.h * p.w.G + part * p.heads, walk.s.first + tok);
     }
     __syncwarp();
-    q.next(p.qs);
+    q.next(C::QS);
     ++count;
     return true;
   });
@@ -532,10 +484,10 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
     atomicOr(p.w.batch.status, kStatusProducer);
   }
   // no copy may land behind the CTA's end: the last turn of every stage
-  for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(p.qs)); ++i) {
+  for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(C::QS)); ++i) {
     const int never = 0;
     if (q.at == 0) q.turn ^= 1;
-    q.at = (q.at == 0 ? p.qs : q.at) - 1;
+    q.at = (q.at == 0 ? C::QS : q.at) - 1;
     ptx::mbar_wait(&B.q_full[q.at], q.turn, 100000000ull, &never);
   }
 }
@@ -553,9 +505,9 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
     head_of[i] = lane * 4 + i - tok_of[i] * p.heads;
   }
   StageRing n;
-  const bool ok = each_chunk(p, [&](const Walk& walk, const Item& it, int c) {
+  const bool ok = each_chunk(p, [&](const Walk& walk, int c) {
     int tok0, part;
-    chunk_at(p, it, c, tok0, part);
+    chunk_at(p, walk.it, c, tok0, part);
     float lse[4];
     int last[4];
 #pragma unroll
@@ -563,7 +515,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
       const int tok = tok0 + tok_of[i], head = part * p.heads + head_of[i];
       lse[i] = INFINITY;
       last[i] = -1;
-      if (tok_of[i] < p.tokens && tok < it.hi && head < w.G) {
+      if (tok_of[i] < p.tokens && tok < walk.it.hi && head < w.G) {
         const float x = __ldg(w.lse + static_cast<int64_t>(walk.s.first + tok) * w.Hq + walk.h * w.G + head);
         lse[i] = x == -INFINITY ? INFINITY : x * kLog2e;
         last[i] = w.causal ? walk.s.len - walk.s.n + tok : walk.s.len - 1;
@@ -588,64 +540,49 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
   using C = WeightTileCfg<D>;
   const volatile int* abort = &B.abort;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
-  const uint64_t q_desc = k_desc + p.ks * (C::TILE >> 4);
+  const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm) + C::OFF_Q, 16, 1024);
   StageRing k, q;
-  uint32_t si[2] = {0, 0};
+  uint32_t ci = 0, s_turns = 0;  // chunks so far; a bit for each buffer of S
   bool ok = true;
   Walk walk;
   for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
-    bool held = false;
+    const Item it = walk.it;
+    if (it.chunks == 0) continue;
+    StageRing second = k;
+    second.next(C::KS);
 #pragma unroll 1
-    for (int pair = walk.pair; pair < walk.pair_end && ok; ++pair) {
-      const Item it = item_of(p, walk, pair);
-      StageRing second = k;
-      second.next(p.ks);
-#pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c) {
-        if (!held) ok = ptx::mbar_wait(&B.q_full[q.at], q.turn, p.limit, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        held = walk.single;
-        const uint32_t idesc = ptx::idesc_bf16(128, (chunk_columns(p, it, c) + 15) & ~15, 0);
-        const uint64_t b = q_desc + q.at * (C::TILE >> 4);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m >= it.tiles) break;
-          const StageRing at = m ? second : k;
-          const uint32_t sb = si[m] & 1;
-          if (c == 0) ok = ptx::mbar_wait(&B.k_full[at.at], at.turn, p.limit, abort);
-          ok = ok && ptx::mbar_wait(&B.s_free[m][sb], (si[m] >> 1 & 1) ^ 1, p.limit, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t a = k_desc + at.at * (C::TILE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::SUB + (kk & 3) * 32) >> 4;
-            ptx::mma_ss_elect(tmem + m * 256 + sb * 128, a + off, b + off, idesc, kk > 0 ? 1u : 0u);
-          }
-          ptx::mma_commit_elect(&B.s_full[m][sb]);
-          if (c == it.chunks - 1) ptx::mma_commit_elect(&B.k_free[at.at]);
-          ++si[m];
-        }
-        if (!ok) break;
-        if (!walk.single) {
-          ptx::mma_commit_elect(&B.q_free[q.at]);
-          q.next(p.qs);
-        }
-      }
-      if (it.chunks > 0) {
-        k.next(p.ks);
-        if (it.tiles == 2) k.next(p.ks);
-      }
-    }
-    if (walk.single && ok) {
-      if (!held) ok = ptx::mbar_wait(&B.q_full[q.at], q.turn, p.limit, abort);
+    for (int c = 0; c < it.chunks; ++c, ++ci) {
+      ok = ptx::mbar_wait(&B.q_full[q.at], q.turn, p.limit, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      const uint32_t idesc = ptx::idesc_bf16(128, (chunk_columns(p, it, c) + 31) & ~31, 0), sb = ci & 1;
+      const uint64_t b = q_desc + q.at * (C::TILE >> 4);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m >= it.tiles) break;
+        const StageRing at = m ? second : k;
+        const uint32_t bit = 1u << (2 * m + sb);
+        if (c == 0) ok = ptx::mbar_wait(&B.k_full[at.at], at.turn, p.limit, abort);
+        ok = ok && ptx::mbar_wait(&B.s_free[m][sb], (s_turns & bit) ? 0 : 1, p.limit, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_turns ^= bit;
+        ptx::tc_fence_after();
+        const uint64_t a = k_desc + at.at * (C::TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::SUB + (kk & 3) * 32) >> 4;
+          ptx::mma_ss_elect(tmem + m * 256 + sb * 128, a + off, b + off, idesc, kk > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit_elect(&B.s_full[m][sb]);
+        if (c == it.chunks - 1) ptx::mma_commit_elect(&B.k_free[at.at]);
+      }
+      if (!ok) break;
       ptx::mma_commit_elect(&B.q_free[q.at]);
-      q.next(p.qs);
+      q.next(C::QS);
     }
+    k.next(C::KS);
+    if (it.tiles == 2) k.next(C::KS);
   }
   if (!ok && (threadIdx.x & 31) == 0) {
     B.abort = 1;
@@ -671,14 +608,14 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   static_assert(sizeof(wtile::KeyNotes) == C::KEY_NOTES, "notes");
   notes.raw = reinterpret_cast<wtile::KeyNotes*>(sm + C::OFF_NOTES);
   notes.key = notes.raw + C::RAWS;
-  notes.lse = reinterpret_cast<float*>(notes.key + C::MOST_KS);
+  notes.lse = reinterpret_cast<float*>(notes.key + C::KS);
   notes.last = reinterpret_cast<int*>(notes.lse + C::NS * 128);
   notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::MOST_KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 16);
-    for (int i = 0; i < C::MOST_QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
-    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 16);
+    for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 16);
+    for (int i = 0; i < C::QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
+    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 8);
     for (int m = 0; m < 2; ++m) {
       for (int i = 0; i < 2; ++i) ptx::mbar_init(&B.s_full[m][i], 1), ptx::mbar_init(&B.s_free[m][i], 4);
       ptx::mbar_init(&B.x_full[m], 4), ptx::mbar_init(&B.x_free[m], 4);
@@ -691,6 +628,10 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
     ptx::tmem_alloc(&B.tmem, C::TM_COLS);
     ptx::tmem_relinquish();
   }
+  // rows behind a chunk's box are never copied to: their columns' weights are 2^-inf
+  for (int i = threadIdx.x; i < C::QS * (D / 64) * 128 * 8; i += C::THREADS)
+    if ((i >> 3) % 128 >= p.heads * p.tokens) ptx::st_shared_v4(ptx::smem_u32(sm) + C::OFF_Q + i * 16, 0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
