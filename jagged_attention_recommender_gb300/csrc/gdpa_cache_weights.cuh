@@ -63,7 +63,7 @@ struct WeightCfg {
   static constexpr int SPAN = 4096 / D, TILES = SPAN / kCacheBlock;
   static constexpr int START = 2;  // what a sequence and head's start costs, in steps
   static constexpr int KSTEPS = D / 16;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D == 64 ? 2 : 3;
   static constexpr int TILE = kCacheBlock * D;
   // of a stage: codes, earlier weights, words with scales, pages
   static constexpr int W_AT = 4096, SF_AT = W_AT + SPAN * 4, PAGE_AT = SF_AT + 16, STAGE = PAGE_AT + 16;
@@ -71,7 +71,7 @@ struct WeightCfg {
   static constexpr int ROWS_AT = QFRAG;               // ... and what it knows of their rows
   static constexpr int WARP = STAGES * STAGE + QFRAG + NT * 8 * 16;
   static constexpr int SMEM = WARPS * WARP;
-  static constexpr int CTAS = NT == 1 || (NT == 3 && D == 64) ? 3 : 2;
+  static constexpr int CTAS = D == 64 ? (NT == 6 ? 3 : 4) : NT <= 2 ? 3 : 2;
   static_assert(STAGE % 16 == 0 && WARP % 16 == 0, "16-byte copies");
 };
 
