@@ -63,7 +63,7 @@ struct WeightCfg {
   static constexpr int SPAN = 4096 / D, TILES = SPAN / kCacheBlock;
   static constexpr int START = 2;  // what a sequence and head's start costs, in steps
   static constexpr int KSTEPS = D / 16;
-  static constexpr int STAGES = D == 64 ? 2 : 3;
+  static constexpr int STAGES = 2;
   static constexpr int TILE = kCacheBlock * D;
   // of a stage: codes, earlier weights, words with scales, pages
   static constexpr int W_AT = 4096, SF_AT = W_AT + SPAN * 4, PAGE_AT = SF_AT + 16, STAGE = PAGE_AT + 16;
@@ -366,42 +366,52 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
       const int k0 = key0 + half * 2 * kCacheBlock;
       float sum[2][2] = {};
       if (seen) {
-        uint32_t a[2][KS][4];
-        float sk[2];
+        float sk[2];  // the tiles' scales
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const int tile = 2 * half + n;
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint32_t ka[4], kc[4];
-            const int c = D == 128 ? 2 * t + j : t;
-            lds128(st + tile * C::TILE + tile_at<D>(g, c), ka);
-            lds128(st + tile * C::TILE + tile_at<D>(g + 8, c), kc);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              a[n][4 * j + w][0] = codes_lo(ka[w]), a[n][4 * j + w][2] = codes_hi(ka[w]);
-              a[n][4 * j + w][1] = codes_lo(kc[w]), a[n][4 * j + w][3] = codes_hi(kc[w]);
-            }
-          }
           // the scale's place in its word: the low bits of its index
-          const int pg = one ? page[0] : page[tile], key = k0 + n * kCacheBlock;
-          const uint32_t block = (static_cast<uint32_t>(pg) * p.cache.H + now.h << (p.cache.lp - 4)) + ((key & pmask) >> 4);
+          const int tile = 2 * half + n, pg = one ? page[0] : page[tile], key = k0 + n * kCacheBlock;
+          const uint32_t block = ((static_cast<uint32_t>(pg) * p.cache.H + now.h) << (p.cache.lp - 4)) + ((key & pmask) >> 4);
           sk[n] = sf_value((one ? sf_word[0] : sf_word[tile]) >> (block & 3) * 8 & 0xff);
+        }
+        // 16-byte chunk j of this lane's two keys of tile n, as the fragments of four k-steps
+        auto keys_of = [&](int n, int j, uint32_t (&a)[4][4]) {
+          uint32_t ka[4], kc[4];
+          const int c = D == 128 ? 2 * t + j : t;
+          lds128(st + (2 * half + n) * C::TILE + tile_at<D>(g, c), ka);
+          lds128(st + (2 * half + n) * C::TILE + tile_at<D>(g + 8, c), kc);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            a[w][0] = codes_lo(ka[w]), a[w][2] = codes_hi(ka[w]);
+            a[w][1] = codes_lo(kc[w]), a[w][3] = codes_hi(kc[w]);
+          }
+        };
+        // (a single row tile takes the fragments as they are made; several keep them)
+        uint32_t a[NT == 1 ? 1 : 2][NT == 1 ? 1 : D / 64][4][4];
+        if constexpr (NT > 1) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) keys_of(n, j, a[n][j]);
         }
         auto tile = [&](auto edge_tag, int nt) {
           constexpr bool EDGE = decltype(edge_tag)::value;
           float x[2][4];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint2 q = qfrag[(nt * KS + k) * 32 + lane];
+          for (int j = 0; j < D / 64; ++j)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              if (k == 0)
-                mma_f16_new(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
-              else
-                mma_f16(x[n], a[n][k][0], a[n][k][1], a[n][k][2], a[n][k][3], q.x, q.y);
+              uint32_t (&f)[4][4] = a[NT == 1 ? 0 : n][NT == 1 ? 0 : j];
+              if constexpr (NT == 1) keys_of(n, j, f);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint2 q = qfrag[(nt * KS + 4 * j + w) * 32 + lane];
+                if (j == 0 && w == 0)
+                  mma_f16_new(x[n], f[w][0], f[w][1], f[w][2], f[w][3], q.x, q.y);
+                else
+                  mma_f16(x[n], f[w][0], f[w][1], f[w][2], f[w][3], q.x, q.y);
+              }
             }
-          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const WeightRow wr = row_of[nt * 8 + 2 * t + c];
@@ -424,8 +434,6 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
           if (edge) {
 #pragma unroll 1
             for (int nt = 0; nt * 8 < count; ++nt) tile(std::true_type{}, nt);
-          } else if (NT == 1) {
-            tile(std::false_type{}, 0);
           } else {
 #pragma unroll 2
             for (int nt = 0; nt * 8 < count; ++nt) tile(std::false_type{}, nt);
