@@ -45,7 +45,7 @@ struct WeightTileCfg {
   static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
   static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
   static constexpr int KEY_NOTES = 2048;           // of each key: its row, its scale, its earlier weight
-  static constexpr int USED = OFF_NOTES + (RAWS + KS) * KEY_NOTES + NS * 1024 + 1024;
+  static constexpr int USED = OFF_NOTES + (RAWS + KS) * KEY_NOTES + NS * 1024 + 1024 + NS * 16;
   static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;  // one CTA an SM (all of its TMEM)
   static constexpr uint32_t TM_COLS = 512;         // S of two tiles, two buffers each
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -78,6 +78,7 @@ struct Notes {
   float* lse;     // [NS][128]: minus each column's logsumexp, in units of log2
   int* last;      // [NS][128]: the last key that each column sees, -1 for none
   float* half;    // [2][128]: sums on their way from one warpgroup to the other
+  int4* chunk;    // [NS]: its columns' blocks of 32, whether all are rows, the last keys of its first and last row
 };
 
 // An item: its first key, its tiles, and the tokens [lo, hi) whose rows see any of
@@ -227,12 +228,12 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
       if (mine) {
         s_turn ^= 1;
         ptx::tc_fence_after();
-        const int columns = chunk_columns(p, it, c), blocks = (columns + 31) >> 5;
+        const int4 chunk = notes.chunk[stage];
+        const int blocks = chunk.x;
         const float* lse = notes.lse + stage * 128;
         const int* last = notes.last + stage * 128;
         // whether all columns are rows that see all of these keys (tokens, and so last keys, ascend)
-        const int end0 = last[0], end1 = last[columns - 1];
-        const bool all = columns == p.heads * p.tokens && end0 >= k_last && (w.window == 0 || end1 - w.window < k0);
+        const bool all = chunk.y && chunk.z >= k_last && (w.window == 0 || chunk.w - w.window < k0);
         auto tile = [&](auto all_tag) {
 #pragma unroll 1
           for (int i = 0; i < blocks; ++i) {
@@ -525,6 +526,11 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
     if (!__all_sync(0xffffffffu, fine)) return false;
     reinterpret_cast<float4*>(notes.lse + n.at * 128)[lane] = make_float4(-lse[0], -lse[1], -lse[2], -lse[3]);
     reinterpret_cast<int4*>(notes.last + n.at * 128)[lane] = make_int4(last[0], last[1], last[2], last[3]);
+    if (lane == 0) {
+      const int columns = chunk_columns(p, walk.it, c), first = w.causal ? walk.s.len - walk.s.n + tok0 : walk.s.len - 1;
+      notes.chunk[n.at] = make_int4((columns + 31) >> 5, columns == p.heads * p.tokens, first,
+                                    w.causal ? first + min(p.tokens, walk.it.hi - tok0) - 1 : first);
+    }
     ptx::mbar_arrive(&B.n_full[n.at]);
     n.next(C::NS);
     return true;
@@ -611,6 +617,7 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   notes.lse = reinterpret_cast<float*>(notes.key + C::KS);
   notes.last = reinterpret_cast<int*>(notes.lse + C::NS * 128);
   notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
+  notes.chunk = reinterpret_cast<int4*>(notes.half + 256);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 16);
