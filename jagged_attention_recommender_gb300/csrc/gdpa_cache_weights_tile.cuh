@@ -41,8 +41,8 @@ struct WeightTileCfg {
   static constexpr int D = D_, THREADS = 736, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
-  static constexpr int KS = 2, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
-  static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
+  static constexpr int KS = 3, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
+  static constexpr int RAW = 128 * D, RAWS = D == 128 ? 1 : 3;  // codes of a tile, on their way
   static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
   static constexpr int KEY_NOTES = 2048;           // of each key: its row, its scale, its earlier weight
   static constexpr int USED = OFF_NOTES + (RAWS + KS) * KEY_NOTES + NS * 1024 + 1024 + NS * 16;
@@ -54,7 +54,7 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
+  uint64_t k_full[3], k_free[3], q_full[3], q_free[3], n_full[4], n_free[4];
   uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
