@@ -81,7 +81,7 @@ gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Devic
   if (rows <= 8) return launch_split<D, 1>(p, dev, s);
   if (rows <= 16) return launch_split<D, 2>(p, dev, s);
   if (rows <= 32) return launch_split<D, 4>(p, dev, s);
-  if (rows <= 48) return launch_split<D, 6>(p, dev, s);
+  if (rows <= 64) return launch_split<D, 8>(p, dev, s);
   if (p.G <= 128 && max_q <= 128 / p.G) return launch_pass<D>(p, dev, s);
   return launch_tile<D>(p, dev, s);
 }

@@ -71,7 +71,7 @@ struct WeightCfg {
   static constexpr int ROWS_AT = QFRAG;               // ... and what it knows of their rows
   static constexpr int WARP = STAGES * STAGE + QFRAG + NT * 8 * 16;
   static constexpr int SMEM = WARPS * WARP;
-  static constexpr int CTAS = D == 64 ? (NT == 6 ? 3 : 4) : NT <= 2 ? 3 : 2;
+  static constexpr int CTAS = D == 64 ? (NT <= 4 ? 4 : NT == 8 ? 3 : 2) : NT <= 2 ? 3 : NT <= 8 ? 2 : 1;
   static_assert(STAGE % 16 == 0 && WARP % 16 == 0, "16-byte copies");
 };
 

@@ -71,4 +71,56 @@ struct StageRing {
   }
 };
 
+// What goes with a tile of 128 keys, by blocks of 16: the first one's row of the
+// cache (-1: no page), the word with its scale's code; and earlier weights.
+struct alignas(16) KeyNotes {
+  int64_t row[8];
+  uint32_t word[8];
+  float old[128];
+  __device__ __forceinline__ float scale(int key) const {  // its block's
+    return sf_value(word[key >> 4] >> static_cast<int>((row[key >> 4] >> 4) & 3) * 8 & 0xff);
+  }
+};
+
+// Brings a tile's notes, by a whole warp; lane i below 8 knows its i-th block's
+// row.  `full` takes 33 arrivals.
+__device__ __forceinline__ void bring_notes(const CacheWeightsParams& w, KeyNotes& note, uint64_t* full, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
+  if (lane < 8) {
+    note.row[lane] = row;
+    if (row >= 0) {
+      const int64_t word = (row >> 4) & ~(int64_t)3;
+      split::cp_async4(ptx::smem_u32(&note.word[lane]), w.cache.k_sf + word,
+                       static_cast<int>(min((int64_t)4, sf_bytes - word)));
+    }
+  }
+  const int64_t at = __shfl_sync(0xffffffffu, row, lane >> 2);
+  if (w.w_in && at >= 0) split::cp_async16(ptx::smem_u32(&note.old[lane * 4]), w.w_in + at + (lane & 3) * 4, 16);
+  ptx::copies_arrive(full);
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(full);
+}
+
+// Brings a tile's codes to `raw`, by a whole warp.  (A block that is not there
+// keeps what the stage held: no other key's score depends on it.)
+template <int D>
+__device__ __forceinline__ void bring_codes(const CacheWeightsParams& w, uint32_t raw, uint64_t* full, int64_t row) {
+  const int lane = threadIdx.x & 31, blocks = __popc(__ballot_sync(0xffffffffu, row >= 0));
+  if (lane == 0) ptx::mbar_arrive_expect_tx(full, blocks * 16 * D);
+  __syncwarp();
+  if (row >= 0) ptx::bulk_load(raw + lane * 16 * D, w.cache.k + row * D, 16 * D, full);
+}
+
+// Waits for the last turns of `stages` stages of which `count` were filled, `at`
+// being the next one's place: no copy may land behind a CTA's end.
+__device__ __forceinline__ void drain_stages(uint64_t* full, StageRing at, uint32_t stages, uint32_t count) {
+  for (uint32_t i = 0; i < min(count, stages); ++i) {
+    const int never = 0;
+    if (at.at == 0) at.turn ^= 1;
+    at.at = (at.at == 0 ? stages : at.at) - 1;
+    ptx::mbar_wait(&full[at.at], at.turn, 100000000ull, &never);
+  }
+}
+
 }  // namespace gdpa

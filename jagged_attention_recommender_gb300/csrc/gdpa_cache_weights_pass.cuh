@@ -60,14 +60,6 @@ struct Bars {
   int abort;  // a wait has given up
 };
 
-// What goes with a tile of keys, by blocks of 16: the first one's row of the
-// cache (-1: no page), the word with its scale's code; and earlier weights.
-struct alignas(16) KeyNotes {
-  int64_t row[8];
-  uint32_t word[8];
-  float old[128];
-};
-
 // What goes with a column: its factor and minus its logsumexp, both in units
 // of log2, and the last key that it sees.
 struct ColumnNotes {
@@ -243,7 +235,7 @@ __device__ void run_sums(const WeightPassParams& p, const Run& run, Bars& B, con
         if (!ok) break;
         const KeyNotes& note = keys[stage];
         row = note.row[key_in >> 4];
-        factor = sf_value(note.word[key_in >> 4] >> static_cast<int>((row >> 4) & 3) * 8 & 0xff);
+        factor = note.scale(key_in);
         if (w.w_in && s.len - s.n - k0 > key_in) old = w.decay * note.old[key_in];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&B.n_free[stage]);
@@ -462,8 +454,7 @@ __device__ void run_copies(const WeightPassParams& p, const Run& run, uint8_t* s
   const int lane = threadIdx.x & 31;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
-  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW + lane * 16 * D;
+  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW;
   StageRing in, n;
   uint32_t count = 0;
   bool ok = true;
@@ -491,30 +482,13 @@ __device__ void run_copies(const WeightPassParams& p, const Run& run, uint8_t* s
     ok = ptx::mbar_wait(&B.n_free[n.at], n.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    KeyNotes& note = keys[n.at];
-    if (lane < 8) {
-      note.row[lane] = row;
-      if (row >= 0) {
-        const int64_t word = (row >> 4) & ~(int64_t)3;
-        split::cp_async4(ptx::smem_u32(&note.word[lane]), w.cache.k_sf + word,
-                         static_cast<int>(min((int64_t)4, sf_bytes - word)));
-      }
-    }
-    const int64_t at = __shfl_sync(0xffffffffu, row, lane >> 2);
-    if (w.w_in && at >= 0) split::cp_async16(ptx::smem_u32(&note.old[lane * 4]), w.w_in + at + (lane & 3) * 4, 16);
-    ptx::copies_arrive(&B.n_full[n.at]);
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&B.n_full[n.at]);
+    bring_notes(w, keys[n.at], &B.n_full[n.at], row);
     n.next(C::NS);
     if (!seen) continue;
     ok = ptx::mbar_wait(&B.raw_free[in.at], in.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    const int blocks = __popc(__ballot_sync(0xffffffffu, row >= 0));
-    if (lane == 0) ptx::mbar_arrive_expect_tx(&B.raw_full[in.at], blocks * 16 * D);
-    __syncwarp();
-    // (a block that is not there keeps what the stage held: no other key's score depends on it)
-    if (row >= 0) ptx::bulk_load(raw + in.at * C::RAW, w.cache.k + row * D, 16 * D, &B.raw_full[in.at]);
+    bring_codes<D>(w, raw + in.at * C::RAW, &B.raw_full[in.at], row);
     in.next(C::RAWS);
     ++count;
   }
@@ -525,12 +499,7 @@ __device__ void run_copies(const WeightPassParams& p, const Run& run, uint8_t* s
   // no copy may land behind the CTA's end: this thread's own, and the last turn of every stage
   split::cp_commit();
   split::cp_wait<0>();
-  for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(C::RAWS)); ++i) {
-    const int never = 0;
-    if (in.at == 0) in.turn ^= 1;
-    in.at = (in.at == 0 ? C::RAWS : in.at) - 1;
-    ptx::mbar_wait(&B.raw_full[in.at], in.turn, 100000000ull, &never);
-  }
+  drain_stages(B.raw_full, in, C::RAWS, count);
 }
 
 template <int D>
@@ -605,8 +574,8 @@ __global__ void __launch_bounds__(WeightPassCfg<D>::THREADS, 1)
   extern __shared__ uint8_t raw[];
   __shared__ wpass::Bars B;
   uint8_t* const sm = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
-  static_assert(sizeof(wpass::KeyNotes) <= C::KEY_NOTES && sizeof(wpass::ColumnNotes) == C::COLUMN_NOTES, "notes");
-  wpass::KeyNotes* const keys = reinterpret_cast<wpass::KeyNotes*>(sm + C::OFF_NOTES);
+  static_assert(sizeof(KeyNotes) <= C::KEY_NOTES && sizeof(wpass::ColumnNotes) == C::COLUMN_NOTES, "notes");
+  KeyNotes* const keys = reinterpret_cast<KeyNotes*>(sm + C::OFF_NOTES);
   wpass::ColumnNotes* const columns = reinterpret_cast<wpass::ColumnNotes*>(sm + C::OFF_NOTES + C::NS * C::KEY_NOTES);
   __shared__ wpass::Run run;
   const int warp = threadIdx.x >> 5;

@@ -15,12 +15,11 @@
 // the grid.  Roles:
 //   warps 0-15   the sums, a key a thread: warpgroups 0 and 2 those of the item's
 //                first 128 keys, 1 and 3 of its second, each every other chunk
-//   warps 16-19  bring codes, scales and earlier weights by their own
-//                asynchronous copies, RAWS tiles ahead, and convert K (128-byte
-//                swizzle)
+//   warps 16-19  convert K (128-byte swizzle)
 //   warp 20      issues the MMAs
 //   warp 21      brings the queries by TMA
 //   warp 22      notes their logsumexp and the last keys they see
+//   warp 23      finds pages and brings codes, scales and earlier weights
 #pragma once
 
 #include "gdpa_cache_append.cuh"
@@ -38,14 +37,13 @@ struct WeightTileParams {
 
 template <int D_>
 struct WeightTileCfg {
-  static constexpr int D = D_, THREADS = 736, COLS = 128;
+  static constexpr int D = D_, THREADS = 768, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
-  static constexpr int KS = 3, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
-  static constexpr int RAW = 128 * D, RAWS = D == 128 ? 1 : 3;  // codes of a tile, on their way
+  static constexpr int KS = 2, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
+  static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
   static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
-  static constexpr int KEY_NOTES = 2048;           // of each key: its row, its scale, its earlier weight
-  static constexpr int USED = OFF_NOTES + (RAWS + KS) * KEY_NOTES + NS * 1024 + 1024 + NS * 16;
+  static constexpr int USED = OFF_NOTES + NS * 640 + NS * 1024 + 1024 + NS * 16;
   static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;  // one CTA an SM (all of its TMEM)
   static constexpr uint32_t TM_COLS = 512;         // S of two tiles, two buffers each
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -54,27 +52,14 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t k_full[3], k_free[3], q_full[3], q_free[3], n_full[4], n_free[4];
+  uint64_t raw_full[6], raw_free[6], key_full[4], key_free[4], k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
   uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
 };
 
-// What goes with a tile of keys: where each one's weight is (-1: nowhere), and
-//   on its way (word, old)  the word with its scale's code, its earlier weight
-//   converted (factor, old) the factor of its scores in units of log2, the weight
-struct KeyNotes {
-  int64_t row[128];
-  union {
-    uint32_t word[128];
-    float factor[128];
-  };
-  float old[128];
-};
-
 struct Notes {
-  KeyNotes* raw;  // [RAWS]
-  KeyNotes* key;  // [KS]
+  KeyNotes* key;  // [NS]: of tiles of keys
   float* lse;     // [NS][128]: minus each column's logsumexp, in units of log2
   int* last;      // [NS][128]: the last key that each column sees, -1 for none
   float* half;    // [2][128]: sums on their way from one warpgroup to the other
@@ -176,7 +161,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
   const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * 256 + turn * 128;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  StageRing k, n;                      // of tiles of K, of this warpgroup's notes (two of the four stages)
+  StageRing k, n;                      // of tiles' notes, of this warpgroup's notes (two of the four stages)
   uint32_t ci = 0, s_turn = 0, xi = 0;  // chunks, turns of S's buffer, and sums in two halves, so far
   bool ok = true;
   Walk walk;
@@ -196,23 +181,24 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
       __syncwarp();
       continue;
     }
-    // (every warp sees every tile arrive: one that skipped some could take a
-    // later turn of a stage for the one it waits for)
+    // (every warp sees every tile's notes arrive: one that skipped some could
+    // take a later turn of a stage for the one it waits for)
     int64_t row = -1;
     float old = 0.0f, factor = 0.0f;
 #pragma unroll 1
     for (int j = 0; j < it.tiles; ++j) {
-      ok = ptx::mbar_wait(&B.k_full[k.at], k.turn, p.limit, abort);
+      ok = ptx::mbar_wait(&B.key_full[k.at], k.turn, p.limit, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (j == m) {
-        row = notes.key[k.at].row[key_in];
-        factor = notes.key[k.at].factor[key_in];
-        old = notes.key[k.at].old[key_in];
+        const KeyNotes& note = notes.key[k.at];
+        row = note.row[key_in >> 4];
+        factor = note.scale(key_in) * w.scale2;
+        if (w.w_in && s.len - s.n - k0 > key_in) old = w.decay * note.old[key_in];
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&B.k_free[k.at]);
-      k.next(C::KS);
+      if (lane == 0) ptx::mbar_arrive(&B.key_free[k.at]);
+      k.next(C::NS);
     }
     if (!ok) break;
     const uint64_t f2 = ptx::f2_splat(factor);
@@ -304,7 +290,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
       }
       ++xi;
     }
-    if (writes && row >= 0) w.w[row] = old + total;
+    if (writes && row >= 0 && s.len - k0 > key_in) w.w[row + (key_in & 15)] = old + total;
     __syncwarp();
   }
   if (!ok && lane == 0) {
@@ -337,20 +323,15 @@ struct TileWalk {
 };
 
 template <int D>
-__device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
+__device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
   using C = WeightTileCfg<D>;
-  constexpr int CPR = D / 16, ROWS = 128 / CPR, N = 128 / ROWS;  // chunks of a key; keys of a pass; passes
   const CacheWeightsParams& w = p.w;
-  const int tid = threadIdx.x - 512, lane = tid & 31;
+  const int lane = threadIdx.x & 31;
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
-  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
-  const int r0 = tid / CPR, c = tid % CPR;  // its row in a pass, and 16 coordinates
-  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW + tid * 16;  // a thread converts what it copied
-  // 16-byte chunks 2c and 2c + 1 of a row, 64 columns a sub-tile
-  const uint32_t base = ptx::smem_u32(sm) + (c >> 2) * C::SUB;
-  uint32_t ri = 0, ki = 0;  // tiles brought, and converted
-  StageRing in, out, k;          // of codes brought, codes converted, tiles of K
+  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW;
+  StageRing in, n;
+  uint32_t count = 0;
   bool ok = true;
   TileWalk tiles;
   bool more = tiles.begin(p);
@@ -362,77 +343,75 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   };
   int page = more ? page_of() : -1;  // (looked up a tile ahead)
   __syncwarp();
-  while (true) {
-    while (more && ri - ki < C::RAWS) {
-      const Walk& at = tiles.walk;
-      const int k0 = tiles.walk.it.k0 + tiles.m * 128, valid = at.s.len - k0;
-      const uint32_t rs = in.at;
-      KeyNotes& note = notes.raw[rs];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {  // (what is not there keeps what it held: no other key's score depends on it)
-        const int r = r0 + i * ROWS, pg = __shfl_sync(0xffffffffu, page, r >> 4);
-        if (pg >= 0)
-          split::cp_async16(raw + rs * C::RAW + i * 2048,
-                            w.cache.k + cache_row(w.cache, pg, at.h, (k0 + r) & pmask) * D + c * 16, 16);
-      }
-      const int pg = __shfl_sync(0xffffffffu, page, tid >> 4);
-      const int64_t row = cache_row(w.cache, max(pg, 0), at.h, (k0 + tid) & pmask);
-      note.row[tid] = pg >= 0 && tid < valid ? row : -1;
-      if (pg >= 0) {
-        const int64_t word = (row >> 4) & ~(int64_t)3;
-        split::cp_async4(ptx::smem_u32(&note.word[tid]), w.cache.k_sf + word,
-                         static_cast<int>(min((int64_t)4, sf_bytes - word)));
-      }
-      // the rows' own keys have no earlier weight
-      if (pg >= 0 && w.w_in && tid < valid && k0 + tid < at.s.len - at.s.n)
-        split::cp_async4(ptx::smem_u32(&note.old[tid]), w.w_in + row, 4);
-      else
-        note.old[tid] = 0.0f;
-      split::cp_commit();
-      ++ri;
-      in.next(C::RAWS);
-      more = tiles.next(p);
-      if (more) page = page_of();
-      __syncwarp();
-    }
-    if (ri == ki) break;
-    const uint32_t ks = k.at, rs = out.at;
-    ok = ptx::mbar_wait_idle(&B.k_free[ks], k.turn ^ 1, p.limit, abort);
+  while (more) {
+    const int k0 = tiles.walk.it.k0 + tiles.m * 128;
+    const int64_t row = page >= 0 ? cache_row(w.cache, page, tiles.walk.h, (k0 + lane * 16) & pmask) : -1;
+    more = tiles.next(p);
+    page = more ? page_of() : -1;
+    __syncwarp();
+    ok = ptx::mbar_wait_idle(&B.key_free[n.at], n.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    if (more)
-      split::cp_wait<C::RAWS - 1>();
-    else
-      split::cp_wait<0>();
-    const KeyNotes& from = notes.raw[rs];
-    KeyNotes& to = notes.key[ks];
-    const int64_t row = from.row[tid];
-    to.row[tid] = row;
-    to.factor[tid] = sf_value(from.word[tid] >> static_cast<int>((row >> 4) & 3) * 8 & 0xff) * w.scale2;
-    to.old[tid] = w.decay * from.old[tid];
+    bring_notes(w, notes.key[n.at], &B.key_full[n.at], row);
+    n.next(C::NS);
+    ok = ptx::mbar_wait_idle(&B.raw_free[in.at], in.turn ^ 1, p.limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    bring_codes<D>(w, raw + in.at * C::RAW, &B.raw_full[in.at], row);
+    in.next(C::RAWS);
+    ++count;
+  }
+  if (!ok && lane == 0) {
+    B.abort = 1;
+    atomicOr(w.batch.status, kStatusProducer);
+  }
+  // no copy may land behind the CTA's end: this thread's own, and the last turn of every stage
+  split::cp_commit();
+  split::cp_wait<0>();
+  drain_stages(B.raw_full, in, C::RAWS, count);
+}
+
+template <int D>
+__device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B) {
+  using C = WeightTileCfg<D>;
+  constexpr int CPR = D / 16, ROWS = 128 / CPR, N = 128 / ROWS;  // chunks of a key; keys of a pass; passes
+  const int tid = threadIdx.x - 512, lane = tid & 31;
+  const volatile int* abort = &B.abort;
+  const int r0 = tid / CPR, c = tid % CPR;  // its row in a pass, and 16 coordinates
+  const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW + tid * 16;
+  // 16-byte chunks 2c and 2c + 1 of a row, 64 columns a sub-tile (the rows of a thread agree modulo 8)
+  const uint32_t j = 2 * c & 7, base = ptx::smem_u32(sm) + (c >> 2) * C::SUB + r0 * 128;
+  const uint32_t to0 = base + ((j ^ (r0 & 7)) << 4), to1 = base + (((j + 1) ^ (r0 & 7)) << 4);
+  StageRing in, k;
+  bool ok = true;
+  TileWalk tiles;
+  for (bool more = tiles.begin(p); more; more = tiles.next(p)) {
+    ok = ptx::mbar_wait_idle(&B.raw_full[in.at], in.turn, p.limit, abort);
+    ok = ok && ptx::mbar_wait_idle(&B.k_free[k.at], k.turn ^ 1, p.limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = r0 + i * ROWS;
-      const uint32_t at = base + ks * C::TILE + r * 128, j = 2 * c & 7;
+      const uint32_t at = k.at * C::TILE + i * ROWS * 128;
       uint32_t x[4], a[8];
-      split::lds128(raw + rs * C::RAW + i * 2048, x);
+      split::lds128(raw + in.at * C::RAW + i * 2048, x);
       codes_bf16(x[0], a[0], a[1]);
       codes_bf16(x[1], a[2], a[3]);
       codes_bf16(x[2], a[4], a[5]);
       codes_bf16(x[3], a[6], a[7]);
-      ptx::st_shared_v4(at + ((j ^ (r & 7)) << 4), a[0], a[1], a[2], a[3]);
-      ptx::st_shared_v4(at + (((j + 1) ^ (r & 7)) << 4), a[4], a[5], a[6], a[7]);
+      ptx::st_shared_v4(to0 + at, a[0], a[1], a[2], a[3]);
+      ptx::st_shared_v4(to1 + at, a[4], a[5], a[6], a[7]);
     }
     ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(&B.k_full[ks]);
-    ++ki;
+    ptx::mbar_arrive(&B.k_full[k.at]);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&B.raw_free[in.at]);
+    in.next(C::RAWS);
     k.next(C::KS);
-    out.next(C::RAWS);
   }
-  split::cp_wait<0>();
   if (!ok && lane == 0) {
     B.abort = 1;
-    atomicOr(w.batch.status, kStatusProducer);
+    atomicOr(p.w.batch.status, kStatusProducer);
   }
 }
 
@@ -484,13 +463,7 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
     B.abort = 1;
     atomicOr(p.w.batch.status, kStatusProducer);
   }
-  // no copy may land behind the CTA's end: the last turn of every stage
-  for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(C::QS)); ++i) {
-    const int never = 0;
-    if (q.at == 0) q.turn ^= 1;
-    q.at = (q.at == 0 ? C::QS : q.at) - 1;
-    ptx::mbar_wait(&B.q_full[q.at], q.turn, 100000000ull, &never);
-  }
+  drain_stages(B.q_full, q, C::QS, count);
 }
 
 template <int D>
@@ -611,16 +584,17 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   __shared__ wtile::Bars B;
   uint8_t* const sm = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   wtile::Notes notes;
-  static_assert(sizeof(wtile::KeyNotes) == C::KEY_NOTES, "notes");
-  notes.raw = reinterpret_cast<wtile::KeyNotes*>(sm + C::OFF_NOTES);
-  notes.key = notes.raw + C::RAWS;
-  notes.lse = reinterpret_cast<float*>(notes.key + C::KS);
+  static_assert(sizeof(KeyNotes) <= 640, "notes");
+  notes.key = reinterpret_cast<KeyNotes*>(sm + C::OFF_NOTES);
+  notes.lse = reinterpret_cast<float*>(sm + C::OFF_NOTES + C::NS * 640);
   notes.last = reinterpret_cast<int*>(notes.lse + C::NS * 128);
   notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
   notes.chunk = reinterpret_cast<int4*>(notes.half + 256);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1 + 16);
+    for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1);
+    for (int i = 0; i < C::RAWS; ++i) ptx::mbar_init(&B.raw_full[i], 1), ptx::mbar_init(&B.raw_free[i], 4);
+    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.key_full[i], 1 + 32), ptx::mbar_init(&B.key_free[i], 16);
     for (int i = 0; i < C::QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
     for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 8);
     for (int m = 0; m < 2; ++m) {
@@ -646,13 +620,15 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   if (warp < 16)
     wtile::run_sums<D>(p, B, notes, tmem);
   else if (warp < 20)
-    wtile::run_convert<D>(p, sm, B, notes);
+    wtile::run_convert<D>(p, sm, B);
   else if (warp == 20)
     wtile::run_mma<D>(p, sm, B, tmem);
   else if (warp == 21)
     wtile::run_queries<D>(p, sm, B);
-  else
+  else if (warp == 22)
     wtile::run_notes<D>(p, B, notes);
+  else
+    wtile::run_copies<D>(p, sm, B, notes);
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
