@@ -20,6 +20,8 @@
 //   warp 21      brings the queries by TMA
 //   warp 22      notes their logsumexp and the last keys they see
 //   warp 23      finds pages and brings codes, scales and earlier weights
+//   warp 24      finds the items, and notes them for the others (each of which
+//                took 4600 cycles an item to find them itself)
 #pragma once
 
 #include "gdpa_cache_append.cuh"
@@ -37,13 +39,13 @@ struct WeightTileParams {
 
 template <int D_>
 struct WeightTileCfg {
-  static constexpr int D = D_, THREADS = 768, COLS = 128;
+  static constexpr int D = D_, THREADS = 800, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
   static constexpr int KS = 2, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
   static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
   static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
-  static constexpr int USED = OFF_NOTES + NS * 640 + NS * 1024 + 1024 + NS * 16;
+  static constexpr int USED = OFF_NOTES + NS * 640 + NS * 1024 + 1024 + NS * 16 + NS * 48;
   static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;  // one CTA an SM (all of its TMEM)
   static constexpr uint32_t TM_COLS = 512;         // S of two tiles, two buffers each
   static_assert(SMEM <= 226 * 1024, "shared memory");
@@ -52,18 +54,19 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t raw_full[6], raw_free[6], key_full[4], key_free[4], k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
+  uint64_t item_full[4], item_free[4], raw_full[6], raw_free[6], key_full[4], key_free[4], k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
   uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
   uint32_t tmem;
   int abort;  // a wait has given up
 };
 
 struct Notes {
+  int4* item;     // [NS][3]: items: first key, tiles, first and last token; chunks (-1: no more), sequence, head; its rows
   KeyNotes* key;  // [NS]: of tiles of keys
   float* lse;     // [NS][128]: minus each column's logsumexp, in units of log2
   int* last;      // [NS][128]: the last key that each column sees, -1 for none
   float* half;    // [2][128]: sums on their way from one warpgroup to the other
-  int4* chunk;    // [NS]: its columns' blocks of 32, whether all are rows, the last keys of its first and last row
+  int4* chunk;    // [NS]: its columns' blocks of 32, how many of them hold rows alone, the last keys of its first and last row
 };
 
 // An item: its first key, its tiles, and the tokens [lo, hi) whose rows see any of
@@ -74,7 +77,7 @@ struct Item {
 
 // The items of one CTA, in order, by a whole warp: its lanes hold 32 sequences, so
 // that the next item is found without a load.
-struct Walk {
+struct Finder {
   int64_t upto;     // items of the sequences up to this lane's
   CacheSeq lane_s;  // this lane's sequence
   int64_t idx;      // the present item, counted from the first lane's sequence
@@ -144,6 +147,56 @@ struct Walk {
   }
 };
 
+__device__ void run_items(const WeightTileParams& p, Bars& B, const Notes& notes) {
+  const int lane = threadIdx.x & 31;
+  const volatile int* abort = &B.abort;
+  StageRing ring;
+  Finder find;
+  bool more = find.begin(p), ok = true;
+  while (true) {
+    ok = ptx::mbar_wait_idle(&B.item_free[ring.at], ring.turn ^ 1, p.limit, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    if (lane == 0) {
+      int4* const to = notes.item + ring.at * 3;
+      to[0] = make_int4(find.it.k0, find.it.tiles, find.it.lo, find.it.hi);
+      to[1] = make_int4(more ? find.it.chunks : -1, find.b, find.h, 0);
+      to[2] = make_int4(find.s.first, find.s.n, find.s.len, find.s.ok);
+      ptx::mbar_arrive(&B.item_full[ring.at]);
+    }
+    __syncwarp();
+    ring.next(4);
+    if (!more) break;
+    more = find.next(p);
+  }
+  if (!ok && lane == 0) {
+    B.abort = 1;
+    atomicOr(p.w.batch.status, kStatusProducer);
+  }
+}
+
+// The items as the other warps read them, every one of them.
+struct Walk {
+  StageRing ring;
+  CacheSeq s;
+  Item it;
+  int b, h;
+  bool ok = true;  // false: a wait has given up
+  __device__ __forceinline__ bool next(const WeightTileParams& p, Bars& B, const Notes& notes) {
+    ok = ptx::mbar_wait(&B.item_full[ring.at], ring.turn, p.limit, &B.abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    const int4 x = notes.item[ring.at * 3], y = notes.item[ring.at * 3 + 1], z = notes.item[ring.at * 3 + 2];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&B.item_free[ring.at]);
+    ring.next(4);
+    it.k0 = x.x, it.tiles = x.y, it.lo = x.z, it.hi = x.w;
+    it.chunks = y.x, b = y.y, h = y.z;
+    s.first = z.x, s.n = z.y, s.len = z.z, s.ok = z.w;
+    return it.chunks >= 0;
+  }
+};
+
 // Columns of chunk c, to the last one that is a row.
 __device__ __forceinline__ int chunk_columns(const WeightTileParams& p, const Item& it, int c) {
   const int part = p.parts == 1 ? 0 : c % p.parts, tok = it.lo + (p.parts == 1 ? c : c / p.parts) * p.tokens;
@@ -165,7 +218,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
   uint32_t ci = 0, s_turn = 0, xi = 0;  // chunks, turns of S's buffer, and sums in two halves, so far
   bool ok = true;
   Walk walk;
-  for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
+  while (ok && walk.next(p, B, notes)) {
     const CacheSeq& s = walk.s;
     const Item it = walk.it;
     const bool mine = m < it.tiles;
@@ -218,11 +271,11 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
         const int blocks = chunk.x;
         const float* lse = notes.lse + stage * 128;
         const int* last = notes.last + stage * 128;
-        // whether all columns are rows that see all of these keys (tokens, and so last keys, ascend)
-        const bool all = chunk.y && chunk.z >= k_last && (w.window == 0 || chunk.w - w.window < k0);
-        auto tile = [&](auto all_tag) {
+        // blocks whose columns are all rows that see all of these keys (tokens, and so last keys, ascend)
+        const int whole = chunk.z >= k_last && (w.window == 0 || chunk.w - w.window < k0) ? chunk.y : 0;
+        auto tile = [&](auto all_tag, int i0, int i1) {
 #pragma unroll 1
-          for (int i = 0; i < blocks; ++i) {
+          for (int i = i0; i < i1; ++i) {
             uint32_t r[32];
             ptx::tmem_read32(from + i * 32, r);
             if (i == blocks - 1) {  // the buffer is read
@@ -255,10 +308,8 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
             }
           }
         };
-        if (all)
-          tile(std::true_type{});
-        else
-          tile(std::false_type{});
+        tile(std::true_type{}, 0, whole);
+        tile(std::false_type{}, whole, blocks);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&B.n_free[stage]);
@@ -293,6 +344,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
     if (writes && row >= 0 && s.len - k0 > key_in) w.w[row + (key_in & 15)] = old + total;
     __syncwarp();
   }
+  ok = ok && walk.ok;
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusActivation);
@@ -310,15 +362,16 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& h
 struct TileWalk {
   Walk walk;
   int m;
-  __device__ __forceinline__ bool settle(const WeightTileParams& p, bool more) {
+  // To the next tile, or the first.
+  __device__ __forceinline__ bool begin(const WeightTileParams& p, Bars& B, const Notes& notes) {
     m = 0;
-    while (more && walk.it.chunks == 0) more = walk.next(p);
-    return more;
+    do
+      if (!walk.next(p, B, notes)) return false;
+    while (walk.it.chunks == 0);
+    return true;
   }
-  __device__ __forceinline__ bool begin(const WeightTileParams& p) { return settle(p, walk.begin(p)); }
-  __device__ __forceinline__ bool next(const WeightTileParams& p) {
-    if (++m < walk.it.tiles) return true;
-    return settle(p, walk.next(p));
+  __device__ __forceinline__ bool next(const WeightTileParams& p, Bars& B, const Notes& notes) {
+    return ++m < walk.it.tiles || begin(p, B, notes);
   }
 };
 
@@ -334,7 +387,7 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
   uint32_t count = 0;
   bool ok = true;
   TileWalk tiles;
-  bool more = tiles.begin(p);
+  bool more = tiles.begin(p, B, notes);
   // lane i: the page of the tile's i-th block of 16 keys
   auto page_of = [&]() {
     const int k0 = tiles.walk.it.k0 + tiles.m * 128;
@@ -346,7 +399,7 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
   while (more) {
     const int k0 = tiles.walk.it.k0 + tiles.m * 128;
     const int64_t row = page >= 0 ? cache_row(w.cache, page, tiles.walk.h, (k0 + lane * 16) & pmask) : -1;
-    more = tiles.next(p);
+    more = tiles.next(p, B, notes);
     page = more ? page_of() : -1;
     __syncwarp();
     ok = ptx::mbar_wait_idle(&B.key_free[n.at], n.turn ^ 1, p.limit, abort);
@@ -361,6 +414,7 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
     in.next(C::RAWS);
     ++count;
   }
+  ok = ok && tiles.walk.ok;
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusProducer);
@@ -372,7 +426,7 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
 }
 
 template <int D>
-__device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B) {
+__device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
   using C = WeightTileCfg<D>;
   constexpr int CPR = D / 16, ROWS = 128 / CPR, N = 128 / ROWS;  // chunks of a key; keys of a pass; passes
   const int tid = threadIdx.x - 512, lane = tid & 31;
@@ -385,7 +439,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B) {
   StageRing in, k;
   bool ok = true;
   TileWalk tiles;
-  for (bool more = tiles.begin(p); more; more = tiles.next(p)) {
+  for (bool more = tiles.begin(p, B, notes); more; more = tiles.next(p, B, notes)) {
     ok = ptx::mbar_wait_idle(&B.raw_full[in.at], in.turn, p.limit, abort);
     ok = ok && ptx::mbar_wait_idle(&B.k_free[k.at], k.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
@@ -409,6 +463,7 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B) {
     in.next(C::RAWS);
     k.next(C::KS);
   }
+  ok = ok && tiles.walk.ok;
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(p.w.batch.status, kStatusProducer);
@@ -417,14 +472,14 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B) {
 
 // f(walk, chunk) for every chunk of this CTA, in order, until it returns false.
 template <class F>
-__device__ __forceinline__ bool each_chunk(const WeightTileParams& p, const F& f) {
+__device__ __forceinline__ bool each_chunk(const WeightTileParams& p, Bars& B, const Notes& notes, const F& f) {
   Walk walk;
-  for (bool more = walk.begin(p); more; more = walk.next(p)) {
+  while (walk.next(p, B, notes)) {
 #pragma unroll 1
     for (int c = 0; c < walk.it.chunks; ++c)
       if (!f(walk, c)) return false;
   }
-  return true;
+  return walk.ok;
 }
 
 // A chunk's first token, and which part of its tokens' heads it is.
@@ -434,7 +489,7 @@ __device__ __forceinline__ void chunk_at(const WeightTileParams& p, const Item& 
 }
 
 template <int D>
-__device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
+__device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes) {
   using C = WeightTileCfg<D>;
   const int lane = threadIdx.x & 31;
   const volatile int* abort = &B.abort;
@@ -442,7 +497,7 @@ __device__ void run_queries(const WeightTileParams& p, uint8_t* sm, Bars& B) {
   const uint32_t to = ptx::smem_u32(sm) + C::OFF_Q;
   StageRing q;
   uint32_t count = 0;
-  const bool ok = each_chunk(p, [&](const Walk& walk, int c) {
+  const bool ok = each_chunk(p, B, notes, [&](const Walk& walk, int c) {
     int tok, part;
     chunk_at(p, walk.it, c, tok, part);
     const bool fine = ptx::mbar_wait_idle(&B.q_free[q.at], q.turn ^ 1, p.limit, abort);
@@ -479,7 +534,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
     head_of[i] = lane * 4 + i - tok_of[i] * p.heads;
   }
   StageRing n;
-  const bool ok = each_chunk(p, [&](const Walk& walk, int c) {
+  const bool ok = each_chunk(p, B, notes, [&](const Walk& walk, int c) {
     int tok0, part;
     chunk_at(p, walk.it, c, tok0, part);
     float lse[4];
@@ -501,7 +556,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
     reinterpret_cast<int4*>(notes.last + n.at * 128)[lane] = make_int4(last[0], last[1], last[2], last[3]);
     if (lane == 0) {
       const int columns = chunk_columns(p, walk.it, c), first = w.causal ? walk.s.len - walk.s.n + tok0 : walk.s.len - 1;
-      notes.chunk[n.at] = make_int4((columns + 31) >> 5, columns == p.heads * p.tokens, first,
+      notes.chunk[n.at] = make_int4((columns + 31) >> 5, columns == p.heads * p.tokens ? (columns + 31) >> 5 : columns >> 5, first,
                                     w.causal ? first + min(p.tokens, walk.it.hi - tok0) - 1 : first);
     }
     ptx::mbar_arrive(&B.n_full[n.at]);
@@ -515,7 +570,7 @@ __device__ void run_notes(const WeightTileParams& p, Bars& B, const Notes& notes
 }
 
 template <int D>
-__device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_t tmem) {
+__device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes, uint32_t tmem) {
   using C = WeightTileCfg<D>;
   const volatile int* abort = &B.abort;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
@@ -524,7 +579,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
   uint32_t ci = 0, s_turns = 0;  // chunks so far; a bit for each buffer of S
   bool ok = true;
   Walk walk;
-  for (bool more = walk.begin(p); more && ok; more = walk.next(p)) {
+  while (ok && walk.next(p, B, notes)) {
     const Item it = walk.it;
     if (it.chunks == 0) continue;
     StageRing second = k;
@@ -563,6 +618,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, uint32_
     k.next(C::KS);
     if (it.tiles == 2) k.next(C::KS);
   }
+  ok = ok && walk.ok;
   if (!ok && (threadIdx.x & 31) == 0) {
     B.abort = 1;
     atomicOr(p.w.batch.status, kStatusMma);
@@ -590,11 +646,13 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   notes.last = reinterpret_cast<int*>(notes.lse + C::NS * 128);
   notes.half = reinterpret_cast<float*>(notes.last + C::NS * 128);
   notes.chunk = reinterpret_cast<int4*>(notes.half + 256);
+  notes.item = notes.chunk + C::NS;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1);
     for (int i = 0; i < C::RAWS; ++i) ptx::mbar_init(&B.raw_full[i], 1), ptx::mbar_init(&B.raw_free[i], 4);
     for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.key_full[i], 1 + 32), ptx::mbar_init(&B.key_free[i], 16);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(&B.item_full[i], 1), ptx::mbar_init(&B.item_free[i], 24);
     for (int i = 0; i < C::QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
     for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 8);
     for (int m = 0; m < 2; ++m) {
@@ -620,15 +678,17 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   if (warp < 16)
     wtile::run_sums<D>(p, B, notes, tmem);
   else if (warp < 20)
-    wtile::run_convert<D>(p, sm, B);
+    wtile::run_convert<D>(p, sm, B, notes);
   else if (warp == 20)
-    wtile::run_mma<D>(p, sm, B, tmem);
+    wtile::run_mma<D>(p, sm, B, notes, tmem);
   else if (warp == 21)
-    wtile::run_queries<D>(p, sm, B);
+    wtile::run_queries<D>(p, sm, B, notes);
   else if (warp == 22)
     wtile::run_notes<D>(p, B, notes);
-  else
+  else if (warp == 23)
     wtile::run_copies<D>(p, sm, B, notes);
+  else
+    wtile::run_items(p, B, notes);
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
