@@ -108,6 +108,11 @@ extern "C" gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const voi
   if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
   if (!lse || !aligned(lse, 4) || !offsets || !kv_lens || !page_table || max_pages == 0) return GDPA_ERR_INVALID_ARG;
   if (!weights || !aligned(weights, 16) || !aligned(weights_in, 16)) return GDPA_ERR_INVALID_ARG;
+  if (weights_in && weights_in != weights) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(weights_in), b = reinterpret_cast<uintptr_t>(weights);
+    const uintptr_t n = (uintptr_t)cache->num_pages * cache->H * cache->page_tokens * sizeof(float);
+    if (a < b + n && b < a + n) return GDPA_ERR_INVALID_ARG;
+  }
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
   CacheWeightsParams p;

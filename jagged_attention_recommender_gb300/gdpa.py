@@ -509,8 +509,9 @@ def gdpa_cache_workspace_size(cache: KvCache, Hq, max_q) -> int:
 
 def _weights_at(where, device, cache, t):
     """The address of one fp32 weight for every slot and head of the cache."""
-    pages, H, tokens = cache.desc.num_pages, cache.H, cache.desc.page_tokens
-    return _at(where, device, _f32, t, pages * H * tokens)
+    if t is None or t.__class__ is int:
+        return t
+    return _at(where, device, _f32, t, cache.desc.num_pages * cache.H * cache.desc.page_tokens)
 
 
 def gdpa_cache_weights(cache: KvCache, q, q_stride, lse, offsets, kv_lens, page_table, T, B, Hq, max_pages, max_q, causal,
@@ -537,7 +538,8 @@ def gdpa_cache_evict(cache: KvCache, weights, kv_lens, page_table, B, max_pages,
         _cache_at(where, d, cache), _weights_at(where, d, cache, weights), _at(where, d, _i32_t, kv_lens, b),
         _table_at(where, d, page_table, b, max_pages), B, max_pages, budget, sink, recent,
         _table_at(where, d, new_table, b, new_max_pages), new_max_pages,
-        _at(where, d, _i32_t, kept, b * cache.H * max(budget, 0)), _at(where, d, _i32_t, new_lens, b),
+        kept if kept is None or kept.__class__ is int else _at(where, d, _i32_t, kept, b * cache.H * max(budget, 0)),
+        _at(where, d, _i32_t, new_lens, b),
         (_raw_stream(d) or None) if stream is None else _stream(stream)), where)
 
 
