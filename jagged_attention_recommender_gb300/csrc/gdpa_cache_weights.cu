@@ -9,7 +9,6 @@
 
 #include "gdpa_cache_host.h"
 #include "gdpa_cache_weights.cuh"
-#include "gdpa_cache_weights_pass.cuh"
 #include "gdpa_cache_weights_tile.cuh"
 
 namespace gdpa {
@@ -55,26 +54,16 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, const Device& dev, cudaSt
   return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
-template <int D>
-gdpa_status_t launch_pass(const CacheWeightsParams& w, const Device& dev, cudaStream_t s) {
-  using C = WeightPassCfg<D>;
-  static std::mutex mu;
-  static bool done[kMaxDevices] = {};
-  const gdpa_status_t st = allow_smem(gdpa_cache_weights_pass_kernel<D>, C::SMEM, 0, dev.id, mu, done);
-  if (st != GDPA_OK) return st;
-  WeightPassParams p;
-  p.w = w;
-  p.heads = std::min(w.G, C::COLS);
-  p.tokens = C::COLS / p.heads;
-  p.parts = (w.G + p.heads - 1) / p.heads;
-  p.limit = bounded_wait_ns();
-  const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp;
-  const int64_t tiles = (int64_t)w.batch.B * w.cache.H * ((keys + 127) / 128);
-  const int ctas = static_cast<int>(std::min<int64_t>(tiles, dev.sms));
-  gdpa_cache_weights_pass_kernel<D><<<ctas, C::THREADS, C::SMEM, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
-}
-
+// The kernel for so many rows of a key head.  Measured (us; 48 sequences of 500
+// to 6001 keys, 4 key heads, D = 128; 128 sequences of 100 to 6000 keys, 8 key
+// heads, D = 64 behind the stroke), with 8, 16, 32, 64 and 128 rows a warp and by
+// the kernel for many:
+//     8 rows      - / 47     - / 50     - / 51     - / 54     - / 72     - / 350
+//    16 rows      -         21 / 57    25 / 58    26 / 61    39 / 79     - / 350
+//    32 rows      -          -         32 / 73    32 / 77    47 / 97     - / 350
+//    64 rows      -          -          -         47 / 112   66 / 142   90 / 348
+//    96 rows      -          -          -          -         93 / 191   92 / 348
+//   128 rows      -          -          -          -        115 / 240   93 / 348
 template <int D>
 gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
   const int64_t rows = (int64_t)max_q * p.G;
@@ -82,7 +71,8 @@ gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Devic
   if (rows <= 16) return launch_split<D, 2>(p, dev, s);
   if (rows <= 32) return launch_split<D, 4>(p, dev, s);
   if (rows <= 64) return launch_split<D, 8>(p, dev, s);
-  if (p.G <= 128 && max_q <= 128 / p.G) return launch_pass<D>(p, dev, s);
+  if constexpr (D == 64)
+    if (rows <= 128) return launch_split<D, 16>(p, dev, s);
   return launch_tile<D>(p, dev, s);
 }
 

@@ -11,7 +11,13 @@
 // gdpa_cache_fwd.cuh (divided by their largest element's power of two), and the
 // scale of a block of 16 tokens that of a whole tile.
 //
-// Bound: memory, D bytes a key and head, and 8 of its weight.
+// Bound: memory, D bytes a key and head, and 8 of its weight, with a warp's own
+// latencies (conversions, fragments, the exponentials' chain) close behind: what
+// hides them is warps, so stages are two and registers few.  Measured: one token of
+// 64 histories of 100 to 8192 keys, 32 query and 8 key heads of 128, 53 us (5.6
+// TB/s, 82 % of a copy's rate); of two histories of 130k keys, 16 and 2 heads, 16 us
+// (4.5 TB/s; 4 us are the start); 32 rows of 128 samples of 100 to 6000 keys, 8 and 8 heads of
+// 64, 73 us (3.1 TB/s, bound by the rows' own work: 47 us with 8 rows).
 //
 // Work split.  A step is 4 KB of codes (32 or 64 keys) of one sequence and head.  The steps of all
 // sequences are counted from the lengths on the device, and every warp takes an
@@ -63,6 +69,7 @@ struct WeightCfg {
   static constexpr int SPAN = 4096 / D, TILES = SPAN / kCacheBlock;
   static constexpr int START = 2;  // what a sequence and head's start costs, in steps
   static constexpr int KSTEPS = D / 16;
+  // (two stages and more CTAs: 32 candidates of 128 samples 74 us so, 94 with three stages and two CTAs an SM)
   static constexpr int STAGES = 2;
   static constexpr int TILE = kCacheBlock * D;
   // of a stage: codes, earlier weights, words with scales, pages
@@ -71,7 +78,8 @@ struct WeightCfg {
   static constexpr int ROWS_AT = QFRAG;               // ... and what it knows of their rows
   static constexpr int WARP = STAGES * STAGE + QFRAG + NT * 8 * 16;
   static constexpr int SMEM = WARPS * WARP;
-  static constexpr int CTAS = D == 64 ? (NT <= 4 ? 4 : NT == 8 ? 3 : 2) : NT <= 2 ? 3 : NT <= 8 ? 2 : 1;
+  // (as registers and shared memory allow; four at D = 128 leave 128 registers: one token of 64 histories 142 us)
+  static constexpr int CTAS = D == 64 ? (NT <= 4 ? 4 : NT == 8 ? 3 : 2) : NT <= 2 ? 3 : 2;
   static_assert(STAGE % 16 == 0 && WARP % 16 == 0, "16-byte copies");
 };
 

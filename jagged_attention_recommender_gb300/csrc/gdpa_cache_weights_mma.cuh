@@ -1,5 +1,5 @@
-// gdpa_cache_weights_mma.cuh -- what the two kernels of the stored keys' weight
-// on the 5th-generation tensor cores share.
+// gdpa_cache_weights_mma.cuh -- pieces of the kernel of the stored keys' weight on
+// the 5th-generation tensor cores.
 #pragma once
 
 #include "gdpa_cache_tile.cuh"
@@ -23,18 +23,9 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 16 or 32 consecutive 32-bit columns of the warp's 32 lanes, there when the call
-// is over: the load and its wait in one, since a wait that names the registers
-// again to keep their uses behind it has the compiler copy them.
-__device__ __forceinline__ void tmem_read16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      " tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
+// 32 consecutive 32-bit columns of the warp's 32 lanes, there when the call is
+// over: the load and its wait in one, since a wait that names the registers
+// again, to keep their uses behind it, has the compiler copy them.
 __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"

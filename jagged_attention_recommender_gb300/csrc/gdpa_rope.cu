@@ -82,6 +82,8 @@ extern "C" gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_
   p.magnitude = magnitude;
   p.sign = inverse ? -magnitude : magnitude;
   for (int i = 0; i < 64; ++i) p.freq[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
+  // A lane takes all heads of its row, or, where rows are too few for four CTAs an
+  // SM, a part of them, four at least (each part computes the angles again).
   const int rows = kRopeThreads / (D / 16);
   const int64_t blocks = (T + rows - 1) / rows;
   const int parts = static_cast<int>(

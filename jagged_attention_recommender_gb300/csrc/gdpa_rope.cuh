@@ -6,7 +6,11 @@
 // The angle is the cache's (gdpa_cache_index.h): p times f as a 64-bit fraction
 // of a turn, modulo 2^64, exact at every position.
 //
-// Bound: memory, 4 bytes an element in and out against about 2 flops.
+// Bound: memory, 4 bytes an element in and out against about 2 flops.  Measured:
+// queries and keys (8 heads of 128) of 267k rows of a training batch, strided in,
+// 171 us (6.4 TB/s, 94 % of a copy's rate); their gradient, strided out, 170; pieces
+// of 36k rows, 9 heads of 64, half rotated, interleaved, 15 us (5.4 TB/s); ten heads of
+// four tokens 2.8 us on the device.
 //
 // Work split.  An item is 16 coordinates of a head, whole pairs of them in two
 // 16-byte chunks (gdpa_cache_append.cuh: ItemAt).  A lane keeps one row and one
