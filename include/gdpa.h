@@ -28,7 +28,10 @@
  * For serving, keys and values of earlier calls stay in a paged cache of e4m3
  * codes (gdpa_cache_t): gdpa_cache_append stores new tokens, rotating them by
  * their position on the way, and gdpa_cache_fwd attends from new tokens to
- * everything that is stored.
+ * everything that is stored.  For long histories gdpa_rope rotates jagged rows by
+ * any positions (and returns the gradient of that), gdpa_cache_weights adds up
+ * the attention weight that stored keys receive, and gdpa_cache_evict cuts
+ * sequences to the tokens that received most.
  *
  * An empty key set gives o_i = 0.  The GELU's tanh is rewritten as a
  * logistic function, gelu(x) = x sigma(2u), whose sigma takes one of two
@@ -656,8 +659,8 @@ gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_t* offsets,
  * Scores, weights and their sums are fp32, summed in an order that does not depend
  * on timing.  Keys that a row does not see take nothing from it, whatever it
  * holds; a NaN in a row or its lse goes to the keys that it sees, one in a key to that key.
- * With few rows (max_q * Hq / H up to 48) queries are rounded as in
- * gdpa_cache_fwd; with more they are taken as they are.
+ * With few rows (max_q * Hq / H up to 64, up to 128 with D = 64) queries are
+ * rounded as in gdpa_cache_fwd; with more they are taken as they are.
  *
  * A page that two sequences of the call share has undefined weights.
  * Asynchronous on `stream`, no allocation, no workspace, no host read of device data (may

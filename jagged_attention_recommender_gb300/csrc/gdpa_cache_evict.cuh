@@ -141,13 +141,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_ch
     __syncthreads();
     // the first digit's histogram while the keys come
 #pragma unroll 4
-    for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+    for (unsigned i = 4 * tid; i < static_cast<unsigned>(n); i += 4 * THREADS) {
       const uint4 k = load4(i);
       if (held) *reinterpret_cast<uint4*>(keys + i) = k;
       atomicAdd(&sh.hist[0][k.x >> 24], 1);
-      if (i + 1 < n) atomicAdd(&sh.hist[0][k.y >> 24], 1);
-      if (i + 2 < n) atomicAdd(&sh.hist[0][k.z >> 24], 1);
-      if (i + 3 < n) atomicAdd(&sh.hist[0][k.w >> 24], 1);
+      if (i + 1 < static_cast<unsigned>(n)) atomicAdd(&sh.hist[0][k.y >> 24], 1);
+      if (i + 2 < static_cast<unsigned>(n)) atomicAdd(&sh.hist[0][k.z >> 24], 1);
+      if (i + 3 < static_cast<unsigned>(n)) atomicAdd(&sh.hist[0][k.w >> 24], 1);
     }
     uint32_t prefix = 0;  // the digits so far of the least key that stays
     int need = keep;      // how many of those that equal them do
@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_ch
           if (((k ^ prefix) & mask) == 0) atomicAdd(&sh.hist[d][k >> shift & 255], 1);
         };
 #pragma unroll 2
-        for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+        for (unsigned i = 4 * tid; i < static_cast<unsigned>(n); i += 4 * THREADS) {
           const uint4 k = keys4(i);
           count(k.x);
-          if (i + 1 < n) count(k.y);
-          if (i + 2 < n) count(k.z);
-          if (i + 3 < n) count(k.w);
+          if (i + 1 < static_cast<unsigned>(n)) count(k.y);
+          if (i + 2 < static_cast<unsigned>(n)) count(k.z);
+          if (i + 3 < static_cast<unsigned>(n)) count(k.w);
         }
       }
       meet();
@@ -211,18 +211,18 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_ch
     }
     // Each warp counts what is above the key and what equals it in its part of
     // the tokens, 4 a lane at a time; then it knows its places.
-    const int part = ((n + WARPS - 1) / WARPS + 127) & ~127, w0 = min(n, part * warp), w1 = min(n, w0 + part);
-    auto flags = [&](int i) {  // of 4 tokens: bits 0-3 above, 16-19 equal
-      if (i >= w1) return 0;
+    const int part = ((n + WARPS - 1) / WARPS + 127) & ~127, w0 = min(n, part * warp), w1 = w0 + min(n - w0, part);
+    auto flags = [&](unsigned i) {  // of 4 tokens: bits 0-3 above, 16-19 equal
+      if (i >= static_cast<unsigned>(w1)) return 0;
       const uint4 k = keys4(i);
       int f = (k.x > prefix) | (k.y > prefix) << 1 | (k.z > prefix) << 2 | (k.w > prefix) << 3 | (k.x == prefix) << 16 |
               (k.y == prefix) << 17 | (k.z == prefix) << 18 | (k.w == prefix) << 19;
-      if (i + 4 > w1) f &= ((1 << (w1 - i)) - 1) * 0x10001;
+      if (i + 4 > static_cast<unsigned>(w1)) f &= ((1 << (w1 - i)) - 1) * 0x10001;
       return f;
     };
     auto counts = [](int f) { return __popc(f & 0xffff) | __popc(f >> 16) << 16; };
     int mine_above = 0, mine_same = 0;
-    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    for (unsigned i = w0 + 4 * lane; i < static_cast<unsigned>(w1); i += 128) {
       const int c = counts(flags(i));
       mine_above += c & 0xffff;
       mine_same += c >> 16;
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_ch
       }
     }
     // `out` counts what is above; of the equal ones the first `need` stay
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-      const int i = i0 + 4 * lane, f = flags(i), mine = counts(f);
+    for (unsigned i0 = w0; i0 < static_cast<unsigned>(w1); i0 += 128) {  // (a length may be as large as 2^31 - 16)
+      const int i = static_cast<int>(i0) + 4 * lane, f = flags(i0 + 4 * lane), mine = counts(f);
       int incl = mine;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
       if (one) {
         if (page_next >= 0) {
           const int64_t row = cache_row(p.cache, page_next, ahead.h, key & pmask);
-          if (key + SPAN > ahead.w.see) {
+          if (key > ahead.w.see - SPAN) {
             const uint8_t* src = p.cache.k + row * D + lane * 16;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
           const int k0 = key + n * kCacheBlock, page = __shfl_sync(0xffffffffu, page_next, n);
           if (page < 0) continue;
           const int64_t row = cache_row(p.cache, page, ahead.h, k0 & pmask);
-          if (k0 + kCacheBlock > ahead.w.see) {
+          if (k0 > ahead.w.see - kCacheBlock) {
             const uint8_t* src = p.cache.k + row * D + lane * 16;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__((WeightCfg<D, NT>::THREADS), (WeightCfg<D, NT>
                  : "=r"(page[0]), "=r"(page[1]), "=r"(page[2]), "=r"(page[3])
                  : "r"(st + C::PAGE_AT));
     lds128(st + C::SF_AT, sf_word);
-    const bool seen = key0 + SPAN > now.w.see;
+    const bool seen = key0 > now.w.see - SPAN;  // (a length may be as large as 2^31 - 16)
     const bool edge = key0 < lo_max || key0 > hi_min - SPAN;
 
 #pragma unroll

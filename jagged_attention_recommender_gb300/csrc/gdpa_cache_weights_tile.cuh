@@ -12,7 +12,7 @@
 // Bound: the chain of hand-overs around the special-function unit, which takes four
 // cycles for a warp's 32 exponentials (measured), 512 for 128 keys and 128 rows, as
 // long as their products at D = 128 do.  Measured: 2321 prompt rows behind 2100 to
-// 8192 keys, 32 query and 8 key heads of 128, 111 us (816 TFLOP/s; the tensor core's
+// 8192 keys, 32 query and 8 key heads of 128, 111 us (865 TFLOP/s; the tensor core's
 // floor is 50); a warp is at its columns for half of that, the rest is waiting and
 // the work around a chunk and an item.
 //
@@ -304,11 +304,11 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
               a = ptx::ex2_approx(a), b = ptx::ex2_approx(b), d = ptx::ex2_approx(d), e = ptx::ex2_approx(e);
               if (!decltype(all_tag)::value) {
                 const int4 end = e4[j];
-                const int width = w.window > 0 ? w.window : 0x7fffffff;  // (key > end - window; none: always)
-                if (key > end.x || key <= end.x - width) a = 0.0f;
-                if (key > end.y || key <= end.y - width) b = 0.0f;
-                if (key > end.z || key <= end.z - width) d = 0.0f;
-                if (key > end.w || key <= end.w - width) e = 0.0f;
+                const int width = w.window > 0 ? w.window : 0x7fffffff;  // (end - key < window; none: always)
+                if (key > end.x || end.x - key >= width) a = 0.0f;
+                if (key > end.y || end.y - key >= width) b = 0.0f;
+                if (key > end.z || end.z - key >= width) d = 0.0f;
+                if (key > end.w || end.w - key >= width) e = 0.0f;
               }
               sum[0] = ptx::f2_add(sum[0], ptx::f2_pack(a, b));
               sum[1] = ptx::f2_add(sum[1], ptx::f2_pack(d, e));

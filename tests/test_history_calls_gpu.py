@@ -200,3 +200,62 @@ def test_rope_of_wide_rows():
     want = hist.rope(rows, [0, 2, 6], None, f, True)
     for got in (y, view):
         assert (np.abs(got.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + rope_bound(rows, 128, f, 0, 1.0, 1) * 1.01).all()
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("window", [0, 100])
+def test_weights_at_the_largest_length(rows, window):
+    """2^31 - 16 keys: all but the last page are one page again and again, whose weights are undefined; the last page's
+    are right."""
+    D, P = 128, 16
+    n = 2 ** 31 - 16
+    x = ref.make(5, 1, 1, D, P, [P], [rows], jitter=0)
+    x.k_sf[:] = 120
+    width = -(-n // P)
+    table = torch.full((1, width), 1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 0
+    codes = torch.zeros((2, 1, P, D), dtype=torch.uint8, device="cuda")
+    codes[0] = cu(x.k_codes[x.table[0, 0]])
+    sf = torch.full((2, 1, P // 16), 120, dtype=torch.uint8, device="cuda")
+    held = n - (width - 1) * P  # tokens of the last page
+    q = ref.bf16(np.random.default_rng(1).standard_normal((rows, 1, D)))
+    lse = np.float32(np.random.default_rng(2).uniform(0, 2, (rows, 1)))
+    w_in = torch.full((2, 1, P), 0.5, dtype=torch.float32, device="cuda")
+    w = torch.full((2, 1, P), SENTINEL, dtype=torch.float32, device="cuda")
+    scale = float(np.float32(D ** -0.5))
+    gdpa.gdpa_cache_weights(gdpa.KvCache(codes, codes, sf, sf), cu_bf16(q), D, cu(lse), cu(np.array([0, rows], np.int32)),
+                            cu(np.array([n], np.int32)), table, rows, 1, 1, width, rows, True, window, scale, 1.0, w_in, w)
+    status()
+    k = ref.e4m3_values(x.k_codes[x.table[0, 0], 0, :held]) * 2.0 ** -7
+    pos, j = n - rows + np.arange(rows)[:, None], (width - 1) * P + np.arange(held)
+    s = scale * q[:, 0] @ k.T
+    p = np.where((j <= pos) & ((j > pos - window) if window else True), np.exp(s - np.float64(lse)), 0)
+    want = p.sum(0) + np.where(j < n - rows, 0.5, 0)
+    got = w[0, 0].double().cpu().numpy()
+    # (a score is off by (D + 8) 2^-23 of sum |q k| / sqrt(D), at most 16 here, its exponential by as much: 2^-12)
+    assert (np.abs(got[:held] - want) <= 2.0 ** -12 * want + 1e-30).all() and (got[held:] == SENTINEL).all()
+
+
+def test_evict_at_the_largest_length():
+    """2^31 - 16 tokens, on one page again and again but for the last: what stays is found there and among the first."""
+    P, n = 16, 2 ** 31 - 16
+    width = -(-n // P)
+    table = torch.full((1, width), 1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 0
+    codes = torch.from_numpy(np.random.default_rng(0).integers(0, 0x7E, (46, 1, P, 64)).astype(np.uint8)).cuda()
+    sf = torch.full((46, 1, P // 16), 120, dtype=torch.uint8, device="cuda")
+    w = torch.zeros((46, 1, P), dtype=torch.float32, device="cuda")
+    held = n - (width - 1) * P
+    w[0, 0, :held] = cu(np.float32(np.random.default_rng(1).uniform(-1, 1, held)))
+    kept = torch.full((1, 1, 700), -1, dtype=torch.int32, device="cuda")
+    lens = torch.empty(1, dtype=torch.int32, device="cuda")
+    gdpa.gdpa_cache_evict(gdpa.KvCache(codes, codes.clone(), sf, sf.clone()), w, cu(np.array([n], np.int32)), table, 1, width, 700,
+                          0, 5, cu(np.arange(2, 46, dtype=np.int32)[None]), 44, kept, lens)
+    status()
+    last = w[0, 0, :held].cpu().numpy()
+    stays = np.flatnonzero((last > 0) | (np.arange(held) >= held - 5))
+    want = np.concatenate([np.arange(700 - len(stays)), (width - 1) * P + stays])
+    assert lens.item() == 700 and np.array_equal(kept.cpu().numpy()[0, 0], want)
+    first = torch.arange(700 - len(stays), device="cuda") % P
+    src = torch.cat([codes[1, 0, first], codes[0, 0, torch.from_numpy(stays).cuda()]])
+    assert torch.equal(codes[2:, 0].reshape(-1, 64)[:700], src)

@@ -212,7 +212,7 @@ def test_weights_of_a_call_sum_to_the_rows(new):
         assert np.abs(s - 3 * new).max() <= 3 * new * 2.0 ** -12
 
 
-@pytest.mark.parametrize("new", [1, 3, 60])
+@pytest.mark.parametrize("new", [1, 3, 60, 200])
 def test_weights_of_empty_rows_and_infinite_statistics(new):
     """A row of logsumexp -inf gives nothing, one of +inf 0; NaN reaches exactly the keys that the row sees."""
     x = ref.make(7, 4, 2, 64, 16, [120, 75], [new, new])
