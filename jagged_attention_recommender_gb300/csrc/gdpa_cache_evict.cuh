@@ -82,7 +82,8 @@ struct ChooseShared {
 // One sequence and head by a cluster of CTAs, each with an equal part of its
 // tokens (a warp with an equal part of those).  `slots`: keys that `keys` holds.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1)
+    gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];
   constexpr int WARPS = THREADS / 32;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1) gdpa_cache_ch
     }
     // Each warp counts what is above the key and what equals it in its part of
     // the tokens, 4 a lane at a time; then it knows its places.
-    const int part = ((n + WARPS - 1) / WARPS + 127) & ~127, w0 = min(n, part * warp), w1 = w0 + min(n - w0, part);
+    const int part = ((n - 1) / WARPS + 128) & ~127, w0 = min(n, part * warp), w1 = w0 + min(n - w0, part);
     auto flags = [&](unsigned i) {  // of 4 tokens: bits 0-3 above, 16-19 equal
       if (i >= static_cast<unsigned>(w1)) return 0;
       const uint4 k = keys4(i);

@@ -259,3 +259,22 @@ def test_evict_at_the_largest_length():
     first = torch.arange(700 - len(stays), device="cuda") % P
     src = torch.cat([codes[1, 0, first], codes[0, 0, torch.from_numpy(stays).cuda()]])
     assert torch.equal(codes[2:, 0].reshape(-1, 64)[:700], src)
+
+
+def test_evict_of_many_heads_at_the_largest_length():
+    """As many heads as take one CTA each: what stays is the last page's alone."""
+    P, H, n = 16, 80, 2 ** 31 - 16
+    width = n // P
+    table = torch.full((1, width), 1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 0
+    codes = torch.from_numpy(np.random.default_rng(0).integers(0, 0x7E, (3, H, P, 64)).astype(np.uint8)).cuda()
+    sf = torch.full((3, H, P // 16), 120, dtype=torch.uint8, device="cuda")
+    w = torch.full((3, H, P), -1.0, dtype=torch.float32, device="cuda")
+    w[0] = 1.0
+    kept = torch.full((1, H, P), -1, dtype=torch.int32, device="cuda")
+    lens = torch.empty(1, dtype=torch.int32, device="cuda")
+    gdpa.gdpa_cache_evict(gdpa.KvCache(codes, codes.clone(), sf, sf.clone()), w, cu(np.array([n], np.int32)), table, 1, width, P, 0, 0,
+                          cu(np.array([[2]], np.int32)), 1, kept, lens)
+    status()
+    assert lens.item() == P and (kept.cpu().numpy()[0] == n - P + np.arange(P)).all()
+    assert torch.equal(codes[2], codes[0]) and torch.equal(w[2], w[0])
