@@ -49,7 +49,8 @@ struct WeightTileCfg {
   static constexpr int D = D_, THREADS = 800, COLS = 128;
   static constexpr int SUB = 128 * 128;            // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int TILE = D / 64 * SUB;
-  static constexpr int KS = 2, QS = 3, NS = 4;     // stages of K, of Q (a chunk's way from L2 is longer than its products), of its notes
+  // stages of K, of Q (a chunk's way from L2 is longer than its products), of notes
+  static constexpr int KS = 2, QS = 3, NS = 4;
   static constexpr int RAW = 128 * D, RAWS = D == 128 ? 3 : 6;  // codes of a tile, on their way
   static constexpr int OFF_Q = KS * TILE, OFF_RAW = OFF_Q + QS * TILE, OFF_NOTES = OFF_RAW + RAWS * RAW;
   static constexpr int USED = OFF_NOTES + NS * 640 + NS * 1024 + 1024 + NS * 16 + NS * 48;
@@ -61,8 +62,11 @@ struct WeightTileCfg {
 namespace wtile {
 
 struct Bars {
-  uint64_t item_full[4], item_free[4], raw_full[6], raw_free[6], key_full[4], key_free[4], k_full[2], k_free[2], q_full[3], q_free[3], n_full[4], n_free[4];
-  uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;
+  uint64_t item_full[4], item_free[4];                          // items
+  uint64_t raw_full[6], raw_free[6], k_full[2], k_free[2];      // tiles' codes, and converted
+  uint64_t key_full[4], key_free[4];                            // tiles' notes
+  uint64_t q_full[3], q_free[3], n_full[4], n_free[4];          // chunks' queries, and notes
+  uint64_t s_full[2][2], s_free[2][2], x_full[2], x_free[2], drain;  // of a tile of an item and buffer; sums' halves
   uint32_t tmem;
   int abort;  // a wait has given up
 };
