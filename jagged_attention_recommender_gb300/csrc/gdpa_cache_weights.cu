@@ -59,12 +59,12 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, const Device& dev, cudaSt
 // to 6001 keys, 4 key heads, D = 128; 128 sequences of 100 to 6000 keys, 8 key
 // heads, D = 64 behind the stroke), with 8, 16, 32, 64 and 128 rows a warp and by
 // the kernel for many:
-//     8 rows      - / 47     - / 50     - / 51     - / 54     - / 72     - / 350
-//    16 rows      -         21 / 57    25 / 58    26 / 61    39 / 79     - / 350
-//    32 rows      -          -         32 / 73    32 / 77    47 / 97     - / 350
-//    64 rows      -          -          -         47 / 112   66 / 142   90 / 348
-//    96 rows      -          -          -          -         93 / 191   92 / 348
-//   128 rows      -          -          -          -        115 / 240   93 / 348
+//     8 rows      - / 47     - / 51     - / 52     - / 57     - / 73     - / 268
+//    16 rows      -         22 / 58    25 / 59    26 / 63    39 / 80    68 / 268
+//    32 rows      -          -         32 / 73    33 / 78    47 / 97    63 / 242
+//    64 rows      -          -          -         49 / 113   66 / 144   65 / 243
+//    96 rows      -          -          -          -         93 / 193   66 / 244
+//   128 rows      -          -          -          -        115 / 239   67 / 245
 template <int D>
 gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
   const int64_t rows = (int64_t)max_q * p.G;

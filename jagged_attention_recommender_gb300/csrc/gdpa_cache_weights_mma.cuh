@@ -39,17 +39,27 @@ __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-// mbar_wait for roles that are far ahead: a warp that waits sleeps between its
-// looks, so that it takes no issue slots from those that compute.
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
-  if (mbar_test_wait(bar, parity)) return true;
+// The rest of a wait for `bar` that was not over at once: one copy of it, since
+// the roles of a kernel share the instruction caches.
+static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort, int idle) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    __nanosleep(100);
-    if (mbar_test_wait(bar, parity)) return true;
+    if (idle) __nanosleep(100);
+    if (idle ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > limit_ns) return false;
   }
+}
+
+// mbar_wait with its loop out of line ...
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
+  return mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_on(bar, parity, limit_ns, abort, 0);
+}
+
+// ... and for roles that are far ahead: a warp that waits sleeps between its
+// looks, so that it takes no issue slots from those that compute.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
+  return mbar_test_wait(bar, parity) || wait_on(bar, parity, limit_ns, abort, 1);
 }
 
 }  // namespace ptx
@@ -73,34 +83,44 @@ struct alignas(16) KeyNotes {
   }
 };
 
-// Brings a tile's notes, by a whole warp; lane i below 8 knows its i-th block's
-// row.  `full` takes 33 arrivals.
-__device__ __forceinline__ void bring_notes(const CacheWeightsParams& w, KeyNotes& note, uint64_t* full, int64_t row) {
-  const int lane = threadIdx.x & 31;
-  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
-  if (lane < 8) {
-    note.row[lane] = row;
-    if (row >= 0) {
-      const int64_t word = (row >> 4) & ~(int64_t)3;
-      split::cp_async4(ptx::smem_u32(&note.word[lane]), w.cache.k_sf + word,
-                       static_cast<int>(min((int64_t)4, sf_bytes - word)));
-    }
-  }
-  const int64_t at = __shfl_sync(0xffffffffu, row, lane >> 2);
-  if (w.w_in && at >= 0) split::cp_async16(ptx::smem_u32(&note.old[lane * 4]), w.w_in + at + (lane & 3) * 4, 16);
-  ptx::copies_arrive(full);
-  __syncwarp();
-  if (lane == 0) ptx::mbar_arrive(full);
+// How many blocks the copy of a lane brings, of a tile's blocks that lie behind each
+// other in a page (a bulk copy takes its warp about 75 cycles, whatever its size);
+// 0 where another lane does, or where there is none.  `there`: a bit for each lane's block.
+__device__ __forceinline__ int blocks_of_copy(const CacheWeightsParams& w, uint32_t there) {
+  const int lane = threadIdx.x & 31, per = 1 << min(w.cache.lp - 4, 3);
+  return (lane & (per - 1)) == 0 ? __popc(there >> lane & ((1u << per) - 1)) : 0;
 }
 
-// Brings a tile's codes to `raw`, by a whole warp.  (A block that is not there
+// Brings the notes of one or two tiles, by a whole warp; lane i below 8 * tiles
+// knows its block's row (the others -1) and its tile's stage.  `full` takes 9 arrivals.
+__device__ __forceinline__ void bring_notes(const CacheWeightsParams& w, KeyNotes& note, uint64_t* full, int64_t row, int tiles) {
+  const int lane = threadIdx.x & 31, block = lane & 7;
+  const bool mine = lane < 8 * tiles;
+  const int64_t sf_bytes = static_cast<int64_t>(w.cache.num_pages) * w.cache.H << (w.cache.lp - 4);
+  if (mine) {
+    note.row[block] = row;
+    if (row >= 0) {
+      const int64_t word = (row >> 4) & ~(int64_t)3;
+      split::cp_async4(ptx::smem_u32(&note.word[block]), w.cache.k_sf + word,
+                       static_cast<int>(min((int64_t)4, sf_bytes - word)));
+    }
+    ptx::copies_arrive(full);
+  }
+  const uint32_t there = w.w_in ? __ballot_sync(0xffffffffu, row >= 0) : 0;
+  if (mine && block == 0) ptx::mbar_arrive_expect_tx(full, __popc(there >> lane & 0xff) * 64);
+  __syncwarp();
+  if (const int n = blocks_of_copy(w, there)) ptx::bulk_load(ptx::smem_u32(&note.old[block * 16]), w.w_in + row, n * 64, full);
+}
+
+// Brings the codes of one or two tiles, likewise.  (A block that is not there
 // keeps what the stage held: no other key's score depends on it.)
 template <int D>
-__device__ __forceinline__ void bring_codes(const CacheWeightsParams& w, uint32_t raw, uint64_t* full, int64_t row) {
-  const int lane = threadIdx.x & 31, blocks = __popc(__ballot_sync(0xffffffffu, row >= 0));
-  if (lane == 0) ptx::mbar_arrive_expect_tx(full, blocks * 16 * D);
+__device__ __forceinline__ void bring_codes(const CacheWeightsParams& w, uint32_t raw, uint64_t* full, int64_t row, int tiles) {
+  const int lane = threadIdx.x & 31, block = lane & 7;
+  const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+  if (lane < 8 * tiles && block == 0) ptx::mbar_arrive_expect_tx(full, __popc(there >> lane & 0xff) * 16 * D);
   __syncwarp();
-  if (row >= 0) ptx::bulk_load(raw + lane * 16 * D, w.cache.k + row * D, 16 * D, full);
+  if (const int n = blocks_of_copy(w, there)) ptx::bulk_load(raw + block * 16 * D, w.cache.k + row * D, n * 16 * D, full);
 }
 
 // Waits for the last turns of `stages` stages of which `count` were filled, `at`

@@ -12,9 +12,11 @@
 // Bound: the chain of hand-overs around the special-function unit, which takes four
 // cycles for a warp's 32 exponentials (measured), 512 for 128 keys and 128 rows, as
 // long as their products at D = 128 do.  Measured: 2321 prompt rows behind 2100 to
-// 8192 keys, 32 query and 8 key heads of 128, 111 us (865 TFLOP/s; the tensor core's
+// 8192 keys, 32 query and 8 key heads of 128, 108 us (892 TFLOP/s; the tensor core's
 // floor is 50); a warp is at its columns for half of that, the rest is waiting and
-// the work around a chunk and an item.
+// the work around a chunk and an item.  Eight roles share the instruction caches, so
+// their code is kept short: loops that are not unrolled, one copy of the waits' loop
+// (128 rows of 48 sequences 67 us instead of 93).
 //
 // Work split.  An item is 256 keys of a sequence and head, converted once and kept
 // in shared memory while all rows that see any of them pass in chunks of 128
@@ -194,7 +196,7 @@ struct Walk {
   int b, h;
   bool ok = true;  // false: a wait has given up
   __device__ __forceinline__ bool next(const WeightTileParams& p, Bars& B, const Notes& notes) {
-    ok = ptx::mbar_wait(&B.item_full[ring.at], ring.turn, p.limit, &B.abort);
+    ok = ptx::mbar_wait_near(&B.item_full[ring.at], ring.turn, p.limit, &B.abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
     const int4 x = notes.item[ring.at * 3], y = notes.item[ring.at * 3 + 1], z = notes.item[ring.at * 3 + 2];
@@ -205,6 +207,13 @@ struct Walk {
     it.chunks = y.x, b = y.y, h = y.z;
     s.first = z.x, s.n = z.y, s.len = z.z, s.ok = z.w;
     return it.chunks >= 0;
+  }
+  // To the next item that any row sees.
+  __device__ __forceinline__ bool next_seen(const WeightTileParams& p, Bars& B, const Notes& notes) {
+    do
+      if (!next(p, B, notes)) return false;
+    while (it.chunks == 0);
+    return true;
   }
 };
 
@@ -251,7 +260,7 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
     float old = 0.0f, factor = 0.0f;
 #pragma unroll 1
     for (int j = 0; j < it.tiles; ++j) {
-      ok = ptx::mbar_wait(&B.key_full[k.at], k.turn, p.limit, abort);
+      ok = ptx::mbar_wait_near(&B.key_full[k.at], k.turn, p.limit, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (j == m) {
@@ -336,14 +345,14 @@ __device__ void run_sums(const WeightTileParams& p, Bars& B, const Notes& notes,
     float total = (a + b) + (c + d);
     if (it.chunks > 1) {  // both warpgroups have a part
       if (turn == 1) {
-        ok = ptx::mbar_wait(&B.x_free[m], (xi & 1) ^ 1, p.limit, abort);
+        ok = ptx::mbar_wait_near(&B.x_free[m], (xi & 1) ^ 1, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         notes.half[m * 128 + key_in] = total;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&B.x_full[m]);
       } else {
-        ok = ptx::mbar_wait(&B.x_full[m], xi & 1, p.limit, abort);
+        ok = ptx::mbar_wait_near(&B.x_full[m], xi & 1, p.limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         total += notes.half[m * 128 + key_in];
@@ -376,10 +385,7 @@ struct TileWalk {
   // To the next tile, or the first.
   __device__ __forceinline__ bool begin(const WeightTileParams& p, Bars& B, const Notes& notes) {
     m = 0;
-    do
-      if (!walk.next(p, B, notes)) return false;
-    while (walk.it.chunks == 0);
-    return true;
+    return walk.next_seen(p, B, notes);
   }
   __device__ __forceinline__ bool next(const WeightTileParams& p, Bars& B, const Notes& notes) {
     return ++m < walk.it.tiles || begin(p, B, notes);
@@ -394,38 +400,52 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
   const volatile int* abort = &B.abort;
   const int pmask = (1 << w.cache.lp) - 1;
   const uint32_t raw = ptx::smem_u32(sm) + C::OFF_RAW;
+  const int second = lane >> 3 & 1;  // lanes 0-7: the blocks of an item's first tile; 8-15: of its second
   StageRing in, n;
-  uint32_t count = 0;
+  uint32_t count = 0, notes_count = 0;
   bool ok = true;
-  TileWalk tiles;
-  bool more = tiles.begin(p, B, notes);
-  // lane i: the page of the tile's i-th block of 16 keys
+  Walk walk;
+  bool more = walk.next_seen(p, B, notes);
+  // The page of this lane's block as the table has it; -1 behind the keys.  (Looked
+  // up an item ahead, and not looked at until then.)
   auto page_of = [&]() {
-    const int k0 = tiles.walk.it.k0 + tiles.m * 128;
-    if (lane >= 8 || tiles.walk.s.len - k0 <= lane * 16) return -1;
-    return load_page(w.cache, w.batch, tiles.walk.b, k0 + lane * 16);
+    if (lane >= 16 || walk.s.len - walk.it.k0 <= lane * 16) return -1;
+    return __ldg(w.batch.table + static_cast<int64_t>(walk.b) * w.batch.max_pages + ((walk.it.k0 + lane * 16) >> w.cache.lp));
   };
-  int page = more ? page_of() : -1;  // (looked up a tile ahead)
-  __syncwarp();
+  int page = more ? page_of() : -1;
   while (more) {
-    const int k0 = tiles.walk.it.k0 + tiles.m * 128;
-    const int64_t row = page >= 0 ? cache_row(w.cache, page, tiles.walk.h, (k0 + lane * 16) & pmask) : -1;
-    more = tiles.next(p, B, notes);
+    const int k0 = walk.it.k0, tiles = walk.it.tiles;
+    int64_t row = -1;
+    if (page >= 0 && page < w.cache.num_pages)
+      row = cache_row(w.cache, page, walk.h, (k0 + lane * 16) & pmask);
+    else if (lane < 16 && walk.s.len - k0 > lane * 16)
+      atomicOr(w.batch.status, kStatusBadPlan);
+    __syncwarp();
+    more = walk.next_seen(p, B, notes);
     page = more ? page_of() : -1;
     __syncwarp();
+    StageRing n2 = n, in2 = in;
+    n2.next(C::NS);
+    in2.next(C::RAWS);
     ok = ptx::mbar_wait_idle(&B.key_free[n.at], n.turn ^ 1, p.limit, abort);
+    if (tiles == 2) ok = ok && ptx::mbar_wait_idle(&B.key_free[n2.at], n2.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    bring_notes(w, notes.key[n.at], &B.key_full[n.at], row);
-    n.next(C::NS);
+    const uint32_t n_at = second ? n2.at : n.at, in_at = second ? in2.at : in.at;
+    bring_notes(w, notes.key[n_at], &B.key_full[n_at], row, tiles);
+    notes_count += tiles;
+    n = n2;
+    if (tiles == 2) n.next(C::NS);
     ok = ptx::mbar_wait_idle(&B.raw_free[in.at], in.turn ^ 1, p.limit, abort);
+    if (tiles == 2) ok = ok && ptx::mbar_wait_idle(&B.raw_free[in2.at], in2.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    bring_codes<D>(w, raw + in.at * C::RAW, &B.raw_full[in.at], row);
-    in.next(C::RAWS);
-    ++count;
+    bring_codes<D>(w, raw + in_at * C::RAW, &B.raw_full[in_at], row, tiles);
+    count += tiles;
+    in = in2;
+    if (tiles == 2) in.next(C::RAWS);
   }
-  ok = ok && tiles.walk.ok;
+  ok = ok && walk.ok;
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusProducer);
@@ -433,6 +453,7 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
   // no copy may land behind the CTA's end: this thread's own, and the last turn of every stage
   split::cp_commit();
   split::cp_wait<0>();
+  drain_stages(B.key_full, n, C::NS, notes_count);
   drain_stages(B.raw_full, in, C::RAWS, count);
 }
 
@@ -451,11 +472,11 @@ __device__ void run_convert(const WeightTileParams& p, uint8_t* sm, Bars& B, con
   bool ok = true;
   TileWalk tiles;
   for (bool more = tiles.begin(p, B, notes); more; more = tiles.next(p, B, notes)) {
-    ok = ptx::mbar_wait_idle(&B.raw_full[in.at], in.turn, p.limit, abort);
-    ok = ok && ptx::mbar_wait_idle(&B.k_free[k.at], k.turn ^ 1, p.limit, abort);
+    ok = ptx::mbar_wait_near(&B.raw_full[in.at], in.turn, p.limit, abort);
+    ok = ok && ptx::mbar_wait_near(&B.k_free[k.at], k.turn ^ 1, p.limit, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-#pragma unroll
+#pragma unroll 1  // (unrolled it alone drives the other roles out of the instruction caches)
     for (int i = 0; i < N; ++i) {
       const uint32_t at = k.at * C::TILE + i * ROWS * 128;
       uint32_t x[4], a[8];
@@ -662,7 +683,7 @@ __global__ void __launch_bounds__(WeightTileCfg<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) ptx::mbar_init(&B.k_full[i], 128), ptx::mbar_init(&B.k_free[i], 1);
     for (int i = 0; i < C::RAWS; ++i) ptx::mbar_init(&B.raw_full[i], 1), ptx::mbar_init(&B.raw_free[i], 4);
-    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.key_full[i], 1 + 32), ptx::mbar_init(&B.key_free[i], 16);
+    for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.key_full[i], 1 + 8), ptx::mbar_init(&B.key_free[i], 16);
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&B.item_full[i], 1), ptx::mbar_init(&B.item_free[i], 24);
     for (int i = 0; i < C::QS; ++i) ptx::mbar_init(&B.q_full[i], 1), ptx::mbar_init(&B.q_free[i], 1);
     for (int i = 0; i < C::NS; ++i) ptx::mbar_init(&B.n_full[i], 32), ptx::mbar_init(&B.n_free[i], 8);
