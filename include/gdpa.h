@@ -659,7 +659,7 @@ gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_t* offsets,
  * Scores, weights and their sums are fp32, summed in an order that does not depend
  * on timing.  Keys that a row does not see take nothing from it, whatever it
  * holds; a NaN in a row or its lse goes to the keys that it sees, one in a key to that key.
- * With few rows (max_q * Hq / H up to 64, up to 128 with D = 64) queries are
+ * With few rows (max_q * Hq / H up to 64, up to 112 with D = 64) queries are
  * rounded as in gdpa_cache_fwd; with more they are taken as they are.
  *
  * A page that two sequences of the call share has undefined weights.

@@ -59,12 +59,12 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, const Device& dev, cudaSt
 // to 6001 keys, 4 key heads, D = 128; 128 sequences of 100 to 6000 keys, 8 key
 // heads, D = 64 behind the stroke), with 8, 16, 32, 64 and 128 rows a warp and by
 // the kernel for many:
-//     8 rows      - / 47     - / 51     - / 52     - / 57     - / 73     - / 268
-//    16 rows      -         22 / 58    25 / 59    26 / 63    39 / 80    68 / 268
-//    32 rows      -          -         32 / 73    33 / 78    47 / 97    63 / 242
-//    64 rows      -          -          -         49 / 113   66 / 144   65 / 243
-//    96 rows      -          -          -          -         93 / 193   66 / 244
-//   128 rows      -          -          -          -        115 / 239   67 / 245
+//     8 rows      - / 47     - / 51     - / 52     - / 57     - / 73     - / 253
+//    16 rows      -         22 / 58    25 / 59    26 / 63    39 / 80    68 / 253
+//    32 rows      -          -         32 / 73    33 / 78    47 / 97    63 / 227
+//    64 rows      -          -          -         49 / 113   66 / 144   65 / 226
+//    96 rows      -          -          -          -         93 / 193   66 / 226
+//   128 rows      -          -          -          -        115 / 239   67 / 226
 template <int D>
 gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Device& dev, cudaStream_t s) {
   const int64_t rows = (int64_t)max_q * p.G;
@@ -73,7 +73,7 @@ gdpa_status_t launch_weights(const CacheWeightsParams& p, int max_q, const Devic
   if (rows <= 32) return launch_split<D, 4>(p, dev, s);
   if (rows <= 64) return launch_split<D, 8>(p, dev, s);
   if constexpr (D == 64)
-    if (rows <= 128) return launch_split<D, 16>(p, dev, s);
+    if (rows <= 112) return launch_split<D, 16>(p, dev, s);
   return launch_tile<D>(p, dev, s);
 }
 

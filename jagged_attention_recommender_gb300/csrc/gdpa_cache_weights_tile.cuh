@@ -12,8 +12,8 @@
 // Bound: the chain of hand-overs around the special-function unit, which takes four
 // cycles for a warp's 32 exponentials (measured), 512 for 128 keys and 128 rows, as
 // long as their products at D = 128 do.  Measured: 2321 prompt rows behind 2100 to
-// 8192 keys, 32 query and 8 key heads of 128, 108 us (892 TFLOP/s; the tensor core's
-// floor is 50); a warp is at its columns for half of that, the rest is waiting and
+// 8192 keys, 32 query and 8 key heads of 128, 108 to 111 us (865 to 890 TFLOP/s; the tensor
+// core's floor is 50); a warp is at its columns for half of that, the rest is waiting and
 // the work around a chunk and an item.  Eight roles share the instruction caches, so
 // their code is kept short: loops that are not unrolled, one copy of the waits' loop
 // (128 rows of 48 sequences 67 us instead of 93).
@@ -605,6 +605,10 @@ template <int D>
 __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, const Notes& notes, uint32_t tmem) {
   using C = WeightTileCfg<D>;
   const volatile int* abort = &B.abort;
+  // Short code for short items (200 rows of 128 samples, D = 64, 320 us instead of 344; 2321
+  // prompt rows 97 either way), quick issues where the products set the pace (those
+  // rows at D = 128: 107 us instead of 112; 192 rows of 48 sequences 94 instead of 88).
+  constexpr int M = D == 64 ? 1 : 2;
   const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, 1024);
   const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm) + C::OFF_Q, 16, 1024);
   StageRing k, q;
@@ -623,7 +627,7 @@ __device__ void run_mma(const WeightTileParams& p, uint8_t* sm, Bars& B, const N
       if (!ok) break;
       const uint32_t idesc = ptx::idesc_bf16(128, (chunk_columns(p, it, c) + 31) & ~31, 0), sb = ci & 1;
       const uint64_t b = q_desc + q.at * (C::TILE >> 4);
-#pragma unroll
+#pragma unroll M
       for (int m = 0; m < 2; ++m) {
         if (m >= it.tiles) break;
         const StageRing at = m ? second : k;

@@ -520,3 +520,12 @@ def test_a_history_is_served_and_cut(Hq, H, D, new):
                 free += held[b]
             held, lens = to, new_lens.cpu().tolist()
     assert cuts >= 2
+
+
+@pytest.mark.parametrize("new", [65, 112, 113])
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("causal,window", [(1, 0), (0, 0), (1, 50)])
+def test_weights_between_few_rows_and_many(new, P, causal, window):
+    """Heads of 64 with more rows than the least kernels hold, on both sides of the rule for many."""
+    x = ref.make(15, 2, 2, 64, P, [511, 130, new], [new, 66, new])
+    check_weights(x, causal, window)
