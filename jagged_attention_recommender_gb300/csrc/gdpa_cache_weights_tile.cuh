@@ -34,6 +34,7 @@
 #pragma once
 
 #include "gdpa_cache_append.cuh"
+#include "gdpa_cache_order.h"
 #include "gdpa_cache_weights_mma.cuh"
 
 namespace gdpa {
@@ -403,49 +404,51 @@ __device__ void run_copies(const WeightTileParams& p, uint8_t* sm, Bars& B, cons
   const int second = lane >> 3 & 1;  // lanes 0-7: the blocks of an item's first tile; 8-15: of its second
   StageRing in, n;
   uint32_t count = 0, notes_count = 0;
-  bool ok = true;
   Walk walk;
-  bool more = walk.next_seen(p, B, notes);
   // The page of this lane's block as the table has it; -1 behind the keys.  (Looked
   // up an item ahead, and not looked at until then.)
-  auto page_of = [&]() {
-    if (lane >= 16 || walk.s.len - walk.it.k0 <= lane * 16) return -1;
-    return __ldg(w.batch.table + static_cast<int64_t>(walk.b) * w.batch.max_pages + ((walk.it.k0 + lane * 16) >> w.cache.lp));
-  };
-  int page = more ? page_of() : -1;
-  while (more) {
-    const int k0 = walk.it.k0, tiles = walk.it.tiles;
-    int64_t row = -1;
-    if (page >= 0 && page < w.cache.num_pages)
-      row = cache_row(w.cache, page, walk.h, (k0 + lane * 16) & pmask);
-    else if (lane < 16 && walk.s.len - k0 > lane * 16)
-      atomicOr(w.batch.status, kStatusBadPlan);
-    __syncwarp();
-    more = walk.next_seen(p, B, notes);
-    page = more ? page_of() : -1;
-    __syncwarp();
-    StageRing n2 = n, in2 = in;
-    n2.next(C::NS);
-    in2.next(C::RAWS);
-    ok = ptx::mbar_wait_idle(&B.key_free[n.at], n.turn ^ 1, p.limit, abort);
-    if (tiles == 2) ok = ok && ptx::mbar_wait_idle(&B.key_free[n2.at], n2.turn ^ 1, p.limit, abort);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const uint32_t n_at = second ? n2.at : n.at, in_at = second ? in2.at : in.at;
-    bring_notes(w, notes.key[n_at], &B.key_full[n_at], row, tiles);
-    notes_count += tiles;
-    n = n2;
-    if (tiles == 2) n.next(C::NS);
-    ok = ptx::mbar_wait_idle(&B.raw_free[in.at], in.turn ^ 1, p.limit, abort);
-    if (tiles == 2) ok = ok && ptx::mbar_wait_idle(&B.raw_free[in2.at], in2.turn ^ 1, p.limit, abort);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    bring_codes<D>(w, raw + in_at * C::RAW, &B.raw_full[in_at], row, tiles);
-    count += tiles;
-    in = in2;
-    if (tiles == 2) in.next(C::RAWS);
-  }
-  ok = ok && walk.ok;
+  int page = -1;
+  // the item whose copies are to be issued: its tiles, and the row of this lane's block
+  int tiles = 0;
+  int64_t row = -1;
+  const bool ok = bring_in_order(
+      [&]() { return walk.next(p, B, notes); }, [&]() { return walk.it.chunks > 0; },
+      [&]() {
+        page = lane >= 16 || walk.s.len - walk.it.k0 <= lane * 16
+                   ? -1
+                   : __ldg(w.batch.table + static_cast<int64_t>(walk.b) * w.batch.max_pages +
+                           ((walk.it.k0 + lane * 16) >> w.cache.lp));
+      },
+      [&]() {
+        tiles = walk.it.tiles;
+        row = -1;
+        if (page >= 0 && page < w.cache.num_pages)
+          row = cache_row(w.cache, page, walk.h, (walk.it.k0 + lane * 16) & pmask);
+        else if (lane < 16 && walk.s.len - walk.it.k0 > lane * 16)
+          atomicOr(w.batch.status, kStatusBadPlan);
+        __syncwarp();
+      },
+      [&]() {
+        StageRing n2 = n, in2 = in;
+        n2.next(C::NS);
+        in2.next(C::RAWS);
+        bool there = ptx::mbar_wait_idle(&B.key_free[n.at], n.turn ^ 1, p.limit, abort);
+        if (tiles == 2) there = there && ptx::mbar_wait_idle(&B.key_free[n2.at], n2.turn ^ 1, p.limit, abort);
+        if (!__all_sync(0xffffffffu, there)) return false;
+        const uint32_t n_at = second ? n2.at : n.at, in_at = second ? in2.at : in.at;
+        bring_notes(w, notes.key[n_at], &B.key_full[n_at], row, tiles);
+        notes_count += tiles;
+        n = n2;
+        if (tiles == 2) n.next(C::NS);
+        there = ptx::mbar_wait_idle(&B.raw_free[in.at], in.turn ^ 1, p.limit, abort);
+        if (tiles == 2) there = there && ptx::mbar_wait_idle(&B.raw_free[in2.at], in2.turn ^ 1, p.limit, abort);
+        if (!__all_sync(0xffffffffu, there)) return false;
+        bring_codes<D>(w, raw + in_at * C::RAW, &B.raw_full[in_at], row, tiles);
+        count += tiles;
+        in = in2;
+        if (tiles == 2) in.next(C::RAWS);
+        return true;
+      }) && walk.ok;
   if (!ok && lane == 0) {
     B.abort = 1;
     atomicOr(w.batch.status, kStatusProducer);
