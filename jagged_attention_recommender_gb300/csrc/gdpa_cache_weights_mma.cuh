@@ -92,7 +92,9 @@ __device__ __forceinline__ int blocks_of_copy(const CacheWeightsParams& w, uint3
 }
 
 // Brings the notes of one or two tiles, by a whole warp; lane i below 8 * tiles
-// knows its block's row (the others -1) and its tile's stage.  `full` takes 9 arrivals.
+// knows its block's row (the others -1) and its tile's stage.  `full` takes 9 arrivals:
+// eight that stand for asynchronous copies alone, and one that releases the rows of all
+// eight lanes, which the warp's barrier in front of it puts before it.
 __device__ __forceinline__ void bring_notes(const CacheWeightsParams& w, KeyNotes& note, uint64_t* full, int64_t row, int tiles) {
   const int lane = threadIdx.x & 31, block = lane & 7;
   const bool mine = lane < 8 * tiles;
@@ -106,6 +108,7 @@ __device__ __forceinline__ void bring_notes(const CacheWeightsParams& w, KeyNote
     }
     ptx::copies_arrive(full);
   }
+  __syncwarp();
   const uint32_t there = w.w_in ? __ballot_sync(0xffffffffu, row >= 0) : 0;
   if (mine && block == 0) ptx::mbar_arrive_expect_tx(full, __popc(there >> lane & 0xff) * 64);
   __syncwarp();
