@@ -85,7 +85,7 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 6 : 1)
     gdpa_cache_choose_kernel(const __grid_constant__ EvictParams p, int slots) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];  // (read four at a time)
   constexpr int WARPS = THREADS / 32;
   __shared__ ChooseShared<WARPS> sh;
   cg::cluster_group cluster = cg::this_cluster();
