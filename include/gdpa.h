@@ -595,7 +595,8 @@ gdpa_status_t gdpa_rope_freqs(int rot_dim, double base, int scaling, double fact
  *
  *   x   device bf16, row t at x + t * x_stride (elements): [H, D]
  *   y   device bf16, row t at y + t * y_stride: [H, D]; may be x itself with
- *       the same stride, and must not overlap x otherwise
+ *       the same stride; otherwise no row of y may overlap one of x (which is
+ *       refused; rows of both may lie between one another)
  *   offsets    device int32 [B+1], offsets[0] = 0, non-decreasing: rows
  *              [offsets[b], offsets[b+1]) are those of sequence b
  *   first      device int32 [B]: the position of each sequence's first row (NULL:

@@ -3,6 +3,7 @@
 // plain C++ for the host.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -54,6 +55,24 @@ GDPA_HD OwnedRows owned_rows(const CacheSeq& s, int r) {
 // token) sees through a window of `window` tokens, 0 for none.  (pos - window
 // alone can lie below -2^31.)
 GDPA_HD int first_key(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
+// Whether any of T rows of `len` elements, x_stride apart from 0 on, shares an
+// element with any of T rows y_stride apart from `apart` on (len <= both strides).
+inline bool rows_overlap(int64_t apart, int64_t x_stride, int64_t y_stride, int64_t len, int64_t T) {
+  auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+  const int64_t x_end = (T - 1) * x_stride + len, y_end = apart + (T - 1) * y_stride + len;
+  if (T <= 0 || apart >= x_end || y_end <= 0) return false;
+  if (x_stride == y_stride) {  // where they begin less than a row apart, modulo the stride
+    const int64_t m = apart - floor_div(apart, x_stride) * x_stride;
+    return m < len || m > x_stride - len;
+  }
+  // each row of x that lies among y's, with the first of y's that ends behind its beginning
+  for (int64_t i = std::max<int64_t>(0, floor_div(apart - len, x_stride) + 1); i < T && i * x_stride < y_end; ++i) {
+    const int64_t at = i * x_stride, j = std::max<int64_t>(0, floor_div(at - len - apart, y_stride) + 1);
+    if (j < T && apart + j * y_stride < at + len) return true;
+  }
+  return false;
+}
 
 // x modulo 1 in units of 2^-64, rounded (the difference is exact: x and its
 // floor are multiples of x's last bit).

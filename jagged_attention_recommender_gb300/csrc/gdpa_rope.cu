@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "gdpa_cache_host.h"
 #include "gdpa_rope.cuh"
@@ -57,12 +56,8 @@ extern "C" gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_
   if (st != GDPA_OK) return st;
   if ((st = check_rows(y, y_stride, H, D)) != GDPA_OK) return st;
   if (x == y && x_stride != y_stride) return GDPA_ERR_INVALID_ARG;
-  if (x != y && x_stride == y_stride) {
-    // rows of one stride overlap where they begin less than a row's heads apart, modulo the stride
-    const int64_t apart = (static_cast<const char*>(y) - static_cast<const char*>(x)) / 2, last = (T - 1) * x_stride + (int64_t)H * D;
-    const int64_t m = ((apart % x_stride) + x_stride) % x_stride;
-    if (std::abs(apart) < last && (m < (int64_t)H * D || m > x_stride - (int64_t)H * D)) return GDPA_ERR_INVALID_ARG;
-  }
+  if (x != y && rows_overlap((static_cast<const char*>(y) - static_cast<const char*>(x)) / 2, x_stride, y_stride, (int64_t)H * D, T))
+    return GDPA_ERR_INVALID_ARG;
   if (!offsets || !aligned(offsets, 4) || !aligned(first, 4)) return GDPA_ERR_INVALID_ARG;
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
