@@ -187,7 +187,7 @@ extern "C" gdpa_status_t gdpa_cache_append(const gdpa_cache_t* cache, const void
     if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
     if ((st = check_rows(q_out, (int64_t)Hq * cache->D, Hq, cache->D)) != GDPA_OK) return st;
   }
-  if (!offsets || !kv_lens || !page_table || max_pages == 0) return GDPA_ERR_INVALID_ARG;
+  if (!words(offsets) || !words(kv_lens) || !words(page_table) || max_pages == 0) return GDPA_ERR_INVALID_ARG;
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
   AppendParams p;
@@ -254,7 +254,8 @@ extern "C" gdpa_status_t gdpa_cache_fwd(const gdpa_cache_t* cache, const void* q
   if (T == 0 || B == 0) return GDPA_OK;
   if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
   if ((st = check_rows(out, (int64_t)Hq * cache->D, Hq, cache->D)) != GDPA_OK) return st;
-  if (!offsets || !kv_lens || !page_table || max_pages == 0 || !aligned(lse, 4)) return GDPA_ERR_INVALID_ARG;
+  if (!words(offsets) || !words(kv_lens) || !words(page_table) || max_pages == 0 || !aligned(lse, 4))
+    return GDPA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 16)) return GDPA_ERR_INVALID_ARG;
   int64_t need = 0;
   if ((st = gdpa_cache_workspace_size(cache, Hq, max_q, &need)) != GDPA_OK) return st;

@@ -64,7 +64,8 @@ extern "C" gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weig
   if (B == 0) return GDPA_OK;
   const int64_t most = (int64_t)max_pages * cache->page_tokens, room = (int64_t)new_max_pages * cache->page_tokens;
   if (max_pages == 0 || room < std::min<int64_t>(budget, most)) return GDPA_ERR_INVALID_ARG;
-  if (!weights || !aligned(weights, 16) || !kv_lens || !page_table || !new_table || !kept || !new_lens)
+  if (!weights || !aligned(weights, 16) || !words(kv_lens) || !words(page_table) || !words(new_table) || !words(kept) ||
+      !words(new_lens))
     return GDPA_ERR_INVALID_ARG;
   const uintptr_t a = reinterpret_cast<uintptr_t>(kv_lens), c = reinterpret_cast<uintptr_t>(new_lens), n = 4 * (uintptr_t)B;
   if (a < c + n && c < a + n) return GDPA_ERR_INVALID_ARG;

@@ -21,6 +21,9 @@ constexpr int kMaxDevices = 64;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether an array of 32-bit words can be there: not null, and aligned.
+inline bool words(const void* p) { return p && aligned(p, 4); }
+
 struct Device {
   int id = 0, sms = 0;
   int* status = nullptr;

@@ -97,7 +97,8 @@ extern "C" gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const voi
   if (T * (Hq / cache->H) >= ((int64_t)1 << 31) - 256) return GDPA_ERR_UNSUPPORTED;  // query rows of a key head
   if (T == 0 || B == 0) return GDPA_OK;
   if ((st = check_rows(q, q_stride, Hq, cache->D)) != GDPA_OK) return st;
-  if (!lse || !aligned(lse, 4) || !offsets || !kv_lens || !page_table || max_pages == 0) return GDPA_ERR_INVALID_ARG;
+  if (!words(lse) || !words(offsets) || !words(kv_lens) || !words(page_table) || max_pages == 0)
+    return GDPA_ERR_INVALID_ARG;
   if (!weights || !aligned(weights, 16) || !aligned(weights_in, 16)) return GDPA_ERR_INVALID_ARG;
   if (weights_in && weights_in != weights) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(weights_in), b = reinterpret_cast<uintptr_t>(weights);

@@ -58,7 +58,7 @@ extern "C" gdpa_status_t gdpa_rope(const void* x, int64_t x_stride, const int32_
   if (x == y && x_stride != y_stride) return GDPA_ERR_INVALID_ARG;
   if (x != y && rows_overlap((static_cast<const char*>(y) - static_cast<const char*>(x)) / 2, x_stride, y_stride, (int64_t)H * D, T))
     return GDPA_ERR_INVALID_ARG;
-  if (!offsets || !aligned(offsets, 4) || !aligned(first, 4)) return GDPA_ERR_INVALID_ARG;
+  if (!words(offsets) || !aligned(first, 4)) return GDPA_ERR_INVALID_ARG;
   Device dev;
   if ((st = current_device(&dev)) != GDPA_OK) return st;
   RopeParams p;
