@@ -569,7 +569,8 @@ typedef enum {
   GDPA_ROPE_SCALE_NONE = 0,   /* f_i = base^(-2 i / rot_dim) */
   GDPA_ROPE_SCALE_LINEAR = 1, /* f_i / factor */
   GDPA_ROPE_SCALE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base: the first pair
-                                 keeps its frequency, the last one's is divided by factor */
+                                 keeps its frequency, the last one's is divided by factor (a base that 64
+                                 bits do not hold is refused) */
   GDPA_ROPE_SCALE_RAMP = 3    /* by wave length: f_i where a pair turns `fast` times or more over the trained
                                  context, f_i / factor where it turns `slow` times or less, a linear ramp of
                                  the pair's index between; magnitude 0.1 ln(factor) + 1 */

@@ -20,8 +20,9 @@ extern "C" gdpa_status_t gdpa_rope_freqs(int rot_dim, double base, int scaling, 
   if (scaling != GDPA_ROPE_SCALE_NONE && !(factor >= 1 && std::isfinite(factor))) return GDPA_ERR_INVALID_ARG;
   if (scaling == GDPA_ROPE_SCALE_RAMP && !(trained > 0 && slow > 0 && fast > slow && std::isfinite(fast)))
     return GDPA_ERR_INVALID_ARG;
-  *magnitude = 1.0f;
   if (scaling == GDPA_ROPE_SCALE_BASE) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  if (!std::isfinite(base)) return GDPA_ERR_UNSUPPORTED;
+  *magnitude = 1.0f;
   for (int i = 0; i < rot_dim / 2; ++i) inv_freq[i] = std::pow(base, -2.0 * i / rot_dim);
   if (scaling == GDPA_ROPE_SCALE_LINEAR)
     for (int i = 0; i < rot_dim / 2; ++i) inv_freq[i] /= factor;
