@@ -12,26 +12,39 @@
 namespace gdpa {
 namespace {
 
-constexpr int kMostCluster = 16;
-
-// `ctas` CTAs a sequence and head, with up to `part` tokens each.
+// What a device has room for: whether a cluster of `cfg`, larger than every device
+// places, fits it.  Asked once for a size of shared memory (a few us), since what fits
+// with more fits with less.
 template <int THREADS>
-gdpa_status_t launch_choose(const EvictParams& p, int ctas, int64_t part, const Device& dev, cudaStream_t s) {
+gdpa_status_t place_wide(const cudaLaunchConfig_t& cfg, const Device& dev, bool* fits) {
   static std::mutex mu;
-  static bool done[kMaxDevices] = {}, wide[kMaxDevices] = {};
+  static int64_t most[kMaxDevices] = {}, least[kMaxDevices] = {};  // bytes that fit, that do not: 1 more, 0 unknown
+  std::lock_guard<std::mutex> lock(mu);
+  const int64_t bytes = static_cast<int64_t>(cfg.dynamicSmemBytes) + 1;
+  *fits = bytes <= most[dev.id];
+  if (*fits || (least[dev.id] && bytes >= least[dev.id])) return GDPA_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (as in allow_smem)
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
+  int n = 0;
+  const bool ok = cudaFuncSetAttribute(gdpa_cache_choose_kernel<THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                       1) == cudaSuccess;
+  // (an error says that no such cluster can be placed)
+  *fits = ok && cudaOccupancyMaxActiveClusters(&n, gdpa_cache_choose_kernel<THREADS>, &cfg) == cudaSuccess && n > 0;
+  cudaGetLastError();
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
+  (*fits ? most : least)[dev.id] = bytes;
+  return GDPA_OK;
+}
+
+// `ctas` CTAs a sequence and head, with up to `part` tokens each.  Nothing is
+// launched, and *placed is false, where the device has no room for such a cluster.
+template <int THREADS>
+gdpa_status_t launch_choose(const EvictParams& p, int ctas, int64_t part, const Device& dev, cudaStream_t s, bool* placed) {
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  *placed = true;
   const gdpa_status_t st = allow_smem(gdpa_cache_choose_kernel<THREADS>, kMostKeys * 4, 0, dev.id, mu, done);
   if (st != GDPA_OK) return st;
-  if (ctas > 8) {  // more CTAs a cluster than every device has room for
-    std::lock_guard<std::mutex> lock(mu);
-    if (!wide[dev.id]) {
-      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (as in allow_smem)
-      if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
-      const bool ok = cudaFuncSetAttribute(gdpa_cache_choose_kernel<THREADS>,
-                                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-      if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess || !ok) return GDPA_ERR_CUDA;
-      wide[dev.id] = true;
-    }
-  }
   const int slots = part <= kMostKeys ? static_cast<int>(part) : 0;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -44,6 +57,10 @@ gdpa_status_t launch_choose(const EvictParams& p, int ctas, int64_t part, const 
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (ctas > kEveryCluster) {
+    const gdpa_status_t wide = place_wide<THREADS>(cfg, dev, placed);
+    if (wide != GDPA_OK || !*placed) return wide;
+  }
   return cudaLaunchKernelEx(&cfg, gdpa_cache_choose_kernel<THREADS>, p, slots) == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
@@ -89,12 +106,13 @@ extern "C" gdpa_status_t gdpa_cache_evict(const gdpa_cache_t* cache, float* weig
   p.status = dev.status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t heads = (int64_t)B * cache->H;
-  // CTAs of a sequence and head: one, or where those are few as many as fill the SMs with 2048 tokens each.
-  int ctas = 1;
-  while (ctas < kMostCluster && heads * ctas * 2 <= dev.sms && most / (ctas * 2) >= 2048) ctas *= 2;
-  const int64_t part = ((most + ctas - 1) / ctas + 3) & ~(int64_t)3;
-  st = part <= 4096 || heads >= 2 * dev.sms ? launch_choose<256>(p, ctas, part, dev, s) : launch_choose<1024>(p, ctas, part, dev, s);
-  if (st != GDPA_OK) return st;
+  bool placed = false;
+  for (int widest = kMostCluster; !placed; widest = kEveryCluster) {
+    const ChooseShape c = choose_shape(heads, most, dev.sms, widest);
+    st = c.threads == 256 ? launch_choose<256>(p, c.ctas, c.part, dev, s, &placed)
+                          : launch_choose<1024>(p, c.ctas, c.part, dev, s, &placed);
+    if (st != GDPA_OK) return st;
+  }
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;

@@ -56,6 +56,23 @@ GDPA_HD OwnedRows owned_rows(const CacheSeq& s, int r) {
 // alone can lie below -2^31.)
 GDPA_HD int first_key(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
+// How an eviction's choice is launched: CTAs of a sequence and head, the most tokens
+// that each of them has, and its threads.
+constexpr int kMostCluster = 16, kEveryCluster = 8;  // CTAs of a cluster: at most; on every device
+struct ChooseShape {
+  int ctas, threads;
+  int64_t part;
+};
+inline ChooseShape choose_shape(int64_t heads, int64_t most, int sms, int widest) {
+  ChooseShape c;
+  // one, or where heads are few as many as fill the SMs with 2048 tokens each
+  c.ctas = 1;
+  while (c.ctas < widest && heads * c.ctas * 2 <= sms && most / (c.ctas * 2) >= 2048) c.ctas *= 2;
+  c.part = ((most + c.ctas - 1) / c.ctas + 3) & ~static_cast<int64_t>(3);
+  c.threads = c.part <= 4096 || heads >= 2 * sms ? 256 : 1024;
+  return c;
+}
+
 // Whether any of T rows of `len` elements, x_stride apart from 0 on, shares an
 // element with any of T rows y_stride apart from `apart` on (len <= both strides).
 inline bool rows_overlap(int64_t apart, int64_t x_stride, int64_t y_stride, int64_t len, int64_t T) {
