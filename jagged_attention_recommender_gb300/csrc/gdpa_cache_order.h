@@ -32,4 +32,11 @@ GDPA_HD bool bring_in_order(const Next& next, const Seen& seen, const Look& look
   return true;
 }
 
+// By how much a wait's limit (some seconds) is stretched: roles wait for whole items,
+// and an item takes as long as its rows do (2^27 of them about a second) and as the
+// search for it (2^26 sequences without rows 1.3 s).
+inline uint64_t wait_stretch(int64_t rows, int64_t sequences) {
+  return 1 + static_cast<uint64_t>(rows >> 27) + static_cast<uint64_t>(sequences >> 26);
+}
+
 }  // namespace gdpa

@@ -46,8 +46,7 @@ gdpa_status_t launch_tile(const CacheWeightsParams& w, const Device& dev, cudaSt
   p.heads = std::min(w.G, C::COLS);
   p.tokens = C::COLS / p.heads;
   p.parts = (w.G + p.heads - 1) / p.heads;
-  // An item takes as long as its rows do (2^27 of them about a second), and roles wait for whole items.
-  p.limit = bounded_wait_ns() * (1 + ((uint64_t)w.batch.T * w.G >> 27));
+  p.limit = bounded_wait_ns() * wait_stretch((int64_t)w.batch.T * w.G, w.batch.B);
   if ((st = encode_heads_3d(&p.tm_q, w.q, w.batch.T, w.Hq, D, w.q_stride, p.heads, p.tokens)) != GDPA_OK) return st;
   const int64_t keys = (int64_t)w.batch.max_pages << w.cache.lp, items = (keys + 255) / 256;
   const int ctas = static_cast<int>(std::min<int64_t>((int64_t)w.batch.B * w.cache.H * items, dev.sms));

@@ -33,3 +33,21 @@ def test_weights_beside_sequences_of_bad_offsets(new, bad):
     want, tol = hist.weights(x, lse, True, 0, scale, 1.0, None)
     at = ~np.isnan(want)
     assert (np.abs(got - want)[at] <= tol[at]).all() and (got[~at] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_weights_behind_many_sequences_without_rows(rows):
+    """Millions of sequences that bring nothing, in front of one that does."""
+    B, D, P = 1 << 22, 128, 16
+    x = ref.make(5, 1, 1, D, P, [P], [rows])
+    lse = np.float64(np.float32(ref.attend(x, 0, 0, float(np.float32(D ** -0.5)))[1]))
+    want, tol = hist.weights(x, lse, False, 0, float(np.float32(D ** -0.5)), 1.0, None)
+    page = int(x.table[0, 0])
+    x.lens, x.new = [P] * B, [0] * (B - 1) + [rows]
+    x.offsets = np.zeros(B + 1, np.int32)
+    x.offsets[-1] = rows
+    x.table = np.full((B, 1), page, np.int32)
+    got = run_weights(x, 0, 0, 1.0, None, lse, with_in=False, max_q=rows)
+    status()
+    at = ~np.isnan(want)
+    assert (np.abs(got - want)[at] <= tol[at]).all() and (got[~at] == SENTINEL).all()
