@@ -28,9 +28,8 @@ gdpa_status_t place_wide(const cudaLaunchConfig_t& cfg, const Device& dev, bool*
   int n = 0;
   const bool ok = cudaFuncSetAttribute(gdpa_cache_choose_kernel<THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                        1) == cudaSuccess;
-  // (an error says that no such cluster can be placed)
   *fits = ok && cudaOccupancyMaxActiveClusters(&n, gdpa_cache_choose_kernel<THREADS>, &cfg) == cudaSuccess && n > 0;
-  cudaGetLastError();
+  if (!*fits) cudaGetLastError();  // (an error of these two says that no such cluster can be placed)
   if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
   (*fits ? most : least)[dev.id] = bytes;
   return GDPA_OK;
