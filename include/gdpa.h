@@ -688,6 +688,11 @@ gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const void* q, int64
  * and codes from smaller ones are rounded to it: e4m3(code * 2^(e - e_new)), to
  * nearest even.
  *
+ * In a sequence that was cut a token's place is no longer its position, and the same
+ * place holds another token in every head.  gdpa_cache_fwd and gdpa_cache_weights go by places:
+ * causal = 1 still hides later tokens from earlier ones, but window_tokens > 0 counts the
+ * kept tokens of a head, however far apart their positions are.
+ *
  *   weights    device fp32 [num_pages, H, page_tokens] (gdpa_cache_weights), read
  *              in the old pages and written in the new ones; 16-byte aligned
  *   kv_lens    device int32 [B];  page_table  device int32 [B, max_pages]
@@ -701,8 +706,10 @@ gdpa_status_t gdpa_cache_weights(const gdpa_cache_t* cache, const void* q, int64
  *   new_lens   device int32 [B]: K; must not overlap kv_lens
  *
  * The cache's codes and scales are read in the old pages and written in the new
- * ones.  max_pages * page_tokens is below 2^31.  Asynchronous on `stream`, no allocation, no
- * workspace, no host read of device data (may be captured).  A sequence whose
+ * ones.  max_pages * page_tokens is below 2^31; a table wider than the sequences costs up
+ * to a fourth more (64 histories cut to 2048 tokens 112 us, with a table of twice the longest
+ * one's width 138).  Asynchronous on `stream`, no allocation, no workspace, no host
+ * read of device data (may be captured).  A sequence whose
  * length does not fit the table is skipped, with new_lens 0; tokens on an old page
  * out of range count as NaN and leave the new slot as it was, as does a new page
  * out of range; gdpa_device_status() then returns GDPA_ERR_INVALID_ARG.

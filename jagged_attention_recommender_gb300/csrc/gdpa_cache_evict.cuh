@@ -9,8 +9,11 @@
 // sequence and head, or a cluster of up to 16 where those are few (each with a
 // part of the tokens; histograms are added through distributed shared memory);
 // keys stay in shared memory.  Bound: latency, about 25 barriers and four rounds
-// of dependent loads a head: 24 us for 512 heads of 4846 tokens, 15 for 4 heads of
-// 130k.
+// of dependent loads a head: 24 us for 512 heads of 4846 tokens, 19 for 4 heads of
+// 130k (under a profiler).  What a CTA keeps in shared memory goes by the table's width:
+// a wide one leaves an SM fewer CTAs, and one of more than 40 960 tokens a CTA has every
+// digit read the weights anew (those 512 heads with their move 112 us; tables of twice, 4 and
+// 16 times the longest sequence 138, 135 and 117).
 //
 // Moving.  A warp moves 32 tokens of one head, two new blocks, K and then V: their scales,
 // the largest of each block, and the codes, which are copied as they are where

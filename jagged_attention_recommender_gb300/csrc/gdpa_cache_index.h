@@ -57,7 +57,20 @@ GDPA_HD OwnedRows owned_rows(const CacheSeq& s, int r) {
 GDPA_HD int first_key(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
 // How an eviction's choice is launched: CTAs of a sequence and head, the most tokens
-// that each of them has, and its threads.
+// that each of them has, and its threads.  Measured (us of a whole eviction in a graph,
+// by CTAs a head, with 256 / 1024 threads; heads of 128; the rule's in brackets):
+//     heads, tokens          1              2              4              8              16
+//       1, 131 072           -              -         51.4 / 28.4    32.1 / 21.6    23.5 / [20.6]
+//       4, 131 071           -              -         54.6 / 31.0    34.9 / 25.7    27.9 / [24.4]
+//       2, 8192         18.8 / 14.6    15.6 / 14.9   [13.2] / 14.3   12.5 / 14.6    14.2 / 17.3
+//       1, 4096         12.8 / 11.8   [11.9] / 12.7   11.0 / 12.8    11.2 / 13.0    12.6 / 15.5
+//      16, 32 768       51.9 / 29.2    36.4 / 26.4    27.0 / 21.7   [22.5] / 28.0   24.8 / 45.1
+//      72, 16 384       42.2 / 29.4    35.7 / [26.7]  28.9 / 34.8    27.8 / 65.5         -
+//     128, 8192         47.4 / [35.8]  40.6 / 44.5    36.8 / 61.2    44.2 / 106          -
+//     256, 8192         78.5 / [65.6]  64.7 / 82.6    65.5 / 111          -              -
+//     304, 8192        [87.9] / 72.9   71.1 / 91.7    75.2 / 128          -              -
+//     512, 8192       [111.8] / 121     114 / 152          -              -              -
+//     320, 4096        [43.8] / 50.7   42.8 / 72.6         -              -              -
 constexpr int kMostCluster = 16, kEveryCluster = 8;  // CTAs of a cluster: at most; on every device
 struct ChooseShape {
   int ctas, threads;
@@ -65,10 +78,11 @@ struct ChooseShape {
 };
 inline ChooseShape choose_shape(int64_t heads, int64_t most, int sms, int widest) {
   ChooseShape c;
-  // one, or where heads are few as many as fill the SMs with 2048 tokens each
+  // one, or where heads are few as many as the SMs hold with 2048 tokens each
   c.ctas = 1;
   while (c.ctas < widest && heads * c.ctas * 2 <= sms && most / (c.ctas * 2) >= 2048) c.ctas *= 2;
   c.part = ((most + c.ctas - 1) / c.ctas + 3) & ~static_cast<int64_t>(3);
+  // few tokens do not keep 1024 threads busy, and of many heads several CTAs share an SM
   c.threads = c.part <= 4096 || heads >= 2 * sms ? 256 : 1024;
   return c;
 }
